@@ -20,6 +20,9 @@ GQ_FORMAT_Q4_0 = 0
 GQ_FORMAT_Q8_0 = 1
 GQ_FORMAT_Q4_K = 2
 GQ_FORMAT_Q6_K = 3
+GQ_TYPE_F32 = 0
+GQ_TYPE_F16 = 1
+GQ_TYPE_BF16 = 2
 GQ_MAX_K = 49152
 GQ_MAX_TOPK = 64
 
@@ -42,10 +45,12 @@ class GQError(RuntimeError):
         super().__init__(f"{what}: {status_string(status)} ({status})")
 
 
-def _declare(L):
+def _declare(dll):
     P = ctypes.c_void_p
     I = ctypes.c_int
     S = ctypes.c_size_t
+    L = ctypes.c_longlong
+    F = ctypes.c_float
     sig = {
         "gq_status_string": ([I], ctypes.c_char_p),
         "gq_packed_bytes": ([I, I, I], S),
@@ -66,11 +71,16 @@ def _declare(L):
         "gq_q4_0_gemm_workspace_bytes": ([I, I], S),
         "gq_q4_0_gemm_q8act": ([P, P, P, P, P, S, I, I, I, P], I),
         "gq_q4_0_gemm_block_dots": ([P, P, P, P, S, I, I, I, P], I),
+        "gq_kv_cache_bytes": ([I, I, I, I], S),
+        "gq_kv_append_q8_0": ([P, L, P, L, I, P, P, P, P, I, I, I, I, I, I, I, P], I),
+        "gq_kv_read_q8_0": ([P, P, P, P, P, L, P, L, I, I, I, I, I, I, I, I, P], I),
+        "gq_kv_attention_workspace_bytes": ([I, I, I], S),
+        "gq_kv_attention_q8_0": ([P, L, P, P, P, P, P, L, I, F, F, I, P, S, I, I, I, I, I, I, I, I, P], I),
         "gq_device_status": ([I], I),
         "gq_selftest_bounded_wait": ([P], I),
     }
     for name, (args, res) in sig.items():
-        fn = getattr(L, name)
+        fn = getattr(dll, name)
         fn.argtypes = args
         fn.restype = res
 
@@ -104,6 +114,17 @@ def _ptr(t):
         raise ValueError("libgq takes CUDA tensors (device memory)")
     if not t.is_contiguous():
         raise ValueError("libgq takes contiguous tensors")
+    return t.data_ptr()
+
+
+def _rows(t):
+    """Device address of a token array: rows with contiguous elements, any stride between them."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise ValueError("libgq takes CUDA tensors (device memory)")
+    if t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError("libgq takes token arrays of two dimensions with contiguous rows")
     return t.data_ptr()
 
 
@@ -204,6 +225,37 @@ def gq_q4_0_gemm_q8act(W, Xq, dx, Y, workspace, workspace_bytes, rows, K, M, str
 def gq_q4_0_gemm_block_dots(W, Xq, D, workspace, workspace_bytes, rows, K, M, stream=None):
     _check(lib().gq_q4_0_gemm_block_dots(_ptr(W), _ptr(Xq), _ptr(D), _ptr(workspace), int(workspace_bytes),
                                          rows, K, M, _stream(stream)), "gq_q4_0_gemm_block_dots")
+
+
+def gq_kv_cache_bytes(n_pages, page_tokens, kv_heads, head_dim) -> int:
+    return int(lib().gq_kv_cache_bytes(n_pages, page_tokens, kv_heads, head_dim))
+
+
+def gq_kv_append_q8_0(K, ldk, V, ldv, type, cache, block_table, kv_len, q_start, n_pages, max_pages, page_tokens,
+                      kv_heads, head_dim, n_seq, n_tokens, stream=None):
+    _check(lib().gq_kv_append_q8_0(_rows(K), ldk, _rows(V), ldv, type, _ptr(cache), _ptr(block_table), _ptr(kv_len),
+                                   _ptr(q_start), n_pages, max_pages, page_tokens, kv_heads, head_dim, n_seq, n_tokens,
+                                   _stream(stream)), "gq_kv_append_q8_0")
+
+
+def gq_kv_read_q8_0(cache, block_table, kv_len, q_start, K, ldk, V, ldv, type, n_pages, max_pages, page_tokens,
+                    kv_heads, head_dim, n_seq, n_tokens, stream=None):
+    _check(lib().gq_kv_read_q8_0(_ptr(cache), _ptr(block_table), _ptr(kv_len), _ptr(q_start), _rows(K), ldk, _rows(V),
+                                 ldv, type, n_pages, max_pages, page_tokens, kv_heads, head_dim, n_seq, n_tokens,
+                                 _stream(stream)), "gq_kv_read_q8_0")
+
+
+def gq_kv_attention_workspace_bytes(heads, kv_heads, head_dim) -> int:
+    return int(lib().gq_kv_attention_workspace_bytes(heads, kv_heads, head_dim))
+
+
+def gq_kv_attention_q8_0(Q, ldq, cache, block_table, kv_len, q_start, O, ldo, type, scale, softcap, window, workspace,
+                         workspace_bytes, heads, n_pages, max_pages, page_tokens, kv_heads, head_dim, n_seq, n_tokens,
+                         stream=None):
+    _check(lib().gq_kv_attention_q8_0(_rows(Q), ldq, _ptr(cache), _ptr(block_table), _ptr(kv_len), _ptr(q_start),
+                                      _rows(O), ldo, type, scale, softcap, window, _ptr(workspace), workspace_bytes,
+                                      heads, n_pages, max_pages, page_tokens, kv_heads, head_dim, n_seq, n_tokens,
+                                      _stream(stream)), "gq_kv_attention_q8_0")
 
 
 def gq_selftest_bounded_wait(stream=None):

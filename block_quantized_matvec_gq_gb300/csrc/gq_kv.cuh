@@ -1,0 +1,140 @@
+// gq_kv.cuh -- the paged Q8_0 key/value cache: its record layout, the batch
+// description that the kernels take, and the code conversions they share.
+// The layout and the batch are specified in include/gq_kv.h.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "gq_host.h"
+#include "gq_internal.cuh"
+#include "gq_kv.h"
+
+namespace gq {
+namespace kv {
+
+constexpr int kRec = 16;          // tokens per record
+constexpr float kMaxD = 515.5f;   // largest block scale: 127 * 515.5 = 65468.5 is finite in fp16
+
+// The batch and the cache as the kernels see them.
+struct Batch {
+    const int32_t *table, *kv_len, *q_start;
+    int n_pages, max_pages, page_tokens, kv_heads, n_seq, n_tokens;
+    int *status;  // device status word
+};
+
+__host__ __device__ __forceinline__ constexpr int rec_bytes(int D) { return 34 * D; }
+// Byte offset of block b of token t's key codes in a record, of token t's key
+// scale, of a value word's 16-byte chunk c of token group g, and of a value
+// scale.
+__host__ __device__ __forceinline__ constexpr int k_key(int t, int nb)
+{
+    return nb > 2 ? ((t & 1) | ((t >> 1) & 2)) : ((t >> 2) & 1);
+}
+__host__ __device__ __forceinline__ constexpr int k_code_off(int t, int b, int nb)
+{
+    return 32 * (t * nb + (b ^ k_key(t, nb)));
+}
+__host__ __device__ __forceinline__ constexpr int k_scale_off(int t, int b, int D) { return 16 * D + 2 * (t * (D / 32) + b); }
+__host__ __device__ __forceinline__ constexpr int v_chunk_off(int g, int c, int D) { return 17 * D + 4 * D * g + 16 * (c ^ (2 * g)); }
+__host__ __device__ __forceinline__ constexpr int v_scale_off(int t, int b, int D) { return 33 * D + 2 * (b * 16 + t); }
+
+__device__ __forceinline__ void flag_shape(const Batch &B)
+{
+    if (B.status) atomicExch(B.status, GQ_ERR_SHAPE);
+}
+
+// One sequence of the batch, with what the lists say brought into bounds.
+struct Seq {
+    int row0;   // first token row
+    int n;      // new tokens (rows)
+    int kv;     // cached tokens
+    int first;  // position of row0 (kv - n; negative if the lists disagree)
+};
+__device__ __forceinline__ Seq load_seq(const Batch &B, int b)
+{
+    Seq s;
+    const int r0 = __ldg(B.q_start + b), r1 = __ldg(B.q_start + b + 1);
+    const int kv = __ldg(B.kv_len + b);
+    s.row0 = min(max(r0, 0), B.n_tokens);
+    const int r1c = min(max(r1, s.row0), B.n_tokens);
+    s.n = r1c - s.row0;
+    const long long room = static_cast<long long>(B.max_pages) * B.page_tokens;
+    s.kv = kv < 0 ? 0 : (kv > room ? static_cast<int>(room) : kv);
+    s.first = s.kv - s.n;
+    if (s.row0 != r0 || r1c != r1 || s.kv != kv) flag_shape(B);
+    return s;
+}
+
+// Page of position `pos` of sequence b, or -1 (flagged) if the table names none.
+__device__ __forceinline__ int page_of(const Batch &B, int b, int pos)
+{
+    const int pg = __ldg(B.table + static_cast<long long>(b) * B.max_pages + pos / B.page_tokens);
+    if (static_cast<unsigned>(pg) < static_cast<unsigned>(B.n_pages)) return pg;
+    flag_shape(B);
+    return -1;
+}
+
+// Byte offset of the record of head h holding position pos of page pg.
+__device__ __forceinline__ long long rec_off(const Batch &B, int pg, int h, int pos, int D)
+{
+    const int per = B.page_tokens / kRec;
+    return ((static_cast<long long>(pg) * B.kv_heads + h) * per + (pos % B.page_tokens) / kRec) * rec_bytes(D);
+}
+
+// ---------------------------------------------------------------- element types
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ float2 half2_f2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+__device__ __forceinline__ uint32_t f2_half2(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t f2_bf162(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Four consecutive elements at p (16-byte aligned for f32, 8-byte for the 16-bit types).
+template <int TYPE>
+__device__ __forceinline__ float4 load4(const void *p)
+{
+    if (TYPE == GQ_TYPE_F32) return __ldg(static_cast<const float4 *>(p));
+    const uint2 w = __ldg(static_cast<const uint2 *>(p));
+    if (TYPE == GQ_TYPE_BF16) return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+    const float2 a = half2_f2(w.x), b = half2_f2(w.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+template <int TYPE>
+__device__ __forceinline__ void store4(void *p, float4 v)
+{
+    if (TYPE == GQ_TYPE_F32) {
+        *static_cast<float4 *>(p) = v;
+    } else if (TYPE == GQ_TYPE_BF16) {
+        *static_cast<uint2 *>(p) = make_uint2(f2_bf162(v.x, v.y), f2_bf162(v.z, v.w));
+    } else {
+        *static_cast<uint2 *>(p) = make_uint2(f2_half2(v.x, v.y), f2_half2(v.z, v.w));
+    }
+}
+__host__ __device__ __forceinline__ constexpr int type_size(int type) { return type == GQ_TYPE_F32 ? 4 : 2; }
+
+// Code bytes 0, 1 (sel 0x4140) or 2, 3 (sel 0x4342) of w -> f16x2, exact: a
+// byte u placed under the exponent of 1024 is 1024 + u, and the code is
+// u - 128.
+__device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sel)
+{
+    const uint32_t m = __byte_perm(w, 0x64646464u, sel);
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&m), __float2half2_rn(1152.0f));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+}  // namespace kv
+
+// gq_kv_attn.cu
+int launch_kv_attention(const void *Q, long long ldq, const uint8_t *cache, const kv::Batch &B, void *O, long long ldo,
+                        int type, float scale, float softcap, int window, void *ws, int heads, int head_dim,
+                        cudaStream_t s);
+size_t kv_attention_workspace_bytes(int head_dim);
+
+}  // namespace gq
