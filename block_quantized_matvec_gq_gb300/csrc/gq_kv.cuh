@@ -136,5 +136,11 @@ int launch_kv_attention(const void *Q, long long ldq, const uint8_t *cache, cons
                         int type, float scale, float softcap, int window, void *ws, int heads, int head_dim,
                         cudaStream_t s);
 size_t kv_attention_workspace_bytes(int head_dim);
+// gq_kv_chunk.cu: the tensor-core form for many query rows (16-bit types);
+// `counter` and `part` are its parts of the workspace.
+size_t kv_chunk_part_bytes(int head_dim);
+int kv_chunk_counters();
+int launch_kv_chunk(const void *Q, long long ldq, const uint8_t *cache, const kv::Batch &B, void *O, long long ldo, int type,
+                    float scale, float softcap, int window, int *counter, float *part, int heads, int head_dim, cudaStream_t s);
 
 }  // namespace gq

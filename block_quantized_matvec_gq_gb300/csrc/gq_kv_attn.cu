@@ -53,7 +53,6 @@ struct SplitCfg {
 
 // Partial results: per CTA two slots of {O[8][D], m[8], l[8]} f32.
 __host__ __device__ constexpr size_t slot_floats(int D) { return kRows * (D + 2); }
-constexpr size_t kCounterBytes = kMaxCtas * sizeof(int);
 
 struct Args {
     const uint8_t *Q, *cache;
@@ -541,15 +540,27 @@ static int launch_split(const Args &A, const Batch &B, cudaStream_t s)
 
 }  // namespace kv
 
+// Workspace: the split form's counters, the chunk form's, then the partial
+// results of whichever runs.
+static size_t counter_bytes() { return ((kv::kMaxCtas + kv_chunk_counters()) * sizeof(int) + 127) / 128 * 128; }
+
 size_t kv_attention_workspace_bytes(int head_dim)
 {
-    return kv::kCounterBytes + 2ull * kv::kMaxCtas * kv::slot_floats(head_dim) * sizeof(float);
+    const size_t split = 2ull * kv::kMaxCtas * kv::slot_floats(head_dim) * sizeof(float), chunk = kv_chunk_part_bytes(head_dim);
+    return counter_bytes() + (split > chunk ? split : chunk);
 }
 
 int launch_kv_attention(const void *Q, long long ldq, const uint8_t *cache, const kv::Batch &B, void *O, long long ldo,
                         int type, float scale, float softcap, int window, void *ws, int heads, int head_dim,
                         cudaStream_t s)
 {
+    int *counter = static_cast<int *>(ws);
+    float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + counter_bytes());
+    // query rows per sequence and kv head, on average
+    const long long rows = static_cast<long long>(B.n_tokens) * (heads / B.kv_heads) / B.n_seq;
+    if (type != GQ_TYPE_F32 && rows >= 64)
+        return launch_kv_chunk(Q, ldq, cache, B, O, ldo, type, scale, softcap, window, counter + kv::kMaxCtas, part, heads,
+                               head_dim, s);
     const int el = kv::type_size(type);
     kv::Args A;
     A.Q = static_cast<const uint8_t *>(Q);
@@ -562,8 +573,8 @@ int launch_kv_attention(const void *Q, long long ldq, const uint8_t *cache, cons
     A.window = window;
     A.scale = scale;
     A.softcap = softcap;
-    A.counter = static_cast<int *>(ws);
-    A.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kv::kCounterBytes);
+    A.counter = counter;
+    A.part = part;
     switch (head_dim) {
     case 64: return kv::launch_split<64>(A, B, s);
     case 128: return kv::launch_split<128>(A, B, s);
