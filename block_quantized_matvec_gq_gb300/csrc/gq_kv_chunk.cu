@@ -15,7 +15,7 @@
 //                tensor memory, running reference m and sum l, p back to
 //                tensor memory as the A operand of p v; the query operand and
 //                the result rows.
-//   dequantizers eight warps: codes and scales of a raw stage -> the f16 operand
+//   dequantizers four warps (eight for head_dim 256): codes and scales of a raw stage -> the f16 operand
 //                tile d * q (11 bits, one rounding) in the K-major layout; keys
 //                along head_dim, values along the tokens (the cache's words
 //                hold four tokens of one element, so neither is transposed).
@@ -55,12 +55,17 @@ struct Cfg {
     static constexpr int kBars = 2 * kRaws + 2 * kOps + 10;
     static constexpr int kOffMisc = kOffBar + 8 * kBars;
     static constexpr int kSmem = kOffMisc + 512;
+    // four warpgroups: softmax (one per row tile), dequantizers, {producer, mma}
     static constexpr int kSoftWarps = 4 * kMt;
-    static constexpr int kDeqWarps = 8;
-    static constexpr int kProdWarp = kSoftWarps + kDeqWarps;
-    static constexpr int kMmaWarp = kProdWarp + 1;
-    static constexpr int kThreads = 32 * (kMmaWarp + 1);
-    static constexpr int kWarpsAll = kMmaWarp + 1;
+    static constexpr int kDeqWarps = 12 - kSoftWarps;
+    static constexpr int kProdWarp = 12;
+    static constexpr int kMmaWarp = 13;
+    static constexpr int kWarpsAll = 16;
+    static constexpr int kThreads = 32 * kWarpsAll;
+    // Registers per thread after the split; with kKt = 128 a softmax thread
+    // holds a whole score row.  The shares add up to the launch's 512 x 128.
+    static constexpr int kSoftRegs = kMt == 2 ? 184 : 0, kDeqRegs = 88, kRestRegs = 56;
+    static_assert(kMt == 1 || 256 * kSoftRegs + 128 * kDeqRegs + 128 * kRestRegs <= 512 * 128, "register split");
     static_assert(kOffOp % 128 == 0 && kOffRaw % 128 == 0 && kOffBar % 8 == 0 && kSmem <= 232448, "shared memory layout");
 };
 constexpr int kTmemCols = 512;
@@ -169,17 +174,25 @@ __device__ __forceinline__ float soft_cap(float x, float cap, float inv_cap)
 }
 
 // ---------------------------------------------------------------- tensor memory
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
+// 32 columns of this thread's lane; tmem_wait_ld has to follow before r is used.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float *r)
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
         : "r"(taddr)
         : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(float (&r)[N])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));  // no use of r moves above the wait
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
 {
@@ -196,16 +209,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -217,6 +225,14 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uin
         " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(tmem_d),
         "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
@@ -347,7 +363,7 @@ __device__ __forceinline__ float load_query(const uint8_t *src, bool live, bool 
     return pow2i(e);
 }
 
-template <int D>
+template <int D, bool kCap>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, Batch B)
 {
     using C = Cfg<D>;
@@ -454,22 +470,23 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
     __syncthreads();
     Walk w = s_walk;
     volatile int *abort = &s_abort;
-
-    if (w.left > 0 && warp < C::kSoftWarps) {
+    // The register split stands at the head of each warpgroup's branch, where
+    // the compiler takes it as the limit of what follows.
+    if (warp < C::kSoftWarps) {
+        if (C::kMt == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMt == 2 ? C::kSoftRegs : 128));
         // ================================================================ softmax: thread = query row
         const int mt = warp >> 2;                       // row tile
         const int row = threadIdx.x & 127;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t o_addr = lane_addr + kOCol + mt * D;
         uint8_t *q_op = smem + mt * C::kQ;
-        const bool capped = A.softcap > 0.f;
-        const float inv_cap = capped ? 1.0f / A.softcap : 0.f;
+        const float inv_cap = kCap ? 1.0f / A.softcap : 0.f;
         constexpr float kLog2e = 1.4426950408889634f;
         bool ok = true;
         uint32_t n_pv = 0;          // tiles of this row tile so far: scores taken, p v products asked for
         uint32_t n_piece = 0;       // pieces of this row tile so far
         uint32_t tile_no = 0;       // key tiles of the CTA so far
-        while (true) {
+        while (w.left > 0) {
             const Seq s = load_seq(B, w.b);
             const Item it = item_of<D>(s, A, w.st);
             const int to = static_cast<int>(min(static_cast<long long>(it.tiles), w.from + w.left));
@@ -484,8 +501,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
                 const uint8_t *src = A.Q + (s.row0 + tok) * A.ldq + static_cast<long long>(head) * D * 2;
                 const float f = A.type == GQ_TYPE_BF16 ? load_query<D, GQ_TYPE_BF16>(src, live, A.scale < 0.f, q_op, row)
                                                        : load_query<D, GQ_TYPE_F16>(src, live, A.scale < 0.f, q_op, row);
-                float zs = fabsf(A.scale) * f;
-                if (!capped) zs *= kLog2e;
+                // a factor of 0 would turn hidden scores (-inf) into NaN
+                const float zs = fmaxf(fabsf(A.scale) * f * (kCap ? 1.0f : kLog2e), 1e-37f);
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full + 8 * mt);
@@ -502,31 +519,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
                     // every row of the warp sees the whole tile?
                     const bool edge = __any_sync(0xffffffffu, p0 < row_lo || p0 + C::kKt - 1 > row_hi) ||
                                       recs != (1u << C::kRecs) - 1u;
-                    float top = -INFINITY;
+                    float v[C::kKt];
 #pragma unroll
-                    for (int c = 0; c < C::kKt; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(s_addr + c, v);
-                        if (edge) {
+                    for (int c = 0; c < C::kKt; c += 32) tmem_ld32_async(s_addr + c, v + c);
+                    tmem_wait_ld(v);
+                    if (kCap) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const int pk = p0 + c + k;
-                                const bool hide = pk < row_lo || pk > row_hi || !((recs >> ((c + k) / kRec)) & 1u);
-                                top = fmaxf(top, hide ? -INFINITY : __uint_as_float(v[k]));
-                            }
-                        } else {
-                            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-                            for (int k = 0; k < 32; k += 4) {
-                                t0 = fmaxf(t0, fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
-                                t1 = fmaxf(t1, fmaxf(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])));
-                            }
-                            top = fmaxf(top, fmaxf(t0, t1));
-                        }
+                        for (int k = 0; k < C::kKt; ++k) v[k] = soft_cap(v[k] * zs, A.softcap, inv_cap) * kLog2e;
                     }
-                    // the cap and the scale (its sign is in q) keep the order of the scores
-                    float zt = top == -INFINITY ? top : top * zs;
-                    if (capped && top != -INFINITY) zt = soft_cap(zt, A.softcap, inv_cap) * kLog2e;
+                    if (edge) {
+                        const int a = row_lo - p0, b = row_hi - p0;
+#pragma unroll
+                        for (int k = 0; k < C::kKt; ++k)
+                            if (k < a || k > b || !((recs >> (k / kRec)) & 1u)) v[k] = -INFINITY;
+                    }
+                    float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
+#pragma unroll
+                    for (int k = 4; k < C::kKt; k += 8) {
+                        t0 = fmaxf(t0, fmaxf(v[k], k + 4 < C::kKt ? v[k + 4] : v[k]));
+                        t1 = fmaxf(t1, fmaxf(v[k + 1], k + 4 < C::kKt ? v[k + 5] : v[k]));
+                        t2 = fmaxf(t2, fmaxf(v[k + 2], k + 4 < C::kKt ? v[k + 6] : v[k]));
+                        t3 = fmaxf(t3, fmaxf(v[k + 3], k + 4 < C::kKt ? v[k + 7] : v[k]));
+                    }
+                    // the scale (its sign is in q) keeps the order of the scores
+                    const float zt = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * (kCap ? 1.0f : zs);
                     if (__any_sync(0xffffffffu, zt > m + kGrow)) {
                         const float nm = fmaxf(m, zt), g = ex2(m - nm);
                         m = nm;
@@ -538,48 +554,34 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t v[32];
-                                tmem_ld32(o_addr + c, v);
+                            for (int c = 0; c < D; c += 8) {
+                                uint32_t x[8];
+                                tmem_ld8(o_addr + c, x);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * g);
-                                tmem_st32(o_addr + c, v);
+                                for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * g);
+                                tmem_st8(o_addr + c, x);
                             }
                             tmem_wait_st();
                         }
                     }
-                    const float ref = kPHead - m;
+                    const float2 ref = make_float2(kPHead - m, kPHead - m), zs2 = kCap ? make_float2(1.f, 1.f) : make_float2(zs, zs);
+                    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
                     for (int c = 0; c < C::kKt; c += 32) {
-                        uint32_t v[32], p[16];
-                        tmem_ld32(s_addr + c, v);
-                        float sum0 = 0.f, sum1 = 0.f;
+                        uint32_t p[16];
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            float a, b;
-                            if (!capped) {
-                                a = fmaf(__uint_as_float(v[k]), zs, ref);
-                                b = fmaf(__uint_as_float(v[k + 1]), zs, ref);
-                            } else {
-                                a = fmaf(soft_cap(__uint_as_float(v[k]) * zs, A.softcap, inv_cap), kLog2e, ref);
-                                b = fmaf(soft_cap(__uint_as_float(v[k + 1]) * zs, A.softcap, inv_cap), kLog2e, ref);
-                            }
-                            a = ex2(a);
-                            b = ex2(b);
-                            if (edge) {
-                                const int pk = p0 + c + k;
-                                const bool rec_ok = (recs >> ((c + k) / kRec)) & 1u;
-                                if (pk < row_lo || pk > row_hi || !rec_ok) a = 0.f;
-                                if (pk + 1 < row_lo || pk + 1 > row_hi || !rec_ok) b = 0.f;
-                            }
-                            sum0 += a;
-                            sum1 += b;
-                            p[k / 2] = f2_half2(a, b);
+                        for (int k = 0; k < 32; k += 4) {
+                            float2 a = ffma2(make_float2(v[c + k], v[c + k + 1]), zs2, ref);
+                            float2 b = ffma2(make_float2(v[c + k + 2], v[c + k + 3]), zs2, ref);
+                            a.x = ex2(a.x), a.y = ex2(a.y), b.x = ex2(b.x), b.y = ex2(b.y);
+                            sum0 = __fadd2_rn(sum0, a);
+                            sum1 = __fadd2_rn(sum1, b);
+                            p[k / 2] = f2_half2(a.x, a.y);
+                            p[k / 2 + 1] = f2_half2(b.x, b.y);
                         }
-                        l += sum0 + sum1;
-                        // p of columns c .. c + 31 goes over score columns that have been read
-                        tmem_st16(s_addr + c / 2, p);
+                        tmem_st16(s_addr + c / 2, p);  // over the scores, which are in registers
                     }
+                    l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -674,12 +676,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
             tile_no += done;
             if (!next_piece<D>(w, B, A, done)) break;
         }
-    } else if (w.left > 0 && warp < C::kProdWarp) {
+    } else if (warp < C::kProdWarp) {
+        if (C::kMt == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMt == 2 ? C::kDeqRegs : 128));
         // ================================================================ dequantizers
         const int tid = threadIdx.x - 32 * C::kSoftWarps;
         bool ok = true;
         uint32_t n = 0, tile_no = 0;  // operand tiles, key tiles
-        while (ok) {
+        while (ok && w.left > 0) {
             const Seq s = load_seq(B, w.b);
             const Item it = item_of<D>(s, A, w.st);
             const int to = static_cast<int>(min(static_cast<long long>(it.tiles), w.from + w.left));
@@ -710,7 +713,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
             }
             if (!ok || !next_piece<D>(w, B, A, to - w.from)) break;
         }
-    } else if (w.left > 0 && warp == C::kProdWarp) {
+    } else {
+        if (C::kMt == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMt == 2 ? C::kRestRegs : 128));
+    if (w.left > 0 && warp == C::kProdWarp) {
         // ================================================================ producer: one lane per record
         bool ok = true;
         uint32_t n = 0, tile_no = 0;
@@ -755,7 +760,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
         // copies in flight land before the CTA's memory is given up
         for (uint32_t i = n > C::kRaws ? n - C::kRaws : 0; i < n; ++i)
             wait_warp(raw_full + 8 * (i % C::kRaws), (i / C::kRaws) & 1, abort, B.status);
-    } else if (w.left > 0 && lane == 0) {
+    } else if (w.left > 0 && warp == C::kMmaWarp && elect_one()) {
         // ================================================================ mma: one thread
         constexpr uint32_t kIdQk = idesc_f16(128, C::kKt, false), kIdPv = idesc_f16(128, D, false);
         bool ok = true;
@@ -769,20 +774,31 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
             return ok;
         };
         // scores of row tile mt with the keys in operand stage os, into buffer buf
+        // The descriptors of successive K steps differ by a constant in their
+        // low word: one add per operand and MMA.  (Building each descriptor
+        // from its address made this thread the limit: 113 cycles per MMA
+        // against the tensor core's 64 for 128 x 128 x 16.)
+        constexpr uint32_t kHi = (128u >> 4) | (1u << 14);  // 128 bytes between row groups; descriptor version 1
+        auto desc_lo = [](uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); };
+        auto desc = [](uint32_t lo) {
+            uint64_t d;
+            asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kHi));
+            return d;
+        };
+        const uint32_t q_lo = desc_lo(base, 2048), k_lo = desc_lo(base + C::kOffOp, C::kKt * 16),
+                       v_lo = desc_lo(base + C::kOffOp, D * 16);
         auto qk = [&](int mt, uint32_t os, int buf) {
-            const uint32_t a = base + mt * C::kQ, b = base + C::kOffOp + os * C::kOp;
+            const uint32_t a = q_lo + mt * (C::kQ >> 4), b = k_lo + os * (C::kOp >> 4);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-                mma_f16(tmem + kSCol * buf, smem_desc(a + k * 4096, 2048, 128),
-                        smem_desc(b + k * 2 * C::kKt * 16, C::kKt * 16, 128), kIdQk, k > 0);
+                mma_f16(tmem + kSCol * buf, desc(a + k * 256), desc(b + k * 2 * C::kKt), kIdQk, k > 0);
             mma_commit(s_full + 8 * buf);
         };
         auto pv = [&](int mt, uint32_t os, int buf, bool first) {
-            const uint32_t b = base + C::kOffOp + os * C::kOp;
+            const uint32_t b = v_lo + os * (C::kOp >> 4);
 #pragma unroll
             for (int k = 0; k < C::kKt / 16; ++k)
-                mma_f16_ts(tmem + kOCol + mt * D, tmem + kSCol * buf + 8 * k, smem_desc(b + k * 2 * D * 16, D * 16, 128), kIdPv,
-                           !first || k > 0);
+                mma_f16_ts(tmem + kOCol + mt * D, tmem + kSCol * buf + 8 * k, desc(b + k * 2 * D), kIdPv, !first || k > 0);
             mma_commit(pv_done + 8 * mt);
         };
         while (ok) {
@@ -848,6 +864,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
             if (!next_piece<D>(w, B, A, nt)) break;
         }
     }
+    }
 
     tc_fence_before();
     __syncthreads();
@@ -862,13 +879,19 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
 constexpr int kMaxCtas = 160;
 constexpr size_t part_floats(int D) { return 2ull * kMaxCtas * (D == 256 ? 1 : 2) * 128 * (D + 2); }
 
+template <int D, bool kCap>
+static int launch_cap(const Args &A, const Batch &B, cudaStream_t s)
+{
+    using C = Cfg<D>;
+    if (ctas_per_sm(reinterpret_cast<const void *>(&k_kv_attn_chunk<D, kCap>), C::kThreads, C::kSmem) < 1) return GQ_ERR_CUDA;
+    const int grid = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+    return status_from(launch_pdl(k_kv_attn_chunk<D, kCap>, dim3(grid), dim3(C::kThreads), C::kSmem, s, A, B));
+}
+
 template <int D>
 static int launch(const Args &A, const Batch &B, cudaStream_t s)
 {
-    using C = Cfg<D>;
-    if (ctas_per_sm(reinterpret_cast<const void *>(&k_kv_attn_chunk<D>), C::kThreads, C::kSmem) < 1) return GQ_ERR_CUDA;
-    const int grid = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
-    return status_from(launch_pdl(k_kv_attn_chunk<D>, dim3(grid), dim3(C::kThreads), C::kSmem, s, A, B));
+    return A.softcap > 0.f ? launch_cap<D, true>(A, B, s) : launch_cap<D, false>(A, B, s);
 }
 
 }  // namespace chunk
