@@ -2,11 +2,11 @@
 // entry points of include/gq_kv.h.
 //
 // One warp handles one unit: a group of four tokens (one word of the value
-// layout) of one 32-block of one kv head's keys or values.  Lane 8 j + s
-// holds elements 4 s .. 4 s + 3 of token j, as in the activation quantizer.
-// The keys' codes are stored as they are (32 bytes per token and block); the
+// layout) of two neighbouring 32-blocks of one kv head's keys or values.  Lane
+// 16 i + 4 j + s holds elements 8 s .. 8 s + 7 of block i of token j.  The
+// keys' codes are stored as they are (32 bytes per token and block); the
 // values' 4 x 4 byte squares are transposed between lanes j with two
-// shuffles, so a lane writes the word of one element with the four tokens'
+// shuffles, so a lane writes the words of two elements with the four tokens'
 // codes.  A group that is only partly new (the ends of a chunk, every decode
 // step) writes the new tokens' bytes alone.
 #include <math.h>
@@ -24,31 +24,78 @@ constexpr int kThreads = 256;
 // floor((n + 6) / 4) <= floor(n / 4) + 2 groups, so the slots of two
 // sequences never overlap, and there are n_tokens / 4 + 2 n_seq of them.
 // Finds the sequence of `slot` by a 32-way search (every lane of the warp
-// takes part).
-__device__ __forceinline__ int find_seq(const Batch &B, long long slot)
+// takes part) and what the lists say of it: the last step's lanes hold
+// neighbouring sequences and load all three numbers at once.
+__device__ __forceinline__ Seq find_seq(const Batch &B, long long slot, int &b)
 {
     const int lane = threadIdx.x & 31;
     int lo = 0, n = B.n_seq;  // the answer lies in [lo, lo + n)
-    while (n > 1) {
+    while (n > 32) {
         const int step = (n + 31) / 32;
-        const int b = lo + lane * step;
-        const bool at = b < lo + n && (__ldg(B.q_start + b) >> 2) + 2ll * b <= slot;
-        // the starts rise with b: the lanes that hold are a prefix
+        const int i = lo + lane * step;
+        const bool at = i < lo + n && (__ldg(B.q_start + i) >> 2) + 2ll * i <= slot;
+        // the starts rise with i: the lanes that hold are a prefix
         const int k = max(__popc(__ballot_sync(0xffffffffu, at)) - 1, 0);
         n = min(step, n - k * step);
         lo += k * step;
     }
-    return lo;
+    const int i = min(lo + lane, B.n_seq - 1);
+    const int r0 = __ldg(B.q_start + i), r1 = __ldg(B.q_start + i + 1), kv = __ldg(B.kv_len + i);
+    const bool at = lane < n && (r0 >> 2) + 2ll * i <= slot;
+    const int k = max(__popc(__ballot_sync(0xffffffffu, at)) - 1, 0);
+    b = lo + k;
+    return seq_of(B, __shfl_sync(0xffffffffu, r0, k), __shfl_sync(0xffffffffu, r1, k), __shfl_sync(0xffffffffu, kv, k));
 }
 
-// 4 x 4 byte transpose between the lanes j = lane / 8 that share lane % 8.
+// 4 x 4 byte transpose between the lanes j = lane / 4 % 4 that agree elsewhere.
 __device__ __forceinline__ uint32_t transpose4(uint32_t x)
 {
-    const int j = (threadIdx.x >> 3) & 3;
-    uint32_t r = __shfl_xor_sync(0xffffffffu, x, 8);
+    const int j = (threadIdx.x >> 2) & 3;
+    uint32_t r = __shfl_xor_sync(0xffffffffu, x, 4);
     x = __byte_perm(x, r, (j & 1) ? 0x3715u : 0x6240u);
-    r = __shfl_xor_sync(0xffffffffu, x, 16);
+    r = __shfl_xor_sync(0xffffffffu, x, 8);
     return __byte_perm(x, r, (j & 2) ? 0x3276u : 0x5410u);
+}
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// The code bytes (code + 128) of eight elements of a block with scale d:
+// the rule of q8_pack4, with its tests made once for all eight.  With r =
+// RN(1 / d) and y = RN(e r), RN(e / d) and y round to the same integer n
+// unless y is within 2^-15 of a half-integer (gq_q8code.cuh); m = RN(y +
+// 1.5 2^23 + 128) holds n + 128 in its low byte, and y - n is exact.  Where an
+// element is that close, or not finite, or the clamp could bite (|y| of the
+// block's largest beyond 127.4: a scale rounded far down, a saturated block,
+// d = 0), the lane takes q8_pack4.
+__device__ __forceinline__ uint2 code_bytes8(const float (&e)[8], float d, float amax)
+{
+    constexpr float kMagic = 12582912.0f + 128.0f;
+    const float r = __frcp_rn(d);
+    float m[8], off = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float y = __fmul_rn(e[i], r);
+        m[i] = __fadd_rn(y, kMagic);
+        off = max_nan(off, fabsf(__fsub_rn(y, __fsub_rn(m[i], kMagic))));
+    }
+    if (off < 0.5f - 0x1p-15f && __fmul_rn(amax, r) < 127.4f) {
+        uint32_t w[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t a = __byte_perm(__float_as_uint(m[4 * k]), __float_as_uint(m[4 * k + 1]), 0x0040u);
+            const uint32_t b = __byte_perm(__float_as_uint(m[4 * k + 2]), __float_as_uint(m[4 * k + 3]), 0x0040u);
+            w[k] = __byte_perm(a, b, 0x5410u);
+        }
+        return make_uint2(w[0], w[1]);
+    }
+    const float lo[4] = {e[0], e[1], e[2], e[3]}, hi[4] = {e[4], e[5], e[6], e[7]};
+    return make_uint2(q8_pack4(lo, d) ^ 0x80808080u, q8_pack4(hi, d) ^ 0x80808080u);
 }
 
 // What a warp's units have in common: the group of four tokens.  Groups are
@@ -56,36 +103,59 @@ __device__ __forceinline__ uint32_t transpose4(uint32_t x)
 // or wholly above (rows below it exist only where the lists disagree).
 struct Group {
     long long row;  // this lane's token's row
-    int t;          // its place in the record
+    long long p0;   // the group's first position
+    int b;          // sequence
+    int t;          // the lane's token's place in the record
     bool mine;      // it is a new token
-    bool whole;     // all four are (warp-uniform)
-    long long rec;  // record offset of kv head 0, -1 if there is none (warp-uniform)
 };
-template <int D>
 __device__ __forceinline__ Group load_group(const Batch &B, long long slot)
 {
     Group g;
-    const int b = find_seq(B, slot);
-    const Seq s = load_seq(B, b);
-    const long long local = slot - ((static_cast<long long>(s.row0) >> 2) + 2ll * b);
-    const long long p0 = 4ll * ((s.first >> 2) + local), pos = p0 + ((threadIdx.x >> 3) & 3);
+    const Seq s = find_seq(B, slot, g.b);
+    const long long local = slot - ((static_cast<long long>(s.row0) >> 2) + 2ll * g.b);
+    g.p0 = 4ll * ((s.first >> 2) + local);
+    const long long pos = g.p0 + ((threadIdx.x >> 2) & 3);
     g.mine = pos >= s.first && pos < s.kv;
     g.row = s.row0 + (pos - s.first);
     g.t = static_cast<int>(pos) & (kRec - 1);
-    g.whole = __all_sync(0xffffffffu, g.mine);
-    g.rec = -1;
-    if (__any_sync(0xffffffffu, g.mine)) {
-        if (p0 < 0) {
-            flag_shape(B);
-        } else {
-            const int pg = page_of(B, b, static_cast<int>(p0));
-            if (pg >= 0) g.rec = rec_off(B, pg, 0, static_cast<int>(p0), D);
-        }
-    }
     return g;
 }
+// Record offset of kv head 0 for the group, -1 if there is none (warp-uniform).
+template <int D>
+__device__ __forceinline__ long long group_rec(const Batch &B, const Group &g)
+{
+    if (!__any_sync(0xffffffffu, g.mine)) return -1;
+    if (g.p0 < 0) {
+        flag_shape(B);
+        return -1;
+    }
+    const int pg = page_of(B, g.b, static_cast<int>(g.p0));
+    return pg >= 0 ? rec_off(B, pg, 0, static_cast<int>(g.p0), D) : -1;
+}
 
-// kUnits units a warp, all loaded before any is used.
+// The unit's place: head, first block, keys or values.
+struct Unit {
+    bool live, isv;
+    int h, b;
+    int elem;  // first element of this lane in a token's row
+};
+template <int D>
+__device__ __forceinline__ Unit unit_of(int u, int kv_heads)
+{
+    constexpr int pairs = D / 64;
+    Unit x;
+    const int half = kv_heads * pairs;
+    x.live = u < 2 * half;
+    x.isv = u >= half;
+    const int hp = x.isv ? u - half : u, lane = threadIdx.x & 31;
+    x.h = hp / pairs;
+    x.b = 2 * (hp % pairs) + (lane >> 4);
+    x.elem = (2 * hp + (lane >> 4)) * 32 + 8 * (lane & 3);
+    return x;
+}
+
+// kUnits units a warp, all loaded before any is used; the page is looked up
+// meanwhile (only the stores need it).
 template <int D, int TYPE, int kUnits>
 __global__ void __launch_bounds__(kThreads) k_kv_append(const uint8_t *__restrict__ K, long long ldk,
                                                         const uint8_t *__restrict__ V, long long ldv,
@@ -94,55 +164,54 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const uint8_t *__restric
     constexpr int nb = D / 32, el = type_size(TYPE);
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31, j = lane >> 3, sub = lane & 7;
-    const Group g = load_group<D>(B, blockIdx.x);
-    if (g.rec < 0) return;  // warp-uniform
-    const long long row = g.row;
+    const int j = (threadIdx.x >> 2) & 3, sub = threadIdx.x & 3;
+    const Group g = load_group(B, blockIdx.x);
     const int t = g.t, quad = t >> 2;
-    const int units = 2 * B.kv_heads * nb;
     const int u0 = (blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5)) * kUnits;
-    const long long head_stride = static_cast<long long>(B.page_tokens / kRec) * rec_bytes(D);
-    float4 v[kUnits];
+    float4 v[kUnits][2];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        const int u = u0 + i;
-        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (u < units && g.mine) {
-            const bool isv = u >= units / 2;
-            const int hb = isv ? u - units / 2 : u;  // head * nb + block: 32 hb is the element's place in the row
-            v[i] = load4<TYPE>((isv ? V + row * ldv * el : K + row * ldk * el) + (hb * 32 + sub * 4) * el);
-        }
+        const Unit u = unit_of<D>(u0 + i, B.kv_heads);
+        v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (u.live && g.mine) load8<TYPE>((u.isv ? V + g.row * ldv * el : K + g.row * ldk * el) + u.elem * el, v[i][0], v[i][1]);
     }
+    const long long rec0 = group_rec<D>(B, g);
+    if (rec0 < 0) return;  // warp-uniform
+    const bool whole = __all_sync(0xffffffffu, g.mine);
+    const long long head_stride = static_cast<long long>(B.page_tokens / kRec) * rec_bytes(D);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        const int u = u0 + i;
-        if (u >= units) break;  // warp-uniform
-        const bool isv = u >= units / 2;
-        const int hb = isv ? u - units / 2 : u;
-        const int h = hb / nb, b = hb % nb;
-        // from 0, so that a block of nothing but NaN has the scale 0
-        float amax = fmaxf(fmaxf(fmaxf(0.f, fabsf(v[i].x)), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
+        const Unit u = unit_of<D>(u0 + i, B.kv_heads);
+        if (!u.live) break;  // warp-uniform
+        const float e[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+        float amax = 0.f;  // so that a block of nothing but NaN has the scale 0
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(e[k]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         const __half dh = __float2half_rn(fminf(__fmul_rn(amax, 1.0f / 127.0f), kMaxD));
-        const float e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        const uint32_t codes = q8_pack4(e, __half2float(dh)) ^ 0x80808080u;
-        uint8_t *rec = cache + g.rec + h * head_stride;
-        if (!isv) {
+        const uint2 codes = code_bytes8(e, __half2float(dh), amax);
+        uint8_t *rec = cache + rec0 + u.h * head_stride;
+        if (!u.isv) {
             if (g.mine) {
-                *reinterpret_cast<uint32_t *>(rec + k_code_off(t, b, nb) + 4 * sub) = codes;
-                if (sub == 0) *reinterpret_cast<__half *>(rec + k_scale_off(t, b, D)) = dh;
+                *reinterpret_cast<uint2 *>(rec + k_code_off(t, u.b, nb) + 8 * sub) = codes;
+                if (sub == 0) *reinterpret_cast<__half *>(rec + k_scale_off(t, u.b, D)) = dh;
             }
         } else {
-            if (g.whole) {
-                // this lane's word: element 4 sub + j of the block, the four tokens' codes
-                *reinterpret_cast<uint32_t *>(rec + v_chunk_off(quad, 8 * b + sub, D) + 4 * j) = transpose4(codes);
+            const int c = 8 * u.b + 2 * sub;  // this lane's 16-byte chunks of four elements: c and c + 1
+            if (whole) {
+                // this lane's words: elements 4 c + j and 4 c + 4 + j, the four tokens' codes
+                *reinterpret_cast<uint32_t *>(rec + v_chunk_off(quad, c, D) + 4 * j) = transpose4(codes.x);
+                *reinterpret_cast<uint32_t *>(rec + v_chunk_off(quad, c + 1, D) + 4 * j) = transpose4(codes.y);
             } else if (g.mine) {
-                uint8_t *p = rec + v_chunk_off(quad, 8 * b + sub, D) + (t & 3);
+                uint8_t *p = rec + v_chunk_off(quad, c, D) + (t & 3), *q = rec + v_chunk_off(quad, c + 1, D) + (t & 3);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) p[4 * k] = static_cast<uint8_t>(codes >> (8 * k));
+                for (int k = 0; k < 4; ++k) {
+                    p[4 * k] = static_cast<uint8_t>(codes.x >> (8 * k));
+                    q[4 * k] = static_cast<uint8_t>(codes.y >> (8 * k));
+                }
             }
-            if (g.mine && sub == 0) *reinterpret_cast<__half *>(rec + v_scale_off(t, b, D)) = dh;
+            if (g.mine && sub == 0) *reinterpret_cast<__half *>(rec + v_scale_off(t, u.b, D)) = dh;
         }
     }
 }
@@ -154,53 +223,55 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const uint8_t *__restrict_
     constexpr int nb = D / 32, el = type_size(TYPE);
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31, j = lane >> 3, sub = lane & 7;
-    const Group g = load_group<D>(B, blockIdx.x);
-    const long long row = g.row;
+    const int j = (threadIdx.x >> 2) & 3, sub = threadIdx.x & 3;
+    const Group g = load_group(B, blockIdx.x);
+    const long long rec0 = group_rec<D>(B, g);
     const int t = g.t, quad = t >> 2;
-    const int units = 2 * B.kv_heads * nb;
     const int u0 = (blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5)) * kUnits;
     const long long head_stride = static_cast<long long>(B.page_tokens / kRec) * rec_bytes(D);
-    uint32_t w[kUnits];
+    uint2 w[kUnits];
     __half d[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        const int u = u0 + i;
-        w[i] = 0x80808080u;
+        const Unit u = unit_of<D>(u0 + i, B.kv_heads);
+        w[i] = make_uint2(0x80808080u, 0x80808080u);
         d[i] = __float2half_rn(0.0f);
-        if (u < units && g.rec >= 0) {
-            const bool isv = u >= units / 2;
-            const int hb = isv ? u - units / 2 : u;
-            const int h = hb / nb, b = hb % nb;
-            const uint8_t *rec = cache + g.rec + h * head_stride;
-            w[i] = __ldg(reinterpret_cast<const uint32_t *>(
-                rec + (isv ? v_chunk_off(quad, 8 * b + sub, D) + 4 * j : k_code_off(t, b, nb) + 4 * sub)));
-            d[i] = __ushort_as_half(__ldg(reinterpret_cast<const uint16_t *>(rec + (isv ? v_scale_off(t, b, D) : k_scale_off(t, b, D)))));
+        if (u.live && rec0 >= 0) {
+            const uint8_t *rec = cache + rec0 + u.h * head_stride;
+            const int c = 8 * u.b + 2 * sub;
+            if (u.isv) {
+                w[i].x = __ldg(reinterpret_cast<const uint32_t *>(rec + v_chunk_off(quad, c, D) + 4 * j));
+                w[i].y = __ldg(reinterpret_cast<const uint32_t *>(rec + v_chunk_off(quad, c + 1, D) + 4 * j));
+            } else {
+                w[i] = __ldg(reinterpret_cast<const uint2 *>(rec + k_code_off(t, u.b, nb) + 8 * sub));
+            }
+            d[i] = __ushort_as_half(
+                __ldg(reinterpret_cast<const uint16_t *>(rec + (u.isv ? v_scale_off(t, u.b, D) : k_scale_off(t, u.b, D)))));
         }
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        const int u = u0 + i;
-        if (u >= units) break;  // warp-uniform
-        const bool isv = u >= units / 2;
-        const int hb = isv ? u - units / 2 : u;
-        uint32_t c = w[i];
-        if (isv) c = transpose4(c);
+        const Unit u = unit_of<D>(u0 + i, B.kv_heads);
+        if (!u.live) break;  // warp-uniform
+        uint2 c = w[i];
+        if (u.isv) c = make_uint2(transpose4(c.x), transpose4(c.y));
         if (!g.mine) continue;
-        const float s = __half2float(d[i]);
-        const float2 a = half2_f2(codes2(c, 0x4140u)), z = half2_f2(codes2(c, 0x4342u));
         // codes and scales have 7 and 11 significant bits: the f32 products are exact
-        store4<TYPE>((isv ? V + row * ldv * el : K + row * ldk * el) + (hb * 32 + sub * 4) * el,
-                     make_float4(a.x * s, a.y * s, z.x * s, z.y * s));
+        const float s = __half2float(d[i]);
+        const float2 a = half2_f2(codes2(c.x, 0x4140u)), b = half2_f2(codes2(c.x, 0x4342u));
+        const float2 e = half2_f2(codes2(c.y, 0x4140u)), f = half2_f2(codes2(c.y, 0x4342u));
+        store8<TYPE>((u.isv ? V + g.row * ldv * el : K + g.row * ldk * el) + u.elem * el,
+                     make_float4(a.x * s, a.y * s, b.x * s, b.y * s), make_float4(e.x * s, e.y * s, f.x * s, f.y * s));
     }
 }
 
 // Units per warp: one where the call is small (a decode step: every unit's
-// load is issued at once, on as many warps as there are units), four where
+// load is issued at once, on as many warps as there are units), kMany where
 // there are enough warps to fill the GPU anyway.
+constexpr int kMany = 4;
 inline int units_per_warp(long long slots, int units)
 {
-    return slots * units >= 4ll * sm_count() * 64 ? 4 : 1;
+    return slots * units >= 4ll * sm_count() * 64 ? kMany : 1;
 }
 
 template <int D, int TYPE>
@@ -208,10 +279,10 @@ cudaError_t append_typed(const void *K, long long ldk, const void *V, long long 
                          cudaStream_t s)
 {
     const long long slots = B.n_tokens / 4 + 2ll * B.n_seq;
-    const int units = 2 * B.kv_heads * (D / 32), per = units_per_warp(slots, units);
+    const int units = 2 * B.kv_heads * (D / 64), per = units_per_warp(slots, units);
     const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>((units + 8 * per - 1) / (8 * per)));
     const uint8_t *k = static_cast<const uint8_t *>(K), *v = static_cast<const uint8_t *>(V);
-    if (per == 4) return launch_pdl(k_kv_append<D, TYPE, 4>, grid, dim3(kThreads), 0, s, k, ldk, v, ldv, cache, B);
+    if (per == kMany) return launch_pdl(k_kv_append<D, TYPE, kMany>, grid, dim3(kThreads), 0, s, k, ldk, v, ldv, cache, B);
     return launch_pdl(k_kv_append<D, TYPE, 1>, grid, dim3(kThreads), 0, s, k, ldk, v, ldv, cache, B);
 }
 
@@ -219,10 +290,10 @@ template <int D, int TYPE>
 cudaError_t read_typed(const uint8_t *cache, void *K, long long ldk, void *V, long long ldv, const Batch &B, cudaStream_t s)
 {
     const long long slots = B.n_tokens / 4 + 2ll * B.n_seq;
-    const int units = 2 * B.kv_heads * (D / 32), per = units_per_warp(slots, units);
+    const int units = 2 * B.kv_heads * (D / 64), per = units_per_warp(slots, units);
     const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>((units + 8 * per - 1) / (8 * per)));
     uint8_t *k = static_cast<uint8_t *>(K), *v = static_cast<uint8_t *>(V);
-    if (per == 4) return launch_pdl(k_kv_read<D, TYPE, 4>, grid, dim3(kThreads), 0, s, cache, k, ldk, v, ldv, B);
+    if (per == kMany) return launch_pdl(k_kv_read<D, TYPE, kMany>, grid, dim3(kThreads), 0, s, cache, k, ldk, v, ldv, B);
     return launch_pdl(k_kv_read<D, TYPE, 1>, grid, dim3(kThreads), 0, s, cache, k, ldk, v, ldv, B);
 }
 

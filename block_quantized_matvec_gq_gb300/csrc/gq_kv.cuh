@@ -51,11 +51,9 @@ struct Seq {
     int kv;     // cached tokens
     int first;  // position of row0 (kv - n; negative if the lists disagree)
 };
-__device__ __forceinline__ Seq load_seq(const Batch &B, int b)
+__device__ __forceinline__ Seq seq_of(const Batch &B, int r0, int r1, int kv)
 {
     Seq s;
-    const int r0 = __ldg(B.q_start + b), r1 = __ldg(B.q_start + b + 1);
-    const int kv = __ldg(B.kv_len + b);
     s.row0 = min(max(r0, 0), B.n_tokens);
     const int r1c = min(max(r1, s.row0), B.n_tokens);
     s.n = r1c - s.row0;
@@ -64,6 +62,11 @@ __device__ __forceinline__ Seq load_seq(const Batch &B, int b)
     s.first = s.kv - s.n;
     if (s.row0 != r0 || r1c != r1 || s.kv != kv) flag_shape(B);
     return s;
+}
+__device__ __forceinline__ Seq load_seq(const Batch &B, int b)
+{
+    const int r0 = __ldg(B.q_start + b), r1 = __ldg(B.q_start + b + 1), kv = __ldg(B.kv_len + b);
+    return seq_of(B, r0, r1, kv);
 }
 
 // Page of position `pos` of sequence b, or -1 (flagged) if the table names none.
@@ -115,6 +118,37 @@ __device__ __forceinline__ void store4(void *p, float4 v)
         *static_cast<uint2 *>(p) = make_uint2(f2_bf162(v.x, v.y), f2_bf162(v.z, v.w));
     } else {
         *static_cast<uint2 *>(p) = make_uint2(f2_half2(v.x, v.y), f2_half2(v.z, v.w));
+    }
+}
+// Eight consecutive elements at p (16-byte aligned).
+template <int TYPE>
+__device__ __forceinline__ void load8(const void *p, float4 &a, float4 &b)
+{
+    if (TYPE == GQ_TYPE_F32) {
+        a = __ldg(static_cast<const float4 *>(p));
+        b = __ldg(static_cast<const float4 *>(p) + 1);
+        return;
+    }
+    const uint4 w = __ldg(static_cast<const uint4 *>(p));
+    if (TYPE == GQ_TYPE_BF16) {
+        a = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+        b = make_float4(bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w));
+    } else {
+        const float2 x = half2_f2(w.x), y = half2_f2(w.y), z = half2_f2(w.z), u = half2_f2(w.w);
+        a = make_float4(x.x, x.y, y.x, y.y);
+        b = make_float4(z.x, z.y, u.x, u.y);
+    }
+}
+template <int TYPE>
+__device__ __forceinline__ void store8(void *p, float4 a, float4 b)
+{
+    if (TYPE == GQ_TYPE_F32) {
+        static_cast<float4 *>(p)[0] = a;
+        static_cast<float4 *>(p)[1] = b;
+    } else if (TYPE == GQ_TYPE_BF16) {
+        *static_cast<uint4 *>(p) = make_uint4(f2_bf162(a.x, a.y), f2_bf162(a.z, a.w), f2_bf162(b.x, b.y), f2_bf162(b.z, b.w));
+    } else {
+        *static_cast<uint4 *>(p) = make_uint4(f2_half2(a.x, a.y), f2_half2(a.z, a.w), f2_half2(b.x, b.y), f2_half2(b.z, b.w));
     }
 }
 __host__ __device__ __forceinline__ constexpr int type_size(int type) { return type == GQ_TYPE_F32 ? 4 : 2; }
