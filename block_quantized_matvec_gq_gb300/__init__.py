@@ -128,10 +128,28 @@ def _rows(t):
     return t.data_ptr()
 
 
+_raw_stream = None  # (current device, its current stream's handle), once torch is up
+
+
+def _current_stream():
+    """Handle of torch's current stream (without the Stream object: 0.2 us a call on the host, not 4.4)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        handle = torch.cuda.current_stream().cuda_stream  # brings CUDA up
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if device is None or raw is None:
+            device, raw = (lambda: None), (lambda _: torch.cuda.current_stream().cuda_stream)
+        _raw_stream = device, raw
+        return handle
+    device, raw = _raw_stream
+    return raw(device())
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
