@@ -716,7 +716,7 @@ int launch_kv_attention(const void *Q, long long ldq, const uint8_t *cache, cons
     float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + counter_bytes());
     // query rows per sequence and kv head, on average
     const long long rows = static_cast<long long>(B.n_tokens) * (heads / B.kv_heads) / B.n_seq;
-    if (type != GQ_TYPE_F32 && rows >= 64)
+    if (rows >= 64 && (type != GQ_TYPE_F32 || head_dim <= 128))
         return launch_kv_chunk(Q, ldq, cache, B, O, ldo, type, scale, softcap, window, counter + kv::kMaxCtas, part, heads,
                                head_dim, s);
     const int el = kv::type_size(type);

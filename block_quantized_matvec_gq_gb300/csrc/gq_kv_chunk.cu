@@ -28,14 +28,11 @@
 // tiles).  Tensor memory: scores (kKt columns, two buffers; p over them) and
 // the accumulators (head_dim columns per row tile).
 // Every wait is bounded (gq_tc.cuh).
-#include "gq_kv.cuh"
-#include "gq_tc.cuh"
+#include "gq_kv_chunk.cuh"
 
 namespace gq {
 namespace kv {
 namespace chunk {
-
-using namespace tcu;
 
 template <int D>
 struct Cfg {
@@ -68,181 +65,6 @@ struct Cfg {
     static_assert(kMt == 1 || 256 * kSoftRegs + 128 * kDeqRegs + 128 * kRestRegs <= 512 * 128, "register split");
     static_assert(kOffOp % 128 == 0 && kOffRaw % 128 == 0 && kOffBar % 8 == 0 && kSmem <= 232448, "shared memory layout");
 };
-constexpr int kTmemCols = 512;
-constexpr int kSCol = 128;        // column step between score buffers
-constexpr int kOCol = 256;        // first accumulator column
-constexpr float kNone = -1e30f;   // reference of a row that has seen no token
-constexpr float kPHead = 7.0f;
-constexpr float kGrow = 8.0f;
-constexpr int kMaskRing = 8;
-
-struct Args {
-    const uint8_t *Q, *cache;
-    uint8_t *O;
-    long long ldq, ldo;  // bytes
-    int type, group, window;
-    float scale, softcap;
-    int *counter;  // [grid][kMt]
-    float *part;
-};
-
-// One item: rows, and the positions they can see.
-struct Item {
-    Seq s;
-    int rows;      // query rows of the sequence
-    int r0;        // first row of the item
-    int lo, hi;    // positions that some row sees (hi < lo: none)
-    int base;      // position of the first tile (whole records)
-    int tiles;
-};
-template <int D>
-__device__ __forceinline__ Item item_of(const Seq &s, const Args &A, int st)
-{
-    using C = Cfg<D>;
-    Item it;
-    it.s = s;
-    it.rows = s.n * A.group;
-    it.r0 = st * C::kRowsItem;
-    const int t0 = it.r0 / A.group, t1 = min(it.r0 + C::kRowsItem, it.rows) - 1;
-    it.hi = s.first + t1 / A.group;
-    it.lo = A.window > 0 ? max(0, s.first + t0 - A.window + 1) : 0;
-    it.base = it.lo & ~(kRec - 1);
-    it.tiles = max(1, (it.hi - it.base + C::kKt) / C::kKt);
-    return it;
-}
-
-// A warp's walk over the pieces (parts of items) of its CTA's stretch.
-struct Walk {
-    int b, h, st;
-    int from;          // first tile of the piece in its item
-    long long left;    // tiles of the stretch still to come, this piece's included
-    long long x;       // place of the piece on the line
-};
-
-__device__ __forceinline__ int row_tiles(const Seq &s, const Args &A, int rows_item)
-{
-    return (s.n * A.group + rows_item - 1) / rows_item;
-}
-
-// tiles of all items of one kv head of a sequence (every lane gets the sum)
-template <int D>
-__device__ __forceinline__ long long head_cost(const Seq &s, const Args &A)
-{
-    const int nst = row_tiles(s, A, Cfg<D>::kRowsItem);
-    long long c = 0;
-    for (int st = threadIdx.x & 31; st < nst; st += 32) c += item_of<D>(s, A, st).tiles;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-    return c;
-}
-
-// Moves to the next piece; false when the stretch is done.
-template <int D>
-__device__ __forceinline__ bool next_piece(Walk &w, const Batch &B, const Args &A, int tiles_done)
-{
-    w.left -= tiles_done;
-    w.x += tiles_done;
-    if (w.left <= 0) return false;
-    w.from = 0;
-    Seq s = load_seq(B, w.b);
-    if (++w.st < row_tiles(s, A, Cfg<D>::kRowsItem)) return true;
-    w.st = 0;
-    if (++w.h < B.kv_heads) return true;
-    w.h = 0;
-    do {
-        if (++w.b >= B.n_seq) return false;
-        s = load_seq(B, w.b);
-    } while (s.n == 0);
-    return true;
-}
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// cap * tanh(x / cap) in f32 (as in gq_kv_attn.cu)
-__device__ __forceinline__ float soft_cap(float x, float cap, float inv_cap)
-{
-    const float y = x * inv_cap, a = fabsf(y);
-    const float e = ex2(-2.885390082f * a);
-    const float big = __fdividef(1.0f - e, 1.0f + e);
-    const float q = y * y;
-    const float small = a * (1.0f + q * (-0.333333333f + q * (0.133333333f + q * (-0.053968254f + q * 0.021869489f))));
-    return copysignf(cap * (a < 0.25f ? small : big), y);
-}
-
-// ---------------------------------------------------------------- tensor memory
-// 32 columns of this thread's lane; tmem_wait_ld has to follow before r is used.
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float *r)
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
-          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
-          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
-        : "r"(taddr)
-        : "memory");
-}
-template <int N>
-__device__ __forceinline__ void tmem_wait_ld(float (&r)[N])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));  // no use of r moves above the wait
-}
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n tcgen05.wait::ld.sync.aligned;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// A from tensor memory (128 rows, two f16 of K per column), B from shared memory.
-__device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
-{
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(tmem_d),
-        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
-    return p != 0;
-}
-
-__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
-{
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
 // ---------------------------------------------------------------- dequantizers
 // Operand tiles are core matrices of 8 rows x 16 bytes (8 elements of K); row
 // group r / 8 at 128 bytes, K group kg at 16 * rows bytes.
@@ -286,9 +108,8 @@ __device__ __forceinline__ void dequant_keys(const uint8_t *raw, uint8_t *op, in
 // Values: row n = (e % 4) * D / 4 + e / 4 for element e (neighbouring lanes,
 // which take neighbouring 16-byte chunks of four elements, then store to
 // neighbouring rows), K = token.  A unit is eight tokens of one chunk.
-// `seen`: tokens of the tile that some row of the item sees and that have a
-// page, as [lo, hi) and a bit per record; the scales of the others count as
-// 0, whatever the page holds there (0 * NaN would be NaN).
+// [lo, hi): tokens of the tile that some row of the item sees; recs: a bit per
+// record that has a page.
 template <int D>
 __device__ __forceinline__ void dequant_values(const uint8_t *raw, uint8_t *op, int tid, int lo, int hi, uint32_t recs)
 {
@@ -300,15 +121,7 @@ __device__ __forceinline__ void dequant_values(const uint8_t *raw, uint8_t *op, 
         const int rec = t8 / 2, g = 2 * (t8 % 2), b = c / 8;
         const uint8_t *src = raw + rec * C::kHalf - 17 * D;  // offsets below count from the record
         uint4 d = *reinterpret_cast<const uint4 *>(src + v_scale_off(4 * g, b, D));  // eight tokens
-        if (edge) {
-            uint32_t dw[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int tok = 8 * t8 + k;
-                if (tok < lo || tok >= hi || !((recs >> rec) & 1u)) dw[k / 2] &= (k & 1) ? 0x0000FFFFu : 0xFFFF0000u;
-            }
-            d = make_uint4(dw[0], dw[1], dw[2], dw[3]);
-        }
+        if (edge) d = hide_scales(d, 8 * t8, lo, hi, (recs >> rec) & 1u);
         const uint4 w0 = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g, c, D));
         const uint4 w1 = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g + 1, c, D));
         uint8_t *dst = op + t8 * (D * 16);
@@ -330,11 +143,6 @@ __device__ __forceinline__ void dequant_values(const uint8_t *raw, uint8_t *op, 
 // This thread's row: elements * 2^-e as f16, e from the row's largest
 // magnitude; returns 2^e.  A dead row is zeros.  The row is read twice (the
 // second time from L1): held in registers it would spill.
-template <int TYPE>
-__device__ __forceinline__ float2 pair_of(uint32_t w)
-{
-    return TYPE == GQ_TYPE_BF16 ? make_float2(bf16_lo(w), bf16_hi(w)) : half2_f2(w);
-}
 template <int D, int TYPE>
 __device__ __forceinline__ float load_query(const uint8_t *src, bool live, bool negate, uint8_t *op, int row)
 {
@@ -412,62 +220,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
     const uint32_t tmem = s_tmem;
     pdl_wait();
 
-    // ---- this CTA's stretch: the sequences' costs, a warp each, twice (the total first)
-    long long total = 0, len = 0, begin = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        long long at = 0;
-        for (int b0 = 0; b0 < B.n_seq; b0 += C::kWarpsAll) {
-            if (pass == 0 || B.n_seq > C::kWarpsAll) {
-                long long c = 0;
-                if (b0 + warp < B.n_seq) {
-                    const Seq s = load_seq(B, b0 + warp);
-                    c = head_cost<D>(s, A) * B.kv_heads;
-                }
-                __syncthreads();
-                if (lane == 0) s_cost[warp] = c;
-                __syncthreads();
-            }
-            for (int i = 0; i < C::kWarpsAll && b0 + i < B.n_seq; ++i) {
-                const long long c = s_cost[i];
-                if (pass == 1 && warp == 0 && begin >= at && begin < at + c) {
-                    // the item that holds tile `begin`: head, then row tile by a scan over the lanes
-                    const Seq s = load_seq(B, b0 + i);
-                    const long long hc = c / B.kv_heads;
-                    const int h = static_cast<int>((begin - at) / hc);
-                    long long rem = begin - at - h * hc;
-                    const int nst = row_tiles(s, A, C::kRowsItem);
-                    for (int st0 = 0; st0 < nst; st0 += 32) {
-                        const int mine = st0 + lane < nst ? item_of<D>(s, A, st0 + lane).tiles : 0;
-                        int inc = mine;
-#pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) {
-                            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-                            if (lane >= o) inc += v;
-                        }
-                        if (rem >= inc - mine && rem < inc) {
-                            s_walk.b = b0 + i;
-                            s_walk.h = h;
-                            s_walk.st = st0 + lane;
-                            s_walk.from = static_cast<int>(rem) - (inc - mine);
-                            s_walk.left = min(len, total - begin);
-                            s_walk.x = begin;
-                        }
-                        const int sum = __shfl_sync(0xffffffffu, inc, 31);
-                        if (rem < sum) break;
-                        rem -= sum;
-                    }
-                }
-                at += c;
-            }
-        }
-        if (pass == 0) {
-            total = at;
-            // a stretch of fewer than four tiles would spend more on its join
-            len = max((total + gridDim.x - 1) / gridDim.x, 4ll);
-            begin = len * blockIdx.x;
-        }
-    }
-    __syncthreads();
+    // ---- this CTA's stretch
+    const long long len = find_stretch<C>(B, A, s_cost, s_walk);
     Walk w = s_walk;
     volatile int *abort = &s_abort;
     // The register split stands at the head of each warpgroup's branch, where
@@ -488,7 +242,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
         uint32_t tile_no = 0;       // key tiles of the CTA so far
         while (w.left > 0) {
             const Seq s = load_seq(B, w.b);
-            const Item it = item_of<D>(s, A, w.st);
+            const Item it = item_of<C>(s, A, w.st);
             const int to = static_cast<int>(min(static_cast<long long>(it.tiles), w.from + w.left));
             const int r = it.r0 + 128 * mt + row;
             const bool tile_live = it.r0 + 128 * mt < it.rows;  // any row: else the mma warp skips the row tile
@@ -674,7 +428,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
             }
             const int done = to - w.from;
             tile_no += done;
-            if (!next_piece<D>(w, B, A, done)) break;
+            if (!next_piece<C>(w, B, A, done)) break;
         }
     } else if (warp < C::kProdWarp) {
         if (C::kMt == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMt == 2 ? C::kDeqRegs : 128));
@@ -684,7 +438,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
         uint32_t n = 0, tile_no = 0;  // operand tiles, key tiles
         while (ok && w.left > 0) {
             const Seq s = load_seq(B, w.b);
-            const Item it = item_of<D>(s, A, w.st);
+            const Item it = item_of<C>(s, A, w.st);
             const int to = static_cast<int>(min(static_cast<long long>(it.tiles), w.from + w.left));
             for (int j = w.from; j < to && ok; ++j, ++tile_no) {
                 const int p0 = it.base + j * C::kKt;
@@ -711,55 +465,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
                     }
                 }
             }
-            if (!ok || !next_piece<D>(w, B, A, to - w.from)) break;
+            if (!ok || !next_piece<C>(w, B, A, to - w.from)) break;
         }
     } else {
         if (C::kMt == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMt == 2 ? C::kRestRegs : 128));
     if (w.left > 0 && warp == C::kProdWarp) {
-        // ================================================================ producer: one lane per record
-        bool ok = true;
-        uint32_t n = 0, tile_no = 0;
-        while (ok) {
-            const Seq s = load_seq(B, w.b);
-            const Item it = item_of<D>(s, A, w.st);
-            const int to = static_cast<int>(min(static_cast<long long>(it.tiles), w.from + w.left));
-            auto page = [&](int j) {  // this lane's record of tile j: its page, -1 if it is bad, -2 if it is beyond the item
-                const int pos = it.base + j * C::kKt + lane * kRec;
-                if (lane >= C::kRecs || j >= to || pos > it.hi) return -2;
-                return page_of(B, w.b, pos);
-            };
-            int pg = page(w.from);
-            for (int j = w.from; j < to && ok; ++j, ++tile_no) {
-                const int pg_next = page(j + 1);
-                // records beyond the item are hidden by position; bad pages by this mask
-                const uint32_t copied = __ballot_sync(0xffffffffu, pg >= 0);
-                const uint32_t bad = __ballot_sync(0xffffffffu, pg == -1);
-                const int pos = it.base + j * C::kKt + lane * kRec;
-#pragma unroll 1
-                for (int part = 0; part < 2; ++part, ++n) {
-                    const uint32_t rs = n % C::kRaws;
-                    if (n >= C::kRaws) {
-                        ok = wait_warp(raw_empty + 8 * rs, (n / C::kRaws - 1) & 1, abort, B.status);
-                        if (!ok) break;
-                    }
-                    if (lane == 0) {
-                        if (part == 0) s_mask[tile_no % kMaskRing] = ((1u << C::kRecs) - 1u) & ~bad;
-                        const uint32_t bytes = __popc(copied) * C::kHalf;
-                        if (bytes) mbar_expect_tx(raw_full + 8 * rs, bytes);
-                        else mbar_arrive(raw_full + 8 * rs);
-                    }
-                    __syncwarp();
-                    if (pg >= 0)
-                        bulk_load(base + C::kOffRaw + rs * C::kRaw + lane * C::kHalf,
-                                  A.cache + rec_off(B, pg, w.h, pos, D) + part * C::kHalf, C::kHalf, raw_full + 8 * rs);
-                }
-                pg = pg_next;
-            }
-            if (!ok || !next_piece<D>(w, B, A, to - w.from)) break;
-        }
-        // copies in flight land before the CTA's memory is given up
-        for (uint32_t i = n > C::kRaws ? n - C::kRaws : 0; i < n; ++i)
-            wait_warp(raw_full + 8 * (i % C::kRaws), (i / C::kRaws) & 1, abort, B.status);
+        produce<D, C>(w, B, A, smem, raw_full, raw_empty, s_mask, abort);
     } else if (w.left > 0 && warp == C::kMmaWarp && elect_one()) {
         // ================================================================ mma: one thread
         constexpr uint32_t kIdQk = idesc_f16(128, C::kKt, false), kIdPv = idesc_f16(128, D, false);
@@ -778,32 +489,25 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
         // low word: one add per operand and MMA.  (Building each descriptor
         // from its address made this thread the limit: 113 cycles per MMA
         // against the tensor core's 64 for 128 x 128 x 16.)
-        constexpr uint32_t kHi = (128u >> 4) | (1u << 14);  // 128 bytes between row groups; descriptor version 1
-        auto desc_lo = [](uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); };
-        auto desc = [](uint32_t lo) {
-            uint64_t d;
-            asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kHi));
-            return d;
-        };
         const uint32_t q_lo = desc_lo(base, 2048), k_lo = desc_lo(base + C::kOffOp, C::kKt * 16),
                        v_lo = desc_lo(base + C::kOffOp, D * 16);
         auto qk = [&](int mt, uint32_t os, int buf) {
             const uint32_t a = q_lo + mt * (C::kQ >> 4), b = k_lo + os * (C::kOp >> 4);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-                mma_f16(tmem + kSCol * buf, desc(a + k * 256), desc(b + k * 2 * C::kKt), kIdQk, k > 0);
+                mma_f16(tmem + kSCol * buf, desc_of(a + k * 256), desc_of(b + k * 2 * C::kKt), kIdQk, k > 0);
             mma_commit(s_full + 8 * buf);
         };
         auto pv = [&](int mt, uint32_t os, int buf, bool first) {
             const uint32_t b = v_lo + os * (C::kOp >> 4);
 #pragma unroll
             for (int k = 0; k < C::kKt / 16; ++k)
-                mma_f16_ts(tmem + kOCol + mt * D, tmem + kSCol * buf + 8 * k, desc(b + k * 2 * D), kIdPv, !first || k > 0);
+                mma_f16_ts(tmem + kOCol + mt * D, tmem + kSCol * buf + 8 * k, desc_of(b + k * 2 * D), kIdPv, !first || k > 0);
             mma_commit(pv_done + 8 * mt);
         };
         while (ok) {
             const Seq s = load_seq(B, w.b);
-            const Item it = item_of<D>(s, A, w.st);
+            const Item it = item_of<C>(s, A, w.st);
             const int to = static_cast<int>(min(static_cast<long long>(it.tiles), w.from + w.left));
             const int nt = to - w.from;
             const bool two = C::kMt == 2 && it.r0 + 128 < it.rows;
@@ -861,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
             ++n_q;
             if (two) ++n_q1;
             key += 2 * nt;
-            if (!next_piece<D>(w, B, A, nt)) break;
+            if (!next_piece<C>(w, B, A, nt)) break;
         }
     }
     }
@@ -916,6 +620,7 @@ int launch_kv_chunk(const void *Q, long long ldq, const uint8_t *cache, const kv
     A.softcap = softcap;
     A.counter = counter;
     A.part = part;
+    if (type == GQ_TYPE_F32) return kv::chunk::launch_chunk_f32(A, B, head_dim, kv::chunk::kMaxCtas, s);
     switch (head_dim) {
     case 64: return kv::chunk::launch<64>(A, B, s);
     case 128: return kv::chunk::launch<128>(A, B, s);
