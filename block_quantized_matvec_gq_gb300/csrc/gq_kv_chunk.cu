@@ -15,7 +15,7 @@
 //                tensor memory, running reference m and sum l, p back to
 //                tensor memory as the A operand of p v; the query operand and
 //                the result rows.
-//   dequantizers four warps (eight for head_dim 256): codes and scales of a raw stage -> the f16 operand
+//   dequantizers eight warps (twelve for head_dim 256): codes and scales of a raw stage -> the f16 operand
 //                tile d * q (11 bits, one rounding) in the K-major layout; keys
 //                along head_dim, values along the tokens (the cache's words
 //                hold four tokens of one element, so neither is transposed).
@@ -52,17 +52,17 @@ struct Cfg {
     static constexpr int kBars = 2 * kRaws + 2 * kOps + 10;
     static constexpr int kOffMisc = kOffBar + 8 * kBars;
     static constexpr int kSmem = kOffMisc + 512;
-    // four warpgroups: softmax (one per row tile), dequantizers, {producer, mma}
+    // five warpgroups: softmax (one per row tile), dequantizers, {producer, mma}
     static constexpr int kSoftWarps = 4 * kMt;
-    static constexpr int kDeqWarps = 12 - kSoftWarps;
-    static constexpr int kProdWarp = 12;
-    static constexpr int kMmaWarp = 13;
-    static constexpr int kWarpsAll = 16;
+    static constexpr int kDeqWarps = 16 - kSoftWarps;
+    static constexpr int kProdWarp = 16;
+    static constexpr int kMmaWarp = 17;
+    static constexpr int kWarpsAll = 20;
     static constexpr int kThreads = 32 * kWarpsAll;
-    // Registers per thread after the split; with kKt = 128 a softmax thread
-    // holds a whole score row.  The shares add up to the launch's 512 x 128.
-    static constexpr int kSoftRegs = kMt == 2 ? 184 : 0, kDeqRegs = 88, kRestRegs = 56;
-    static_assert(kMt == 1 || 256 * kSoftRegs + 128 * kDeqRegs + 128 * kRestRegs <= 512 * 128, "register split");
+    // Registers per thread after the split (a softmax thread holds a whole
+    // score row); the shares stay within the launch's 640 x 96.
+    static constexpr int kSoftRegs = kMt == 2 ? 168 : 144, kDeqRegs = kMt == 2 ? 48 : 72, kRestRegs = 40;
+    static_assert(32 * (kSoftWarps * kSoftRegs + kDeqWarps * kDeqRegs + 4 * kRestRegs) <= kThreads * 96, "register split");
     static_assert(kOffOp % 128 == 0 && kOffRaw % 128 == 0 && kOffBar % 8 == 0 && kSmem <= 232448, "shared memory layout");
 };
 // ---------------------------------------------------------------- dequantizers
@@ -73,70 +73,92 @@ struct Cfg {
 // lanes fill one core matrix; the two halves of the 32 codes are read in an
 // order that depends on the token, which with the record's own exclusive or
 // spreads eight tokens over all banks.
-template <int D>
-__device__ __forceinline__ void dequant_keys(const uint8_t *raw, uint8_t *op, int tid)
+// `taken` is called when the raw stage has been read (so it is refilled while
+// the conversion runs) and waits for the operand stage; false ends the tile.
+template <int D, class Taken>
+__device__ __forceinline__ bool dequant_keys(const uint8_t *raw, uint8_t *op, int tid, Taken taken)
 {
     using C = Cfg<D>;
-    constexpr int nb = D / 32;
-#pragma unroll 2
-    for (int u = tid; u < C::kKt * nb; u += C::kDeqWarps * 32) {
-        const int tok = u % C::kKt, b = u / C::kKt;  // warp-uniform b
-        const int rec = tok / kRec, t = tok % kRec;
-        const uint8_t *src = raw + rec * C::kHalf;
-        const uint32_t d = *reinterpret_cast<const uint16_t *>(src + k_scale_off(t, b, D));
-        const uint32_t d2 = d | (d << 16);
+    constexpr int nb = D / 32, kTh = C::kDeqWarps * 32, kAll = C::kKt * nb, kN = (kAll + kTh - 1) / kTh;
+    uint4 w[kN][2];
+    uint32_t d[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int u = tid + i * kTh, tok = u % C::kKt, b = u / C::kKt, t = tok % kRec;
+        if (kAll % kTh != 0 && u >= kAll) break;
+        const uint8_t *src = raw + tok / kRec * C::kHalf;
+        d[i] = *reinterpret_cast<const uint16_t *>(src + k_scale_off(t, b, D));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            w[i][h] = *reinterpret_cast<const uint4 *>(src + k_code_off(t, b, nb) + 16 * (h ^ ((t >> 1) & 1)));
+    }
+    if (!taken()) return false;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int u = tid + i * kTh, tok = u % C::kKt, b = u / C::kKt, t = tok % kRec;
+        if (kAll % kTh != 0 && u >= kAll) break;
+        const uint32_t d2 = d[i] | (d[i] << 16);
         uint8_t *dst = op + (tok >> 3) * 128 + (tok & 7) * 16;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int half = i ^ ((t >> 1) & 1);
-            const uint4 w = *reinterpret_cast<const uint4 *>(src + k_code_off(t, b, nb) + 16 * half);
+        for (int h = 0; h < 2; ++h) {
+            const uint4 x = w[i][h];
             uint4 a, c;
-            a.x = hmul2(codes2(w.x, 0x4140u), d2);
-            a.y = hmul2(codes2(w.x, 0x4342u), d2);
-            a.z = hmul2(codes2(w.y, 0x4140u), d2);
-            a.w = hmul2(codes2(w.y, 0x4342u), d2);
-            c.x = hmul2(codes2(w.z, 0x4140u), d2);
-            c.y = hmul2(codes2(w.z, 0x4342u), d2);
-            c.z = hmul2(codes2(w.w, 0x4140u), d2);
-            c.w = hmul2(codes2(w.w, 0x4342u), d2);
-            uint8_t *o = dst + (4 * b + 2 * half) * (C::kKt * 16);
+            a.x = hmul2(codes2(x.x, 0x4140u), d2);
+            a.y = hmul2(codes2(x.x, 0x4342u), d2);
+            a.z = hmul2(codes2(x.y, 0x4140u), d2);
+            a.w = hmul2(codes2(x.y, 0x4342u), d2);
+            c.x = hmul2(codes2(x.z, 0x4140u), d2);
+            c.y = hmul2(codes2(x.z, 0x4342u), d2);
+            c.z = hmul2(codes2(x.w, 0x4140u), d2);
+            c.w = hmul2(codes2(x.w, 0x4342u), d2);
+            uint8_t *o = dst + (4 * b + 2 * (h ^ ((t >> 1) & 1))) * (C::kKt * 16);
             *reinterpret_cast<uint4 *>(o) = a;
             *reinterpret_cast<uint4 *>(o + C::kKt * 16) = c;
         }
     }
+    return true;
 }
 // Values: row n = (e % 4) * D / 4 + e / 4 for element e (neighbouring lanes,
 // which take neighbouring 16-byte chunks of four elements, then store to
 // neighbouring rows), K = token.  A unit is eight tokens of one chunk.
 // [lo, hi): tokens of the tile that some row of the item sees; recs: a bit per
 // record that has a page.
-template <int D>
-__device__ __forceinline__ void dequant_values(const uint8_t *raw, uint8_t *op, int tid, int lo, int hi, uint32_t recs)
+template <int D, class Taken>
+__device__ __forceinline__ bool dequant_values(const uint8_t *raw, uint8_t *op, int tid, int lo, int hi, uint32_t recs, Taken taken)
 {
     using C = Cfg<D>;
+    constexpr int kTh = C::kDeqWarps * 32, kAll = (C::kKt / 8) * (D / 4), kN = (kAll + kTh - 1) / kTh;
     const bool edge = lo > 0 || hi < C::kKt || recs != (1u << C::kRecs) - 1u;
-#pragma unroll 2
-    for (int u = tid; u < (C::kKt / 8) * (D / 4); u += C::kDeqWarps * 32) {
-        const int c = u % (D / 4), t8 = u / (D / 4);
-        const int rec = t8 / 2, g = 2 * (t8 % 2), b = c / 8;
-        const uint8_t *src = raw + rec * C::kHalf - 17 * D;  // offsets below count from the record
-        uint4 d = *reinterpret_cast<const uint4 *>(src + v_scale_off(4 * g, b, D));  // eight tokens
-        if (edge) d = hide_scales(d, 8 * t8, lo, hi, (recs >> rec) & 1u);
-        const uint4 w0 = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g, c, D));
-        const uint4 w1 = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g + 1, c, D));
-        uint8_t *dst = op + t8 * (D * 16);
-        const uint32_t a[4] = {w0.x, w0.y, w0.z, w0.w}, z[4] = {w1.x, w1.y, w1.z, w1.w};
+    uint4 w[kN][2], d[kN];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = i * (D / 4) + c;
+    for (int i = 0; i < kN; ++i) {
+        const int u = tid + i * kTh, c = u % (D / 4), t8 = u / (D / 4), g = 2 * (t8 % 2);
+        if (kAll % kTh != 0 && u >= kAll) break;
+        const uint8_t *src = raw + t8 / 2 * C::kHalf - 17 * D;  // offsets below count from the record
+        d[i] = *reinterpret_cast<const uint4 *>(src + v_scale_off(4 * g, c / 8, D));  // eight tokens
+        w[i][0] = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g, c, D));
+        w[i][1] = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g + 1, c, D));
+    }
+    if (!taken()) return false;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int u = tid + i * kTh, c = u % (D / 4), t8 = u / (D / 4);
+        if (kAll % kTh != 0 && u >= kAll) break;
+        const uint4 s = edge ? hide_scales(d[i], 8 * t8, lo, hi, (recs >> (t8 / 2)) & 1u) : d[i];
+        uint8_t *dst = op + t8 * (D * 16);
+        const uint32_t a[4] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w}, z[4] = {w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int n = k * (D / 4) + c;
             uint4 o;
-            o.x = hmul2(codes2(a[i], 0x4140u), d.x);
-            o.y = hmul2(codes2(a[i], 0x4342u), d.y);
-            o.z = hmul2(codes2(z[i], 0x4140u), d.z);
-            o.w = hmul2(codes2(z[i], 0x4342u), d.w);
+            o.x = hmul2(codes2(a[k], 0x4140u), s.x);
+            o.y = hmul2(codes2(a[k], 0x4342u), s.y);
+            o.z = hmul2(codes2(z[k], 0x4140u), s.z);
+            o.w = hmul2(codes2(z[k], 0x4342u), s.w);
             *reinterpret_cast<uint4 *>(dst + (n >> 3) * 128 + (n & 7) * 16) = o;
         }
     }
+    return true;
 }
 
 // ---------------------------------------------------------------- the query operand
@@ -227,7 +249,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
     // The register split stands at the head of each warpgroup's branch, where
     // the compiler takes it as the limit of what follows.
     if (warp < C::kSoftWarps) {
-        if (C::kMt == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMt == 2 ? C::kSoftRegs : 128));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
         // ================================================================ softmax: thread = query row
         const int mt = warp >> 2;                       // row tile
         const int row = threadIdx.x & 127;
@@ -431,7 +453,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
             if (!next_piece<C>(w, B, A, done)) break;
         }
     } else if (warp < C::kProdWarp) {
-        if (C::kMt == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMt == 2 ? C::kDeqRegs : 128));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kDeqRegs));
         // ================================================================ dequantizers
         const int tid = threadIdx.x - 32 * C::kSoftWarps;
         bool ok = true;
@@ -447,28 +469,26 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
                     const uint32_t rs = n % C::kRaws, os = n % C::kOps;
                     ok = wait_warp(raw_full + 8 * rs, (n / C::kRaws) & 1, abort, B.status);
                     if (!ok) break;
-                    if (n >= C::kOps) {
-                        ok = wait_warp(op_empty + 8 * os, (n / C::kOps - 1) & 1, abort, B.status);
-                        if (!ok) break;
-                    }
                     const uint8_t *raw = smem + C::kOffRaw + rs * C::kRaw;
                     uint8_t *op = smem + C::kOffOp + os * C::kOp;
-                    if (part == 0) dequant_keys<D>(raw, op, tid);
-                    else
-                        dequant_values<D>(raw, op, tid, max(it.lo - p0, 0), min(max(it.hi + 1 - p0, 0), C::kKt),
-                                          s_mask[tile_no % kMaskRing]);
+                    const uint32_t recs = s_mask[tile_no % kMaskRing];
+                    auto taken = [&]() {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(raw_empty + 8 * rs);
+                        return n < C::kOps || wait_warp(op_empty + 8 * os, (n / C::kOps - 1) & 1, abort, B.status);
+                    };
+                    if (part == 0) ok = dequant_keys<D>(raw, op, tid, taken);
+                    else ok = dequant_values<D>(raw, op, tid, max(it.lo - p0, 0), min(max(it.hi + 1 - p0, 0), C::kKt), recs, taken);
+                    if (!ok) break;
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(op_full + 8 * os);
-                        mbar_arrive(raw_empty + 8 * rs);
-                    }
+                    if (lane == 0) mbar_arrive(op_full + 8 * os);
                 }
             }
             if (!ok || !next_piece<C>(w, B, A, to - w.from)) break;
         }
     } else {
-        if (C::kMt == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMt == 2 ? C::kRestRegs : 128));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRestRegs));
     if (w.left > 0 && warp == C::kProdWarp) {
         produce<D, C>(w, B, A, smem, raw_full, raw_empty, s_mask, abort);
     } else if (w.left > 0 && warp == C::kMmaWarp && elect_one()) {
