@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
 {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ long long s_cost[C::kWarpsAll];
+    __shared__ long long s_cost[C::kWarpsAll], s_cut[2];
     __shared__ Walk s_walk;
     __shared__ volatile int s_abort;
     __shared__ uint32_t s_tmem;
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
     pdl_wait();
 
     // ---- this CTA's stretch
-    const long long len = find_stretch<C>(B, A, s_cost, s_walk);
+    const long long len = find_stretch<C>(B, A, s_cost, s_cut, s_walk);
     Walk w = s_walk;
     volatile int *abort = &s_abort;
     // The register split stands at the head of each warpgroup's branch, where
@@ -262,38 +262,66 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
         uint32_t n_pv = 0;          // tiles of this row tile so far: scores taken, p v products asked for
         uint32_t n_piece = 0;       // pieces of this row tile so far
         uint32_t tile_no = 0;       // key tiles of the CTA so far
-        while (w.left > 0) {
+        // A piece as this thread sees it; its query row is loaded, and its first
+        // scores asked for, before the result of the piece before is written.
+        struct Piece {
+            int base, tiles, from, to;
+            long long x;
+            bool tile_live, live;  // any row of the row tile (else the mma warp skips it); this row
+            int row_lo, row_hi;    // positions that the row sees
+            float zs;              // score = sum * zs
+            uint8_t *dst;
+        };
+        auto begin = [&]() {
+            Piece p;
             const Seq s = load_seq(B, w.b);
             const Item it = item_of<C>(s, A, w.st);
-            const int to = static_cast<int>(min(static_cast<long long>(it.tiles), w.from + w.left));
+            p.base = it.base;
+            p.tiles = it.tiles;
+            p.from = w.from;
+            p.to = static_cast<int>(min(static_cast<long long>(it.tiles), w.from + w.left));
+            p.x = w.x;
             const int r = it.r0 + 128 * mt + row;
-            const bool tile_live = it.r0 + 128 * mt < it.rows;  // any row: else the mma warp skips the row tile
-            if (tile_live) {
-                const bool live = r < it.rows;
-                const int tok = live ? r / A.group : 0, head = w.h * A.group + (live ? r % A.group : 0);
-                const int pos = s.first + tok;
-                const int row_hi = live ? pos : -1;
-                const int row_lo = A.window > 0 ? max(0, pos - A.window + 1) : 0;
-                const uint8_t *src = A.Q + (s.row0 + tok) * A.ldq + static_cast<long long>(head) * D * 2;
-                const float f = A.type == GQ_TYPE_BF16 ? load_query<D, GQ_TYPE_BF16>(src, live, A.scale < 0.f, q_op, row)
-                                                       : load_query<D, GQ_TYPE_F16>(src, live, A.scale < 0.f, q_op, row);
+            p.tile_live = it.r0 + 128 * mt < it.rows;
+            p.live = r < it.rows;
+            const int tok = p.live ? r / A.group : 0, head = w.h * A.group + (p.live ? r % A.group : 0);
+            const int pos = s.first + tok;
+            p.row_hi = p.live ? pos : -1;
+            p.row_lo = A.window > 0 ? max(0, pos - A.window + 1) : 0;
+            const long long at = static_cast<long long>(head) * D * 2;
+            p.dst = A.O + (s.row0 + tok) * A.ldo + at;
+            p.zs = 0.f;
+            if (p.tile_live) {
+                // every q k of the piece before is done: its last scores have been taken
+                const uint8_t *src = A.Q + (s.row0 + tok) * A.ldq + at;
+                const float f = A.type == GQ_TYPE_BF16 ? load_query<D, GQ_TYPE_BF16>(src, p.live, A.scale < 0.f, q_op, row)
+                                                       : load_query<D, GQ_TYPE_F16>(src, p.live, A.scale < 0.f, q_op, row);
                 // a factor of 0 would turn hidden scores (-inf) into NaN
-                const float zs = fmaxf(fabsf(A.scale) * f * (kCap ? 1.0f : kLog2e), 1e-37f);
+                p.zs = fmaxf(fabsf(A.scale) * f * (kCap ? 1.0f : kLog2e), 1e-37f);
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full + 8 * mt);
-                float m = kNone, l = 0.f;
-                for (int j = w.from; j < to; ++j) {
+            }
+            return p;
+        };
+        bool more = w.left > 0;
+        Piece pc = {};
+        if (more) pc = begin();
+        while (more) {
+            float m = kNone, l = 0.f;
+            if (pc.tile_live) {
+                const float zs = pc.zs;
+                for (int j = pc.from; j < pc.to; ++j) {
                     const int buf = C::kMt == 2 ? mt : static_cast<int>(n_pv & 1);
                     const uint32_t s_addr = lane_addr + kSCol * buf;
                     // kMt = 2: one buffer per row tile; kMt = 1: two in turn
                     if (ok) ok = wait_warp(s_full + 8 * buf, (C::kMt == 2 ? n_pv : n_pv >> 1) & 1, abort, B.status);
                     if (!ok) break;
                     tc_fence_after();
-                    const int p0 = it.base + j * C::kKt;
-                    const uint32_t recs = s_mask[(tile_no + (j - w.from)) % kMaskRing];
+                    const int p0 = pc.base + j * C::kKt;
+                    const uint32_t recs = s_mask[(tile_no + (j - pc.from)) % kMaskRing];
                     // every row of the warp sees the whole tile?
-                    const bool edge = __any_sync(0xffffffffu, p0 < row_lo || p0 + C::kKt - 1 > row_hi) ||
+                    const bool edge = __any_sync(0xffffffffu, p0 < pc.row_lo || p0 + C::kKt - 1 > pc.row_hi) ||
                                       recs != (1u << C::kRecs) - 1u;
                     float v[C::kKt];
 #pragma unroll
@@ -304,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
                         for (int k = 0; k < C::kKt; ++k) v[k] = soft_cap(v[k] * zs, A.softcap, inv_cap) * kLog2e;
                     }
                     if (edge) {
-                        const int a = row_lo - p0, b = row_hi - p0;
+                        const int a = pc.row_lo - p0, b = pc.row_hi - p0;
 #pragma unroll
                         for (int k = 0; k < C::kKt; ++k)
                             if (k < a || k > b || !((recs >> (k / kRec)) & 1u)) v[k] = -INFINITY;
@@ -323,7 +351,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
                         const float nm = fmaxf(m, zt), g = ex2(m - nm);
                         m = nm;
                         l *= g;
-                        if (j > w.from) {
+                        if (j > pc.from) {
                             // the accumulator is at rest once the previous tile's p v is done (the one
                             // before that is: these scores were asked for after it)
                             ok = wait_warp(pv_done + 8 * mt, (n_pv - 1) & 1, abort, B.status);
@@ -364,93 +392,94 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
                     if (lane == 0) mbar_arrive(p_full + 8 * buf);
                     ++n_pv;
                 }
-                // ---- the piece's result
-                if (ok) ok = wait_warp(o_done + 8 * mt, n_piece & 1, abort, B.status);
-                ++n_piece;
-                tc_fence_after();
-                const bool whole = w.from == 0 && to == it.tiles;
-                uint8_t *dst = A.O + (s.row0 + tok) * A.ldo + static_cast<long long>(head) * D * 2;
-                // column i * D / 4 + c is element 4 c + i
-                auto put = [&](int c, const float (&x)[32], float inv) {
-                    uint32_t o[16];
+            }
+            const Piece cur = pc;
+            tile_no += cur.to - cur.from;
+            more = next_piece<C>(w, B, A, cur.to - cur.from);
+            if (more) pc = begin();
+            if (!cur.tile_live) continue;
+            // ---- the piece's result
+            if (ok) ok = wait_warp(o_done + 8 * mt, n_piece & 1, abort, B.status);
+            ++n_piece;
+            tc_fence_after();
+            // column i * D / 4 + c is element 4 c + i
+            auto put = [&](int c, const float (&x)[32], float inv) {
+                uint32_t o[16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        // elements 2 k, 2 k + 1 of this group of 32: columns 8 i + cc with i = e % 4, cc = e / 4
-                        const float a = x[8 * ((2 * k) & 3) + (2 * k) / 4] * inv, b = x[8 * ((2 * k + 1) & 3) + (2 * k + 1) / 4] * inv;
-                        o[k] = A.type == GQ_TYPE_BF16 ? f2_bf162(a, b) : f2_half2(a, b);
-                    }
+                for (int k = 0; k < 16; ++k) {
+                    // elements 2 k, 2 k + 1 of this group of 32: columns 8 i + cc with i = e % 4, cc = e / 4
+                    const float a = x[8 * ((2 * k) & 3) + (2 * k) / 4] * inv, b = x[8 * ((2 * k + 1) & 3) + (2 * k + 1) / 4] * inv;
+                    o[k] = A.type == GQ_TYPE_BF16 ? f2_bf162(a, b) : f2_half2(a, b);
+                }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        *reinterpret_cast<uint4 *>(dst + (4 * c + 8 * k) * 2) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                };
-                constexpr int kSlot = 128 * (D + 2);  // floats of one row tile's partial: [D][128], m, l
-                float *slot = A.part + ((2ll * blockIdx.x + (w.from == 0 ? 1 : 0)) * C::kMt + mt) * kSlot;
-                const float inv = l == 0.f ? 0.f : 1.0f / l;
+                for (int k = 0; k < 4; ++k)
+                    *reinterpret_cast<uint4 *>(cur.dst + (4 * c + 8 * k) * 2) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            };
+            const bool whole = cur.from == 0 && cur.to == cur.tiles;
+            constexpr int kSlot = 128 * (D + 2);  // floats of one row tile's partial: [D][128], m, l
+            float *slot = A.part + ((2ll * blockIdx.x + (cur.from == 0 ? 1 : 0)) * C::kMt + mt) * kSlot;
+            const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll 1
+            for (int c = 0; c < D / 4; c += 8) {
+                float x[32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t v[8];
+                    tmem_ld8(o_addr + i * (D / 4) + c, v);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[8 * i + k] = __uint_as_float(v[k]);
+                }
+                if (whole) {
+                    if (cur.live) put(c, x, inv);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) slot[(i * (D / 4) + c + k) * 128 + row] = x[8 * i + k];
+                }
+            }
+            // the next piece's first p v overwrites the accumulator only after this warp's next p
+            tc_fence_before();
+            if (whole) continue;
+            slot[D * 128 + row] = m;
+            slot[(D + 1) * 128 + row] = l;
+            const long long item_x = cur.x - cur.from;
+            const int c0 = first_cta(item_x, cur.tiles, len), c1 = last_cta(item_x, cur.tiles, len);
+            __threadfence();
+            bar_sync(1 + mt, 128);
+            if (row == 0) {
+                const int old = atomicAdd(A.counter + c0 * C::kMt + mt, 1);
+                s_last[mt] = old == c1 - c0;
+                if (old == c1 - c0) A.counter[c0 * C::kMt + mt] = 0;
+            }
+            bar_sync(1 + mt, 128);
+            if (s_last[mt]) {
+                __threadfence();
+                auto part = [&](int c) { return A.part + ((2ll * c + (c == c0 ? 1 : 0)) * C::kMt + mt) * kSlot; };
+                float M = kNone, L = 0.f;
+#pragma unroll 4
+                for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(part(c) + D * 128 + row));
+#pragma unroll 4
+                for (int c = c0; c <= c1; ++c) L += ex2(__ldcg(part(c) + D * 128 + row) - M) * __ldcg(part(c) + (D + 1) * 128 + row);
+                const float linv = L == 0.f ? 0.f : 1.0f / L;
 #pragma unroll 1
                 for (int c = 0; c < D / 4; c += 8) {
                     float x[32];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t v[8];
-                        tmem_ld8(o_addr + i * (D / 4) + c, v);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) x[8 * i + k] = __uint_as_float(v[k]);
-                    }
-                    if (whole) {
-                        if (live) put(c, x, inv);
-                    } else {
+                    for (int k = 0; k < 32; ++k) x[k] = 0.f;
+#pragma unroll 2
+                    for (int cc = c0; cc <= c1; ++cc) {
+                        const float *src = part(cc);
+                        const float g = ex2(__ldcg(src + D * 128 + row) - M);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) slot[(i * (D / 4) + c + k) * 128 + row] = x[8 * i + k];
+                            for (int k = 0; k < 8; ++k) x[8 * i + k] += g * __ldcg(src + (i * (D / 4) + c + k) * 128 + row);
                     }
-                }
-                // the next piece's first p v overwrites the accumulator only after this warp's next p
-                tc_fence_before();
-                if (!whole) {
-                    slot[D * 128 + row] = m;
-                    slot[(D + 1) * 128 + row] = l;
-                    const long long item_x = w.x - w.from;
-                    const int c0 = static_cast<int>(item_x / len), c1 = static_cast<int>((item_x + it.tiles - 1) / len);
-                    __threadfence();
-                    bar_sync(1 + mt, 128);
-                    if (row == 0) {
-                        const int old = atomicAdd(A.counter + c0 * C::kMt + mt, 1);
-                        s_last[mt] = old == c1 - c0;
-                        if (old == c1 - c0) A.counter[c0 * C::kMt + mt] = 0;
-                    }
-                    bar_sync(1 + mt, 128);
-                    if (s_last[mt]) {
-                        __threadfence();
-                        auto part = [&](int c) { return A.part + ((2ll * c + (c == c0 ? 1 : 0)) * C::kMt + mt) * kSlot; };
-                        float M = kNone, L = 0.f;
-                        for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(part(c) + D * 128 + row));
-                        for (int c = c0; c <= c1; ++c)
-                            L += ex2(__ldcg(part(c) + D * 128 + row) - M) * __ldcg(part(c) + (D + 1) * 128 + row);
-                        const float linv = L == 0.f ? 0.f : 1.0f / L;
-#pragma unroll 1
-                        for (int c = 0; c < D / 4; c += 8) {
-                            float x[32];
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) x[k] = 0.f;
-                            for (int cc = c0; cc <= c1; ++cc) {
-                                const float *src2 = part(cc);
-                                const float g = ex2(__ldcg(src2 + D * 128 + row) - M);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                    for (int k = 0; k < 8; ++k)
-                                        x[8 * i + k] += g * __ldcg(src2 + (i * (D / 4) + c + k) * 128 + row);
-                            }
-                            if (live) put(c, x, linv);
-                        }
-                    }
-                    bar_sync(1 + mt, 128);  // s_last may be written again
+                    if (cur.live) put(c, x, linv);
                 }
             }
-            const int done = to - w.from;
-            tile_no += done;
-            if (!next_piece<C>(w, B, A, done)) break;
+            bar_sync(1 + mt, 128);  // s_last may be written again
         }
     } else if (warp < C::kProdWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kDeqRegs));

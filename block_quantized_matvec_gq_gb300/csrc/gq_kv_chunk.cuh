@@ -199,51 +199,64 @@ __device__ __forceinline__ uint4 hide_scales(uint4 d, int tok, int lo, int hi, b
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A cut closer than kSnap tiles to an item's end is moved there: joining the
+// parts of a cut item costs about as much as that many tiles.
+constexpr int kSnap = 2;
+__device__ __forceinline__ long long snap(long long x, long long x0, int n)
+{
+    return x - x0 < kSnap ? x0 : (x0 + n - x < kSnap ? x0 + n : x);
+}
+// First and last CTA of a cut item of n tiles that begins at x0: the cuts
+// moved to its start come before the first, those that stayed inside it
+// separate the others.
+__device__ __forceinline__ int first_cta(long long x0, int n, long long len) { return static_cast<int>((x0 + min(kSnap, n) - 1) / len); }
+__device__ __forceinline__ int last_cta(long long x0, int n, long long len) { return static_cast<int>((x0 + n - kSnap) / len); }
+
 // This CTA's stretch of the line, into `walk` (left = 0 if it has none); all
-// threads take part, a warp per sequence, twice (the total first).  Returns
-// the length of a stretch.
+// threads take part: a warp per sequence for the total, then two warps look
+// for the stretch's two cuts.  Returns the length of a stretch.
 template <class C>
-__device__ __forceinline__ long long find_stretch(const Batch &B, const Args &A, long long *s_cost, Walk &s_walk)
+__device__ __forceinline__ long long find_stretch(const Batch &B, const Args &A, long long *s_cost, long long *s_cut, Walk &s_walk)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    long long total = 0, len = 0, begin = 0;
+    long long total = 0, len = 0, mine = 0;  // mine: this warp's cut
     for (int pass = 0; pass < 2; ++pass) {
         long long at = 0;
         for (int b0 = 0; b0 < B.n_seq; b0 += C::kWarpsAll) {
             if (pass == 0 || B.n_seq > C::kWarpsAll) {
                 long long c = 0;
-                if (b0 + warp < B.n_seq) {
-                    const Seq s = load_seq(B, b0 + warp);
-                    c = head_cost<C>(s, A) * B.kv_heads;
-                }
+                if (b0 + warp < B.n_seq) c = head_cost<C>(load_seq(B, b0 + warp), A) * B.kv_heads;
                 __syncthreads();
                 if (lane == 0) s_cost[warp] = c;
                 __syncthreads();
             }
             for (int i = 0; i < C::kWarpsAll && b0 + i < B.n_seq; ++i) {
                 const long long c = s_cost[i];
-                if (pass == 1 && warp == 0 && begin >= at && begin < at + c) {
-                    // the item that holds tile `begin`: head, then row tile by a scan over the lanes
+                if (pass == 1 && warp < 2 && mine >= at && mine < at + c) {
+                    // the item that holds tile `mine`: head, then row tile by a scan over the lanes
                     const Seq s = load_seq(B, b0 + i);
                     const long long hc = c / B.kv_heads;
-                    const int h = static_cast<int>((begin - at) / hc);
-                    long long rem = begin - at - h * hc;
+                    const int h = static_cast<int>((mine - at) / hc);
+                    long long rem = mine - at - h * hc;
                     const int nst = row_tiles(s, A, C::kRowsItem);
                     for (int st0 = 0; st0 < nst; st0 += 32) {
-                        const int mine = st0 + lane < nst ? item_of<C>(s, A, st0 + lane).tiles : 0;
-                        int inc = mine;
+                        const int n = st0 + lane < nst ? item_of<C>(s, A, st0 + lane).tiles : 0;
+                        int inc = n;
 #pragma unroll
                         for (int o = 1; o < 32; o <<= 1) {
                             const int v = __shfl_up_sync(0xffffffffu, inc, o);
                             if (lane >= o) inc += v;
                         }
-                        if (rem >= inc - mine && rem < inc) {
-                            s_walk.b = b0 + i;
-                            s_walk.h = h;
-                            s_walk.st = st0 + lane;
-                            s_walk.from = static_cast<int>(rem) - (inc - mine);
-                            s_walk.left = min(len, total - begin);
-                            s_walk.x = begin;
+                        if (rem >= inc - n && rem < inc) {
+                            const long long x0 = mine - rem + (inc - n), cut = snap(mine, x0, n);
+                            s_cut[warp] = cut;
+                            if (warp == 0) {
+                                s_walk.b = b0 + i;
+                                s_walk.h = h;
+                                s_walk.st = st0 + lane;
+                                s_walk.from = static_cast<int>(cut - x0);  // = n: the item after it
+                                s_walk.x = cut;
+                            }
                         }
                         const int sum = __shfl_sync(0xffffffffu, inc, 31);
                         if (rem < sum) break;
@@ -257,8 +270,17 @@ __device__ __forceinline__ long long find_stretch(const Batch &B, const Args &A,
             total = at;
             // a stretch of fewer than four tiles would spend more on its join
             len = max((total + gridDim.x - 1) / gridDim.x, 4ll);
-            begin = len * blockIdx.x;
+            mine = len * (blockIdx.x + warp);
+            if (threadIdx.x == 0) s_cut[0] = s_cut[1] = total;
+            __syncthreads();
         }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        Walk w = s_walk;
+        w.left = s_cut[0] < total ? s_cut[1] - s_cut[0] : 0;
+        if (w.left > 0 && w.from == item_of<C>(load_seq(B, w.b), A, w.st).tiles) next_piece<C>(w, B, A, 0);
+        s_walk = w;
     }
     __syncthreads();
     return len;

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
 {
     using C = CfgF32<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ long long s_cost[C::kWarpsAll];
+    __shared__ long long s_cost[C::kWarpsAll], s_cut[2];
     __shared__ Walk s_walk;
     __shared__ volatile int s_abort;
     __shared__ uint32_t s_tmem;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     pdl_wait();
-    const long long len = find_stretch<C>(B, A, s_cost, s_walk);
+    const long long len = find_stretch<C>(B, A, s_cost, s_cut, s_walk);
     Walk w = s_walk;
     volatile int *abort = &s_abort;
     // {m, l} of a tile's rows, from the softmax to the accumulation.  A slot is
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
                 slot[D * 128 + row] = m;
                 slot[(D + 1) * 128 + row] = l;
                 const long long item_x = w.x - w.from;
-                const int c0 = static_cast<int>(item_x / len), c1 = static_cast<int>((item_x + it.tiles - 1) / len);
+                const int c0 = first_cta(item_x, it.tiles, len), c1 = last_cta(item_x, it.tiles, len);
                 __threadfence();
                 bar_sync(1, 128);
                 if (row == 0) {
@@ -406,6 +406,7 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
                     __threadfence();
                     auto part = [&](int c) { return A.part + (2ll * c + (c == c0 ? 1 : 0)) * kSlot; };
                     float M = kNone, L = 0.f;
+#pragma unroll 4
                     for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(part(c) + D * 128 + row));
 #pragma unroll
                     for (int c = 0; c < D; ++c) acc[c] = 0.f;
