@@ -48,11 +48,11 @@ struct CfgF32 {
     // raw full/empty, operand full/empty, q full, s full [2], p full [2], o full [2], o empty [2]
     static constexpr int kBars = 2 * kRaws + 2 * kOps + 9;
     static constexpr int kSmem = kOffBar + 8 * kBars;
-    static constexpr int kDeqWarp = 8, kDeqWarps = 4, kProdWarp = 12, kMmaWarp = 13, kWarpsAll = 16;
+    static constexpr int kDeqWarp = 8, kDeqWarps = 8, kProdWarp = 16, kMmaWarp = 17, kWarpsAll = 20;
     static constexpr int kThreads = 32 * kWarpsAll;
-    // registers per thread: softmax keeps the launch's 128
-    static constexpr int kAccRegs = D == 128 ? 184 : 128, kDeqRegs = 112, kRestRegs = 56;
-    static_assert(128 + kAccRegs + kDeqRegs + kRestRegs <= 512, "register split");
+    // registers per thread after the split; the shares stay within the launch's 640 x 96
+    static constexpr int kSoftRegs = 128, kAccRegs = 184, kDeqRegs = 64, kRestRegs = 40;
+    static_assert(kSoftRegs + kAccRegs + 2 * kDeqRegs + kRestRegs <= 5 * 96, "register split");
     static_assert(kOffOp % 128 == 0 && kOffRaw % 128 == 0 && kOffState % 16 == 0 && kSmem <= 230000, "shared memory layout");
 };
 
@@ -66,70 +66,90 @@ __device__ __forceinline__ void pieces(uint32_t c, uint32_t d, uint32_t &hi, uin
 }
 
 // As dequant_keys of the 16-bit kernel: rows 0-63 the rounded values of 64
-// tokens, rows 64-127 the remainders.
-template <int D>
-__device__ __forceinline__ void dequant_keys2(const uint8_t *raw, uint8_t *op, int tid)
+// tokens, rows 64-127 the remainders.  `taken` is called when the raw stage has
+// been read and waits for the operand stage.
+template <int D, class Taken>
+__device__ __forceinline__ bool dequant_keys2(const uint8_t *raw, uint8_t *op, int tid, Taken taken)
 {
     using C = CfgF32<D>;
-    constexpr int nb = D / 32;
-#pragma unroll 1
-    for (int u = tid; u < C::kKt * nb; u += C::kDeqWarps * 32) {
-        const int tok = u % C::kKt, b = u / C::kKt;
-        const int rec = tok / kRec, t = tok % kRec;
-        const uint8_t *src = raw + rec * C::kHalf;
-        const uint32_t d = *reinterpret_cast<const uint16_t *>(src + k_scale_off(t, b, D));
-        const uint32_t d2 = d | (d << 16);
+    constexpr int nb = D / 32, kTh = C::kDeqWarps * 32, kAll = C::kKt * nb, kN = (kAll + kTh - 1) / kTh;
+    uint4 w[kN][2];
+    uint32_t d[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int u = tid + i * kTh, tok = u % C::kKt, b = u / C::kKt, t = tok % kRec;
+        if (u >= kAll) break;
+        const uint8_t *src = raw + tok / kRec * C::kHalf;
+        d[i] = *reinterpret_cast<const uint16_t *>(src + k_scale_off(t, b, D));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            w[i][h] = *reinterpret_cast<const uint4 *>(src + k_code_off(t, b, nb) + 16 * (h ^ ((t >> 1) & 1)));
+    }
+    if (!taken()) return false;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int u = tid + i * kTh, tok = u % C::kKt, b = u / C::kKt, t = tok % kRec;
+        if (u >= kAll) break;
+        const uint32_t d2 = d[i] | (d[i] << 16);
         uint8_t *dst = op + (tok >> 3) * 128 + (tok & 7) * 16;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int half = i ^ ((t >> 1) & 1);
-            const uint4 w = *reinterpret_cast<const uint4 *>(src + k_code_off(t, b, nb) + 16 * half);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                pieces(codes2(ww[k], 0x4140u), d2, hi[2 * k], lo[2 * k]);
-                pieces(codes2(ww[k], 0x4342u), d2, hi[2 * k + 1], lo[2 * k + 1]);
-            }
-            uint8_t *o = dst + (4 * b + 2 * half) * 2048;
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t ww[4] = {w[i][h].x, w[i][h].y, w[i][h].z, w[i][h].w};
+            uint8_t *o = dst + (4 * b + 2 * (h ^ ((t >> 1) & 1))) * 2048;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                *reinterpret_cast<uint4 *>(o + k * 2048) = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
-                *reinterpret_cast<uint4 *>(o + k * 2048 + 1024) = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                uint4 hi, lo;
+                pieces(codes2(ww[2 * k], 0x4140u), d2, hi.x, lo.x);
+                pieces(codes2(ww[2 * k], 0x4342u), d2, hi.y, lo.y);
+                pieces(codes2(ww[2 * k + 1], 0x4140u), d2, hi.z, lo.z);
+                pieces(codes2(ww[2 * k + 1], 0x4342u), d2, hi.w, lo.w);
+                *reinterpret_cast<uint4 *>(o + k * 2048) = hi;
+                *reinterpret_cast<uint4 *>(o + k * 2048 + 1024) = lo;
             }
         }
     }
+    return true;
 }
 // As dequant_values of the 16-bit kernel: the rounded values' tile, then the remainders'.
-template <int D>
-__device__ __forceinline__ void dequant_values2(const uint8_t *raw, uint8_t *op, int tid, int lo_tok, int hi_tok, uint32_t recs)
+template <int D, class Taken>
+__device__ __forceinline__ bool dequant_values2(const uint8_t *raw, uint8_t *op, int tid, int lo_tok, int hi_tok, uint32_t recs,
+                                                Taken taken)
 {
     using C = CfgF32<D>;
+    constexpr int kTh = C::kDeqWarps * 32, kAll = (C::kKt / 8) * (D / 4), kN = (kAll + kTh - 1) / kTh;
     const bool edge = lo_tok > 0 || hi_tok < C::kKt || recs != (1u << C::kRecs) - 1u;
-#pragma unroll 1
-    for (int u = tid; u < (C::kKt / 8) * (D / 4); u += C::kDeqWarps * 32) {
-        const int c = u % (D / 4), t8 = u / (D / 4);
-        const int rec = t8 / 2, g = 2 * (t8 % 2), b = c / 8;
-        const uint8_t *src = raw + rec * C::kHalf - 17 * D;  // offsets below count from the record
-        uint4 d = *reinterpret_cast<const uint4 *>(src + v_scale_off(4 * g, b, D));  // eight tokens
-        if (edge) d = hide_scales(d, 8 * t8, lo_tok, hi_tok, (recs >> rec) & 1u);
-        const uint4 w0 = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g, c, D));
-        const uint4 w1 = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g + 1, c, D));
-        uint8_t *dst = op + t8 * (D * 16);
-        const uint32_t a[4] = {w0.x, w0.y, w0.z, w0.w}, z[4] = {w1.x, w1.y, w1.z, w1.w};
+    uint4 w[kN][2], d[kN];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = i * (D / 4) + c;
+    for (int i = 0; i < kN; ++i) {
+        const int u = tid + i * kTh, c = u % (D / 4), t8 = u / (D / 4), g = 2 * (t8 % 2);
+        if (u >= kAll) break;
+        const uint8_t *src = raw + t8 / 2 * C::kHalf - 17 * D;  // offsets below count from the record
+        d[i] = *reinterpret_cast<const uint4 *>(src + v_scale_off(4 * g, c / 8, D));  // eight tokens
+        w[i][0] = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g, c, D));
+        w[i][1] = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g + 1, c, D));
+    }
+    if (!taken()) return false;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int u = tid + i * kTh, c = u % (D / 4), t8 = u / (D / 4);
+        if (u >= kAll) break;
+        const uint4 s = edge ? hide_scales(d[i], 8 * t8, lo_tok, hi_tok, (recs >> (t8 / 2)) & 1u) : d[i];
+        uint8_t *dst = op + t8 * (D * 16);
+        const uint32_t a[4] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w}, z[4] = {w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int n = k * (D / 4) + c;
             uint4 hi, lo;
-            pieces(codes2(a[i], 0x4140u), d.x, hi.x, lo.x);
-            pieces(codes2(a[i], 0x4342u), d.y, hi.y, lo.y);
-            pieces(codes2(z[i], 0x4140u), d.z, hi.z, lo.z);
-            pieces(codes2(z[i], 0x4342u), d.w, hi.w, lo.w);
+            pieces(codes2(a[k], 0x4140u), s.x, hi.x, lo.x);
+            pieces(codes2(a[k], 0x4342u), s.y, hi.y, lo.y);
+            pieces(codes2(z[k], 0x4140u), s.z, hi.z, lo.z);
+            pieces(codes2(z[k], 0x4342u), s.w, hi.w, lo.w);
             uint8_t *o = dst + (n >> 3) * 128 + (n & 7) * 16;
             *reinterpret_cast<uint4 *>(o) = hi;
             *reinterpret_cast<uint4 *>(o + C::kKt * D * 2) = lo;
         }
     }
+    return true;
 }
 
 __device__ __forceinline__ uint32_t split_lo(float2 x, uint32_t hi)
@@ -230,6 +250,7 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
 
     if (warp < 4) {
         // ================================================================ softmax: thread = query row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
         const float inv_cap = kCap ? 1.0f / A.softcap : 0.f;
         constexpr float kLog2e = 1.4426950408889634f;
         bool ok = true;
@@ -333,7 +354,7 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
         }
     } else if (warp < C::kDeqWarp) {
         // ================================================================ accumulation: thread = query row
-        if (D == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kAccRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kAccRegs));
         bool ok = true;
         uint32_t n = 0;
         while (w.left > 0) {
@@ -425,7 +446,7 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
         }
     } else if (warp < C::kProdWarp) {
         // ================================================================ dequantizers
-        if (D == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kDeqRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kDeqRegs));
         const int tid = threadIdx.x - 32 * C::kDeqWarp;
         bool ok = true;
         uint32_t n = 0, tile_no = 0;  // operand tiles, key tiles
@@ -440,28 +461,26 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
                     const uint32_t rs = n % C::kRaws, os = n % C::kOps;
                     ok = wait_warp(raw_full + 8 * rs, (n / C::kRaws) & 1, abort, B.status);
                     if (!ok) break;
-                    if (n >= C::kOps) {
-                        ok = wait_warp(op_empty + 8 * os, (n / C::kOps - 1) & 1, abort, B.status);
-                        if (!ok) break;
-                    }
                     const uint8_t *raw = smem + C::kOffRaw + rs * C::kRaw;
                     uint8_t *op = smem + C::kOffOp + os * C::kOp;
-                    if (part == 0) dequant_keys2<D>(raw, op, tid);
-                    else
-                        dequant_values2<D>(raw, op, tid, max(it.lo - p0, 0), min(max(it.hi + 1 - p0, 0), C::kKt),
-                                           s_mask[tile_no % kMaskRing]);
+                    const uint32_t recs = s_mask[tile_no % kMaskRing];
+                    auto taken = [&]() {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(raw_empty + 8 * rs);
+                        return n < C::kOps || wait_warp(op_empty + 8 * os, (n / C::kOps - 1) & 1, abort, B.status);
+                    };
+                    if (part == 0) ok = dequant_keys2<D>(raw, op, tid, taken);
+                    else ok = dequant_values2<D>(raw, op, tid, max(it.lo - p0, 0), min(max(it.hi + 1 - p0, 0), C::kKt), recs, taken);
+                    if (!ok) break;
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(op_full + 8 * os);
-                        mbar_arrive(raw_empty + 8 * rs);
-                    }
+                    if (lane == 0) mbar_arrive(op_full + 8 * os);
                 }
             }
             if (!ok || !next_piece<C>(w, B, A, to - w.from)) break;
         }
     } else {
-        if (D == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRestRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRestRegs));
         if (w.left > 0 && warp == C::kProdWarp) {
             produce<D, C>(w, B, A, smem, raw_full, raw_empty, s_mask, abort);
         } else if (w.left > 0 && warp == C::kMmaWarp && elect_one()) {
