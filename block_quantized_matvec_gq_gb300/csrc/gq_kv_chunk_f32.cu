@@ -40,7 +40,10 @@ struct CfgF32 {
     static constexpr int kRecs = kKt / kRec;
     static constexpr int kHalf = 17 * D;
     static constexpr int kRaw = kRecs * kHalf;
-    static constexpr int kOps = 3, kRaws = 3;
+    // Four operand tiles: with three, the keys of the next tile could only be
+    // converted once this tile's p v had freed its values, just when the tensor
+    // core asks for them.
+    static constexpr int kOps = 4, kRaws = 3;
     static constexpr int kOffOp = 2 * kQ;
     static constexpr int kOffRaw = kOffOp + kOps * kOp;
     static constexpr int kOffState = kOffRaw + kRaws * kRaw;      // {m, l}[4 tiles][128 rows]
@@ -53,7 +56,7 @@ struct CfgF32 {
     // registers per thread after the split; the shares stay within the launch's 640 x 96
     static constexpr int kSoftRegs = 128, kAccRegs = 184, kDeqRegs = 64, kRestRegs = 40;
     static_assert(kSoftRegs + kAccRegs + 2 * kDeqRegs + kRestRegs <= 5 * 96, "register split");
-    static_assert(kOffOp % 128 == 0 && kOffRaw % 128 == 0 && kOffState % 16 == 0 && kSmem <= 230000, "shared memory layout");
+    static_assert(kOffOp % 128 == 0 && kOffRaw % 128 == 0 && kOffState % 16 == 0 && kSmem <= 231000, "shared memory layout");
 };
 
 // c * d as f16x2 rounded, and the exact remainder (18 bits in two pieces).
