@@ -129,8 +129,8 @@ __device__ __forceinline__ long long group_rec(const Batch &B, const Group &g)
         flag_shape(B);
         return -1;
     }
-    const int pg = page_of(B, g.b, static_cast<int>(g.p0));
-    return pg >= 0 ? rec_off(B, pg, 0, static_cast<int>(g.p0), D) : -1;
+    const int rec = static_cast<int>(g.p0) / kRec, pg = page_of(B, g.b, rec);
+    return pg >= 0 ? rec_off(B, pg, 0, rec, D) : -1;
 }
 
 // The unit's place: head, first block, keys or values.
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const uint8_t *__restric
     const long long rec0 = group_rec<D>(B, g);
     if (rec0 < 0) return;  // warp-uniform
     const bool whole = __all_sync(0xffffffffu, g.mine);
-    const long long head_stride = static_cast<long long>(B.page_tokens / kRec) * rec_bytes(D);
+    const long long head_stride = static_cast<long long>(B.per) * rec_bytes(D);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         const Unit u = unit_of<D>(u0 + i, B.kv_heads);
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const uint8_t *__restrict_
     const long long rec0 = group_rec<D>(B, g);
     const int t = g.t, quad = t >> 2;
     const int u0 = (blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5)) * kUnits;
-    const long long head_stride = static_cast<long long>(B.page_tokens / kRec) * rec_bytes(D);
+    const long long head_stride = static_cast<long long>(B.per) * rec_bytes(D);
     uint2 w[kUnits];
     __half d[kUnits];
 #pragma unroll
@@ -348,7 +348,7 @@ inline int check_batch(const void *cache, const int32_t *block_table, const int3
     if (!aligned16(cache) || !aligned4(block_table) || !aligned4(kv_len) || !aligned4(q_start)) return GQ_ERR_ALIGN;
     if (!valid_dim(head_dim) || check_cache(n_pages, page_tokens, kv_heads, head_dim) != GQ_OK) return GQ_ERR_SHAPE;
     // positions and rows are 32-bit numbers in the kernels
-    if (max_pages < 1 || static_cast<long long>(max_pages) * page_tokens > (1 << 30) || n_seq < 1 || n_seq > (1 << 24) ||
+    if (max_pages < 1 || static_cast<long long>(max_pages) * page_tokens > (1 << 28) || n_seq < 1 || n_seq > (1 << 24) ||
         n_tokens < 0 || n_tokens > (1 << 28))
         return GQ_ERR_SHAPE;
     return GQ_OK;
@@ -379,7 +379,8 @@ int gq_kv_append_q8_0(const void *K, long long ldk, const void *V, long long ldv
     if (st == GQ_OK) st = check_rows(V, ldv, kv_heads * head_dim, type);
     if (st != GQ_OK) return st;
     if (n_tokens == 0) return GQ_OK;
-    const Batch B = {block_table, kv_len, q_start, n_pages, max_pages, page_tokens, kv_heads, n_seq, n_tokens, status_word()};
+    const Batch B = make_batch(block_table, kv_len, q_start, n_pages, max_pages, page_tokens, kv_heads, n_seq, n_tokens,
+                               status_word());
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t *c = static_cast<uint8_t *>(cache);
     switch (head_dim) {
@@ -399,7 +400,8 @@ int gq_kv_read_q8_0(const void *cache, const int32_t *block_table, const int32_t
     if (st == GQ_OK) st = check_rows(V, ldv, kv_heads * head_dim, type);
     if (st != GQ_OK) return st;
     if (n_tokens == 0) return GQ_OK;
-    const Batch B = {block_table, kv_len, q_start, n_pages, max_pages, page_tokens, kv_heads, n_seq, n_tokens, status_word()};
+    const Batch B = make_batch(block_table, kv_len, q_start, n_pages, max_pages, page_tokens, kv_heads, n_seq, n_tokens,
+                               status_word());
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const uint8_t *c = static_cast<const uint8_t *>(cache);
     switch (head_dim) {
@@ -433,7 +435,8 @@ int gq_kv_attention_q8_0(const void *Q, long long ldq, const void *cache, const 
     if (!workspace || workspace_bytes < need) return GQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return GQ_ERR_ALIGN;
     if (n_tokens == 0) return GQ_OK;
-    const Batch B = {block_table, kv_len, q_start, n_pages, max_pages, page_tokens, kv_heads, n_seq, n_tokens, status_word()};
+    const Batch B = make_batch(block_table, kv_len, q_start, n_pages, max_pages, page_tokens, kv_heads, n_seq, n_tokens,
+                               status_word());
     return launch_kv_attention(Q, ldq, static_cast<const uint8_t *>(cache), B, O, ldo, type, scale, softcap, window,
                                workspace, heads, head_dim, reinterpret_cast<cudaStream_t>(stream));
 }

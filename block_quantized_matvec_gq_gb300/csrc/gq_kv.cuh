@@ -20,8 +20,16 @@ constexpr float kMaxD = 515.5f;   // largest block scale: 127 * 515.5 = 65468.5 
 struct Batch {
     const int32_t *table, *kv_len, *q_start;
     int n_pages, max_pages, page_tokens, kv_heads, n_seq, n_tokens;
-    int *status;  // device status word
+    int *status;             // device status word
+    uint32_t per, per_mul;   // records per page, and 2^32 / per rounded up
 };
+inline Batch make_batch(const int32_t *table, const int32_t *kv_len, const int32_t *q_start, int n_pages, int max_pages,
+                        int page_tokens, int kv_heads, int n_seq, int n_tokens, int *status)
+{
+    const uint32_t per = static_cast<uint32_t>(page_tokens / kRec);
+    return Batch{table, kv_len, q_start, n_pages, max_pages, page_tokens, kv_heads, n_seq, n_tokens, status, per,
+                 static_cast<uint32_t>(((1ull << 32) + per - 1) / per)};
+}
 
 __host__ __device__ __forceinline__ constexpr int rec_bytes(int D) { return 34 * D; }
 // Byte offset of block b of token t's key codes in a record, of token t's key
@@ -69,20 +77,30 @@ __device__ __forceinline__ Seq load_seq(const Batch &B, int b)
     return seq_of(B, r0, r1, kv);
 }
 
-// Page of position `pos` of sequence b, or -1 (flagged) if the table names none.
-__device__ __forceinline__ int page_of(const Batch &B, int b, int pos)
+// Entry of a sequence's table that holds record `rec` (16 tokens), by a
+// product: exact for rec * per < 2^32, which the checked range (2^28 tokens,
+// 256 records a page) keeps.
+__device__ __forceinline__ int page_entry(const Batch &B, int rec)
 {
-    const int pg = __ldg(B.table + static_cast<long long>(b) * B.max_pages + pos / B.page_tokens);
+    return B.per == 1 ? rec : static_cast<int>(__umulhi(static_cast<uint32_t>(rec), B.per_mul));
+}
+__device__ __forceinline__ const int32_t *page_at(const Batch &B, int b, int rec)
+{
+    return B.table + static_cast<long long>(b) * B.max_pages + page_entry(B, rec);
+}
+// A table entry, or -1 (flagged) if it names no page.
+__device__ __forceinline__ int checked_page(const Batch &B, int pg)
+{
     if (static_cast<unsigned>(pg) < static_cast<unsigned>(B.n_pages)) return pg;
     flag_shape(B);
     return -1;
 }
+__device__ __forceinline__ int page_of(const Batch &B, int b, int rec) { return checked_page(B, __ldg(page_at(B, b, rec))); }
 
-// Byte offset of the record of head h holding position pos of page pg.
-__device__ __forceinline__ long long rec_off(const Batch &B, int pg, int h, int pos, int D)
+// Byte offset of head h's record `rec` of the sequence in page pg.
+__device__ __forceinline__ long long rec_off(const Batch &B, int pg, int h, int rec, int D)
 {
-    const int per = B.page_tokens / kRec;
-    return ((static_cast<long long>(pg) * B.kv_heads + h) * per + (pos % B.page_tokens) / kRec) * rec_bytes(D);
+    return ((static_cast<long long>(pg) * B.kv_heads + h) * B.per + (rec - page_entry(B, rec) * static_cast<int>(B.per))) * rec_bytes(D);
 }
 
 // ---------------------------------------------------------------- element types

@@ -279,8 +279,8 @@ __global__ void __launch_bounds__(kAttnThreads, D == 256 ? 2 : (D == 128 ? 3 : 4
             const int rec = base + lane / kUnit * kStep + lane % kUnit;
             off = -1;
             if (rec < rec1) {
-                const int pg = page_of(B, b, rec * kRec);
-                if (pg >= 0) off = rec_off(B, pg, h, rec * kRec, D);
+                const int pg = page_of(B, b, rec);
+                if (pg >= 0) off = rec_off(B, pg, h, rec, D);
             }
             off_ok = __ballot_sync(0xffffffffu, off >= 0);
             off_base = base;

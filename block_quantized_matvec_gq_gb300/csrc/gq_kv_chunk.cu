@@ -19,7 +19,8 @@
 //                tile d * q (11 bits, one rounding) in the K-major layout; keys
 //                along head_dim, values along the tokens (the cache's words
 //                hold four tokens of one element, so neither is transposed).
-//   producer     one warp: page numbers, and one bulk copy per record half.
+//   producers    two warps (keys, values): page numbers, and one bulk copy per
+//                record half.
 //   mma          one thread.  Per tile of a row tile: p v of this tile, then q k
 //                of the next, so the other row tile's softmax runs meanwhile.
 // p is kept times 2^7 and the state rescaled only when the row's reference
@@ -73,10 +74,12 @@ struct Cfg {
 // lanes fill one core matrix; the two halves of the 32 codes are read in an
 // order that depends on the token, which with the record's own exclusive or
 // spreads eight tokens over all banks.
-// `taken` is called when the raw stage has been read (so it is refilled while
-// the conversion runs) and waits for the operand stage; false ends the tile.
-template <int D, class Taken>
-__device__ __forceinline__ bool dequant_keys(const uint8_t *raw, uint8_t *op, int tid, Taken taken)
+// `op_free` waits for the operand stage, while the raw stage's words arrive;
+// false ends the tile.  The raw stage is given back only after the conversion:
+// an arrival right after the loads does not wait for their data, and a refill
+// overtook them.
+template <int D, class Free>
+__device__ __forceinline__ bool dequant_keys(const uint8_t *raw, uint8_t *op, int tid, Free op_free)
 {
     using C = Cfg<D>;
     constexpr int nb = D / 32, kTh = C::kDeqWarps * 32, kAll = C::kKt * nb, kN = (kAll + kTh - 1) / kTh;
@@ -92,7 +95,7 @@ __device__ __forceinline__ bool dequant_keys(const uint8_t *raw, uint8_t *op, in
         for (int h = 0; h < 2; ++h)
             w[i][h] = *reinterpret_cast<const uint4 *>(src + k_code_off(t, b, nb) + 16 * (h ^ ((t >> 1) & 1)));
     }
-    if (!taken()) return false;
+    if (!op_free()) return false;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
         const int u = tid + i * kTh, tok = u % C::kKt, b = u / C::kKt, t = tok % kRec;
@@ -123,8 +126,8 @@ __device__ __forceinline__ bool dequant_keys(const uint8_t *raw, uint8_t *op, in
 // neighbouring rows), K = token.  A unit is eight tokens of one chunk.
 // [lo, hi): tokens of the tile that some row of the item sees; recs: a bit per
 // record that has a page.
-template <int D, class Taken>
-__device__ __forceinline__ bool dequant_values(const uint8_t *raw, uint8_t *op, int tid, int lo, int hi, uint32_t recs, Taken taken)
+template <int D, class Free>
+__device__ __forceinline__ bool dequant_values(const uint8_t *raw, uint8_t *op, int tid, int lo, int hi, uint32_t recs, Free op_free)
 {
     using C = Cfg<D>;
     constexpr int kTh = C::kDeqWarps * 32, kAll = (C::kKt / 8) * (D / 4), kN = (kAll + kTh - 1) / kTh;
@@ -139,7 +142,7 @@ __device__ __forceinline__ bool dequant_values(const uint8_t *raw, uint8_t *op, 
         w[i][0] = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g, c, D));
         w[i][1] = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g + 1, c, D));
     }
-    if (!taken()) return false;
+    if (!op_free()) return false;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
         const int u = tid + i * kTh, c = u % (D / 4), t8 = u / (D / 4);
@@ -501,25 +504,26 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
                     const uint8_t *raw = smem + C::kOffRaw + rs * C::kRaw;
                     uint8_t *op = smem + C::kOffOp + os * C::kOp;
                     const uint32_t recs = s_mask[tile_no % kMaskRing];
-                    auto taken = [&]() {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(raw_empty + 8 * rs);
+                    auto op_free = [&]() {
                         return n < C::kOps || wait_warp(op_empty + 8 * os, (n / C::kOps - 1) & 1, abort, B.status);
                     };
-                    if (part == 0) ok = dequant_keys<D>(raw, op, tid, taken);
-                    else ok = dequant_values<D>(raw, op, tid, max(it.lo - p0, 0), min(max(it.hi + 1 - p0, 0), C::kKt), recs, taken);
+                    if (part == 0) ok = dequant_keys<D>(raw, op, tid, op_free);
+                    else ok = dequant_values<D>(raw, op, tid, max(it.lo - p0, 0), min(max(it.hi + 1 - p0, 0), C::kKt), recs, op_free);
                     if (!ok) break;
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(op_full + 8 * os);
+                    if (lane == 0) {
+                        mbar_arrive(op_full + 8 * os);
+                        mbar_arrive(raw_empty + 8 * rs);
+                    }
                 }
             }
             if (!ok || !next_piece<C>(w, B, A, to - w.from)) break;
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRestRegs));
-    if (w.left > 0 && warp == C::kProdWarp) {
-        produce<D, C>(w, B, A, smem, raw_full, raw_empty, s_mask, abort);
+    if (w.left > 0 && (warp == C::kProdWarp || warp == C::kProdWarp + 2)) {
+        produce<D, C>(warp != C::kProdWarp, w, B, A, smem, raw_full, raw_empty, s_mask, abort);
     } else if (w.left > 0 && warp == C::kMmaWarp && elect_one()) {
         // ================================================================ mma: one thread
         constexpr uint32_t kIdQk = idesc_f16(128, C::kKt, false), kIdPv = idesc_f16(128, D, false);

@@ -286,59 +286,57 @@ __device__ __forceinline__ long long find_stretch(const Batch &B, const Args &A,
     return len;
 }
 
-// The producer warp: page numbers one tile ahead, and one bulk copy per half
-// of a record (its keys, then its values) into the ring of raw stages, a lane
-// per record.  mask: a bit per record of a tile, 0 where the page is bad (its
-// tokens are then hidden); records beyond the item are hidden by position and
-// not copied.
+// A producer warp: the key halves (part 0) or the value halves (part 1) of a
+// tile's records into the ring of raw stages, tile t into stage number 2 t +
+// part; a lane per record, one bulk copy each (two warps, because the copies of
+// a warp are issued one lane at a time).  Page numbers are fetched a tile ahead
+// and looked at only then.  mask: a bit per record of a tile, 0 where the page is
+// bad (its tokens are then hidden); records beyond the item are hidden by
+// position and not copied.
 template <int D, class C>
-__device__ __forceinline__ void produce(Walk &w, const Batch &B, const Args &A, uint8_t *smem, uint32_t raw_full,
+__device__ __forceinline__ void produce(int part, Walk &w, const Batch &B, const Args &A, uint8_t *smem, uint32_t raw_full,
                                         uint32_t raw_empty, uint32_t *s_mask, volatile int *abort)
 {
     const int lane = threadIdx.x & 31;
     bool ok = true;
-    uint32_t n = 0, tile_no = 0;
+    uint32_t tile_no = 0;
     while (ok) {
         const Seq s = load_seq(B, w.b);
         const Item it = item_of<C>(s, A, w.st);
         const int to = static_cast<int>(min(static_cast<long long>(it.tiles), w.from + w.left));
-        auto page = [&](int j) {  // this lane's record of tile j: its page, -1 if it is bad, -2 if it is beyond the item
-            const int pos = it.base + j * C::kKt + lane * kRec;
-            if (lane >= C::kRecs || j >= to || pos > it.hi) return -2;
-            return page_of(B, w.b, pos);
-        };
-        int pg = page(w.from);
-        for (int j = w.from; j < to && ok; ++j, ++tile_no) {
-            const int pg_next = page(j + 1);
-            // records beyond the item are hidden by position; bad pages by this mask
-            const uint32_t copied = __ballot_sync(0xffffffffu, pg >= 0);
-            const uint32_t bad = __ballot_sync(0xffffffffu, pg == -1);
-            const int pos = it.base + j * C::kKt + lane * kRec;
-#pragma unroll 1
-            for (int part = 0; part < 2; ++part, ++n) {
-                const uint32_t rs = n % C::kRaws;
-                if (n >= C::kRaws) {
-                    ok = wait_warp(raw_empty + 8 * rs, (n / C::kRaws - 1) & 1, abort, B.status);
-                    if (!ok) break;
-                }
-                if (lane == 0) {
-                    if (part == 0) s_mask[tile_no % kMaskRing] = ((1u << C::kRecs) - 1u) & ~bad;
-                    const uint32_t bytes = __popc(copied) * C::kHalf;
-                    if (bytes) mbar_expect_tx(raw_full + 8 * rs, bytes);
-                    else mbar_arrive(raw_full + 8 * rs);
-                }
-                __syncwarp();
-                if (pg >= 0)
-                    bulk_load(smem_u32(smem) + C::kOffRaw + rs * C::kRaw + lane * C::kHalf,
-                              A.cache + rec_off(B, pg, w.h, pos, D) + part * C::kHalf, C::kHalf, raw_full + 8 * rs);
+        const int rec0 = it.base / kRec + lane;  // this lane's record of tile 0
+        auto wanted = [&](int j) { return lane < C::kRecs && j < to && (rec0 + j * C::kRecs) * kRec <= it.hi; };
+        auto entry = [&](int j) { return wanted(j) ? __ldg(page_at(B, w.b, rec0 + j * C::kRecs)) : 0; };
+        int next = entry(w.from);
+        for (int j = w.from; j < to; ++j, ++tile_no) {
+            const bool want = wanted(j);
+            const int pg = want ? checked_page(B, next) : -1;
+            next = entry(j + 1);
+            const uint32_t copied = __ballot_sync(0xffffffffu, pg >= 0), bad = __ballot_sync(0xffffffffu, want && pg < 0);
+            const uint32_t n = 2 * tile_no + part, rs = n % C::kRaws;
+            const uint8_t *src = A.cache + (pg >= 0 ? rec_off(B, pg, w.h, rec0 + j * C::kRecs, D) : 0) + part * C::kHalf;
+            if (n >= C::kRaws) {
+                ok = wait_warp(raw_empty + 8 * rs, (n / C::kRaws - 1) & 1, abort, B.status);
+                if (!ok) break;
             }
-            pg = pg_next;
+            if (lane == 0) {
+                if (part == 0) s_mask[tile_no % kMaskRing] = ((1u << C::kRecs) - 1u) & ~bad;
+                const uint32_t bytes = __popc(copied) * C::kHalf;
+                if (bytes) mbar_expect_tx(raw_full + 8 * rs, bytes);
+                else mbar_arrive(raw_full + 8 * rs);
+            }
+            __syncwarp();
+            if (pg >= 0) bulk_load(smem_u32(smem) + C::kOffRaw + rs * C::kRaw + lane * C::kHalf, src, C::kHalf, raw_full + 8 * rs);
         }
-        if (!ok || !next_piece<C>(w, B, A, to - w.from)) break;
+        if (!ok || !next_piece<C>(w, B, A, to - w.from)) {
+            break;
+        }
     }
-    // copies in flight land before the CTA's memory is given up
-    for (uint32_t i = n > C::kRaws ? n - C::kRaws : 0; i < n; ++i)
-        wait_warp(raw_full + 8 * (i % C::kRaws), (i / C::kRaws) & 1, abort, B.status);
+    // the last copies land before the CTA's memory is given up
+    for (uint32_t t = tile_no > C::kRaws ? tile_no - C::kRaws : 0; t < tile_no; ++t) {
+        const uint32_t n = 2 * t + part;
+        if (n + C::kRaws >= 2 * tile_no + part) wait_warp(raw_full + 8 * (n % C::kRaws), (n / C::kRaws) & 1, abort, B.status);
+    }
 }
 
 // Shared-memory descriptors of operand tiles in 8 x 16-byte core matrices, 128

@@ -68,92 +68,98 @@ __device__ __forceinline__ void pieces(uint32_t c, uint32_t d, uint32_t &hi, uin
     lo = *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// As dequant_keys of the 16-bit kernel: rows 0-63 the rounded values of 64
-// tokens, rows 64-127 the remainders.  `taken` is called when the raw stage has
-// been read and waits for the operand stage.
-template <int D, class Taken>
-__device__ __forceinline__ bool dequant_keys2(const uint8_t *raw, uint8_t *op, int tid, Taken taken)
-{
+// A thread's share of a raw stage, read before the stage before it is
+// converted: units of one (token, block) of keys, or of eight tokens of four
+// elements of values (as in the 16-bit kernel).
+template <int D>
+struct RawKeys {
     using C = CfgF32<D>;
-    constexpr int nb = D / 32, kTh = C::kDeqWarps * 32, kAll = C::kKt * nb, kN = (kAll + kTh - 1) / kTh;
+    static constexpr int kTh = C::kDeqWarps * 32, kAll = C::kKt * (D / 32), kN = (kAll + kTh - 1) / kTh;
     uint4 w[kN][2];
     uint32_t d[kN];
+    __device__ __forceinline__ void load(const uint8_t *raw, int tid)
+    {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        const int u = tid + i * kTh, tok = u % C::kKt, b = u / C::kKt, t = tok % kRec;
-        if (u >= kAll) break;
-        const uint8_t *src = raw + tok / kRec * C::kHalf;
-        d[i] = *reinterpret_cast<const uint16_t *>(src + k_scale_off(t, b, D));
+        for (int i = 0; i < kN; ++i) {
+            const int u = tid + i * kTh, tok = u % C::kKt, b = u / C::kKt, t = tok % kRec;
+            if (u >= kAll) break;
+            const uint8_t *src = raw + tok / kRec * C::kHalf;
+            d[i] = *reinterpret_cast<const uint16_t *>(src + k_scale_off(t, b, D));
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            w[i][h] = *reinterpret_cast<const uint4 *>(src + k_code_off(t, b, nb) + 16 * (h ^ ((t >> 1) & 1)));
+            for (int h = 0; h < 2; ++h)
+                w[i][h] = *reinterpret_cast<const uint4 *>(src + k_code_off(t, b, D / 32) + 16 * (h ^ ((t >> 1) & 1)));
+        }
     }
-    if (!taken()) return false;
+    // rows 0-63 the rounded values of 64 tokens, rows 64-127 the remainders
+    __device__ __forceinline__ void convert(uint8_t *op, int tid) const
+    {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        const int u = tid + i * kTh, tok = u % C::kKt, b = u / C::kKt, t = tok % kRec;
-        if (u >= kAll) break;
-        const uint32_t d2 = d[i] | (d[i] << 16);
-        uint8_t *dst = op + (tok >> 3) * 128 + (tok & 7) * 16;
+        for (int i = 0; i < kN; ++i) {
+            const int u = tid + i * kTh, tok = u % C::kKt, b = u / C::kKt, t = tok % kRec;
+            if (u >= kAll) break;
+            const uint32_t d2 = d[i] | (d[i] << 16);
+            uint8_t *dst = op + (tok >> 3) * 128 + (tok & 7) * 16;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t ww[4] = {w[i][h].x, w[i][h].y, w[i][h].z, w[i][h].w};
-            uint8_t *o = dst + (4 * b + 2 * (h ^ ((t >> 1) & 1))) * 2048;
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t ww[4] = {w[i][h].x, w[i][h].y, w[i][h].z, w[i][h].w};
+                uint8_t *o = dst + (4 * b + 2 * (h ^ ((t >> 1) & 1))) * 2048;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint4 hi, lo;
-                pieces(codes2(ww[2 * k], 0x4140u), d2, hi.x, lo.x);
-                pieces(codes2(ww[2 * k], 0x4342u), d2, hi.y, lo.y);
-                pieces(codes2(ww[2 * k + 1], 0x4140u), d2, hi.z, lo.z);
-                pieces(codes2(ww[2 * k + 1], 0x4342u), d2, hi.w, lo.w);
-                *reinterpret_cast<uint4 *>(o + k * 2048) = hi;
-                *reinterpret_cast<uint4 *>(o + k * 2048 + 1024) = lo;
+                for (int k = 0; k < 2; ++k) {
+                    uint4 hi, lo;
+                    pieces(codes2(ww[2 * k], 0x4140u), d2, hi.x, lo.x);
+                    pieces(codes2(ww[2 * k], 0x4342u), d2, hi.y, lo.y);
+                    pieces(codes2(ww[2 * k + 1], 0x4140u), d2, hi.z, lo.z);
+                    pieces(codes2(ww[2 * k + 1], 0x4342u), d2, hi.w, lo.w);
+                    *reinterpret_cast<uint4 *>(o + k * 2048) = hi;
+                    *reinterpret_cast<uint4 *>(o + k * 2048 + 1024) = lo;
+                }
             }
         }
     }
-    return true;
-}
-// As dequant_values of the 16-bit kernel: the rounded values' tile, then the remainders'.
-template <int D, class Taken>
-__device__ __forceinline__ bool dequant_values2(const uint8_t *raw, uint8_t *op, int tid, int lo_tok, int hi_tok, uint32_t recs,
-                                                Taken taken)
-{
+};
+template <int D>
+struct RawValues {
     using C = CfgF32<D>;
-    constexpr int kTh = C::kDeqWarps * 32, kAll = (C::kKt / 8) * (D / 4), kN = (kAll + kTh - 1) / kTh;
-    const bool edge = lo_tok > 0 || hi_tok < C::kKt || recs != (1u << C::kRecs) - 1u;
+    static constexpr int kTh = C::kDeqWarps * 32, kAll = (C::kKt / 8) * (D / 4), kN = (kAll + kTh - 1) / kTh;
     uint4 w[kN][2], d[kN];
+    __device__ __forceinline__ void load(const uint8_t *raw, int tid)
+    {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        const int u = tid + i * kTh, c = u % (D / 4), t8 = u / (D / 4), g = 2 * (t8 % 2);
-        if (u >= kAll) break;
-        const uint8_t *src = raw + t8 / 2 * C::kHalf - 17 * D;  // offsets below count from the record
-        d[i] = *reinterpret_cast<const uint4 *>(src + v_scale_off(4 * g, c / 8, D));  // eight tokens
-        w[i][0] = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g, c, D));
-        w[i][1] = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g + 1, c, D));
-    }
-    if (!taken()) return false;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        const int u = tid + i * kTh, c = u % (D / 4), t8 = u / (D / 4);
-        if (u >= kAll) break;
-        const uint4 s = edge ? hide_scales(d[i], 8 * t8, lo_tok, hi_tok, (recs >> (t8 / 2)) & 1u) : d[i];
-        uint8_t *dst = op + t8 * (D * 16);
-        const uint32_t a[4] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w}, z[4] = {w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int n = k * (D / 4) + c;
-            uint4 hi, lo;
-            pieces(codes2(a[k], 0x4140u), s.x, hi.x, lo.x);
-            pieces(codes2(a[k], 0x4342u), s.y, hi.y, lo.y);
-            pieces(codes2(z[k], 0x4140u), s.z, hi.z, lo.z);
-            pieces(codes2(z[k], 0x4342u), s.w, hi.w, lo.w);
-            uint8_t *o = dst + (n >> 3) * 128 + (n & 7) * 16;
-            *reinterpret_cast<uint4 *>(o) = hi;
-            *reinterpret_cast<uint4 *>(o + C::kKt * D * 2) = lo;
+        for (int i = 0; i < kN; ++i) {
+            const int u = tid + i * kTh, c = u % (D / 4), t8 = u / (D / 4), g = 2 * (t8 % 2);
+            if (u >= kAll) break;
+            const uint8_t *src = raw + t8 / 2 * C::kHalf - 17 * D;  // offsets below count from the record
+            d[i] = *reinterpret_cast<const uint4 *>(src + v_scale_off(4 * g, c / 8, D));  // eight tokens
+            w[i][0] = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g, c, D));
+            w[i][1] = *reinterpret_cast<const uint4 *>(src + v_chunk_off(g + 1, c, D));
         }
     }
-    return true;
-}
+    // the rounded values' tile, then the remainders'
+    __device__ __forceinline__ void convert(uint8_t *op, int tid, int lo_tok, int hi_tok, uint32_t recs) const
+    {
+        const bool edge = lo_tok > 0 || hi_tok < C::kKt || recs != (1u << C::kRecs) - 1u;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int u = tid + i * kTh, c = u % (D / 4), t8 = u / (D / 4);
+            if (u >= kAll) break;
+            const uint4 s = edge ? hide_scales(d[i], 8 * t8, lo_tok, hi_tok, (recs >> (t8 / 2)) & 1u) : d[i];
+            uint8_t *dst = op + t8 * (D * 16);
+            const uint32_t a[4] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w}, z[4] = {w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int n = k * (D / 4) + c;
+                uint4 hi, lo;
+                pieces(codes2(a[k], 0x4140u), s.x, hi.x, lo.x);
+                pieces(codes2(a[k], 0x4342u), s.y, hi.y, lo.y);
+                pieces(codes2(z[k], 0x4140u), s.z, hi.z, lo.z);
+                pieces(codes2(z[k], 0x4342u), s.w, hi.w, lo.w);
+                uint8_t *o = dst + (n >> 3) * 128 + (n & 7) * 16;
+                *reinterpret_cast<uint4 *>(o) = hi;
+                *reinterpret_cast<uint4 *>(o + C::kKt * D * 2) = lo;
+            }
+        }
+    }
+};
 
 __device__ __forceinline__ uint32_t split_lo(float2 x, uint32_t hi)
 {
@@ -452,40 +458,53 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kDeqRegs));
         const int tid = threadIdx.x - 32 * C::kDeqWarp;
         bool ok = true;
-        uint32_t n = 0, tile_no = 0;  // operand tiles, key tiles
+        uint32_t n = 0, tile_no = 0;  // operand tiles (keys 2 t, values 2 t + 1 of tile t), key tiles
+        RawKeys<D> keys;
+        RawValues<D> vals;
+        auto raw_of = [&](uint32_t i) -> const uint8_t * {  // waits for raw stage i
+            if (ok) ok = wait_warp(raw_full + 8 * (i % C::kRaws), (i / C::kRaws) & 1, abort, B.status);
+            return smem + C::kOffRaw + (i % C::kRaws) * C::kRaw;
+        };
+        auto op_of = [&](uint32_t i) {  // waits for operand stage i
+            if (ok && i >= C::kOps) ok = wait_warp(op_empty + 8 * (i % C::kOps), (i / C::kOps - 1) & 1, abort, B.status);
+            return smem + C::kOffOp + (i % C::kOps) * C::kOp;
+        };
+        // the raw stage is given back only now: an arrival right after the loads
+        // would not wait for their data
+        auto op_done = [&](uint32_t i) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(op_full + 8 * (i % C::kOps));
+                mbar_arrive(raw_empty + 8 * (i % C::kRaws));
+            }
+        };
         while (ok && w.left > 0) {
             const Seq s = load_seq(B, w.b);
             const Item it = item_of<C>(s, A, w.st);
             const int to = static_cast<int>(min(static_cast<long long>(it.tiles), w.from + w.left));
-            for (int j = w.from; j < to && ok; ++j, ++tile_no) {
+            keys.load(raw_of(n), tid);
+            if (!ok) break;
+            for (int j = w.from; j < to; ++j, ++tile_no, n += 2) {
                 const int p0 = it.base + j * C::kKt;
-#pragma unroll 1
-                for (int part = 0; part < 2; ++part, ++n) {
-                    const uint32_t rs = n % C::kRaws, os = n % C::kOps;
-                    ok = wait_warp(raw_full + 8 * rs, (n / C::kRaws) & 1, abort, B.status);
-                    if (!ok) break;
-                    const uint8_t *raw = smem + C::kOffRaw + rs * C::kRaw;
-                    uint8_t *op = smem + C::kOffOp + os * C::kOp;
-                    const uint32_t recs = s_mask[tile_no % kMaskRing];
-                    auto taken = [&]() {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(raw_empty + 8 * rs);
-                        return n < C::kOps || wait_warp(op_empty + 8 * os, (n / C::kOps - 1) & 1, abort, B.status);
-                    };
-                    if (part == 0) ok = dequant_keys2<D>(raw, op, tid, taken);
-                    else ok = dequant_values2<D>(raw, op, tid, max(it.lo - p0, 0), min(max(it.hi + 1 - p0, 0), C::kKt), recs, taken);
-                    if (!ok) break;
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(op_full + 8 * os);
-                }
+                const uint32_t recs = s_mask[tile_no % kMaskRing];
+                vals.load(raw_of(n + 1), tid);
+                uint8_t *op = op_of(n);
+                if (!ok) break;
+                keys.convert(op, tid);
+                op_done(n);
+                if (j + 1 < to) keys.load(raw_of(n + 2), tid);
+                op = op_of(n + 1);
+                if (!ok) break;
+                vals.convert(op, tid, max(it.lo - p0, 0), min(max(it.hi + 1 - p0, 0), C::kKt), recs);
+                op_done(n + 1);
             }
             if (!ok || !next_piece<C>(w, B, A, to - w.from)) break;
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRestRegs));
-        if (w.left > 0 && warp == C::kProdWarp) {
-            produce<D, C>(w, B, A, smem, raw_full, raw_empty, s_mask, abort);
+        if (w.left > 0 && (warp == C::kProdWarp || warp == C::kProdWarp + 2)) {
+            produce<D, C>(warp != C::kProdWarp, w, B, A, smem, raw_full, raw_empty, s_mask, abort);
         } else if (w.left > 0 && warp == C::kMmaWarp && elect_one()) {
             // ============================================================ mma: one thread
             constexpr uint32_t kIdQk1 = idesc_f16(128, 128, false), kIdQk2 = idesc_f16(128, 64, false), kIdPv = idesc_f16(128, D, false);
