@@ -48,7 +48,6 @@ constexpr float kFloor = -1e30f;    // reference of a row that has seen no token
 constexpr float kHead = 6.0f;       // p is kept times 2^6: with the 2^8 slack below 2^15
 constexpr float kSlack = 8.0f;
 
-constexpr int kSnap = 16;           // a cut closer than this to an item's end is moved there
 
 template <int D, int kRows>
 struct SplitCfg {
@@ -57,9 +56,10 @@ struct SplitCfg {
     static constexpr int kStages = D == 256 ? 3 : (D == 128 ? 2 : 3);
     static constexpr int kStage = kUnit * rec_bytes(D);
     static constexpr int kRing = kStages * kStage;
-    // head_dim 256: the accumulators take half the registers, so the query
-    // fragments (the same for all warps) lie in shared memory
-    static constexpr bool kQSmem = D == 256;
+    // the accumulators take most of the registers, so the query fragments (the
+    // same for all warps) lie in shared memory (head_dim 128, 16 rows: 98.6 us
+    // with them in registers, 86.5 us here)
+    static constexpr bool kQSmem = D >= 128;
     static constexpr int kQ = kQSmem ? (D / 16) * 32 * 16 : 0;
     // the merge of the warps' states, and the weights of an item's parts, reuse the ring
     static constexpr int kMerge = kWarps * kRows * (D + 4) * 4, kJoin = kRows * kMaxCtas * 4;
@@ -99,10 +99,18 @@ __device__ __forceinline__ long long seq_cost(const Seq &s, const Batch &B, cons
     const int tiles = (s.n * A.group + rows - 1) / rows;
     return static_cast<long long>(tiles) * B.kv_heads * span_of(s, A.window).n;
 }
-// A cut at x inside an item of n units that begins at x0.
-__device__ __forceinline__ long long snap(long long x, long long x0, int n)
+// A cut at x inside an item of n units that begins at x0: moved to the item's
+// end if that is closer than `tol`, the units that a CTA streams in the time
+// which beginning another piece and joining its part would take it (about 7 us),
+// and at most a stretch.
+template <int D>
+__device__ __forceinline__ int snap_tol(long long len)
 {
-    return x - x0 < kSnap ? x0 : (x0 + n - x < kSnap ? x0 + n : x);
+    return static_cast<int>(min(len, static_cast<long long>(D == 256 ? 12 : 32)));
+}
+__device__ __forceinline__ long long snap(long long x, long long x0, int n, int tol)
+{
+    return x - x0 < tol ? x0 : (x0 + n - x < tol ? x0 + n : x);
 }
 
 // Lays the sequences on the line: the call's total, and the part [b0, b1) of
@@ -218,6 +226,7 @@ __global__ void __launch_bounds__(kAttnThreads, D == 256 ? 2 : (D == 128 ? 3 : 4
     // at least two records a warp: a shorter stretch would spend more on its start
     const long long len = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(2 * kWarps));
     const long long cut0 = len * blockIdx.x, cut1 = cut0 + len;
+    const int tol = snap_tol<D>(len);
     if (cut0 >= total) return;
     {
         long long at = excl;
@@ -226,11 +235,11 @@ __global__ void __launch_bounds__(kAttnThreads, D == 256 ? 2 : (D == 128 ? 3 : 4
             const long long c = seq_cost(s, B, A, kRows);
             const int n = span_of(s, A.window).n;
             if (cut0 >= at && cut0 < at + c) {
-                s_begin = snap(cut0, at + (cut0 - at) / n * n, n);
+                s_begin = snap(cut0, at + (cut0 - at) / n * n, n, tol);
                 s_seq = b;
                 s_at = at;
             }
-            if (cut1 >= at && cut1 < at + c) s_end = snap(cut1, at + (cut1 - at) / n * n, n);
+            if (cut1 >= at && cut1 < at + c) s_end = snap(cut1, at + (cut1 - at) / n * n, n, tol);
             at += c;
         }
         if (cut1 >= total && threadIdx.x == 0) s_end = total;
@@ -625,8 +634,8 @@ __global__ void __launch_bounds__(kAttnThreads, D == 256 ? 2 : (D == 128 ? 3 : 4
             // the last of the item's CTAs joins their parts, in the order of the stretches: the first
             // is the one after the last cut that was moved to the item's start, and there is one more
             // for every cut that stayed inside
-            const int c0 = static_cast<int>((item_x + min(kSnap, sp.n) - 1) / len);
-            const int c1 = static_cast<int>((item_x + sp.n - kSnap) / len);
+            const int c0 = static_cast<int>((item_x + min(tol, sp.n) - 1) / len);
+            const int c1 = static_cast<int>((item_x + sp.n - tol) / len);
             __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {

@@ -201,7 +201,7 @@ __device__ __forceinline__ uint4 hide_scales(uint4 d, int tok, int lo, int hi, b
 
 // A cut closer than kSnap tiles to an item's end is moved there: joining the
 // parts of a cut item costs about as much as that many tiles.
-constexpr int kSnap = 2;
+constexpr int kSnap = 4;
 __device__ __forceinline__ long long snap(long long x, long long x0, int n)
 {
     return x - x0 < kSnap ? x0 : (x0 + n - x < kSnap ? x0 + n : x);
