@@ -157,7 +157,7 @@ __device__ __forceinline__ Unit unit_of(int u, int kv_heads)
 // kUnits units a warp, all loaded before any is used; the page is looked up
 // meanwhile (only the stores need it).
 template <int D, int TYPE, int kUnits>
-__global__ void __launch_bounds__(kThreads) k_kv_append(const uint8_t *__restrict__ K, long long ldk,
+__global__ void __launch_bounds__(kThreads, 4) k_kv_append(const uint8_t *__restrict__ K, long long ldk,
                                                         const uint8_t *__restrict__ V, long long ldv,
                                                         uint8_t *__restrict__ cache, Batch B)
 {

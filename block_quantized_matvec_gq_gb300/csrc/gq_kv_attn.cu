@@ -278,6 +278,12 @@ __global__ void __launch_bounds__(kAttnThreads, D == 256 ? 2 : (D == 128 ? 3 : 4
         const int rec0 = max(sp.lo + from, item_lo / kRec);
         const int rec1 = item_hi < 0 ? rec0 : min(sp.lo + to, item_hi / kRec + 1);
 
+        {   // the query rows on their way while the pages are looked up
+            const int r = r0 + g < rows ? r0 + g : 0, el = type_size(A.type);
+            const uint8_t *p = A.Q + (s.row0 + r / A.group) * A.ldq + (static_cast<long long>(h * A.group + r % A.group) * D + 8 * t) * el;
+#pragma unroll
+            for (int i = 0; i < nb; ++i) asm volatile("prefetch.global.L1 [%0];" ::"l"(p + 32 * i * el));
+        }
         // ---- the ring's first records; the places of the next 32 of this warp's sit one per lane
         const int mine0 = rec0 + warp * kUnit;
         constexpr int kStep = kWarps * kUnit, kAhead = 32 / kUnit;
