@@ -406,6 +406,115 @@ def test_append_then_attend_agrees_with_attention_over_the_written_values():
         assert np.all(np.abs(got.cpu().numpy().reshape(ref.shape) - ref) <= bound)
 
 
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+def test_many_sequences(typ):
+    """More sequences than a search step, a plan's threads or its warps look at in one go."""
+    t = torch()
+    rng = np.random.default_rng(980)
+    n_seq = 1100
+    kv_len = [int(x) for x in rng.integers(1, 40, n_seq)]
+    counts = [int(rng.integers(0, 3)) if kv > 2 else kv for kv in kv_len]
+    batch = kp.make(kv_len, [kv for kv in kv_len], 1, 64, 16, rng)
+    k = rng.standard_normal((batch.n_tokens, 1, 64)).astype(np.float32)
+    v = rng.standard_normal((batch.n_tokens, 1, 64)).astype(np.float32)
+    kd, k = token_array(k, typ)
+    vd, v = token_array(v, typ)
+    cache = dev(batch.cache)
+    gq.gq_kv_append_q8_0(kd, kd.stride(0), vd, vd.stride(0), TYPES[typ], cache, *lists(batch), *sizes(batch))
+    for b in range(n_seq):
+        for i, p in enumerate(batch.positions(b)):
+            kp.write(batch, b, p, k[batch.starts[b] + i], v[batch.starts[b] + i])
+    assert np.array_equal(cache.cpu().numpy(), batch.cache)
+    gq.gq_kv_read_q8_0(cache, *lists(batch), kd, kd.stride(0), vd, vd.stride(0), TYPES[typ], *sizes(batch))
+    ref = np.concatenate([kp.values(batch, b, batch.positions(b))[0] for b in range(n_seq)]).reshape(-1, 64)
+    assert t.equal(kd.cpu(), t.from_numpy(ref).float().to(tt(typ)))
+    batch.counts = counts
+    check_attention(batch, 2, typ, rng)
+    # and in the form for many rows: 30 sequences of 70 to 90 rows
+    chunk = random_batch([int(x) for x in rng.integers(90, 200, 30)], [int(x) for x in rng.integers(70, 90, 30)], 1, 64, 16, rng)
+    check_attention(chunk, 1, typ, rng)
+    assert gq.gq_device_status() == gq.GQ_OK
+
+
+@pytest.mark.parametrize("typ,dim", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f16", 64), ("f32", 64), ("f32", 128)])
+def test_chunk_results_do_not_vary(typ, dim):
+    """The same call many times over gives the same bits: a stage refilled too early, or a wait for the wrong
+    phase, would show as now and then another row."""
+    t = torch()
+    rng = np.random.default_rng(981)
+    batch = random_batch([700, 390, 1100], [300, 390, 90], 2, dim, 16, rng)
+    heads = 4
+    ws = t.zeros(gq.gq_kv_attention_workspace_bytes(heads, 2, dim), dtype=t.uint8, device="cuda")
+    q = (rng.standard_normal((batch.n_tokens, heads, dim)) * 1.5).astype(np.float32)
+    first = check_attention(batch, heads, typ, rng, q=q, ws=ws)
+    qd, _ = token_array(q, typ)
+    out = t.empty((batch.n_tokens, heads * dim), dtype=tt(typ), device="cuda")
+    cache, ls = dev(batch.cache), lists(batch)
+    for _ in range(200):
+        out.fill_(float("nan"))
+        gq.gq_kv_attention_q8_0(qd, qd.stride(0), cache, *ls, out, out.stride(0), TYPES[typ], dim ** -0.5, 0.0, 0, ws, ws.numel(),
+                                heads, *sizes(batch))
+        assert t.equal(out, first)
+
+
+@pytest.mark.parametrize("n", [1, 70])
+def test_a_cache_beyond_32_bit_offsets(n):
+    """Pages more than 2^32 bytes into the cache, against the same pages at its start."""
+    t = torch()
+    rng = np.random.default_rng(982)
+    batch = random_batch([150], [n], 1, 64, 16, rng)
+    heads, page_bytes = 2, 34 * 64
+    small = dev(batch.cache)
+    n_small = batch.cache.shape[0]
+    n_large = 2 ** 32 // page_bytes + 1000
+    large = t.empty(n_large * page_bytes, dtype=t.uint8, device="cuda")
+    shift = n_large - n_small
+    large[shift * page_bytes:].copy_(small.reshape(-1))
+    table, kv_len, start = lists(batch)
+    far = t.where(table >= 0, table + shift, table).to(t.int32)
+    x = dev(rng.standard_normal((n, 64)).astype(np.float32))
+    q = dev(rng.standard_normal((n, heads * 64)).astype(np.float32))
+    ws = t.zeros(gq.gq_kv_attention_workspace_bytes(heads, 1, 64), dtype=t.uint8, device="cuda")
+    got = []
+    for cache, tab, pages in ((small, table, n_small), (large, far, n_large)):
+        s = (pages, *sizes(batch)[1:])
+        gq.gq_kv_append_q8_0(x, 64, x, 64, gq.GQ_TYPE_F32, cache, tab, kv_len, start, *s)
+        k, v = t.empty_like(x), t.empty_like(x)
+        gq.gq_kv_read_q8_0(cache, tab, kv_len, start, k, 64, v, 64, gq.GQ_TYPE_F32, *s)
+        outs = [k, v]
+        for typ in ("f32", "bf16"):
+            qt = q.to(tt(typ))
+            o = t.empty_like(qt)
+            gq.gq_kv_attention_q8_0(qt, qt.stride(0), cache, tab, kv_len, start, o, o.stride(0), TYPES[typ], 0.125, 0.0, 0, ws,
+                                    ws.numel(), heads, *s)
+            outs.append(o)
+        got.append(outs)
+    assert all(t.equal(a, b) for a, b in zip(*got))
+    assert t.equal(large[shift * page_bytes:], small.reshape(-1))
+    assert gq.gq_device_status() == gq.GQ_OK
+
+
+@pytest.mark.parametrize("n", [2, 70])
+def test_rows_beyond_the_token_arrays_are_reported_and_not_touched(n):
+    t = torch()
+    rng = np.random.default_rng(983)
+    batch = random_batch([100, 90], [n, n], 1, 64, 16, rng)
+    cache = dev(batch.cache)
+    table, kv_len, start = lists(batch)
+    start[2] += 5  # five rows more than the arrays have
+    ws = t.zeros(gq.gq_kv_attention_workspace_bytes(1, 1, 64), dtype=t.uint8, device="cuda")
+    full = t.full((2 * n + 8, 64), 7.5, device="cuda")
+    x = full[:2 * n]
+    gq.gq_kv_read_q8_0(cache, table, kv_len, start, x, 64, x, 64, gq.GQ_TYPE_F32, *sizes(batch))
+    assert gq.gq_device_status() == gq.GQ_ERR_SHAPE
+    q = dev(rng.standard_normal((2 * n, 64)).astype(np.float32))
+    gq.gq_kv_attention_q8_0(q, 64, cache, table, kv_len, start, x, 64, gq.GQ_TYPE_F32, 0.1, 0.0, 0, ws, ws.numel(), 1, *sizes(batch))
+    assert gq.gq_device_status() == gq.GQ_ERR_SHAPE
+    gq.gq_kv_append_q8_0(q, 64, q, 64, gq.GQ_TYPE_F32, cache, table, kv_len, start, *sizes(batch))
+    assert gq.gq_device_status() == gq.GQ_ERR_SHAPE
+    assert bool((full[2 * n:] == 7.5).all())
+
+
 def test_calls_without_tokens_do_nothing():
     t = torch()
     rng = np.random.default_rng(978)
