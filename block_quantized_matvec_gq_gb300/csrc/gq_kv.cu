@@ -9,6 +9,13 @@
 // shuffles, so a lane writes the words of two elements with the four tokens'
 // codes.  A group that is only partly new (the ends of a chunk, every decode
 // step) writes the new tokens' bytes alone.
+//
+// What bounds them: long calls stream.  Appending 17 k tokens of 8 heads x 128
+// in f32 (197 MB with the codes) takes 35.2 us, 5.6 TB/s, 0.82 of the measured
+// copy rate; the instructions of the code rule keep it there (12 a code with
+// its tests per element: 59 us; 6 with one test per eight: 35).  Reading 46 k
+// tokens back in bf16 (360 MB) takes 64.8 us, 5.6 TB/s; in f32 89.7 us, 6.6
+// TB/s.  A decode step is launch latency: one token 2.1 us, 64 sequences 3.5.
 #include <math.h>
 
 #include "gq_kv.cuh"
@@ -265,13 +272,16 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const uint8_t *__restrict_
     }
 }
 
-// Units per warp: one where the call is small (a decode step: every unit's
-// load is issued at once, on as many warps as there are units), kMany where
-// there are enough warps to fill the GPU anyway.
+// Units per warp: one where the call is small (every unit's load is issued at
+// once, on as many warps as there are units), kMany where there are warps
+// enough to fill the GPU anyway.  Measured with 8 heads x 128 in f32, one unit
+// against four: 500 tokens (4 k units) 2.9 and 4.4 us, 1500 5.3 and 5.4, 3000
+// (24 k units) 9.7 and 7.7, 12000 36.4 and 23.5 (append); 3.2 and 4.0, 4.8 and
+// 5.9, 8.1 and 6.8, 26.8 and 22.0 (read).
 constexpr int kMany = 4;
 inline int units_per_warp(long long slots, int units)
 {
-    return slots * units >= 4ll * sm_count() * 64 ? kMany : 1;
+    return slots * units >= 2ll * sm_count() * 64 ? kMany : 1;
 }
 
 template <int D, int TYPE>

@@ -47,8 +47,8 @@
  * a call.
  *
  * Range: head_dim 64, 128 or 256; heads a multiple of kv_heads; page_tokens
- * a multiple of 16, at most 4096; n_tokens = 0 is a valid call that does
- * nothing.
+ * a multiple of 16, at most 4096; max_pages * page_tokens at most 2^28;
+ * n_tokens = 0 is a valid call that does nothing.
  * Errors before any launch: GQ_ERR_NULL, GQ_ERR_ALIGN, GQ_ERR_SHAPE,
  * GQ_ERR_FORMAT for an unknown type, GQ_ERR_WORKSPACE; after it GQ_ERR_CUDA.
  * What only the device can see -- a page number outside 0 .. n_pages - 1, a
@@ -62,6 +62,11 @@
 #define GQ_KV_H
 
 #include "gq.h"
+
+/* Sources: "Metal kernel capability table (Phase B ground truth)", section 3
+ * (attention over a cache, append fused with it) and section 9 (legal
+ * dimensions are checked at dispatch); "Gemma 4 M4 Max kernel roadmap", K3 and
+ * K5 (split attention over long caches, grouped heads, sliding windows). */
 
 #ifdef __cplusplus
 extern "C" {
@@ -114,8 +119,9 @@ int gq_kv_read_q8_0(const void *cache, const int32_t *block_table, const int32_t
  *   finite, window >= 0.
  * Accuracy: with GQ_TYPE_F32 the products are formed from operands of 22 bits
  * or more and summed in f32 (within 1e-5 of the definition in the 2-norm);
- * with the 16-bit types operands of 11 bits are allowed, and O is rounded
- * once from f32.
+ * with the 16-bit types operands of 11 bits are allowed (the cached values
+ * d * q and the probabilities, within 1e-3 of the definition together), the
+ * sums are f32 and O is rounded once from them.  |q| < 2^100.
  *   workspace: device memory, 16-byte aligned, at least
  *   gq_kv_attention_workspace_bytes bytes.  ZERO-FILL IT ONCE before its
  *   first use; every completed call leaves it ready for the next.  Two calls
