@@ -445,6 +445,10 @@ int gq_kv_attention_q8_0(const void *Q, long long ldq, const void *cache, const 
     if (!workspace || workspace_bytes < need) return GQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return GQ_ERR_ALIGN;
     if (n_tokens == 0) return GQ_OK;
+    // A row's window begins at position - window + 1, a 32-bit number in the
+    // kernels, and a row may lie up to 2^28 positions before 0: windows beyond
+    // every position are all the same.
+    if (window > kMaxWindow) window = kMaxWindow;
     const Batch B = make_batch(block_table, kv_len, q_start, n_pages, max_pages, page_tokens, kv_heads, n_seq, n_tokens,
                                status_word());
     return launch_kv_attention(Q, ldq, static_cast<const uint8_t *>(cache), B, O, ldo, type, scale, softcap, window,

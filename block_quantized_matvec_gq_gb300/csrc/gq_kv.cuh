@@ -14,6 +14,7 @@ namespace gq {
 namespace kv {
 
 constexpr int kRec = 16;          // tokens per record
+constexpr int kMaxWindow = 1 << 30;
 constexpr float kMaxD = 515.5f;   // largest block scale: 127 * 515.5 = 65468.5 is finite in fp16
 
 // The batch and the cache as the kernels see them.
