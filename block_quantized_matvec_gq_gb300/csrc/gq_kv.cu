@@ -106,8 +106,9 @@ __device__ __forceinline__ uint2 code_bytes8(const float (&e)[8], float d, float
 }
 
 // What a warp's units have in common: the group of four tokens.  Groups are
-// aligned in position, so one lies in one record, and wholly below position 0
-// or wholly above (rows below it exist only where the lists disagree).
+// aligned in position, so one lies in one record, and wholly inside the table's
+// positions or wholly outside (rows there exist only where the lists are
+// wrong: they are not written, and read as zeros).
 struct Group {
     long long row;  // this lane's token's row
     long long p0;   // the group's first position
@@ -122,7 +123,7 @@ __device__ __forceinline__ Group load_group(const Batch &B, long long slot)
     const long long local = slot - ((static_cast<long long>(s.row0) >> 2) + 2ll * g.b);
     g.p0 = 4ll * ((s.first >> 2) + local);
     const long long pos = g.p0 + ((threadIdx.x >> 2) & 3);
-    g.mine = pos >= s.first && pos < s.kv;
+    g.mine = pos >= s.first && pos < s.first + s.n;
     g.row = s.row0 + (pos - s.first);
     g.t = static_cast<int>(pos) & (kRec - 1);
     return g;
@@ -132,7 +133,7 @@ template <int D>
 __device__ __forceinline__ long long group_rec(const Batch &B, const Group &g)
 {
     if (!__any_sync(0xffffffffu, g.mine)) return -1;
-    if (g.p0 < 0) {
+    if (g.p0 < 0 || g.p0 >= static_cast<long long>(B.max_pages) * B.page_tokens) {
         flag_shape(B);
         return -1;
     }

@@ -53,13 +53,17 @@ __device__ __forceinline__ void flag_shape(const Batch &B)
     if (B.status) atomicExch(B.status, GQ_ERR_SHAPE);
 }
 
-// One sequence of the batch, with what the lists say brought into bounds.
+// One sequence of the batch: what the lists say, brought into bounds.  Rows and
+// cached tokens outside are cut off; the rows that stay keep the positions that
+// the lists give them (some of these below 0 or at kv and beyond if the lists
+// disagree with each other or with the sizes).
 struct Seq {
     int row0;   // first token row
     int n;      // new tokens (rows)
     int kv;     // cached tokens
-    int first;  // position of row0 (kv - n; negative if the lists disagree)
+    int first;  // position of row0
 };
+constexpr int kFar = 1 << 30;  // beyond every position, and far from overflow
 __device__ __forceinline__ Seq seq_of(const Batch &B, int r0, int r1, int kv)
 {
     Seq s;
@@ -68,7 +72,8 @@ __device__ __forceinline__ Seq seq_of(const Batch &B, int r0, int r1, int kv)
     s.n = r1c - s.row0;
     const long long room = static_cast<long long>(B.max_pages) * B.page_tokens;
     s.kv = kv < 0 ? 0 : (kv > room ? static_cast<int>(room) : kv);
-    s.first = s.kv - s.n;
+    const long long first = static_cast<long long>(kv) - r1 + s.row0;
+    s.first = static_cast<int>(first < -kFar ? -kFar : (first > kFar ? kFar : first));
     if (s.row0 != r0 || r1c != r1 || s.kv != kv) flag_shape(B);
     return s;
 }

@@ -279,9 +279,9 @@ __global__ void __launch_bounds__(kAttnThreads, D == 256 ? 2 : (D == 128 ? 3 : 4
 
         const int rows = s.n * A.group, r0 = kRows * tile;
         const int last_tok = min((r0 + kRows - 1) / A.group, s.n - 1), first_tok = r0 / A.group;
-        const int item_hi = s.first + last_tok;                                    // positions that some row sees
+        const int item_hi = min(s.first + last_tok, s.kv - 1);                     // positions that some row sees
         const int item_lo = A.window > 0 ? max(0, s.first + first_tok - A.window + 1) : 0;
-        const int all_hi = s.first + first_tok;                                    // and that every row sees
+        const int all_hi = min(s.first + first_tok, s.kv - 1);                     // and that every row sees
         const int all_lo = A.window > 0 ? max(0, s.first + last_tok - A.window + 1) : 0;
         // this CTA's records of the item
         const int rec0 = max(sp.lo + from, item_lo / kRec);
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kAttnThreads, D == 256 ? 2 : (D == 128 ? 3 : 4
             const int r = r0 + g + 8 * e;
             const bool live = r < rows;
             const int tok = live ? r / A.group : 0, pos = s.first + tok;
-            row_hi[e] = live ? pos : -1;
+            row_hi[e] = live ? min(pos, s.kv - 1) : -1;
             row_lo[e] = A.window > 0 ? max(0, pos - A.window + 1) : 0;
             const int el = type_size(A.type);
             const uint8_t *p = A.Q + (s.row0 + tok) * A.ldq +

@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
             p.live = r < it.rows;
             const int tok = p.live ? r / A.group : 0, head = w.h * A.group + (p.live ? r % A.group : 0);
             const int pos = s.first + tok;
-            p.row_hi = p.live ? pos : -1;
+            p.row_hi = p.live ? min(pos, s.kv - 1) : -1;
             p.row_lo = A.window > 0 ? max(0, pos - A.window + 1) : 0;
             const long long at = static_cast<long long>(head) * D * 2;
             p.dst = A.O + (s.row0 + tok) * A.ldo + at;

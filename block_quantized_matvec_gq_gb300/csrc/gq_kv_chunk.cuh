@@ -48,7 +48,7 @@ __device__ __forceinline__ Item item_of(const Seq &s, const Args &A, int st)
     it.rows = s.n * A.group;
     it.r0 = st * C::kRowsItem;
     const int t0 = it.r0 / A.group, t1 = min(it.r0 + C::kRowsItem, it.rows) - 1;
-    it.hi = s.first + t1 / A.group;
+    it.hi = min(s.first + t1 / A.group, s.kv - 1);
     it.lo = A.window > 0 ? max(0, s.first + t0 - A.window + 1) : 0;
     it.base = it.lo & ~(kRec - 1);
     it.tiles = max(1, (it.hi - it.base + C::kKt) / C::kKt);

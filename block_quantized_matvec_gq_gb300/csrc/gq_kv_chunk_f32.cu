@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
             const bool live = r < it.rows;
             const int tok = live ? r / A.group : 0, head = w.h * A.group + (live ? r % A.group : 0);
             const int pos = s.first + tok;
-            const int row_hi = live ? pos : -1;
+            const int row_hi = live ? min(pos, s.kv - 1) : -1;
             const int row_lo = A.window > 0 ? max(0, pos - A.window + 1) : 0;
             // every q k of the piece before is done: its last scores have been taken
             const float f = load_query_f32<D>(

@@ -56,7 +56,8 @@
  * at a negative position -- is never followed out of bounds: the tokens
  * concerned are not written (append), read as zeros (read) or not attended
  * to (attention), and the device status (gq_device_status) becomes
- * GQ_ERR_SHAPE.
+ * GQ_ERR_SHAPE.  All other rows keep the positions that the lists give them,
+ * and nothing else that is cached changes.
  */
 #ifndef GQ_KV_H
 #define GQ_KV_H

@@ -58,3 +58,103 @@ def test_a_window_beyond_every_position_hides_nothing(counts, typ, dim):
         assert np.array_equal(attend(batch, q, typ, 2, 0.1, window=window), want), window
     check_attention(batch, 2, typ, rng, window=2 ** 31 - 1)
     assert gq.gq_device_status() == gq.GQ_OK
+
+
+# ---------------------------------------------------------------- lists that lead outside
+
+def full_batch(kv_len, counts, kv_heads, dim, page, rng):
+    """A batch whose table has no entry to spare: the first sequence fills it."""
+    batch = random_batch(kv_len, counts, kv_heads, dim, page, rng)
+    batch.table = np.ascontiguousarray(batch.table[:, :-1])
+    assert batch.table.shape[1] * page == kv_len[0]
+    return batch
+
+
+# kv_len past the table's last position, new tokens of that sequence, window
+LONG = [(1, 1, 0), (1, 3, 0), (3, 3, 20), (7, 5, 0), (2, 90, 0), (100, 90, 40), (10 ** 6, 70, 0), (2 ** 31 - 1 - 96, 2, 0),
+        (40, 1, 5), (17, 9, 16)]
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+@pytest.mark.parametrize("over,n,window", LONG)
+def test_a_length_past_the_table_moves_no_token(over, n, window, typ):
+    """kv_len beyond max_pages * page_tokens: rows keep their positions, those past the last one are not written, read
+    as zeros and not attended to, and nothing that was cached changes."""
+    t = torch()
+    rng = np.random.default_rng(1010)
+    hk, heads, dim, page, room = 2, 4, 64, 16, 96
+    batch = full_batch([room, 40], [n, 3], hk, dim, page, rng)
+    table, kv_len, start = lists(batch)
+    kv_len[0] = room + over
+    ls = (table, kv_len, start)
+    pos = [room + over - n + i for i in range(n)] + [37, 38, 39]
+    seq = [0] * n + [1] * 3
+    k = rng.standard_normal((n + 3, hk, dim)).astype(np.float32)
+    v = rng.standard_normal((n + 3, hk, dim)).astype(np.float32)
+    kd, k = token_array(k, typ)
+    vd, v = token_array(v, typ)
+    cache = dev(batch.cache)
+    gq.gq_kv_append_q8_0(kd, kd.stride(0), vd, vd.stride(0), TYPES[typ], cache, *ls, *sizes(batch))
+    assert gq.gq_device_status() == gq.GQ_ERR_SHAPE
+    for i, (b, p) in enumerate(zip(seq, pos)):
+        if 0 <= p < room:
+            kp.write(batch, b, p, k[i], v[i])
+    assert np.array_equal(cache.cpu().numpy(), batch.cache)
+
+    kd.fill_(7.5), vd.fill_(7.5)
+    gq.gq_kv_read_q8_0(cache, *ls, kd, kd.stride(0), vd, vd.stride(0), TYPES[typ], *sizes(batch))
+    assert gq.gq_device_status() == gq.GQ_ERR_SHAPE
+    for i, (b, p) in enumerate(zip(seq, pos)):
+        want = kp.values(batch, b, [p]) if p < room else np.zeros((2, 1, hk, dim))
+        for got, ref in zip((kd, vd), want):
+            assert t.equal(got[i].cpu(), t.from_numpy(ref.reshape(-1)).float().to(tt(typ))), (i, p)
+
+    q, qh = token_array((rng.standard_normal((n + 3, heads, dim)) * 1.5).astype(np.float32), typ)
+    got = attend(batch, q, typ, heads, 0.125, window=window, ls=ls)
+    assert gq.gq_device_status() == gq.GQ_ERR_SHAPE
+    for i, (b, p) in enumerate(zip(seq, pos)):
+        lo = max(0, p - window + 1) if window else 0
+        ref, a = row_attention(batch, b, qh[i], lo, min(p + 1, room), 0.125)
+        # scores up to 8 sqrt(64) * 0.125 * 1.5 in size: Z < 32
+        bound = (2.1 * 2.0 ** -15 + 2.0 ** -16) * a if typ == "f32" else (2.1 * 2.0 ** -5 + 2.0 ** -10) * a + ROUND[typ] * np.abs(ref)
+        assert np.all(np.abs(got[i] - ref) <= bound), (i, p)
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+@pytest.mark.parametrize("n,extra,window", [(2, 5, 0), (3, 1, 0), (70, 5, 0), (70, 33, 11), (90, 2 ** 31 - 200, 0)])
+def test_rows_past_the_token_arrays_move_no_token(n, extra, window, typ):
+    """A q_start beyond n_tokens: the rows that the arrays have keep the positions that the lists give them."""
+    t = torch()
+    rng = np.random.default_rng(1011)
+    hk, heads, dim, page = 1, 2, 64, 16
+    batch = random_batch([100, 96], [n, n], hk, dim, page, rng)
+    table, kv_len, start = lists(batch)
+    start[2] += extra
+    ls = (table, kv_len, start)
+    pos = [100 - n + i for i in range(n)] + [96 - (n + extra) + i for i in range(n)]
+    seq = [0] * n + [1] * n
+    k = rng.standard_normal((2 * n, hk, dim)).astype(np.float32)
+    kd, k = token_array(k, typ)
+    vd = -kd
+    cache = dev(batch.cache)
+    gq.gq_kv_append_q8_0(kd, kd.stride(0), vd, vd.stride(0), TYPES[typ], cache, *ls, *sizes(batch))
+    assert gq.gq_device_status() == gq.GQ_ERR_SHAPE
+    for i, (b, p) in enumerate(zip(seq, pos)):
+        if p >= 0:
+            kp.write(batch, b, p, k[i], -k[i])
+    assert np.array_equal(cache.cpu().numpy(), batch.cache)
+    kd.fill_(7.5), vd.fill_(7.5)
+    gq.gq_kv_read_q8_0(cache, *ls, kd, kd.stride(0), vd, vd.stride(0), TYPES[typ], *sizes(batch))
+    assert gq.gq_device_status() == gq.GQ_ERR_SHAPE
+    for i, (b, p) in enumerate(zip(seq, pos)):
+        want = kp.values(batch, b, [p]) if p >= 0 else np.zeros((2, 1, hk, dim))
+        for got, ref in zip((kd, vd), want):
+            assert t.equal(got[i].cpu(), t.from_numpy(ref.reshape(-1)).float().to(tt(typ))), (i, p)
+    q, qh = token_array((rng.standard_normal((2 * n, heads, dim)) * 1.5).astype(np.float32), typ)
+    got = attend(batch, q, typ, heads, 0.125, window=window, ls=ls)
+    assert gq.gq_device_status() == gq.GQ_ERR_SHAPE
+    for i, (b, p) in enumerate(zip(seq, pos)):
+        lo = max(0, p - window + 1) if window else 0
+        ref, a = row_attention(batch, b, qh[i], lo, p + 1, 0.125)
+        bound = (2.1 * 2.0 ** -15 + 2.0 ** -16) * a if typ == "f32" else (2.1 * 2.0 ** -5 + 2.0 ** -10) * a + ROUND[typ] * np.abs(ref)
+        assert np.all(np.abs(got[i] - ref) <= bound), (i, p)
