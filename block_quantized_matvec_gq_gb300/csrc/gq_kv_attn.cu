@@ -175,12 +175,15 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// About log2 of a positive fp16 given by its bits (below it by at most 0.09
-// for normal numbers; -15 for 0 and about that for subnormals): the bits
-// count 1/1024 octaves.  They are placed under the exponent of 2^23.
-__device__ __forceinline__ float half_octaves(uint32_t h2, uint32_t sel)
+// About log2 of a value scale (below it by at most 0.09): the upper 24 bits of
+// the f32 number count 2^-15 octaves; they are placed under the exponent of
+// 2^23.  A scale of 0, a token without a value, counts as 2^-80: its p, which
+// only the sum l takes, stays in f32's range (2^94), and the reference is that
+// of the tokens with values unless they lie 80 octaves further down.
+__device__ __forceinline__ float octaves(float d)
 {
-    return fmaf(__uint_as_float(__byte_perm(h2, 0x4B000000u, sel)), 0x1p-10f, -(8192.0f + 15.0f));
+    const uint32_t bits = __float_as_uint(fmaxf(d, 0x1p-80f));
+    return fmaf(__uint_as_float(__byte_perm(bits, 0x4B000000u, 0x7321u)), 0x1p-15f, -(256.0f + 127.0f));
 }
 // (a, b) -> f16x2 of the rounded values and of the remainders.
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo)
@@ -488,8 +491,8 @@ __global__ void __launch_bounds__(kAttnThreads, D == 256 ? 2 : (D == 128 ? 3 : 4
                     mx0 = __vmaxu2(mx0, d.x);  // non-negative fp16 order like integers
                     mx1 = __vmaxu2(mx1, d.y);
                 }
-                const float lg[4] = {half_octaves(mx0, 0x7610u), half_octaves(mx0, 0x7632u), half_octaves(mx1, 0x7610u),
-                                     half_octaves(mx1, 0x7632u)};
+                const float2 d01 = half2_f2(mx0), d23 = half2_f2(mx1);
+                const float lg[4] = {octaves(d01.x), octaves(d01.y), octaves(d23.x), octaves(d23.y)};
 #pragma unroll
                 for (int e = 0; e < NR; ++e) {
                     z[e][u][0] = sc[e][u][0].x * zs[e], z[e][u][1] = sc[e][u][0].y * zs[e];

@@ -6,6 +6,8 @@ size, calls without tokens, scales next to a tie of the fp16 rounding.
 The reference is written here for single rows, in 64 bits, on kv_plain's
 cache; tolerances as derived in test_gpu_kv, with what is said at each test."""
 
+import functools
+
 import numpy as np
 import pytest
 
@@ -17,13 +19,19 @@ from test_gpu_kv import ROUND, TYPES, check_attention, lists, random_batch, size
 pytestmark = pytest.mark.gpu
 
 
+_values = {}
+
+
 def row_attention(batch, b, q, lo, hi, scale, softcap=0.0):
     """One query row [heads][dim] over the positions lo .. hi - 1 of sequence b: (o, sum w |v|), zeros where there is none."""
     heads = q.shape[0]
     o, a = np.zeros(q.shape), np.zeros(q.shape)
     if hi <= lo:
         return o, a
-    k, v = kp.values(batch, b, range(lo, hi))
+    key = (id(batch), b)
+    if _values.get("of") != key:  # the last sequence's cached values, for the rows that follow
+        _values.update(of=key, batch=batch, kv=kp.values(batch, b, range(min(batch.kv_len[b], batch.table.shape[1] * batch.page))))
+    k, v = (x[lo:hi] for x in _values["kv"])
     for h in range(heads):
         g = h // (heads // batch.kv_heads)
         s = scale * (k[:, g] @ q[h].astype(np.float64))
@@ -158,3 +166,73 @@ def test_rows_past_the_token_arrays_move_no_token(n, extra, window, typ):
         ref, a = row_attention(batch, b, qh[i], lo, p + 1, 0.125)
         bound = (2.1 * 2.0 ** -15 + 2.0 ** -16) * a if typ == "f32" else (2.1 * 2.0 ** -5 + 2.0 ** -10) * a + ROUND[typ] * np.abs(ref)
         assert np.all(np.abs(got[i] - ref) <= bound), (i, p)
+
+
+# ---------------------------------------------------------------- a strong key with a small value
+
+LOW, HIGH = 127 * 2.0 ** -12, 127 * 2.0 ** -5
+
+
+@functools.lru_cache
+def sink_batch(value, dim, weak):
+    """1400 tokens of which one, in the middle, has a key of HIGH throughout and values of size `value`; the others' are LOW
+    and `weak`.  The keys' codes and scales are exact, so is d * q in 11 bits: the scores carry no error of the cached
+    numbers."""
+    rng = np.random.default_rng(1020)
+    batch = kp.make([1400], [1], 1, dim, 64, rng)
+    for p in range(1400):
+        v = rng.standard_normal((1, dim)).astype(np.float32)
+        key, size = (HIGH, value) if p == 700 else (LOW, weak)
+        kp.write(batch, 0, p, np.full((1, dim), key, np.float32), v * np.float32(size))
+    return batch
+
+
+SINK = [(typ, dim, n) for typ, dim in (("f32", 64), ("f32", 128), ("f32", 256), ("bf16", 64), ("bf16", 128), ("bf16", 256), ("f16", 128))
+        for n in (1, 5)] + [("f32", 256, 80)]
+
+
+@pytest.mark.parametrize("typ,dim,n", SINK)
+@pytest.mark.parametrize("gap", [14.0, 18.0, 24.0, 45.0])
+@pytest.mark.parametrize("value", [0.0, 1e-4])
+def test_a_strong_key_with_a_small_value(value, gap, typ, dim, n):
+    """The weak keys make the result where the strong one's value is small, however small their weights are: held to the
+    2-norm of the type (f32: 1e-5; 16 bits: values and probabilities of 11 bits, together 2^-10, and the result's rounding,
+    or half its smallest number)."""
+    if typ == "f16" and gap > 24.0:
+        gap = 20.0
+    batch = sink_batch(value, dim, 1.0 if typ == "f32" else 8000.0)  # so that f16 holds the result
+    batch.counts = [n]
+    scale = float(gap / (dim * (HIGH - LOW)))
+    q, qh = token_array(np.ones((n, 2, dim), np.float32), typ)
+    got = attend(batch, q, typ, 2, scale)
+    for i in {*range(0, n, 11), n - 1}:
+        ref, _ = row_attention(batch, 0, qh[i], 0, 1400 - n + i + 1, scale)
+        err = np.linalg.norm(got[i] - ref)
+        tol = 1e-5 if typ == "f32" else 2.0 ** -10 + ROUND[typ]
+        floor = 2.0 ** -25 * np.sqrt(ref.size) if typ == "f16" else 0.0
+        assert err <= tol * np.linalg.norm(ref) + floor, (i, err / np.linalg.norm(ref))
+
+
+ANYWHERE = [("f32", 1), ("bf16", 1)]
+
+
+@pytest.mark.parametrize("typ,n", ANYWHERE)
+def test_strong_keys_with_small_values_anywhere(typ, n):
+    """Several of them, in several tiles, seen by some rows only, with a window; values of one token many orders apart
+    from the next one's elsewhere."""
+    rng = np.random.default_rng(1021)
+    kv, dim, heads = 900, 128, 4
+    batch = kp.make([kv], [n], 2, dim, 16, rng, fill=0xFF)
+    strong = set(rng.choice(kv, 12, replace=False).tolist()) | {kv - 60, 0}
+    for p in range(kv):
+        k = rng.standard_normal((2, dim)).astype(np.float32) * np.float32(0.25)
+        v = rng.standard_normal((2, dim)).astype(np.float32)
+        if p in strong:
+            k = k + np.float32(1.0)
+            v = v * np.float32(10.0 ** rng.integers(-7, -3))
+        elif p % 13 == 0:
+            v = v * np.float32(10.0 ** rng.integers(-3, 3))
+        kp.write(batch, 0, p, k, v)
+    q = (np.full((n, heads, dim), 1.0) + rng.standard_normal((n, heads, dim)) * 0.3).astype(np.float32)
+    for window in (0, 333):
+        check_attention(batch, heads, typ, rng, q=q, window=window, norm=typ == "f32")
