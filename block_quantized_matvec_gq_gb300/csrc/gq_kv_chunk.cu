@@ -15,12 +15,13 @@
 //                tensor memory, running reference m and sum l, p back to
 //                tensor memory as the A operand of p v; the query operand and
 //                the result rows.
-//   dequantizers eight warps (twelve at head_dim 256): codes and scales of a raw stage -> the f16 operand
-//                tile d * q (11 bits, one rounding) in the K-major layout; keys
-//                along head_dim, values along the tokens (the cache's words
-//                hold four tokens of one element, so neither is transposed).
+//   dequantizers eight warps (twelve at head_dim 256): codes and scales of a
+//                raw stage -> the f16 operand tile d * q (11 bits, one rounding)
+//                in the K-major layout; keys along head_dim, values along the
+//                tokens (the cache's words hold four tokens of one element, so
+//                neither is transposed).
 //   producers    two warps (keys, values): page numbers, and one bulk copy per
-//                record half.
+//                record half; the first also looks at the values' sizes.
 //   mma          one thread.  Per tile of a row tile: p v of this tile, then q k
 //                of the next, so the other row tile's softmax runs meanwhile.
 // p is kept times 2^7 and the state rescaled only when the row's reference
@@ -35,8 +36,9 @@
 // since tensor memory holds one score buffer per row tile beside the
 // accumulators.  (Two buffers of 64 columns each took longer: twice the
 // waits and N = 64 products.)  A chunk of 2048 tokens behind 30720 cached ones,
-// 32 heads over 8 x 128, bf16: 818 us, 1.30 PFLOP/s, 0.69 of the measured bf16
-// rate; head_dim 64 700 us, head_dim 256 (16 heads) 1250 us.
+// 32 heads over 8 x 128, bf16: 824 us in a graph, 1.29 PFLOP/s, 0.68 of the
+// measured bf16 rate (called one by one on another GB300: 876 us); head_dim 64
+// 712 us, head_dim 256 (16 heads) 1215 us; capped, 2048 of 16384 tokens, 1053.
 // Every wait is bounded (gq_tc.cuh).
 #include "gq_kv_chunk.cuh"
 
@@ -58,10 +60,10 @@ struct Cfg {
     static constexpr int kOffOp = kMt * kQ;
     static constexpr int kOffRaw = kOffOp + kOps * kOp;
     static constexpr int kOffBar = kOffRaw + kRaws * kRaw;
-    // raw full/empty, operand full/empty, q full [2], s full [2], p full [2], pv done [2], piece done [2]
-    static constexpr int kBars = 2 * kRaws + 2 * kOps + 10;
+    // raw full/empty, operand full/empty, q full [2], s full [2], p full [2], pv done [2], piece done [2], fixed
+    static constexpr int kBars = 2 * kRaws + 2 * kOps + 11;
     static constexpr int kOffMisc = kOffBar + 8 * kBars;
-    static constexpr int kSmem = kOffMisc + 512;
+    static constexpr int kSmem = kOffMisc + 512;  // and 7.5 KB of static arrays
     // five warpgroups: softmax (one per row tile), dequantizers, {producer, mma}
     static constexpr int kSoftWarps = 4 * kMt;
     static constexpr int kDeqWarps = 16 - kSoftWarps;
@@ -71,9 +73,9 @@ struct Cfg {
     static constexpr int kThreads = 32 * kWarpsAll;
     // Registers per thread after the split (a softmax thread holds a whole
     // score row); the shares stay within the launch's 640 x 96.
-    static constexpr int kSoftRegs = kMt == 2 ? 168 : 144, kDeqRegs = kMt == 2 ? 48 : 72, kRestRegs = 40;
+    static constexpr int kSoftRegs = kMt == 2 ? 168 : 144, kDeqRegs = kMt == 2 ? 48 : 72, kRestRegs = 48;
     static_assert(32 * (kSoftWarps * kSoftRegs + kDeqWarps * kDeqRegs + 4 * kRestRegs) <= kThreads * 96, "register split");
-    static_assert(kOffOp % 128 == 0 && kOffRaw % 128 == 0 && kOffBar % 8 == 0 && kSmem <= 232448, "shared memory layout");
+    static_assert(kOffOp % 128 == 0 && kOffRaw % 128 == 0 && kOffBar % 8 == 0 && kSmem + 7680 <= 232448, "shared memory layout");
 };
 // ---------------------------------------------------------------- dequantizers
 // Operand tiles are core matrices of 8 rows x 16 bytes (8 elements of K); row
@@ -133,14 +135,11 @@ __device__ __forceinline__ bool dequant_keys(const uint8_t *raw, uint8_t *op, in
 // Values: row n = (e % 4) * D / 4 + e / 4 for element e (neighbouring lanes,
 // which take neighbouring 16-byte chunks of four elements, then store to
 // neighbouring rows), K = token.  A unit is eight tokens of one chunk.
-// [lo, hi): tokens of the tile that some row of the item sees; recs: a bit per
-// record that has a page.
 template <int D, class Free>
-__device__ __forceinline__ bool dequant_values(const uint8_t *raw, uint8_t *op, int tid, int lo, int hi, uint32_t recs, Free op_free)
+__device__ __forceinline__ bool dequant_values(const uint8_t *raw, uint8_t *op, int tid, Free op_free)
 {
     using C = Cfg<D>;
     constexpr int kTh = C::kDeqWarps * 32, kAll = (C::kKt / 8) * (D / 4), kN = (kAll + kTh - 1) / kTh;
-    const bool edge = lo > 0 || hi < C::kKt || recs != (1u << C::kRecs) - 1u;
     uint4 w[kN][2], d[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
@@ -156,7 +155,7 @@ __device__ __forceinline__ bool dequant_values(const uint8_t *raw, uint8_t *op, 
     for (int i = 0; i < kN; ++i) {
         const int u = tid + i * kTh, c = u % (D / 4), t8 = u / (D / 4);
         if (kAll % kTh != 0 && u >= kAll) break;
-        const uint4 s = edge ? hide_scales(d[i], 8 * t8, lo, hi, (recs >> (t8 / 2)) & 1u) : d[i];
+        const uint4 s = d[i];
         uint8_t *dst = op + t8 * (D * 16);
         const uint32_t a[4] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w}, z[4] = {w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
 #pragma unroll
@@ -215,13 +214,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
     __shared__ volatile int s_abort;
     __shared__ uint32_t s_tmem;
     __shared__ uint32_t s_mask[kMaskRing];
+    __shared__ __align__(16) float s_dn[kMaskRing * C::kKt];
+    __shared__ __align__(16) uint16_t s_scratch[C::kKt];
+    __shared__ float2 s_sum[128 * C::kMt];
     __shared__ int s_last[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = smem_u32(smem);
     const uint32_t bar = base + C::kOffBar;
     const uint32_t raw_full = bar, raw_empty = raw_full + 8 * C::kRaws, op_full = raw_empty + 8 * C::kRaws,
                    op_empty = op_full + 8 * C::kOps, q_full = op_empty + 8 * C::kOps, s_full = q_full + 16,
-                   p_full = s_full + 16, pv_done = p_full + 16, o_done = pv_done + 16;
+                   p_full = s_full + 16, pv_done = p_full + 16, o_done = pv_done + 16, fixed = o_done + 16;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kRaws; ++i) {
             mbar_init(raw_full + 8 * i, 1);
@@ -231,6 +233,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
             mbar_init(op_full + 8 * i, C::kDeqWarps);
             mbar_init(op_empty + 8 * i, 1);
         }
+        mbar_init(fixed, C::kDeqWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + 8 * i, 4);
             mbar_init(s_full + 8 * i, 1);
@@ -331,18 +334,18 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
                     if (!ok) break;
                     tc_fence_after();
                     const int p0 = pc.base + j * C::kKt;
-                    const uint32_t recs = s_mask[(tile_no + (j - pc.from)) % kMaskRing];
+                    const uint32_t slot = (tile_no + (j - pc.from)) % kMaskRing, word = s_mask[slot], recs = word & ~kMixed;
                     // every row of the warp sees the whole tile?
                     const bool edge = __any_sync(0xffffffffu, p0 < pc.row_lo || p0 + C::kKt - 1 > pc.row_hi) ||
                                       recs != (1u << C::kRecs) - 1u;
+                    if (kCap) cap_scores<C::kKt, false>(s_addr, zs, A.softcap, inv_cap);
+                    if (__builtin_expect(word & kMixed, 0))
+                        shift_scores<C::kKt, false>(s_addr, kCap ? 1.0f : zs, pc.row_lo - p0, pc.row_hi - p0, recs, s_dn + slot * C::kKt,
+                                                   s_sum + threadIdx.x);
                     float v[C::kKt];
 #pragma unroll
                     for (int c = 0; c < C::kKt; c += 32) tmem_ld32_async(s_addr + c, v + c);
                     tmem_wait_ld(v);
-                    if (kCap) {
-#pragma unroll
-                        for (int k = 0; k < C::kKt; ++k) v[k] = soft_cap(v[k] * zs, A.softcap, inv_cap) * kLog2e;
-                    }
                     if (edge) {
                         const int a = pc.row_lo - p0, b = pc.row_hi - p0;
 #pragma unroll
@@ -397,7 +400,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
                         }
                         tmem_st16(s_addr + c / 2, p);  // over the scores, which are in registers
                     }
-                    l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                    float sum = (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                    if (__builtin_expect(s_mask[(tile_no + (j - pc.from)) % kMaskRing] & kMixed, 0))
+                        sum = s_sum[threadIdx.x].y * ex2(s_sum[threadIdx.x].x - m);
+                    l += sum;
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -498,7 +504,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
         // ================================================================ dequantizers
         const int tid = threadIdx.x - 32 * C::kSoftWarps;
         bool ok = true;
-        uint32_t n = 0, tile_no = 0;  // operand tiles, key tiles
+        uint32_t n = 0, tile_no = 0, n_fixed = 0;  // operand tiles, key tiles
         while (ok && w.left > 0) {
             const Seq s = load_seq(B, w.b);
             const Item it = item_of<C>(s, A, w.st);
@@ -510,14 +516,18 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
                     const uint32_t rs = n % C::kRaws, os = n % C::kOps;
                     ok = wait_warp(raw_full + 8 * rs, (n / C::kRaws) & 1, abort, B.status);
                     if (!ok) break;
-                    const uint8_t *raw = smem + C::kOffRaw + rs * C::kRaw;
+                    uint8_t *raw = smem + C::kOffRaw + rs * C::kRaw;
                     uint8_t *op = smem + C::kOffOp + os * C::kOp;
-                    const uint32_t recs = s_mask[tile_no % kMaskRing];
                     auto op_free = [&]() {
                         return n < C::kOps || wait_warp(op_empty + 8 * os, (n / C::kOps - 1) & 1, abort, B.status);
                     };
-                    if (part == 0) ok = dequant_keys<D>(raw, op, tid, op_free);
-                    else ok = dequant_values<D>(raw, op, tid, max(it.lo - p0, 0), min(max(it.hi + 1 - p0, 0), C::kKt), recs, op_free);
+                    if (part == 0) {
+                        ok = dequant_keys<D>(raw, op, tid, op_free);
+                    } else {
+                        ok = fix_scales<D, C>(raw, tid, it.lo - p0, it.hi + 1 - p0, s_mask[tile_no % kMaskRing],
+                                              s_dn + tile_no % kMaskRing * C::kKt, fixed, n_fixed, abort, B.status);
+                        if (ok) ok = dequant_values<D>(raw, op, tid, op_free);
+                    }
                     if (!ok) break;
                     fence_async_smem();
                     __syncwarp();
@@ -532,7 +542,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRestRegs));
     if (w.left > 0 && (warp == C::kProdWarp || warp == C::kProdWarp + 2)) {
-        produce<D, C>(warp != C::kProdWarp, w, B, A, smem, raw_full, raw_empty, s_mask, abort);
+        produce<D, C>(warp != C::kProdWarp, w, B, A, smem, raw_full, raw_empty, s_mask, s_dn, s_scratch, abort);
     } else if (w.left > 0 && warp == C::kMmaWarp && elect_one()) {
         // ================================================================ mma: one thread
         constexpr uint32_t kIdQk = idesc_f16(128, C::kKt, false), kIdPv = idesc_f16(128, D, false);

@@ -187,18 +187,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// The value scales of tokens tok .. tok + 7 of a tile, 0 for those that no row
-// of the item sees ([lo, hi) are seen) or whose record has no page, whatever
-// the page holds there (0 * NaN would be NaN).
-__device__ __forceinline__ uint4 hide_scales(uint4 d, int tok, int lo, int hi, bool rec)
-{
-    uint32_t w[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (tok + k < lo || tok + k >= hi || !rec) w[k / 2] &= (k & 1) ? 0x0000FFFFu : 0xFFFF0000u;
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // A cut closer than kSnap tiles to an item's end is moved there: joining the
 // parts of a cut item costs about as much as that many tiles.
 constexpr int kSnap = 4;
@@ -286,20 +274,202 @@ __device__ __forceinline__ long long find_stretch(const Batch &B, const Args &A,
     return len;
 }
 
+// ---------------------------------------------------------------- the size of a token's values
+// p reaches the products in f16, some 32 octaves above whose smallest number a
+// strong key's p may stand.  If that key's values are small, the others make
+// the result although their p is far smaller.  So a token whose values are much
+// smaller (or larger) than most enters with its values times 2^dn and its p
+// times 2^-dn, where dn brings its largest value scale to the usual size; the
+// reference m is that of the scores less dn, and only the sum l takes p itself.
+// The usual size is the mean over the first tile of a piece, or the size before
+// where that tile agrees with it (any would do: the products do not depend on
+// it); tokens within kNear octaves of it have dn = 0, and a tile of nothing
+// else is as if there were no dn.  The others are
+// `mixed` and rare.
+// Of all this, a tile that is not mixed costs its test alone.  The rest is kept
+// short and out of the hot loops, which together fill the SM's instruction
+// cache: a second copy of the producer's loop, nothing else changed, took 509 of
+// 8191 tokens in f32 from 179 to 245 us (cache misses 0.7 to 4.5 million).
+constexpr int kNear = 3;
+constexpr int kNoValue = 90;           // in place of 8 - log2 of a scale of 0: its p, 2^105 at most, stays in f32
+constexpr int kMostBase = 20;          // values are brought to scales of 2^-12 at least, so that they keep their bits
+constexpr uint32_t kMixed = 1u << 31;  // in a tile's word of the mask ring
+
+// 8 - floor(log2 of a largest value scale), from its fp16 bits
+__device__ __forceinline__ int value_shift(uint32_t h)
+{
+    return h == 0 ? kNoValue : 135 - static_cast<int>(__float_as_uint(half2_f2(h).x) >> 23);
+}
+
+// The value scales of a tile, as the keys' producer sees them: lane l has
+// tokens 8 (l % kGroups) .. + 7 of the blocks l / kGroups, + kParts, ...
+template <int D, class C>
+struct TileScales {
+    static constexpr int kGroups = C::kKt / 8, kParts = 32 / kGroups, nb = D / 32, kWords = (nb + kParts - 1) / kParts;
+    uint4 w[kWords];
+    // off: offset of the lane's record in the cache (lanes below kRecs), negative if it has none
+    __device__ __forceinline__ void load(const uint8_t *cache, long long off)
+    {
+        const int lane = threadIdx.x & 31, t8 = lane % kGroups;
+        const long long o = __shfl_sync(0xffffffffu, off, t8 / 2);
+        const uint8_t *src = cache + o + v_scale_off(8 * (t8 % 2), lane / kGroups, D);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            w[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (o >= 0 && (kParts * kWords == nb || lane / kGroups < nb)) w[i] = __ldg(reinterpret_cast<const uint4 *>(src + 2 * kRec * kParts * i));
+        }
+    }
+    // The largest scale of every token (each lane: its eight tokens')
+    __device__ __forceinline__ void largest(uint32_t (&m)[4]) const
+    {
+        m[0] = w[0].x, m[1] = w[0].y, m[2] = w[0].z, m[3] = w[0].w;
+#pragma unroll
+        for (int i = 1; i < kWords; ++i) {
+            m[0] = __vmaxu2(m[0], w[i].x), m[1] = __vmaxu2(m[1], w[i].y);
+            m[2] = __vmaxu2(m[2], w[i].z), m[3] = __vmaxu2(m[3], w[i].w);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int o = kGroups; o < 32; o <<= 1) m[k] = __vmaxu2(m[k], __shfl_xor_sync(0xffffffffu, m[k], o));
+    }
+};
+// The usual size of a piece and the bounds that it sets, fp16 bits twice.
+struct Usual {
+    int base;
+    uint32_t above, below;  // larger, smaller ones make a tile mixed
+};
+// Looks at every token of a tile where some scale is out of bounds; at the first
+// tile of a piece (`first`) also for the usual size.  scratch: the tokens'
+// largest scales; [lo, hi) and recs: the tokens that count.  Writes dn; returns
+// the base, and in bit 8 whether the tile is mixed.  Out of line, with loops
+// instead of registers.
+template <int kKt>
+static __device__ __noinline__ int look_closer(const uint16_t *scratch, float *dn, int lo, int hi, uint32_t recs, int base, bool first)
+{
+    const int lane = threadIdx.x & 31;
+    if (first) {
+        int sum = 0, n = 0;
+#pragma unroll 1
+        for (int tok = lane; tok < kKt; tok += 32)
+            if (tok >= lo && tok < hi && (recs >> (tok / kRec) & 1u)) sum += min(value_shift(scratch[tok]), 30), ++n;
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        n = __reduce_add_sync(0xffffffffu, n);
+        base = n > 0 ? min(__float2int_rn(__fdividef(static_cast<float>(sum), static_cast<float>(n))), kMostBase) : kMostBase;
+        base = max(base, 0);
+    }
+    bool mixed = false;
+#pragma unroll 1
+    for (int tok = lane; tok < kKt; tok += 32) {
+        const int d = value_shift(scratch[tok]) - base;
+        const bool far = tok >= lo && tok < hi && (recs >> (tok / kRec) & 1u) && (d < -kNear || d > kNear);
+        dn[tok] = far ? static_cast<float>(d) : 0.f;
+        mixed = mixed || far;
+    }
+    return base | (__any_sync(0xffffffffu, mixed) ? 0x100 : 0);
+}
+// The value scales of a raw stage of values, in place: 0 for tokens outside [lo,
+// hi) or without a page (recs), whatever the page holds there (0 * NaN would be
+// NaN), times 2^dn in a mixed tile.  All dequantizer threads, which then wait
+// for one another at `fixed` (n_fixed: how often so far); false if that gave up.
+// Every other tile passes by.
+template <int D, class C>
+__device__ __forceinline__ bool fix_scales(uint8_t *raw, int tid, int lo, int hi, uint32_t word, const float *dn, uint32_t fixed,
+                                           uint32_t &n_fixed, volatile int *abort, int *status)
+{
+    if (__builtin_expect(lo <= 0 && hi >= C::kKt && word == (1u << C::kRecs) - 1u, 1)) return true;
+#pragma unroll 1
+    for (int u = tid; u < C::kKt * (D / 32); u += 32 * C::kDeqWarps) {
+        const int tok = u % C::kKt;
+        __half *d = reinterpret_cast<__half *>(raw + tok / kRec * C::kHalf - 17 * D + v_scale_off(tok % kRec, u / C::kKt, D));
+        const float f = word & kMixed ? ex2(dn[tok]) : 1.0f;
+        *d = __float2half_rn(tok >= lo && tok < hi && (word >> (tok / kRec) & 1u) ? __half2float(*d) * f : 0.f);
+    }
+    __syncwarp();
+    if ((tid & 31) == 0) mbar_arrive(fixed);
+    return wait_warp(fixed, n_fixed++ & 1, abort, status);
+}
+// The scores of a tile (kSums: two columns each, kKt apart) capped and in octaves,
+// in place in tensor memory.  (Unrolled over a row in registers it was 17
+// instructions a score, more code than the SM's instruction cache holds.)
+template <int kKt, bool kSums>
+__device__ __forceinline__ void cap_scores(uint32_t s_addr, float zs, float cap, float inv_cap)
+{
+#pragma unroll 1
+    for (int c = 0; c < kKt; c += 16) {
+        float x[16], y[16];
+        tmem_ld16(s_addr + c, x);
+        if (kSums) tmem_ld16(s_addr + kKt + c, y);
+        uint32_t o[16], zero[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float v = (kSums ? x[k] + y[k] : x[k]) * zs;
+            o[k] = __float_as_uint(soft_cap(v, cap, inv_cap) * 1.4426950408889634f);
+            zero[k] = 0u;
+        }
+        tmem_st16(s_addr + c, o);
+        if (kSums) tmem_st16(s_addr + kKt + c, zero);
+    }
+    tmem_wait_st();
+}
+// A mixed tile's scores (kSums: as above) less dn, in place in tensor memory, for
+// the common path to go on with; unit: what it multiplies them by to have
+// octaves.  Of the tokens lo .. hi that have a page, into `out`: the largest, in
+// octaves, and the sum of p = 2^(score + dn - largest + head), where the products
+// take p 2^-dn.
+template <int kKt, bool kSums>
+__device__ __forceinline__ void shift_scores(uint32_t s_addr, float unit, int lo, int hi, uint32_t recs, const float *dn, float2 *out)
+{
+    const float back = 1.0f / unit;
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < kKt; c += 8) {
+        uint32_t x[8], y[8];
+        tmem_ld8(s_addr + c, x);
+        if (kSums) tmem_ld8(s_addr + kKt + c, y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float v = __uint_as_float(x[k]);
+            if (kSums) v += __uint_as_float(y[k]);
+            v = fmaf(-dn[c + k], back, v);
+            if (c + k >= lo && c + k <= hi && (recs >> (c / kRec) & 1u)) top = fmaxf(top, v);
+            x[k] = __float_as_uint(v);
+            y[k] = 0u;
+        }
+        tmem_st8(s_addr + c, x);
+        if (kSums) tmem_st8(s_addr + kKt + c, y);
+    }
+    tmem_wait_st();
+    top *= unit;
+#pragma unroll 1
+    for (int c = 0; c < kKt; c += 8) {
+        uint32_t x[8];
+        tmem_ld8(s_addr + c, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (c + k >= lo && c + k <= hi && (recs >> (c / kRec) & 1u))
+                sum = fmaf(ex2(fmaf(__uint_as_float(x[k]), unit, kPHead - top)), ex2(dn[c + k]), sum);
+    }
+    *out = make_float2(top, sum);
+}
+
 // A producer warp: the key halves (part 0) or the value halves (part 1) of a
 // tile's records into the ring of raw stages, tile t into stage number 2 t +
 // part; a lane per record, one bulk copy each (two warps, because the copies of
 // a warp are issued one lane at a time).  Page numbers are fetched a tile ahead
-// and looked at only then.  mask: a bit per record of a tile, 0 where the page is
-// bad (its tokens are then hidden); records beyond the item are hidden by
-// position and not copied.
+// and looked at only then.  The keys' producer also writes the tile's word of the
+// mask ring -- a bit per record, 0 where the page is bad (its tokens are then
+// hidden; records beyond the item are hidden by position and not copied), and
+// whether the values are mixed -- before the stage can fill: their scales are
+// fetched a tile ahead too.  s_dn: [kMaskRing][kKt]; scratch: [kKt].
 template <int D, class C>
 __device__ __forceinline__ void produce(int part, Walk &w, const Batch &B, const Args &A, uint8_t *smem, uint32_t raw_full,
-                                        uint32_t raw_empty, uint32_t *s_mask, volatile int *abort)
+                                        uint32_t raw_empty, uint32_t *s_mask, float *s_dn, uint16_t *scratch, volatile int *abort)
 {
     const int lane = threadIdx.x & 31;
     bool ok = true;
     uint32_t tile_no = 0;
+    Usual usual = {};
     while (ok) {
         const Seq s = load_seq(B, w.b);
         const Item it = item_of<C>(s, A, w.st);
@@ -307,26 +477,65 @@ __device__ __forceinline__ void produce(int part, Walk &w, const Batch &B, const
         const int rec0 = it.base / kRec + lane;  // this lane's record of tile 0
         auto wanted = [&](int j) { return lane < C::kRecs && j < to && (rec0 + j * C::kRecs) * kRec <= it.hi; };
         auto entry = [&](int j) { return wanted(j) ? __ldg(page_at(B, w.b, rec0 + j * C::kRecs)) : 0; };
+        TileScales<D, C> scales;
+        long long off = -1;
         int next = entry(w.from);
-        for (int j = w.from; j < to; ++j, ++tile_no) {
-            const bool want = wanted(j);
-            const int pg = want ? checked_page(B, next) : -1;
-            next = entry(j + 1);
-            const uint32_t copied = __ballot_sync(0xffffffffu, pg >= 0), bad = __ballot_sync(0xffffffffu, want && pg < 0);
-            const uint32_t n = 2 * tile_no + part, rs = n % C::kRaws;
-            const uint8_t *src = A.cache + (pg >= 0 ? rec_off(B, pg, w.h, rec0 + j * C::kRecs, D) : 0) + part * C::kHalf;
-            if (n >= C::kRaws) {
-                ok = wait_warp(raw_empty + 8 * rs, (n / C::kRaws - 1) & 1, abort, B.status);
-                if (!ok) break;
+        // a turn early: places and scales of the first tile
+        for (int j = w.from - 1; j < to; ++j) {
+            const long long cur = off;  // of tile j
+            const uint32_t n = 2 * tile_no + part, bar = raw_full + 8 * (n % C::kRaws);
+            if (j >= w.from) {
+                if (n >= C::kRaws) {
+                    ok = wait_warp(raw_empty + 8 * (n % C::kRaws), (n / C::kRaws - 1) & 1, abort, B.status);
+                    if (!ok) break;
+                }
+                // the stage is full when these have landed and lane 0 has arrived
+                if (cur >= 0) bulk_load(smem_u32(smem) + C::kOffRaw + n % C::kRaws * C::kRaw + lane * C::kHalf, A.cache + cur + part * C::kHalf, C::kHalf, bar);
+            }
+            // offset of this lane's record of tile j + 1, -1 without one, -2 where the page is bad
+            off = -1;
+            if (wanted(j + 1)) {
+                const int pg = checked_page(B, next);
+                off = pg >= 0 ? rec_off(B, pg, w.h, rec0 + (j + 1) * C::kRecs, D) : -2;
+            }
+            next = entry(j + 2);
+            const TileScales<D, C> now = scales;  // of tile j; looked at only after the next ones have been asked for
+            if (part == 0) scales.load(A.cache, off);
+            if (j < w.from) continue;
+            const uint32_t copied = __ballot_sync(0xffffffffu, cur >= 0);
+            if (part == 0) {
+                uint32_t word = ((1u << C::kRecs) - 1u) & ~__ballot_sync(0xffffffffu, cur == -2);
+                const int p0 = it.base + j * C::kKt, lo = it.lo - p0, hi = it.hi + 1 - p0;
+                // Whether some scale is out of bounds: of any token of the records here, seen or
+                // not, and at a piece's beginning by the last piece's usual size.
+                uint32_t m[4], above = usual.above, below = usual.below;
+                now.largest(m);
+                if (copied >> (lane % (C::kKt / 8) / 2) & 1u) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        above = __vmaxu2(above, m[k]);
+                        below = __vminu2(below, m[k]);
+                    }
+                }
+                if (__builtin_expect(__any_sync(0xffffffffu, above != usual.above || below != usual.below), 0)) {
+                    if (lane < C::kKt / 8) reinterpret_cast<uint4 *>(scratch)[lane] = make_uint4(m[0], m[1], m[2], m[3]);
+                    __syncwarp();
+                    const int got = look_closer<C::kKt>(scratch, s_dn + tile_no % kMaskRing * C::kKt, lo, hi, word, usual.base, j == w.from);
+                    usual.base = got & 0xFF;
+                    const float top = pow2i(9 + kNear - usual.base), low = pow2i(8 - kNear - usual.base);
+                    usual.above = f2_half2(top, top) - 0x00010001u;
+                    usual.below = f2_half2(low, low);
+                    if (got & 0x100) word |= kMixed;
+                }
+                if (lane == 0) s_mask[tile_no % kMaskRing] = word;
+                __syncwarp();
             }
             if (lane == 0) {
-                if (part == 0) s_mask[tile_no % kMaskRing] = ((1u << C::kRecs) - 1u) & ~bad;
                 const uint32_t bytes = __popc(copied) * C::kHalf;
-                if (bytes) mbar_expect_tx(raw_full + 8 * rs, bytes);
-                else mbar_arrive(raw_full + 8 * rs);
+                if (bytes) mbar_expect_tx(bar, bytes);
+                else mbar_arrive(bar);
             }
-            __syncwarp();
-            if (pg >= 0) bulk_load(smem_u32(smem) + C::kOffRaw + rs * C::kRaw + lane * C::kHalf, src, C::kHalf, raw_full + 8 * rs);
+            ++tile_no;
         }
         if (!ok || !next_piece<C>(w, B, A, to - w.from)) {
             break;

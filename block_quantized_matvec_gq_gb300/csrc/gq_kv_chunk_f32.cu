@@ -24,10 +24,12 @@
 // over them) and two product tiles of head_dim columns.
 // What bounds it: per tile of 64 tokens the tensor core takes 8 (64 + 48)
 // cycles for S and 12 * 64 for O at head_dim 128, 1664 in all; a tile takes
-// about 2350, the rest being waits between the roles.  2048 tokens behind 30720
-// cached ones, 32 heads over 8 x 128: 2147 us, 496 TFLOP/s of the attention's
-// own products (three times that on the tensor cores); 509 behind 7682: 178 us,
-// of which some 40 are the beginning of the items and the joining of cut ones.
+// about 2500, the rest being waits between the roles and for instructions.  2048
+// tokens behind 30720 cached ones, 32 heads over 8 x 128: 2428 us, 439 TFLOP/s
+// of the attention's own products (three times that on the tensor cores); 509
+// behind 7682: 192 us, of which some 40 are the beginning of the items and the
+// joining of cut ones.  (2176 and 179 us before the values' sizes were looked
+// at; gq_kv_chunk.cuh.)
 #include "gq_kv_chunk.cuh"
 
 namespace gq {
@@ -52,15 +54,15 @@ struct CfgF32 {
     static constexpr int kOffRaw = kOffOp + kOps * kOp;
     static constexpr int kOffState = kOffRaw + kRaws * kRaw;      // {m, l}[4 tiles][128 rows]
     static constexpr int kOffBar = kOffState + 4 * 128 * 8;
-    // raw full/empty, operand full/empty, q full, s full [2], p full [2], o full [2], o empty [2]
-    static constexpr int kBars = 2 * kRaws + 2 * kOps + 9;
-    static constexpr int kSmem = kOffBar + 8 * kBars;
+    // raw full/empty, operand full/empty, q full, s full [2], p full [2], o full [2], o empty [2], fixed
+    static constexpr int kBars = 2 * kRaws + 2 * kOps + 10;
+    static constexpr int kSmem = kOffBar + 8 * kBars;  // and 4.5 KB of static arrays
     static constexpr int kDeqWarp = 8, kDeqWarps = 8, kProdWarp = 16, kMmaWarp = 17, kWarpsAll = 20;
     static constexpr int kThreads = 32 * kWarpsAll;
     // registers per thread after the split; the shares stay within the launch's 640 x 96
-    static constexpr int kSoftRegs = 128, kAccRegs = 184, kDeqRegs = 64, kRestRegs = 40;
+    static constexpr int kSoftRegs = 128, kAccRegs = 176, kDeqRegs = 64, kRestRegs = 48;
     static_assert(kSoftRegs + kAccRegs + 2 * kDeqRegs + kRestRegs <= 5 * 96, "register split");
-    static_assert(kOffOp % 128 == 0 && kOffRaw % 128 == 0 && kOffState % 16 == 0 && kSmem <= 231000, "shared memory layout");
+    static_assert(kOffOp % 128 == 0 && kOffRaw % 128 == 0 && kOffState % 16 == 0 && kSmem + 4608 <= 232448, "shared memory layout");
 };
 
 // c * d as f16x2 rounded, and the exact remainder (18 bits in two pieces).
@@ -139,14 +141,13 @@ struct RawValues {
         }
     }
     // the rounded values' tile, then the remainders'
-    __device__ __forceinline__ void convert(uint8_t *op, int tid, int lo_tok, int hi_tok, uint32_t recs) const
+    __device__ __forceinline__ void convert(uint8_t *op, int tid) const
     {
-        const bool edge = lo_tok > 0 || hi_tok < C::kKt || recs != (1u << C::kRecs) - 1u;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const int u = tid + i * kTh, c = u % (D / 4), t8 = u / (D / 4);
             if (u >= kAll) break;
-            const uint4 s = edge ? hide_scales(d[i], 8 * t8, lo_tok, hi_tok, (recs >> (t8 / 2)) & 1u) : d[i];
+            const uint4 s = d[i];
             uint8_t *dst = op + t8 * (D * 16);
             const uint32_t a[4] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w}, z[4] = {w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
 #pragma unroll
@@ -214,12 +215,15 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
     __shared__ volatile int s_abort;
     __shared__ uint32_t s_tmem;
     __shared__ uint32_t s_mask[kMaskRing];
+    __shared__ __align__(16) float s_dn[kMaskRing * C::kKt];
+    __shared__ __align__(16) uint16_t s_scratch[C::kKt];
+    __shared__ float2 s_sum[128];
     __shared__ int s_last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = smem_u32(smem);
     const uint32_t raw_full = base + C::kOffBar, raw_empty = raw_full + 8 * C::kRaws, op_full = raw_empty + 8 * C::kRaws,
                    op_empty = op_full + 8 * C::kOps, q_full = op_empty + 8 * C::kOps, s_full = q_full + 8, p_full = s_full + 16,
-                   o_full = p_full + 16, o_empty = o_full + 16;
+                   o_full = p_full + 16, o_empty = o_full + 16, fixed = o_empty + 16;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kRaws; ++i) {
             mbar_init(raw_full + 8 * i, 1);
@@ -230,6 +234,7 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
             mbar_init(op_empty + 8 * i, 1);
         }
         mbar_init(q_full, 4);
+        mbar_init(fixed, C::kDeqWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + 8 * i, 1);
             mbar_init(p_full + 8 * i, 4);
@@ -294,8 +299,12 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
                 if (!ok) break;
                 tc_fence_after();
                 const int p0 = it.base + j * C::kKt;
-                const uint32_t recs = s_mask[n % kMaskRing];
+                const uint32_t word = s_mask[n % kMaskRing], recs = word & ~kMixed;
                 const bool edge = __any_sync(0xffffffffu, p0 < row_lo || p0 + C::kKt - 1 > row_hi) || recs != (1u << C::kRecs) - 1u;
+                if (kCap) cap_scores<C::kKt, true>(s_addr, zs, A.softcap, inv_cap);
+                if (__builtin_expect(word & kMixed, 0))
+                    shift_scores<C::kKt, true>(s_addr, kCap ? 1.0f : zs, row_lo - p0, row_hi - p0, recs, s_dn + n % kMaskRing * C::kKt,
+                                               s_sum + threadIdx.x);
                 float v[C::kKt];
 #pragma unroll
                 for (int c = 0; c < C::kKt; c += 32) {
@@ -309,10 +318,6 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
                         const float2 sum = __fadd2_rn(make_float2(x[k], x[k + 1]), make_float2(y[k], y[k + 1]));
                         v[c + k] = sum.x, v[c + k + 1] = sum.y;
                     }
-                }
-                if (kCap) {
-#pragma unroll
-                    for (int k = 0; k < C::kKt; ++k) v[k] = soft_cap(v[k] * zs, A.softcap, inv_cap) * kLog2e;
                 }
                 if (edge) {
                     const int a = row_lo - p0, b = row_hi - p0;
@@ -355,7 +360,9 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
                     tmem_st16(s_addr + c / 2, hi);  // over the scores, which are in registers
                     tmem_st16(s_addr + 32 + c / 2, lo);
                 }
-                l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                float sum = (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                if (__builtin_expect(s_mask[n % kMaskRing] & kMixed, 0)) sum = s_sum[threadIdx.x].y * ex2(s_sum[threadIdx.x].x - m);
+                l += sum;
                 state[(n & 3) * 128 + row] = make_float2(m, l);
                 tmem_wait_st();
                 tc_fence_before();
@@ -388,7 +395,10 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
                     const float g = ex2(m - ml.x);
                     m = ml.x;
 #pragma unroll
-                    for (int c = 0; c < D; ++c) acc[c] *= g;
+                    for (int c = 0; c < D; c += 2) {
+                        const float2 a = __fmul2_rn(make_float2(acc[c], acc[c + 1]), make_float2(g, g));
+                        acc[c] = a.x, acc[c + 1] = a.y;
+                    }
                 }
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
@@ -463,6 +473,7 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
         const int tid = threadIdx.x - 32 * C::kDeqWarp;
         bool ok = true;
         uint32_t n = 0, tile_no = 0;  // operand tiles (keys 2 t, values 2 t + 1 of tile t), key tiles
+        uint32_t n_fixed = 0;
         RawKeys<D> keys;
         RawValues<D> vals;
         auto raw_of = [&](uint32_t i) -> const uint8_t * {  // waits for raw stage i
@@ -491,8 +502,13 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
             if (!ok) break;
             for (int j = w.from; j < to; ++j, ++tile_no, n += 2) {
                 const int p0 = it.base + j * C::kKt;
-                const uint32_t recs = s_mask[tile_no % kMaskRing];
-                vals.load(raw_of(n + 1), tid);
+                raw_of(n + 1);
+                if (!ok) break;
+                uint8_t *raw = smem + C::kOffRaw + (n + 1) % C::kRaws * C::kRaw;
+                ok = fix_scales<D, C>(raw, tid, it.lo - p0, it.hi + 1 - p0, s_mask[tile_no % kMaskRing], s_dn + tile_no % kMaskRing * C::kKt,
+                                      fixed, n_fixed, abort, B.status);
+                if (!ok) break;
+                vals.load(raw, tid);
                 uint8_t *op = op_of(n);
                 if (!ok) break;
                 keys.convert(op, tid);
@@ -500,7 +516,7 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
                 if (j + 1 < to) keys.load(raw_of(n + 2), tid);
                 op = op_of(n + 1);
                 if (!ok) break;
-                vals.convert(op, tid, max(it.lo - p0, 0), min(max(it.hi + 1 - p0, 0), C::kKt), recs);
+                vals.convert(op, tid);
                 op_done(n + 1);
             }
             if (!ok || !next_piece<C>(w, B, A, to - w.from)) break;
@@ -508,7 +524,7 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRestRegs));
         if (w.left > 0 && (warp == C::kProdWarp || warp == C::kProdWarp + 2)) {
-            produce<D, C>(warp != C::kProdWarp, w, B, A, smem, raw_full, raw_empty, s_mask, abort);
+            produce<D, C>(warp != C::kProdWarp, w, B, A, smem, raw_full, raw_empty, s_mask, s_dn, s_scratch, abort);
         } else if (w.left > 0 && warp == C::kMmaWarp && elect_one()) {
             // ============================================================ mma: one thread
             constexpr uint32_t kIdQk1 = idesc_f16(128, 128, false), kIdQk2 = idesc_f16(128, 64, false), kIdPv = idesc_f16(128, D, false);
@@ -522,9 +538,9 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
             const uint32_t q_lo = desc_lo(base, 2048), k_lo = desc_lo(base + C::kOffOp, 2048), v_lo = desc_lo(base + C::kOffOp, D * 16);
             auto qk = [&](uint32_t os, uint32_t buf) {
                 const uint32_t b = k_lo + os * (C::kOp >> 4), d = tmem + kSCol * buf;
-#pragma unroll
+#pragma unroll 2  // unrolled wholly it crowds the instruction cache (509 of 8191 tokens 193 -> 223 us)
                 for (int k = 0; k < D / 16; ++k) mma_f16(d, desc_of(q_lo + k * 256), desc_of(b + k * 256), kIdQk1, k > 0);
-#pragma unroll
+#pragma unroll 2
                 for (int k = 0; k < D / 16; ++k)
                     mma_f16(d, desc_of(q_lo + (C::kQ >> 4) + k * 256), desc_of(b + k * 256), kIdQk2, 1);
                 mma_commit(s_full + 8 * buf);
@@ -533,11 +549,11 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
             auto pv = [&](uint32_t os, uint32_t buf) {
                 const uint32_t b = v_lo + os * (C::kOp >> 4), d = tmem + kOCol + buf * D, p = tmem + kSCol * buf;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_f16_ts(d, p + 8 * k, desc_of(b + k * 2 * D), kIdPv, k > 0);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mma_f16_ts(d, p + 32 + 8 * k, desc_of(b + k * 2 * D), kIdPv, 1);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mma_f16_ts(d, p + 8 * k, desc_of(b + ((C::kKt * D * 2) >> 4) + k * 2 * D), kIdPv, 1);
+                for (int k = 0; k < 4; ++k) {
+                    mma_f16_ts(d, p + 8 * k, desc_of(b + k * 2 * D), kIdPv, k > 0);
+                    mma_f16_ts(d, p + 32 + 8 * k, desc_of(b + k * 2 * D), kIdPv, 1);
+                    mma_f16_ts(d, p + 8 * k, desc_of(b + ((C::kKt * D * 2) >> 4) + k * 2 * D), kIdPv, 1);
+                }
                 mma_commit(o_full + 8 * buf);
                 mma_commit(op_empty + 8 * os);
             };

@@ -189,6 +189,8 @@ def sink_batch(value, dim, weak):
 
 SINK = [(typ, dim, n) for typ, dim in (("f32", 64), ("f32", 128), ("f32", 256), ("bf16", 64), ("bf16", 128), ("bf16", 256), ("f16", 128))
         for n in (1, 5)] + [("f32", 256, 80)]
+SINK += [("f32", 64, 80), ("f32", 128, 80)]
+SINK += [("bf16", 64, 80), ("bf16", 128, 80), ("bf16", 256, 80), ("f16", 128, 80)]
 
 
 @pytest.mark.parametrize("typ,dim,n", SINK)
@@ -214,6 +216,8 @@ def test_a_strong_key_with_a_small_value(value, gap, typ, dim, n):
 
 
 ANYWHERE = [("f32", 1), ("bf16", 1)]
+ANYWHERE += [("f32", 200)]
+ANYWHERE += [("bf16", 200), ("f16", 200)]
 
 
 @pytest.mark.parametrize("typ,n", ANYWHERE)
