@@ -43,7 +43,7 @@
 // The running reference m is the largest s + log2(largest value scale of the
 // token), not the largest s: then p times a scale is at most 1 whatever the
 // scales are, and stays in f16's range.  The state is rescaled only when the
-// reference would grow by more than 2^8 (one vote per record otherwise).
+// reference would grow by more than 2^7 (one vote per record otherwise).
 #include "gq_kv.cuh"
 #include "gq_tc.cuh"
 
@@ -53,9 +53,12 @@ namespace kv {
 constexpr int kWarps = 4;
 constexpr int kAttnThreads = kWarps * 32;
 constexpr int kMaxCtas = 1024;      // stretches per call, at most
-constexpr float kFloor = -1e30f;    // reference of a row that has seen no token
-constexpr float kHead = 6.0f;       // p is kept times 2^6: with the 2^8 slack below 2^15
-constexpr float kSlack = 8.0f;
+constexpr float kFloor = -FLT_MAX;  // reference of a row that has seen no token: below every score
+// p is kept times 2^7, and with the slack of 2^7 below 2^15.  Both of 7 so that it
+// stays there for scores whose spacing is some octaves: m - 7 is then rounded by
+// less than what the spacing keeps a score away from m + 7.
+constexpr float kHead = 7.0f;
+constexpr float kSlack = 7.0f;
 
 
 template <int D, int kRows>

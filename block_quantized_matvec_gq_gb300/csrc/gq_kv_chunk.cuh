@@ -15,7 +15,7 @@ using namespace tcu;
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 128;        // column step between score buffers
 constexpr int kOCol = 256;        // first accumulator column
-constexpr float kNone = -1e30f;   // reference of a row that has seen no token
+constexpr float kNone = -FLT_MAX;  // reference of a row that has seen no token: below every score
 constexpr float kPHead = 7.0f;
 constexpr float kGrow = 8.0f;
 constexpr int kMaskRing = 8;

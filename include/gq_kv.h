@@ -122,7 +122,8 @@ int gq_kv_read_q8_0(const void *cache, const int32_t *block_table, const int32_t
  * or more and summed in f32 (within 1e-5 of the definition in the 2-norm);
  * with the 16-bit types operands of 11 bits are allowed (the cached values
  * d * q and the probabilities, within 1e-3 of the definition together), the
- * sums are f32 and O is rounded once from them.  |q| < 2^100.
+ * sums are f32 and O is rounded once from them.
+ * Range: |q| < 2^100, and |scale * (q . k_j)| <= 2^19.
  *   workspace: device memory, 16-byte aligned, at least
  *   gq_kv_attention_workspace_bytes bytes.  ZERO-FILL IT ONCE before its
  *   first use; every completed call leaves it ready for the next.  Two calls

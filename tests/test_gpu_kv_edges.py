@@ -240,3 +240,32 @@ def test_strong_keys_with_small_values_anywhere(typ, n):
     q = (np.full((n, heads, dim), 1.0) + rng.standard_normal((n, heads, dim)) * 0.3).astype(np.float32)
     for window in (0, 333):
         check_attention(batch, heads, typ, rng, q=q, window=window, norm=typ == "f32")
+
+
+# ---------------------------------------------------------------- scores of any size
+
+SCORES = [(typ, dim, n, scale) for typ, dim in (("f32", 64), ("f32", 256), ("bf16", 64), ("bf16", 256), ("f16", 128))
+          for n in (1, 6) for scale in (50.0, 1e3, 1e4, 1e5, 1e7, 1e28)]
+SCORES += [("f32", 256, 80, 1e28)]
+# the chunk kernels: scores up to 2^19, the stated range
+SCORES += [("f32", 64, 80, 50.0), ("f32", 128, 80, 50.0), ("bf16", 64, 80, 50.0), ("bf16", 256, 80, 50.0), ("f16", 128, 80, 50.0)]
+
+
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("typ,dim,n,scale", SCORES)
+def test_scores_of_any_size(typ, dim, n, scale, sign):
+    """One visible key counts whatever its score (down to -1e32 here), and of several the one with the largest."""
+    rng = np.random.default_rng(1030)
+    kv = 100
+    batch = kp.make([kv], [n], 1, dim, 16, rng)
+    for p in range(kv):
+        kp.write(batch, 0, p, np.full((1, dim), 1.0 + 0.125 * (p * 7 % 11), np.float32), rng.standard_normal((1, dim)).astype(np.float32))
+    q, qh = token_array(np.full((n, 2, dim), sign * 4096.0 / dim, np.float32), typ)
+    for window in (1, 3, 9, 0):
+        got = attend(batch, q, typ, 2, scale, window=window)
+        for i in {*range(0, n, 7), n - 1}:
+            p = kv - n + i
+            lo = max(0, p - window + 1) if window else 0
+            ref, _ = row_attention(batch, 0, qh[i], lo, p + 1, scale)
+            # equal scores among the visible keys are equal sums of equal products: their mean, by the type's rounding
+            assert np.linalg.norm(got[i] - ref) <= (1e-5 if typ == "f32" else 2.0 ** -10 + ROUND[typ]) * np.linalg.norm(ref), (window, i)
