@@ -188,6 +188,28 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sel)
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+// ---------------------------------------------------------------- what the attention kernels share
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 1 / cap, finite also for a subnormal cap (0 times an infinity would be NaN)
+__device__ __forceinline__ float inverse_cap(float cap) { return fminf(1.0f / cap, FLT_MAX); }
+// cap * tanh(x / cap) in f32: tanh|y| = (1 - e) / (1 + e), e = exp(-2|y|).
+// For small |y| the difference 1 - e cancels; there the odd series is used.
+__device__ __forceinline__ float soft_cap(float x, float cap, float inv_cap)
+{
+    const float y = x * inv_cap, a = fabsf(y);
+    const float e = ex2(-2.885390082f * a);
+    const float big = __fdividef(1.0f - e, 1.0f + e);
+    const float q = y * y;
+    // y - y^3/3 + 2 y^5/15 - 17 y^7/315 + 62 y^9/2835: below 2^-24 relative for |y| < 0.25
+    const float small = a * (1.0f + q * (-0.333333333f + q * (0.133333333f + q * (-0.053968254f + q * 0.021869489f))));
+    return copysignf(cap * (a < 0.25f ? small : big), y);
+}
+
 }  // namespace kv
 
 // gq_kv_attn.cu

@@ -172,12 +172,6 @@ __device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32
 // Code bytes of w as f16 subnormals (u 2^-24): bytes 0, 1 or 2, 3.
 __device__ __forceinline__ uint32_t bytes01(uint32_t w) { return __byte_perm(w, 0u, 0x4140u); }
 __device__ __forceinline__ uint32_t bytes23(uint32_t w) { return __byte_perm(w, 0u, 0x4342u); }
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // About log2 of a value scale (below it by at most 0.09): the upper 24 bits of
 // the f32 number count 2^-15 octaves; they are placed under the exponent of
 // 2^23.  A scale of 0, a token without a value, counts as 2^-80: its p, which
@@ -195,19 +189,6 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
     const float2 r = ffma2(half2_f2(hi), make_float2(-1.f, -1.f), make_float2(a, b));
     lo = f2_half2(r.x, r.y);
 }
-// cap * tanh(x / cap) in f32: tanh|y| = (1 - e) / (1 + e), e = exp(-2|y|).
-// For small |y| the difference 1 - e cancels; there the odd series is used.
-__device__ __forceinline__ float soft_cap(float x, float cap, float inv_cap)
-{
-    const float y = x * inv_cap, a = fabsf(y);
-    const float e = ex2(-2.885390082f * a);
-    const float big = __fdividef(1.0f - e, 1.0f + e);
-    const float q = y * y;
-    // y - y^3/3 + 2 y^5/15 - 17 y^7/315 + 62 y^9/2835: below 2^-24 relative for |y| < 0.25
-    const float small = a * (1.0f + q * (-0.333333333f + q * (0.133333333f + q * (-0.053968254f + q * 0.021869489f))));
-    return copysignf(cap * (a < 0.25f ? small : big), y);
-}
-
 // kRows = 8: two pieces per operand (any type); 16: the 16-bit types' single
 // piece, rows 8-15 of the fragments being query rows.
 template <int D, int kRows>
@@ -424,7 +405,7 @@ __global__ void __launch_bounds__(kAttnThreads, D == 256 ? 2 : (D == 128 ? 3 : 4
         };
         const float kLog2e = 1.4426950408889634f;
         const bool capped = A.softcap > 0.f;
-        const float inv_cap = capped ? 1.0f / A.softcap : 0.f;
+        const float inv_cap = capped ? inverse_cap(A.softcap) : 0.f;
         if (!capped) {
 #pragma unroll
             for (int e = 0; e < NR; ++e) zs[e] *= kLog2e;

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_kv_attn_chunk(Args A, B
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t o_addr = lane_addr + kOCol + mt * D;
         uint8_t *q_op = smem + mt * C::kQ;
-        const float inv_cap = kCap ? 1.0f / A.softcap : 0.f;
+        const float inv_cap = kCap ? inverse_cap(A.softcap) : 0.f;
         constexpr float kLog2e = 1.4426950408889634f;
         bool ok = true;
         uint32_t n_pv = 0;          // tiles of this row tile so far: scores taken, p v products asked for

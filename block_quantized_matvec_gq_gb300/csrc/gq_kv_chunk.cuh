@@ -100,23 +100,6 @@ __device__ __forceinline__ bool next_piece(Walk &w, const Batch &B, const Args &
     return true;
 }
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// cap * tanh(x / cap) in f32 (as in gq_kv_attn.cu)
-__device__ __forceinline__ float soft_cap(float x, float cap, float inv_cap)
-{
-    const float y = x * inv_cap, a = fabsf(y);
-    const float e = ex2(-2.885390082f * a);
-    const float big = __fdividef(1.0f - e, 1.0f + e);
-    const float q = y * y;
-    const float small = a * (1.0f + q * (-0.333333333f + q * (0.133333333f + q * (-0.053968254f + q * 0.021869489f))));
-    return copysignf(cap * (a < 0.25f ? small : big), y);
-}
-
 // ---------------------------------------------------------------- tensor memory
 // 32 columns of this thread's lane; tmem_wait_ld has to follow before r is used.
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float *r)

@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
     if (warp < 4) {
         // ================================================================ softmax: thread = query row
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
-        const float inv_cap = kCap ? 1.0f / A.softcap : 0.f;
+        const float inv_cap = kCap ? inverse_cap(A.softcap) : 0.f;
         constexpr float kLog2e = 1.4426950408889634f;
         bool ok = true;
         uint32_t n = 0;  // tiles so far

@@ -269,3 +269,22 @@ def test_scores_of_any_size(typ, dim, n, scale, sign):
             ref, _ = row_attention(batch, 0, qh[i], lo, p + 1, scale)
             # equal scores among the visible keys are equal sums of equal products: their mean, by the type's rounding
             assert np.linalg.norm(got[i] - ref) <= (1e-5 if typ == "f32" else 2.0 ** -10 + ROUND[typ]) * np.linalg.norm(ref), (window, i)
+
+
+
+# ---------------------------------------------------------------- soft-caps
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 80])
+@pytest.mark.parametrize("cap", [1e-44, 1e-39, 1e-30, 1e30])
+def test_soft_caps_of_any_size(cap, n, typ):
+    """A tiny cap makes every score 0 (the mean of the visible values, a score of exactly 0 included), a huge one none."""
+    rng = np.random.default_rng(1031)
+    batch = random_batch([120], [n], 1, 64, 16, rng)
+    q = rng.standard_normal((n, 2, 64)).astype(np.float32)
+    q[:, 1] = 0.0  # scores of exactly 0
+    q, qh = token_array(q, typ)
+    got = attend(batch, q, typ, 2, 0.125, softcap=cap)
+    for i in range(n):
+        ref, a = row_attention(batch, 0, qh[i], 0, 120 - n + i + 1, 0.125 if cap > 1 else 0.0)
+        bound = (2.1 * 2.0 ** -16 + 2.0 ** -16) * a if typ == "f32" else (2.1 * 2.0 ** -6 + 2.0 ** -10) * a + ROUND[typ] * np.abs(ref)
+        assert np.all(np.abs(got[i] - ref) <= bound), i
