@@ -72,6 +72,17 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+// a / 127 rounded to nearest: the product with the rounded reciprocal, corrected
+// by its remainder (Markstein's theorem; equal to the division for every f32 in
+// a trial over all mantissas).  The product alone is an ulp off often enough
+// that the fp16 scale of one block in some millions is another.
+__device__ __forceinline__ float over127(float a)
+{
+    constexpr float r = 1.0f / 127.0f;
+    const float q = __fmul_rn(a, r);
+    return __fmaf_rn(__fmaf_rn(-127.0f, q, a), r, q);  // NaN for an infinity: fminf takes the other operand
+}
+
 // The code bytes (code + 128) of eight elements of a block with scale d:
 // the rule of q8_pack4, with its tests made once for all eight.  With r =
 // RN(1 / d) and y = RN(e r), RN(e / d) and y round to the same integer n
@@ -197,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_kv_append(const uint8_t *__rest
         for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(e[k]));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const __half dh = __float2half_rn(fminf(__fmul_rn(amax, 1.0f / 127.0f), kMaxD));
+        const __half dh = __float2half_rn(fminf(over127(amax), kMaxD));
         const uint2 codes = code_bytes8(e, __half2float(dh), amax);
         uint8_t *rec = cache + rec0 + u.h * head_stride;
         if (!u.isv) {

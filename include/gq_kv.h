@@ -84,8 +84,8 @@ size_t gq_kv_cache_bytes(int n_pages, int page_tokens, int kv_heads, int head_di
 
 /* ---------------------------------------------------------------------------
  * Write the new tokens' keys and values.  For every 32-block x of a head:
- *   d = fp16(min(max|x| * r, 515.5))   (r = 1/127 rounded to f32, one f32
- *       product, then one rounding: the scale is kept in 11 bits),
+ *   d = fp16(min(max|x| / 127, 515.5))   (the f32 quotient as in
+ *       gq_quantize_q8_0, then one rounding: the scale is kept in 11 bits),
  *   q = clamp(round_half_away(x / d), -127, 127) with the f32 quotient by the
  *       stored d; q = 0 when d = 0.
  * 515.5 keeps d * q within fp16: larger magnitudes saturate at +-65468.5.  An

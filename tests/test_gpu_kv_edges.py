@@ -288,3 +288,34 @@ def test_soft_caps_of_any_size(cap, n, typ):
         ref, a = row_attention(batch, 0, qh[i], 0, 120 - n + i + 1, 0.125 if cap > 1 else 0.0)
         bound = (2.1 * 2.0 ** -16 + 2.0 ** -16) * a if typ == "f32" else (2.1 * 2.0 ** -6 + 2.0 ** -10) * a + ROUND[typ] * np.abs(ref)
         assert np.all(np.abs(got[i] - ref) <= bound), i
+
+
+# ---------------------------------------------------------------- the scale
+
+def test_the_scale_is_the_rounded_quotient():
+    """d = fp16(max|x| / 127), the quotient rounded to f32 as in the library's quantizer.  Next to a tie of the fp16
+    rounding a product with a rounded 1 / 127 gives another scale: at these magnitudes, found by trying all."""
+    near = np.array([float.fromhex(x) for x in ("0x1.fc3f82p+0", "0x1.fd3d82p+0", "0x1.fe3b82p+0", "0x1.ff3982p+0")], np.float32)
+    amax = np.concatenate([near * np.float32(2.0 ** e) for e in (-8, -1, 0, 3, 11)] + [np.float32([1e-30, 6e4, 3e38, 127.0, 1.0])])
+    rng = np.random.default_rng(1040)
+    n, dim = len(amax), 64
+    x = (rng.uniform(-1, 1, (n, dim)) * amax[:, None]).astype(np.float32)
+    x[:, 5] = amax
+    x[:, 40] = -amax
+    batch = kp.make([n], [n], 1, dim, 16, rng)
+    xd = dev(x)
+    cache = dev(batch.cache)
+    gq.gq_kv_append_q8_0(xd, dim, xd, dim, gq.GQ_TYPE_F32, cache, *lists(batch), *sizes(batch))
+    raw = cache.cpu().numpy()
+    kc, ks, vc, vs = kp.layout(dim)
+    want = np.minimum(amax / np.float32(127), np.float32(515.5)).astype(np.float16)
+    for p in range(n):
+        pg, rec, tk = batch.record(0, p)
+        r = raw[pg, 0, rec]
+        d = want[p].astype(np.float32)
+        y = x[p] / d if d > 0 else np.zeros(dim, np.float32)
+        code = np.clip(np.sign(y) * np.floor(np.abs(y.astype(np.float64)) + 0.5), -127, 127)
+        for c, s in ((kc, ks), (vc, vs)):
+            got = (r[s[tk]].astype(np.uint16) | (r[s[tk] + 1].astype(np.uint16) << 8)).view(np.float16)
+            assert np.array_equal(got, np.repeat(want[p], 2)), (p, amax[p], got, want[p])
+            assert np.array_equal(r[c[tk]].astype(np.int64) - 128, code), p
