@@ -352,10 +352,11 @@ inline int check_cache(int n_pages, int page_tokens, int kv_heads, int head_dim)
     return GQ_OK;
 }
 
-// A token array: rows of `width` elements, `ld` apart.
-inline int check_rows(const void *p, long long ld, int width, int type)
+// A token array: n_tokens rows of `width` elements, `ld` apart.  Without rows it
+// may be null, as an empty tensor's address is.
+inline int check_rows(const void *p, long long ld, int width, int type, int n_tokens)
 {
-    if (!p) return GQ_ERR_NULL;
+    if (!p && n_tokens > 0) return GQ_ERR_NULL;
     if (!aligned16(p)) return GQ_ERR_ALIGN;
     if (ld < width) return GQ_ERR_SHAPE;
     return ld * type_size(type) % 16 == 0 ? GQ_OK : GQ_ERR_ALIGN;
@@ -397,8 +398,8 @@ int gq_kv_append_q8_0(const void *K, long long ldk, const void *V, long long ldv
 {
     int st = check_batch(cache, block_table, kv_len, q_start, type, n_pages, max_pages, page_tokens, kv_heads, head_dim,
                          n_seq, n_tokens);
-    if (st == GQ_OK) st = check_rows(K, ldk, kv_heads * head_dim, type);
-    if (st == GQ_OK) st = check_rows(V, ldv, kv_heads * head_dim, type);
+    if (st == GQ_OK) st = check_rows(K, ldk, kv_heads * head_dim, type, n_tokens);
+    if (st == GQ_OK) st = check_rows(V, ldv, kv_heads * head_dim, type, n_tokens);
     if (st != GQ_OK) return st;
     if (n_tokens == 0) return GQ_OK;
     const Batch B = make_batch(block_table, kv_len, q_start, n_pages, max_pages, page_tokens, kv_heads, n_seq, n_tokens,
@@ -418,8 +419,8 @@ int gq_kv_read_q8_0(const void *cache, const int32_t *block_table, const int32_t
 {
     int st = check_batch(cache, block_table, kv_len, q_start, type, n_pages, max_pages, page_tokens, kv_heads, head_dim,
                          n_seq, n_tokens);
-    if (st == GQ_OK) st = check_rows(K, ldk, kv_heads * head_dim, type);
-    if (st == GQ_OK) st = check_rows(V, ldv, kv_heads * head_dim, type);
+    if (st == GQ_OK) st = check_rows(K, ldk, kv_heads * head_dim, type, n_tokens);
+    if (st == GQ_OK) st = check_rows(V, ldv, kv_heads * head_dim, type, n_tokens);
     if (st != GQ_OK) return st;
     if (n_tokens == 0) return GQ_OK;
     const Batch B = make_batch(block_table, kv_len, q_start, n_pages, max_pages, page_tokens, kv_heads, n_seq, n_tokens,
@@ -451,8 +452,8 @@ int gq_kv_attention_q8_0(const void *Q, long long ldq, const void *cache, const 
     if (st != GQ_OK) return st;
     const size_t need = gq_kv_attention_workspace_bytes(heads, kv_heads, head_dim);
     if (need == 0 || window < 0 || !isfinite(scale) || !isfinite(softcap)) return GQ_ERR_SHAPE;
-    st = check_rows(Q, ldq, heads * head_dim, type);
-    if (st == GQ_OK) st = check_rows(O, ldo, heads * head_dim, type);
+    st = check_rows(Q, ldq, heads * head_dim, type, n_tokens);
+    if (st == GQ_OK) st = check_rows(O, ldo, heads * head_dim, type, n_tokens);
     if (st != GQ_OK) return st;
     if (!workspace || workspace_bytes < need) return GQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return GQ_ERR_ALIGN;

@@ -48,7 +48,8 @@
  *
  * Range: head_dim 64, 128 or 256; heads a multiple of kv_heads; page_tokens
  * a multiple of 16, at most 4096; max_pages * page_tokens at most 2^28;
- * n_tokens = 0 is a valid call that does nothing.
+ * n_tokens = 0 is a valid call that does nothing (the token arrays may then be
+ * null).
  * Errors before any launch: GQ_ERR_NULL, GQ_ERR_ALIGN, GQ_ERR_SHAPE,
  * GQ_ERR_FORMAT for an unknown type, GQ_ERR_WORKSPACE; after it GQ_ERR_CUDA.
  * What only the device can see -- a page number outside 0 .. n_pages - 1, a

@@ -319,3 +319,20 @@ def test_the_scale_is_the_rounded_quotient():
             got = (r[s[tk]].astype(np.uint16) | (r[s[tk] + 1].astype(np.uint16) << 8)).view(np.float16)
             assert np.array_equal(got, np.repeat(want[p], 2)), (p, amax[p], got, want[p])
             assert np.array_equal(r[c[tk]].astype(np.int64) - 128, code), p
+
+
+# ---------------------------------------------------------------- nothing to do
+
+def test_calls_without_tokens_take_empty_arrays():
+    """n_tokens = 0 does nothing, also where the token arrays are empty tensors (whose address is null)."""
+    t = torch()
+    rng = np.random.default_rng(1050)
+    batch = random_batch([20], [0], 1, 64, 16, rng)
+    cache = dev(batch.cache)
+    x = t.empty((0, 64), device="cuda")
+    ws = t.zeros(gq.gq_kv_attention_workspace_bytes(1, 1, 64), dtype=t.uint8, device="cuda")
+    gq.gq_kv_append_q8_0(x, 64, x, 64, gq.GQ_TYPE_F32, cache, *lists(batch), *sizes(batch))
+    gq.gq_kv_read_q8_0(cache, *lists(batch), x, 64, x, 64, gq.GQ_TYPE_F32, *sizes(batch))
+    gq.gq_kv_attention_q8_0(x, 64, cache, *lists(batch), x, 64, gq.GQ_TYPE_F32, 1.0, 0.0, 0, ws, ws.numel(), 1, *sizes(batch))
+    assert np.array_equal(cache.cpu().numpy(), batch.cache)
+    assert gq.gq_device_status() == gq.GQ_OK
