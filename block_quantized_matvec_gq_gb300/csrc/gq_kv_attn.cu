@@ -52,7 +52,7 @@ namespace kv {
 
 constexpr int kWarps = 4;
 constexpr int kAttnThreads = kWarps * 32;
-constexpr int kMaxCtas = 1024;      // stretches per call, at most
+constexpr int kMaxCtas = 640;       // stretches per call, at most: four CTAs on each of 160 SMs
 constexpr float kFloor = -FLT_MAX;  // reference of a row that has seen no token: below every score
 // p is kept times 2^7, and with the slack of 2^7 below 2^15.  Both of 7 so that it
 // stays there for scores whose spacing is some octaves: m - 7 is then rounded by
@@ -73,10 +73,12 @@ struct SplitCfg {
     // with them in registers, 86.5 us here)
     static constexpr bool kQSmem = D >= 128;
     static constexpr int kQ = kQSmem ? (D / 16) * 32 * 16 : 0;
-    // the merge of the warps' states, and the weights of an item's parts, reuse the ring
-    static constexpr int kMerge = kWarps * kRows * (D + 4) * 4, kJoin = kRows * kMaxCtas * 4;
-    static constexpr int kMin = kMerge > kJoin ? kMerge : kJoin;
-    static constexpr int kRings = kWarps * kRing > kMin ? kWarps * kRing : kMin;
+    // the merge of the warps' states, and the weights of an item's parts, reuse the
+    // rings; they must not set the size (weights of 1024 parts did at head_dim 64
+    // with 16 rows, and cost the fourth CTA of an SM: 76.3 us against 73.3, 16
+    // sequences of 16384 tokens, four new ones each)
+    static constexpr int kRings = kWarps * kRing;
+    static_assert(kWarps * kRows * (D + 4) * 4 <= kRings && kRows * kMaxCtas * 4 <= kRings, "merge and join fit the rings");
     static constexpr int kSmem = kRings + kQ;
 };
 
