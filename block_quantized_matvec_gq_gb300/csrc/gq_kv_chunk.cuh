@@ -335,11 +335,11 @@ static __device__ __noinline__ int look_closer(const uint16_t *scratch, float *d
         int sum = 0, n = 0;
 #pragma unroll 1
         for (int tok = lane; tok < kKt; tok += 32)
-            if (tok >= lo && tok < hi && (recs >> (tok / kRec) & 1u)) sum += min(value_shift(scratch[tok]), 30), ++n;
+            if (tok >= lo && tok < hi && (recs >> (tok / kRec) & 1u) && scratch[tok] != 0) sum += value_shift(scratch[tok]), ++n;
         sum = __reduce_add_sync(0xffffffffu, sum);
         n = __reduce_add_sync(0xffffffffu, n);
-        base = n > 0 ? min(__float2int_rn(__fdividef(static_cast<float>(sum), static_cast<float>(n))), kMostBase) : kMostBase;
-        base = max(base, 0);
+        // a tile without values says nothing
+        if (n > 0) base = min(max(__float2int_rn(__fdividef(static_cast<float>(sum), static_cast<float>(n))), 0), kMostBase);
     }
     bool mixed = false;
 #pragma unroll 1
@@ -452,7 +452,7 @@ __device__ __forceinline__ void produce(int part, Walk &w, const Batch &B, const
     const int lane = threadIdx.x & 31;
     bool ok = true;
     uint32_t tile_no = 0;
-    Usual usual = {};
+    Usual usual = {12, 0u, ~0u};  // bounds that every tile is outside of, until one has been looked at
     while (ok) {
         const Seq s = load_seq(B, w.b);
         const Item it = item_of<C>(s, A, w.st);

@@ -215,6 +215,27 @@ def test_a_strong_key_with_a_small_value(value, gap, typ, dim, n):
         assert err <= tol * np.linalg.norm(ref) + floor, (i, err / np.linalg.norm(ref))
 
 
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 80])
+@pytest.mark.parametrize("first", [0, 60, 300])
+def test_whole_tiles_without_values(first, n, typ):
+    """Tokens `first` .. `first` + 299 have values of 0, and among them is the strong key."""
+    rng = np.random.default_rng(1022)
+    kv, dim, gap = 900, 64, 24.0
+    batch = kp.make([kv], [n], 1, dim, 64, rng)
+    for p in range(kv):
+        key = HIGH if p == first + 130 else LOW
+        v = rng.standard_normal((1, dim)) * (0.0 if first <= p < first + 300 else 1.0)
+        kp.write(batch, 0, p, np.full((1, dim), key, np.float32), v.astype(np.float32))
+    q, qh = token_array(np.ones((n, 2, dim), np.float32), typ)
+    scale = float(gap / (dim * (HIGH - LOW)))
+    got = attend(batch, q, typ, 2, scale)
+    for i in {*range(0, n, 11), n - 1}:
+        ref, _ = row_attention(batch, 0, qh[i], 0, kv - n + i + 1, scale)
+        tol = 1e-5 if typ == "f32" else 2.0 ** -10 + ROUND[typ]
+        assert np.linalg.norm(got[i] - ref) <= tol * np.linalg.norm(ref), (i, np.linalg.norm(got[i] - ref) / np.linalg.norm(ref))
+
+
 ANYWHERE = [("f32", 1), ("bf16", 1)]
 ANYWHERE += [("f32", 200)]
 ANYWHERE += [("bf16", 200), ("f16", 200)]
