@@ -10,12 +10,14 @@
 // codes.  A group that is only partly new (the ends of a chunk, every decode
 // step) writes the new tokens' bytes alone.
 //
-// What bounds them: long calls stream.  Appending 17 k tokens of 8 heads x 128
-// in f32 (197 MB with the codes) takes 35.2 us, 5.6 TB/s, 0.82 of the measured
+// What bounds them: long calls stream.  Appending 19008 tokens of 8 heads x 128
+// in f32 (197 MB with the codes) takes 35.8 us, 5.5 TB/s, 0.81 of the measured
 // copy rate; the instructions of the code rule keep it there (12 a code with
-// its tests per element: 59 us; 6 with one test per eight: 35).  Reading 46 k
-// tokens back in bf16 (360 MB) takes 64.8 us, 5.6 TB/s; in f32 89.7 us, 6.6
-// TB/s.  A decode step is launch latency: one token 2.1 us, 64 sequences 3.5.
+// its tests per element: 59 us; 6 with one test per eight: 35), so bf16 (119 MB)
+// takes no less: 39 us.  Narrow caches leave most of a CTA's warps without a
+// unit (65536 tokens of 1 x 128: 47 us for 85 MB).  Reading 57410 tokens back
+// in bf16 (360 MB) takes 64.3 us, 5.6 TB/s; in f32 90.3 us, 6.6 TB/s.  A decode
+// step is launch latency: one token 2.2 us, 64 sequences 3.7.
 #include <math.h>
 
 #include "gq_kv.cuh"

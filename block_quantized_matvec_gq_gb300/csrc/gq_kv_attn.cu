@@ -31,15 +31,19 @@
 // 0-7 and the remainder in rows 8-15 (22 bits together): f32 accuracy at no
 // extra product.  With 16 rows (the 16-bit types, where a call has more than
 // eight) the rounded value alone is used.
-// What bounds it: the code stream (HBM) for long caches, against about 450
-// instructions per record (32 MMAs, 64 permutes and 80 half conversions of
-// them) on three warps a scheduler, which registers (168 a thread, 64 of them
-// accumulators) do not let be more.  131072 tokens of 8 heads x 128, 4 query
-// heads each (285 MB): 65 us, 4.4 TB/s, 0.65 of the measured copy rate, about 9
+// What bounds it: the code stream (HBM) for long caches, against the chain of
+// one turn (scores, vote, exponentials, conversions, products; about 460
+// instructions per record) in three warps a scheduler, which registers (168 a
+// thread, 64 of them accumulators) do not let be more: issue is active half of
+// the time, the tensor pipe 29 %.  131072 tokens of 8 heads x 128, 4 query
+// heads each (285 MB): 66 us, 4.3 TB/s, 0.64 of the measured copy rate, about 9
 // us of it beginning and joining; 48 sequences of up to 9000 tokens of 8 x 256
-// in f32 (1.1 GB): 194 us, 5.7 TB/s, 0.84.  A short call is latency: looking
+// in f32 (1.1 GB): 192 us, 5.7 TB/s, 0.84.  A short call is latency: looking
 // the lists up, the pages, the queries and the first record follow one another
-// (5 us), then the record loop, then the join (2-6 us): 129 tokens 7.2 us.
+// (5 us), then the record loop, then the join (2-6 us): 129 tokens 7.7 us.  A
+// CTA with several pieces goes through that for each, since the merge uses the
+// rings: nothing of the next piece is asked for before it (16 sequences with
+// five new tokens each and a window of 1024: 27 us, 10.6 for the bytes).
 // The running reference m is the largest s + log2(largest value scale of the
 // token), not the largest s: then p times a scale is at most 1 whatever the
 // scales are, and stays in f16's range.  The state is rescaled only when the
@@ -731,8 +735,11 @@ int launch_kv_attention(const void *Q, long long ldq, const uint8_t *cache, cons
     // cores' form is faster: 16 sequences of 4096 tokens, 8 kv heads x 128, 4
     // query heads each, bf16: 32 rows 70 us here and 100 there, 64 rows 110 and
     // 101, 128 rows 202 and 79; f32: 94 and 121, 177 and 123, 336 and 119.  (One
-    // sequence of 8192: 64 rows 37 and 43 us, 128 rows 45 and 41.)  head_dim 256
-    // in f32 has no form there: two pieces of its operands do not fit.
+    // sequence of 8192: 64 rows 37 and 43 us, 128 rows 45 and 41.)  These are calls
+    // of equal sequences; one kernel serves the whole call, so that in a call of
+    // single tokens beside a long chunk one or the other runs in the form that is
+    // slower for it.  head_dim 256 in f32 has no form there: both pieces of its
+    // query operand do not fit a CTA's shared memory beside keys and values.
     const long long rows = static_cast<long long>(B.n_tokens) * (heads / B.kv_heads) / B.n_seq;
     if (rows >= 64 && (type != GQ_TYPE_F32 || head_dim <= 128))
         return launch_kv_chunk(Q, ldq, cache, B, O, ldo, type, scale, softcap, window, counter + kv::kMaxCtas, part, heads,

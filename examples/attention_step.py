@@ -24,7 +24,9 @@ import synth
 
 
 class AttentionBlock:
-    """Weights and buffers of one block; every call runs on torch's current stream and allocates nothing."""
+    """Weights and buffers of one block; every call runs on torch's current stream.  What the library reads and writes is
+    allocated once; a step makes only its result, and for a single token the normalised row (torch: the library's norm gives
+    Q8_0 codes, the matrix-vector product takes f32)."""
 
     def __init__(self, hidden, heads, kv_heads, dim, max_tokens, n_pages, page_tokens=64, seed=7):
         self.hidden, self.heads, self.kv_heads, self.dim = hidden, heads, kv_heads, dim

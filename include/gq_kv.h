@@ -36,8 +36,8 @@
  * with nb = head_dim / 32, key(t) = (t & 1) | ((t >> 1) & 2) for nb > 2 and
  * (t >> 2) & 1 for nb = 2; a code byte is code XOR 0x80.  The two exclusive
  * ors are there so that the attention kernels, which copy whole records into
- * shared memory, read them without bank conflicts; keys are contiguous along
- * the head (the contraction of q k) and values along the tokens (the
+ * shared memory, read the codes without bank conflicts; keys are contiguous
+ * along the head (the contraction of q k) and values along the tokens (the
  * contraction of p v).
  *
  * Token arrays (K, V, Q, O) have rows of heads * head_dim contiguous
@@ -119,16 +119,25 @@ int gq_kv_read_q8_0(const void *cache, const int32_t *block_table, const int32_t
  * (p < 0, or a sequence of length 0) gives zeros.
  *   Q, O: row stride ldq, ldo elements; O is overwritten.  scale and softcap
  *   finite, window >= 0.
- * Accuracy: with GQ_TYPE_F32 the products are formed from operands of 22 bits
- * or more and summed in f32 (within 1e-5 of the definition in the 2-norm);
- * with the 16-bit types operands of 11 bits are allowed (the cached values
- * d * q and the probabilities, within 1e-3 of the definition together), the
- * sums are f32 and O is rounded once from them.
+ * Accuracy: with A = sum_j w_j |v_j| (w_j the softmax weights, element by
+ * element) and Z the row's largest |scale| * sum_i |q_i k_ji|,
+ *   GQ_TYPE_F32:  |error| <= (2.1 * 2^-20 Z + 2^-16) A.  Operands of 22 bits or
+ *     more, f32 sums.  In the 2-norm, where roundings average, within 1e-5 of
+ *     the result for scores of ordinary size (Z up to about 16).
+ *   16-bit types: |error| <= (2.1 * 2^-10 Z + 2^-10 + 2^-27 N) A for N visible
+ *     tokens, and the rounding of O.  Keys and values d * q and the weights may
+ *     be rounded to 11 bits; sums are f32, truncated by the tensor core (N).
+ *     Rounded keys shift a score by some 2^-12 of its terms, so large scores
+ *     cost accuracy: with scores of standard deviation 2.5 the error in the
+ *     2-norm is 6e-4 before O is rounded.  For less, use GQ_TYPE_F32.
+ * Beside that, tokens whose w_j max|v_j| is below 2^-26 of the row's largest may
+ * count as 0.
  * Range: |q| < 2^100, and |scale * (q . k_j)| <= 2^19.
  *   workspace: device memory, 16-byte aligned, at least
  *   gq_kv_attention_workspace_bytes bytes.  ZERO-FILL IT ONCE before its
- *   first use; every completed call leaves it ready for the next.  Two calls
- *   that may run concurrently must not share it.
+ *   first use; every completed call leaves it ready for the next.  Zero-fill it
+ *   again after GQ_ERR_TIMEOUT: a call whose waits gave up leaves counts in it.
+ *   Two calls that may run concurrently must not share it.
  * ------------------------------------------------------------------------ */
 size_t gq_kv_attention_workspace_bytes(int heads, int kv_heads, int head_dim); /* 0 if out of range */
 int gq_kv_attention_q8_0(const void *Q, long long ldq, const void *cache, const int32_t *block_table,
