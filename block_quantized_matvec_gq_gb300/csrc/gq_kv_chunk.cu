@@ -36,9 +36,9 @@
 // since tensor memory holds one score buffer per row tile beside the
 // accumulators.  (Two buffers of 64 columns each took longer: twice the
 // waits and N = 64 products.)  A chunk of 2048 tokens behind 30720 cached ones,
-// 32 heads over 8 x 128, bf16: 824 us in a graph, 1.29 PFLOP/s, 0.68 of the
-// measured bf16 rate (called one by one on another GB300: 876 us); head_dim 64
-// 712 us, head_dim 256 (16 heads) 1215 us; capped, 2048 of 16384 tokens, 1053.
+// 32 heads over 8 x 128, bf16: 804 us in a graph, 1.32 PFLOP/s, 0.70 of the
+// measured bf16 rate (840 us called one by one; 876 on another GB300); head_dim
+// 64 712 us, head_dim 256 (16 heads) 1220 us; capped, 2048 of 16384 tokens, 1053.
 // Every wait is bounded (gq_tc.cuh).
 #include "gq_kv_chunk.cuh"
 

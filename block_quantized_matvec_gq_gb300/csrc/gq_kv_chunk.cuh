@@ -272,7 +272,9 @@ __device__ __forceinline__ long long find_stretch(const Batch &B, const Args &A,
 // Of all this, a tile that is not mixed costs its test alone.  The rest is kept
 // short and out of the hot loops, which together fill the SM's instruction
 // cache: a second copy of the producer's loop, nothing else changed, took 509 of
-// 8191 tokens in f32 from 179 to 245 us (cache misses 0.7 to 4.5 million).
+// 8191 tokens in f32 from 179 to 245 us (cache misses 0.7 to 4.5 million).  A
+// call whose every tile is mixed takes two to three times as long (2048 of 32768
+// tokens 817 and 2628 us).
 constexpr int kNear = 3;
 constexpr int kNoValue = 90;           // in place of 8 - log2 of a scale of 0: its p, 2^105 at most, stays in f32
 constexpr int kMostBase = 20;          // values are brought to scales of 2^-12 at least, so that they keep their bits
@@ -284,37 +286,38 @@ __device__ __forceinline__ int value_shift(uint32_t h)
     return h == 0 ? kNoValue : 135 - static_cast<int>(__float_as_uint(half2_f2(h).x) >> 23);
 }
 
-// The value scales of a tile, as the keys' producer sees them: lane l has
-// tokens 8 (l % kGroups) .. + 7 of the blocks l / kGroups, + kParts, ...
+// The value scales of a tile, as the keys' producer sees them: a lane has
+// kTokens neighbouring tokens, two to a word, of every block.
 template <int D, class C>
 struct TileScales {
-    static constexpr int kGroups = C::kKt / 8, kParts = 32 / kGroups, nb = D / 32, kWords = (nb + kParts - 1) / kParts;
-    uint4 w[kWords];
+    static constexpr int kTokens = C::kKt / 32, kWords = kTokens / 2, nb = D / 32;
+    uint32_t w[nb][kWords];
+    static __device__ __forceinline__ int record() { return (threadIdx.x & 31) * kTokens / kRec; }
     // off: offset of the lane's record in the cache (lanes below kRecs), negative if it has none
     __device__ __forceinline__ void load(const uint8_t *cache, long long off)
     {
-        const int lane = threadIdx.x & 31, t8 = lane % kGroups;
-        const long long o = __shfl_sync(0xffffffffu, off, t8 / 2);
-        const uint8_t *src = cache + o + v_scale_off(8 * (t8 % 2), lane / kGroups, D);
+        const long long o = __shfl_sync(0xffffffffu, off, record());
+        const uint8_t *src = cache + o + v_scale_off((threadIdx.x & 31) * kTokens % kRec, 0, D);
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-            w[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (o >= 0 && (kParts * kWords == nb || lane / kGroups < nb)) w[i] = __ldg(reinterpret_cast<const uint4 *>(src + 2 * kRec * kParts * i));
+        for (int b = 0; b < nb; ++b) {
+            uint2 v = make_uint2(0u, 0u);
+            if (o >= 0) {
+                if (kWords == 2) v = __ldg(reinterpret_cast<const uint2 *>(src + 2 * kRec * b));
+                else v.x = __ldg(reinterpret_cast<const uint32_t *>(src + 2 * kRec * b));
+            }
+            w[b][0] = v.x;
+            if (kWords == 2) w[b][kWords - 1] = v.y;
         }
     }
-    // The largest scale of every token (each lane: its eight tokens')
-    __device__ __forceinline__ void largest(uint32_t (&m)[4]) const
+    // The largest scale of every token
+    __device__ __forceinline__ void largest(uint32_t (&m)[kWords]) const
     {
-        m[0] = w[0].x, m[1] = w[0].y, m[2] = w[0].z, m[3] = w[0].w;
 #pragma unroll
-        for (int i = 1; i < kWords; ++i) {
-            m[0] = __vmaxu2(m[0], w[i].x), m[1] = __vmaxu2(m[1], w[i].y);
-            m[2] = __vmaxu2(m[2], w[i].z), m[3] = __vmaxu2(m[3], w[i].w);
+        for (int k = 0; k < kWords; ++k) {
+            m[k] = w[0][k];
+#pragma unroll
+            for (int b = 1; b < nb; ++b) m[k] = __vmaxu2(m[k], w[b][k]);
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int o = kGroups; o < 32; o <<= 1) m[k] = __vmaxu2(m[k], __shfl_xor_sync(0xffffffffu, m[k], o));
     }
 };
 // The usual size of a piece and the bounds that it sets, fp16 bits twice.
@@ -491,17 +494,19 @@ __device__ __forceinline__ void produce(int part, Walk &w, const Batch &B, const
                 const int p0 = it.base + j * C::kKt, lo = it.lo - p0, hi = it.hi + 1 - p0;
                 // Whether some scale is out of bounds: of any token of the records here, seen or
                 // not, and at a piece's beginning by the last piece's usual size.
-                uint32_t m[4], above = usual.above, below = usual.below;
+                constexpr int kWords = TileScales<D, C>::kWords;
+                uint32_t m[kWords], above = usual.above, below = usual.below;
                 now.largest(m);
-                if (copied >> (lane % (C::kKt / 8) / 2) & 1u) {
+                if (copied >> now.record() & 1u) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < kWords; ++k) {
                         above = __vmaxu2(above, m[k]);
                         below = __vminu2(below, m[k]);
                     }
                 }
                 if (__builtin_expect(__any_sync(0xffffffffu, above != usual.above || below != usual.below), 0)) {
-                    if (lane < C::kKt / 8) reinterpret_cast<uint4 *>(scratch)[lane] = make_uint4(m[0], m[1], m[2], m[3]);
+#pragma unroll
+                    for (int k = 0; k < kWords; ++k) reinterpret_cast<uint32_t *>(scratch)[kWords * lane + k] = m[k];
                     __syncwarp();
                     const int got = look_closer<C::kKt>(scratch, s_dn + tile_no % kMaskRing * C::kKt, lo, hi, word, usual.base, j == w.from);
                     usual.base = got & 0xFF;

@@ -25,11 +25,11 @@
 // What bounds it: per tile of 64 tokens the tensor core takes 8 (64 + 48)
 // cycles for S and 12 * 64 for O at head_dim 128, 1664 in all; a tile takes
 // about 2500, the rest being waits between the roles and for instructions.  2048
-// tokens behind 30720 cached ones, 32 heads over 8 x 128: 2428 us, 439 TFLOP/s
+// tokens behind 30720 cached ones, 32 heads over 8 x 128: 2356 us, 452 TFLOP/s
 // of the attention's own products (three times that on the tensor cores); 509
-// behind 7682: 192 us, of which some 40 are the beginning of the items and the
-// joining of cut ones.  (2176 and 179 us before the values' sizes were looked
-// at; gq_kv_chunk.cuh.)
+// behind 7682: 199 us, of which some 40 are the beginning of the items and the
+// joining of cut ones.  (2187 and 179 us before the values' sizes were looked
+// at, gq_kv_chunk.cuh; head_dim 64 2050 us before and after.)
 #include "gq_kv_chunk.cuh"
 
 namespace gq {
@@ -60,7 +60,7 @@ struct CfgF32 {
     static constexpr int kDeqWarp = 8, kDeqWarps = 8, kProdWarp = 16, kMmaWarp = 17, kWarpsAll = 20;
     static constexpr int kThreads = 32 * kWarpsAll;
     // registers per thread after the split; the shares stay within the launch's 640 x 96
-    static constexpr int kSoftRegs = 128, kAccRegs = 176, kDeqRegs = 64, kRestRegs = 48;
+    static constexpr int kSoftRegs = 120, kAccRegs = 168, kDeqRegs = 64, kRestRegs = 64;
     static_assert(kSoftRegs + kAccRegs + 2 * kDeqRegs + kRestRegs <= 5 * 96, "register split");
     static_assert(kOffOp % 128 == 0 && kOffRaw % 128 == 0 && kOffState % 16 == 0 && kSmem + 4608 <= 232448, "shared memory layout");
 };
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(CfgF32<D>::kThreads, 1) k_kv_attn_chunk_f32(Ar
             const uint32_t q_lo = desc_lo(base, 2048), k_lo = desc_lo(base + C::kOffOp, 2048), v_lo = desc_lo(base + C::kOffOp, D * 16);
             auto qk = [&](uint32_t os, uint32_t buf) {
                 const uint32_t b = k_lo + os * (C::kOp >> 4), d = tmem + kSCol * buf;
-#pragma unroll 2  // unrolled wholly it crowds the instruction cache (509 of 8191 tokens 193 -> 223 us)
+#pragma unroll 2  // unrolled wholly it crowds the instruction cache (509 of 8191 tokens 202 -> 217 us)
                 for (int k = 0; k < D / 16; ++k) mma_f16(d, desc_of(q_lo + k * 256), desc_of(b + k * 256), kIdQk1, k > 0);
 #pragma unroll 2
                 for (int k = 0; k < D / 16; ++k)
