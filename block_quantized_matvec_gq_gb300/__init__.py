@@ -76,6 +76,11 @@ def _declare(dll):
         "gq_kv_read_q8_0": ([P, P, P, P, P, L, P, L, I, I, I, I, I, I, I, I, P], I),
         "gq_kv_attention_workspace_bytes": ([I, I, I], S),
         "gq_kv_attention_q8_0": ([P, L, P, P, P, P, P, L, I, F, F, I, P, S, I, I, I, I, I, I, I, I, P], I),
+        "gq_kv_plan": ([P, P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, P], I),
+        "gq_embed": ([I, P, P, F, P, L, I, I, I, I, P], I),
+        "gq_lora_workspace_bytes": ([I, I, I], S),
+        "gq_lora_add": ([P, P, I, P, P, P, P, L, P, L, P, L, P, S, I, I, I, I, I, I, P], I),
+        "gq_lora_add_q8act": ([P, P, I, P, P, P, P, P, P, L, P, L, P, S, I, I, I, I, I, I, P], I),
         "gq_device_status": ([I], I),
         "gq_selftest_bounded_wait": ([P], I),
     }
@@ -274,6 +279,35 @@ def gq_kv_attention_q8_0(Q, ldq, cache, block_table, kv_len, q_start, O, ldo, ty
                                       _rows(O), ldo, type, scale, softcap, window, _ptr(workspace), workspace_bytes,
                                       heads, n_pages, max_pages, page_tokens, kv_heads, head_dim, n_seq, n_tokens,
                                       _stream(stream)), "gq_kv_attention_q8_0")
+
+
+def gq_kv_plan(n_new, kv_len_in, ring_in, free_pages, block_table, kv_len, q_start, ring, slot_or_null, position_or_null,
+               sequence_or_null, n_pages, max_pages, page_tokens, n_seq, n_tokens, stream=None):
+    _check(lib().gq_kv_plan(_ptr(n_new), _ptr(kv_len_in), _ptr(ring_in), _ptr(free_pages), _ptr(block_table), _ptr(kv_len),
+                            _ptr(q_start), _ptr(ring), _ptr(slot_or_null), _ptr(position_or_null), _ptr(sequence_or_null),
+                            n_pages, max_pages, page_tokens, n_seq, n_tokens, _stream(stream)), "gq_kv_plan")
+
+
+def gq_embed(format, W, ids, scale, Y, ldy, type, rows, K, M, stream=None):
+    _check(lib().gq_embed(format, _ptr(W), _ptr(ids), scale, _rows(Y), ldy, type, rows, K, M, _stream(stream)), "gq_embed")
+
+
+def gq_lora_workspace_bytes(rank, K, M) -> int:
+    return int(lib().gq_lora_workspace_bytes(rank, K, M))
+
+
+def gq_lora_add(A, B, type, scale, adapter, sequence_or_null, X, ldx, Y0, ldy0, Y, ldy, workspace, workspace_bytes, n_adapters,
+                rank, rows, K, n_seq, M, stream=None):
+    _check(lib().gq_lora_add(_ptr(A), _ptr(B), type, _ptr(scale), _ptr(adapter), _ptr(sequence_or_null), _rows(X), ldx, _rows(Y0),
+                             ldy0, _rows(Y), ldy, _ptr(workspace), workspace_bytes, n_adapters, rank, rows, K, n_seq, M,
+                             _stream(stream)), "gq_lora_add")
+
+
+def gq_lora_add_q8act(A, B, type, scale, adapter, sequence_or_null, Xq, dx, Y0, ldy0, Y, ldy, workspace, workspace_bytes,
+                      n_adapters, rank, rows, K, n_seq, M, stream=None):
+    _check(lib().gq_lora_add_q8act(_ptr(A), _ptr(B), type, _ptr(scale), _ptr(adapter), _ptr(sequence_or_null), _ptr(Xq), _ptr(dx),
+                                   _rows(Y0), ldy0, _rows(Y), ldy, _ptr(workspace), workspace_bytes, n_adapters, rank, rows, K,
+                                   n_seq, M, _stream(stream)), "gq_lora_add_q8act")
 
 
 def gq_selftest_bounded_wait(stream=None):

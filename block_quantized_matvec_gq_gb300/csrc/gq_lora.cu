@@ -1,0 +1,503 @@
+// gq_lora.cu -- low-rank adapters of a batch's requests (include/gq_lora.h).
+//
+//   v = A_a x (rank numbers a token), then Y = Y0 + scale_a B_a v.
+//
+// Two kernels: `shrink` writes v to the workspace, `expand` adds.  Both work on
+// tiles of 8 or 32 neighbouring tokens.  A tile's distinct adapters (its
+// groups) are found with one warp vote; each is multiplied with the whole tile
+// and kept for its own tokens, so no sorting of the batch precedes them, and an
+// adapter's weights pass only by its own tokens' results.  Decode batches,
+// whose neighbours differ, take tiles of 8 (the width of the matrix
+// instruction) with the groups in different CTAs; prompts take 32, nearly
+// always one group.
+//
+// The products run on mma.sync with tf32 operands: 16-bit weights are exact in
+// tf32, f32 activations and v are two pieces of 11 bits, and Q8_0 codes are
+// exact, their scale applied to each block's sum.  The order of the contraction
+// is free, so a lane takes 8 consecutive elements of a row as its operands of
+// four instructions: weights and activations come in 16-byte loads straight
+// from memory, without shared memory between.  Sums of more than 32 products
+// are added in f32 registers, because the tensor core truncates its own.
+//
+// tcgen05 is not used: the contraction is 8 to 128 deep, so the work is the
+// bytes of Y (and, for few tokens, of the adapters), not the products.
+#include "gq_host.h"
+#include "gq_internal.cuh"
+#include "gq_lora.h"
+
+namespace gq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRowBlock = 32;  // output rows of a warp's step
+
+struct Batch {
+    const int32_t *adapter, *sequence;
+    const float *scale;
+    int n_adapters, n_seq, M;
+    int *status;
+};
+
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const float (&a)[4], float b0, float b1)
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])),
+                   "r"(__float_as_uint(a[3])), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+
+// The two 16-bit weights of a word, exact.
+template <bool BF16>
+__device__ __forceinline__ float2 weights2(uint32_t w)
+{
+    if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// The 11 leading bits of x; the rest, x - head(x), is exact and tf32 keeps 11 bits of it.
+__device__ __forceinline__ float head(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFFE000u); }
+
+// Tokens of a tile: which group (distinct adapter, by first appearance) each
+// belongs to, -1 for none, and the groups' adapters.  All threads take part.
+struct Tile {
+    int group[32], adapter[32];
+    int groups;
+};
+template <int TT>
+__device__ __forceinline__ void find_groups(Tile &tile, const Batch &B, int t0)
+{
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x, t = t0 + lane;
+        int a = -1;
+        if (lane < TT && t < B.M) {
+            const int b = B.sequence ? __ldg(B.sequence + t) : t;
+            if (b >= 0 && b < B.n_seq) a = __ldg(B.adapter + b);
+            if ((b >= B.n_seq || a >= B.n_adapters) && B.status) atomicExch(B.status, GQ_ERR_SHAPE);
+            if (a < 0 || a >= B.n_adapters) a = -1;
+        }
+        const unsigned same = __match_any_sync(0xffffffffu, a);
+        const int first = __ffs(same) - 1;
+        const unsigned leaders = __ballot_sync(0xffffffffu, a >= 0 && first == lane);
+        const int g = __popc(leaders & ((1u << first) - 1u));
+        tile.group[lane] = a >= 0 ? g : -1;
+        if (a >= 0 && first == lane) tile.adapter[g] = a;
+        if (lane == 0) tile.groups = __popc(leaders);
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- v = A x
+// CTA: a tile of 8 NT tokens, one slice of K.  The warps take the slice's
+// 32-element chunks in turn, each for all of rank (16 MT), and add up in
+// shared memory; the slices' sums are added by `expand`.
+template <int MT, int NT, bool BF16, bool Q8>
+__global__ void __launch_bounds__(kThreads)
+    k_lora_shrink(const uint16_t *__restrict__ A, Batch B, const float *__restrict__ X, long long ldx,
+                  const int8_t *__restrict__ Xq, const float *__restrict__ dx, float *__restrict__ V, int rank, int K,
+                  int slice_chunks)
+{
+    extern __shared__ __align__(16) float red[];  // [kWarps][16 MT][8 NT]
+    __shared__ Tile tile;
+    constexpr int TT = 8 * NT, kOut = 16 * MT * TT;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int t0 = blockIdx.x * TT, chunks = K / 32;
+    const int c0 = blockIdx.y * slice_chunks, c1 = min(c0 + slice_chunks, chunks);
+    pdl_wait();
+    // only now: what the next kernel reads before its own wait is complete then
+    pdl_launch_dependents();
+    find_groups<TT>(tile, B, t0);
+    for (int j = blockIdx.z; j < tile.groups; j += gridDim.z) {
+        const uint16_t *a = A + static_cast<long long>(tile.adapter[j]) * rank * K;
+        float acc[MT][NT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+        bool in[NT];  // lane's token (column g) of every n-tile
+#pragma unroll
+        for (int n = 0; n < NT; ++n) in[n] = tile.group[8 * n + g] == j;
+#pragma unroll 2
+        for (int c = c0 + warp; c < c1; c += kWarps) {
+            const int k = 32 * c + 8 * t;
+            uint4 aw[MT][2];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = 16 * m + 8 * h + g;
+                    aw[m][h] = r < rank ? __ldg(reinterpret_cast<const uint4 *>(a + static_cast<long long>(r) * K + k))
+                                        : make_uint4(0, 0, 0, 0);
+                }
+            float x[NT][8], dt[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const long long tok = t0 + 8 * n + g;
+                if (Q8) {
+                    const uint2 q = in[n] ? __ldg(reinterpret_cast<const uint2 *>(Xq + tok * K + k)) : make_uint2(0, 0);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        // a code's byte + 128 as the low bits of 2^23
+                        const uint32_t w = (i < 4 ? q.x : q.y) ^ 0x80808080u;
+                        x[n][i] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 | (i & 3))) - 8388736.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int col = 8 * n + 2 * t + i;
+                        dt[n][i] = tile.group[col] == j ? __ldg(dx + static_cast<long long>(t0 + col) * chunks + c) : 0.f;
+                    }
+                } else {
+                    const float4 *p = reinterpret_cast<const float4 *>(X + tok * ldx + k);
+                    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float4 u = in[n] ? __ldg(p) : zero, v = in[n] ? __ldg(p + 1) : zero;
+                    x[n][0] = u.x, x[n][1] = u.y, x[n][2] = u.z, x[n][3] = u.w;
+                    x[n][4] = v.x, x[n][5] = v.y, x[n][6] = v.z, x[n][7] = v.w;
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float af[4][4];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const float2 lo = weights2<BF16>((&aw[m][0].x)[s]), hi = weights2<BF16>((&aw[m][1].x)[s]);
+                    af[s][0] = lo.x, af[s][1] = hi.x, af[s][2] = lo.y, af[s][3] = hi.y;
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                    if (!Q8) {
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            mma_tf32(d, af[s], x[n][2 * s] - head(x[n][2 * s]), x[n][2 * s + 1] - head(x[n][2 * s + 1]));
+                    }
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) mma_tf32(d, af[s], head(x[n][2 * s]), head(x[n][2 * s + 1]));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[m][n][i] = Q8 ? fmaf(dt[n][i & 1], d[i], acc[m][n][i]) : acc[m][n][i] + d[i];
+                }
+            }
+        }
+        float *mine = red + warp * kOut;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mine[(8 * n + 2 * t + (i & 1)) * 16 * MT + 16 * m + g + 8 * (i >> 1)] = acc[m][n][i];
+        __syncthreads();
+        float *out = V + static_cast<long long>(blockIdx.y) * B.M * rank;
+        for (int i = threadIdx.x; i < kOut; i += kThreads) {
+            const int tok = i / (16 * MT), r = i - tok * 16 * MT;
+            if (r < rank && tile.group[tok] == j) {
+                float s = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) s += red[w * kOut + i];
+                out[static_cast<long long>(t0 + tok) * rank + r] = s;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- Y = Y0 + scale B v
+// CTA: a tile of 8 NT tokens and a range of row blocks, which its warps take in
+// turn.  Row slots are dealt so that a lane's four results of a token are four
+// consecutive rows: slot g (+ 8) of instruction m is row 4 g + 2 m (+ 1).
+// KC = 16: a rank of up to 16, where a lane's chunk is four elements.
+template <int KC, int NT, bool BF16>
+__global__ void __launch_bounds__(kThreads)
+    k_lora_expand(const uint16_t *__restrict__ W, Batch B, const float *__restrict__ V, const float *Y0, long long ldy0,
+                  float *Y, long long ldy, int rank, int rows, int slices, int row_groups, int group_blocks)
+{
+    extern __shared__ __align__(16) float vs[];  // [8 NT][stride]
+    __shared__ Tile tile;
+    constexpr int TT = 8 * NT, E = KC / 4;  // elements of a lane's chunk
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int tile_no = blockIdx.x / row_groups, rg = blockIdx.x - tile_no * row_groups;
+    const int t0 = tile_no * TT;
+    const int blocks = (rows + kRowBlock - 1) / kRowBlock;
+    const int rb0 = rg * group_blocks, rb1 = min(rb0 + group_blocks, blocks);
+    const int depth = (rank + KC - 1) / KC * KC, stride = depth + 4;
+    pdl_launch_dependents();
+    // the lists, Y0 and the weights were complete before `shrink` let this
+    // kernel begin; v is complete after the wait
+    find_groups<TT>(tile, B, t0);
+    const int groups = tile.groups;
+    if (static_cast<int>(blockIdx.z) >= max(groups, 1)) {
+        pdl_wait();
+        return;
+    }
+    bool waited = false;
+    for (int j = blockIdx.z; j < max(groups, 1); j += gridDim.z) {
+        const bool product = j < groups;
+        if (!waited) pdl_wait();
+        waited = true;
+        const float scale = product ? __ldg(B.scale + tile.adapter[j]) : 0.f;
+        for (int i = threadIdx.x; i < TT * depth; i += kThreads) {
+            const int tok = i / depth, r = i - tok * depth;
+            float s = 0.f;
+            if (r < rank && tile.group[tok] == j) {
+                const float *p = V + static_cast<long long>(t0 + tok) * rank + r;
+                for (int c = 0; c < slices; ++c) s += __ldcg(p + static_cast<long long>(c) * B.M * rank);
+            }
+            vs[tok * stride + r] = s * scale;
+        }
+        __syncthreads();
+        // tokens whose rows this pass writes: the group's, and with the first group those without an adapter, if
+        // their rows have to be copied
+        bool put[NT][2], add[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int tok = 8 * n + 2 * t + i;
+                add[n][i] = product && tile.group[tok] == j;
+                put[n][i] = add[n][i] || (j == 0 && tile.group[tok] < 0 && t0 + tok < B.M && Y != Y0);
+            }
+        const uint16_t *w = W + static_cast<long long>(product ? tile.adapter[j] : 0) * rows * rank;
+        for (int rb = rb0 + warp; rb < rb1; rb += kWarps) {
+            const int row = rb * kRowBlock + 4 * g;
+            const bool in = row < rows;
+            float4 y[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (in && put[n][i])
+                        y[n][i] = *reinterpret_cast<const float4 *>(Y0 + static_cast<long long>(t0 + 8 * n + 2 * t + i) * ldy0 + row);
+            if (product) {
+                float acc[NT][2][4];
+                for (int k0 = 0; k0 < depth; k0 += KC) {
+                    const int k = k0 + E * t;
+                    uint32_t aw[2][2][E / 2];
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint16_t *p = w + static_cast<long long>(row + 2 * m + h) * rank + k;
+                            const bool have = in && k < rank;
+                            if (E == 8) {
+                                const uint4 v = have ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0, 0, 0, 0);
+                                aw[m][h][0] = v.x, aw[m][h][1] = v.y, aw[m][h][E / 2 - 2] = v.z, aw[m][h][E / 2 - 1] = v.w;
+                            } else {
+                                const uint2 v = have ? __ldg(reinterpret_cast<const uint2 *>(p)) : make_uint2(0, 0);
+                                aw[m][h][0] = v.x, aw[m][h][1] = v.y;
+                            }
+                        }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float v[E];
+#pragma unroll
+                        for (int q = 0; q < E / 4; ++q) {
+                            const float4 u = *reinterpret_cast<const float4 *>(vs + (8 * n + g) * stride + k + 4 * q);
+                            v[4 * q] = u.x, v[4 * q + 1] = u.y, v[4 * q + 2] = u.z, v[4 * q + 3] = u.w;
+                        }
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+                            float af[E / 2][4];
+#pragma unroll
+                            for (int s = 0; s < E / 2; ++s) {
+                                const float2 lo = weights2<BF16>(aw[m][0][s]), hi = weights2<BF16>(aw[m][1][s]);
+                                af[s][0] = lo.x, af[s][1] = hi.x, af[s][2] = lo.y, af[s][3] = hi.y;
+                            }
+#pragma unroll
+                            for (int s = 0; s < E / 2; ++s)
+                                mma_tf32(d, af[s], v[2 * s] - head(v[2 * s]), v[2 * s + 1] - head(v[2 * s + 1]));
+#pragma unroll
+                            for (int s = 0; s < E / 2; ++s) mma_tf32(d, af[s], head(v[2 * s]), head(v[2 * s + 1]));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[n][m][i] = k0 == 0 ? d[i] : acc[n][m][i] + d[i];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (add[n][i]) {
+                            y[n][i].x += acc[n][0][i];
+                            y[n][i].y += acc[n][0][2 + i];
+                            y[n][i].z += acc[n][1][i];
+                            y[n][i].w += acc[n][1][2 + i];
+                        }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (in && put[n][i])
+                        *reinterpret_cast<float4 *>(Y + static_cast<long long>(t0 + 8 * n + 2 * t + i) * ldy + row) = y[n][i];
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- host
+// Slices of K: enough CTAs for two per SM, at least one chunk for every warp.
+constexpr int kWantCtas = 304;
+int most_slices(int K, int M)
+{
+    const int tiles = (M + 7) / 8, by_k = (K / 32 + kWarps - 1) / kWarps;
+    const int want = (kWantCtas + tiles - 1) / tiles;
+    return want < by_k ? want : by_k;
+}
+
+struct Call {
+    const uint16_t *A, *W;
+    Batch B;
+    const float *X;
+    long long ldx;
+    const int8_t *Xq;
+    const float *dx;
+    const float *Y0;
+    long long ldy0;
+    float *Y;
+    long long ldy;
+    float *V;
+    int rank, rows, K;
+    cudaStream_t s;
+};
+
+template <int MT, int NT, bool BF16, bool Q8>
+cudaError_t shrink(const Call &c, int tiles, int groups, int slices, int slice_chunks)
+{
+    auto kern = k_lora_shrink<MT, NT, BF16, Q8>;
+    const size_t smem = sizeof(float) * kWarps * 16 * MT * 8 * NT;
+    if (ctas_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
+    return launch_pdl(kern, dim3(tiles, slices, groups), dim3(kThreads), smem, c.s, c.A, c.B, c.X, c.ldx, c.Xq, c.dx, c.V,
+                      c.rank, c.K, slice_chunks);
+}
+template <int MT, int NT>
+cudaError_t shrink_typed(const Call &c, bool bf16, int tiles, int groups, int slices, int slice_chunks)
+{
+    if (c.Xq)
+        return bf16 ? shrink<MT, NT, true, true>(c, tiles, groups, slices, slice_chunks)
+                    : shrink<MT, NT, false, true>(c, tiles, groups, slices, slice_chunks);
+    return bf16 ? shrink<MT, NT, true, false>(c, tiles, groups, slices, slice_chunks)
+                : shrink<MT, NT, false, false>(c, tiles, groups, slices, slice_chunks);
+}
+template <int NT>
+cudaError_t shrink_rank(const Call &c, bool bf16, int tiles, int groups, int slices, int slice_chunks)
+{
+    if (c.rank <= 16) return shrink_typed<1, NT>(c, bf16, tiles, groups, slices, slice_chunks);
+    if (c.rank <= 32) return shrink_typed<2, NT>(c, bf16, tiles, groups, slices, slice_chunks);
+    if (c.rank <= 64) return shrink_typed<4, NT>(c, bf16, tiles, groups, slices, slice_chunks);
+    return shrink_typed<8, NT>(c, bf16, tiles, groups, slices, slice_chunks);
+}
+
+template <int KC, int NT, bool BF16>
+cudaError_t expand(const Call &c, int tiles, int groups, int slices)
+{
+    auto kern = k_lora_expand<KC, NT, BF16>;
+    const int depth = (c.rank + KC - 1) / KC * KC;
+    const size_t smem = sizeof(float) * 8 * NT * (depth + 4);
+    if (ctas_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
+    // four row blocks a warp, fewer where that leaves SMs without a CTA
+    const int blocks = (c.rows + kRowBlock - 1) / kRowBlock, most = (blocks + kWarps - 1) / kWarps;
+    const long long have = static_cast<long long>(tiles) * groups;
+    long long rg = (kWantCtas + have - 1) / have;
+    if (rg < (most + 3) / 4) rg = (most + 3) / 4;
+    if (rg > most) rg = most;
+    const int group_blocks = static_cast<int>((blocks + rg - 1) / rg);
+    const int row_groups = (blocks + group_blocks - 1) / group_blocks;
+    const long long grid = static_cast<long long>(tiles) * row_groups;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(grid), 1, groups), dim3(kThreads), smem, c.s, c.W, c.B, c.V, c.Y0,
+                      c.ldy0, c.Y, c.ldy, c.rank, c.rows, slices, row_groups, group_blocks);
+}
+template <int NT>
+cudaError_t expand_rank(const Call &c, bool bf16, int tiles, int groups, int slices)
+{
+    if (c.rank <= 16)
+        return bf16 ? expand<16, NT, true>(c, tiles, groups, slices) : expand<16, NT, false>(c, tiles, groups, slices);
+    return bf16 ? expand<32, NT, true>(c, tiles, groups, slices) : expand<32, NT, false>(c, tiles, groups, slices);
+}
+
+int run(const Call &c, int type)
+{
+    const bool bf16 = type == GQ_TYPE_BF16;
+    // Neighbouring tokens of one request share their adapter: tiles of 32 where
+    // requests have 16 tokens or more on average.
+    const bool long_runs = c.B.sequence != nullptr && c.B.M / 16 >= c.B.n_seq;
+    const int tt = long_runs ? 32 : 8, st = long_runs ? 16 : 8;  // tokens of an expand and of a shrink tile
+    const int distinct = long_runs ? 1 : (c.B.n_adapters < tt ? c.B.n_adapters : tt);
+    const int tiles = (c.B.M + tt - 1) / tt, shrink_tiles = (c.B.M + st - 1) / st, chunks = c.K / 32;
+    int slices = most_slices(c.K, c.B.M);
+    const int enough = static_cast<int>((kWantCtas + static_cast<long long>(shrink_tiles) * distinct - 1) /
+                                        (static_cast<long long>(shrink_tiles) * distinct));
+    if (slices > enough) slices = enough;
+    const int slice_chunks = (chunks + slices - 1) / slices;
+    slices = (chunks + slice_chunks - 1) / slice_chunks;
+    cudaError_t e = long_runs ? shrink_rank<2>(c, bf16, shrink_tiles, distinct, slices, slice_chunks)
+                              : shrink_rank<1>(c, bf16, shrink_tiles, distinct, slices, slice_chunks);
+    if (e == cudaSuccess)
+        e = long_runs ? expand_rank<4>(c, bf16, tiles, distinct, slices) : expand_rank<1>(c, bf16, tiles, distinct, slices);
+    return status_from(e);
+}
+
+inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int check_and_run(Call c, int type, size_t workspace_bytes)
+{
+    const Batch &B = c.B;
+    if (type != GQ_TYPE_F16 && type != GQ_TYPE_BF16) return GQ_ERR_FORMAT;
+    if (B.M < 0 || B.n_adapters < 1 || B.n_seq < 1 || c.rows < 4 || c.rows % 4 != 0 || c.rows > (1 << 24)) return GQ_ERR_SHAPE;
+    if (B.M == 0) return GQ_OK;
+    const size_t need = gq_lora_workspace_bytes(c.rank, c.K, B.M);
+    if (need == 0) return GQ_ERR_SHAPE;
+    const bool q8 = c.ldx < 0;
+    if (!c.A || !c.W || !B.scale || !B.adapter || !c.Y0 || !c.Y || (q8 ? !c.Xq || !c.dx : !c.X)) return GQ_ERR_NULL;
+    if (!aligned16(c.A) || !aligned16(c.W) || !aligned16(c.X) || !aligned16(c.Xq) || !aligned16(c.dx) || !aligned16(c.Y0) ||
+        !aligned16(c.Y) || !aligned4(B.scale) || !aligned4(B.adapter) || !aligned4(B.sequence))
+        return GQ_ERR_ALIGN;
+    if (!B.sequence && B.M > B.n_seq) return GQ_ERR_SHAPE;
+    if ((!q8 && c.ldx < c.K) || c.ldy0 < c.rows || c.ldy < c.rows || (c.Y == c.Y0 && c.ldy != c.ldy0)) return GQ_ERR_SHAPE;
+    if ((!q8 && c.ldx % 4 != 0) || c.ldy0 % 4 != 0 || c.ldy % 4 != 0) return GQ_ERR_ALIGN;
+    if (!c.V || workspace_bytes < need) return GQ_ERR_WORKSPACE;
+    if (!aligned16(c.V)) return GQ_ERR_ALIGN;
+    c.B.status = status_word();
+    return run(c, type);
+}
+
+}  // namespace
+}  // namespace gq
+
+using namespace gq;
+
+extern "C" {
+
+size_t gq_lora_workspace_bytes(int rank, int K, int M)
+{
+    if (rank < 8 || rank % 8 != 0 || rank > GQ_MAX_LORA_RANK || K < 32 || K % 32 != 0 || K > (1 << 24) || M < 1 || M > (1 << 28))
+        return 0;
+    return static_cast<size_t>(most_slices(K, M)) * M * rank * sizeof(float);
+}
+
+int gq_lora_add(const void *A, const void *B, int type, const float *scale, const int32_t *adapter,
+                const int32_t *sequence_or_null, const float *X, long long ldx, const float *Y0, long long ldy0,
+                float *Y, long long ldy, void *workspace, size_t workspace_bytes, int n_adapters, int rank, int rows,
+                int K, int n_seq, int M, gq_stream_t stream)
+{
+    if (ldx < 0) return GQ_ERR_SHAPE;
+    const Call c{static_cast<const uint16_t *>(A), static_cast<const uint16_t *>(B),
+                 Batch{adapter, sequence_or_null, scale, n_adapters, n_seq, M, nullptr}, X, ldx, nullptr, nullptr, Y0, ldy0, Y,
+                 ldy, static_cast<float *>(workspace), rank, rows, K, reinterpret_cast<cudaStream_t>(stream)};
+    return check_and_run(c, type, workspace_bytes);
+}
+
+int gq_lora_add_q8act(const void *A, const void *B, int type, const float *scale, const int32_t *adapter,
+                      const int32_t *sequence_or_null, const int8_t *Xq, const float *dx, const float *Y0,
+                      long long ldy0, float *Y, long long ldy, void *workspace, size_t workspace_bytes,
+                      int n_adapters, int rank, int rows, int K, int n_seq, int M, gq_stream_t stream)
+{
+    const Call c{static_cast<const uint16_t *>(A), static_cast<const uint16_t *>(B),
+                 Batch{adapter, sequence_or_null, scale, n_adapters, n_seq, M, nullptr}, nullptr, -1, Xq, dx, Y0, ldy0, Y, ldy,
+                 static_cast<float *>(workspace), rank, rows, K, reinterpret_cast<cudaStream_t>(stream)};
+    return check_and_run(c, type, workspace_bytes);
+}
+
+}  // extern "C"
