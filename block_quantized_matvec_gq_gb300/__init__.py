@@ -25,6 +25,9 @@ GQ_TYPE_F16 = 1
 GQ_TYPE_BF16 = 2
 GQ_MAX_K = 49152
 GQ_MAX_TOPK = 64
+GQ_MAX_PLAN_SEQ = 8192
+GQ_MAX_LORA_RANK = 128
+GQ_MAX_VOCAB = 1048576
 
 GQ_OK = 0
 GQ_ERR_NULL = -1
@@ -81,6 +84,8 @@ def _declare(dll):
         "gq_lora_workspace_bytes": ([I, I, I], S),
         "gq_lora_add": ([P, P, I, P, P, P, P, L, P, L, P, L, P, S, I, I, I, I, I, I, P], I),
         "gq_lora_add_q8act": ([P, P, I, P, P, P, P, P, P, L, P, L, P, S, I, I, I, I, I, I, P], I),
+        "gq_sample_workspace_bytes": ([I, I], S),
+        "gq_sample": ([P, L, I, P, P, P, P, P, P, P, P, S, I, I, P], I),
         "gq_device_status": ([I], I),
         "gq_selftest_bounded_wait": ([P], I),
     }
@@ -308,6 +313,17 @@ def gq_lora_add_q8act(A, B, type, scale, adapter, sequence_or_null, Xq, dx, Y0, 
     _check(lib().gq_lora_add_q8act(_ptr(A), _ptr(B), type, _ptr(scale), _ptr(adapter), _ptr(sequence_or_null), _ptr(Xq), _ptr(dx),
                                    _rows(Y0), ldy0, _rows(Y), ldy, _ptr(workspace), workspace_bytes, n_adapters, rank, rows, K,
                                    n_seq, M, _stream(stream)), "gq_lora_add_q8act")
+
+
+def gq_sample_workspace_bytes(vocab, n_rows) -> int:
+    return int(lib().gq_sample_workspace_bytes(vocab, n_rows))
+
+
+def gq_sample(logits, ldl, type, temperature, top_k, top_p, min_p, u, token, prob_or_null, workspace, workspace_bytes, vocab,
+              n_rows, stream=None):
+    _check(lib().gq_sample(_rows(logits), ldl, type, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u),
+                           _ptr(token), _ptr(prob_or_null), _ptr(workspace), workspace_bytes, vocab, n_rows, _stream(stream)),
+           "gq_sample")
 
 
 def gq_selftest_bounded_wait(stream=None):

@@ -1,0 +1,1002 @@
+// gq_sample.cu -- temperature, top-k, top-p and min-p sampling (include/gq_sample.h).
+//
+// Every limit keeps a beginning of one order (falling logit, then rising
+// index), and the drawn token is the first of that order whose running weight
+// exceeds a target.  So the whole operator is: sums of weights, and "the first
+// element at which a running count or weight reaches X".  Nothing sorts a row.
+//
+// Weights are whole numbers of 2^-43 of about the largest weight, w = M 2^(A - 31)
+// with A = rint(l log2(e) / T) and a 32-bit M: A and M depend on the logit and T
+// alone, so sums are exact integers in any order, the running weights and the
+// total agree to the last unit, and a slice can be summed before the row's
+// largest logit is known.
+//
+//   scan   streams the row once, a slice per CTA held in registers: largest
+//          logit, sum of weights, and a list of the slice's leading elements.
+//          The list's threshold is the want-th largest of the threads' own
+//          maxima, found by bisection with a vote of the CTA per step: at least
+//          `want` elements reach it, and few more.
+//   pick   one CTA per row: lists above the slices' highest threshold hold every
+//          element above it, some hundreds.  They are sorted, and where the
+//          limits and the draw fall among them, which they do for a language
+//          model's usual rows, the row is done.
+//   deep   the other rows (flat ones, a large top_k), a cluster of CTAs each: a
+//          histogram of the row over 2048 equal steps of the exponent gives the
+//          step in which X is reached, exactly for counts, by an estimate for
+//          weights; the step's elements are collected and sorted, with the exact
+//          weight in front of them, which also shows whether the estimate was
+//          right.  A step with too many elements is divided further, by the bits
+//          of (logit, index), which no two elements share.
+//
+// What bounds it: the one pass over the logits, and for small batches the
+// latency of the three kernels.
+#include <cooperative_groups.h>
+#include <math.h>
+
+#include "gq_host.h"
+#include "gq_internal.cuh"
+#include "gq_kv.cuh"
+#include "gq_sample.h"
+
+namespace gq {
+namespace {
+
+namespace cg = cooperative_groups;
+using u64 = unsigned long long;
+
+constexpr int kScanThreads = 512;
+constexpr int kPickThreads = 1024;
+constexpr int kDeepThreads = 512;
+constexpr int kDeepCtas = 8;
+constexpr int kList = 2048;  // elements that are sorted at once
+constexpr int kBins = 2048;
+constexpr uint32_t kNone = 0x007FFFFFu;        // key of -infinity: no candidate
+constexpr uint32_t kUnknown = 0xFFFFFFFFu;     // threshold of a slice whose list is empty
+constexpr float kRound = 12582912.0f;          // 1.5 * 2^23: adding it rounds to a whole number
+constexpr float kFarDown = -2097152.0f;        // exponents below give no weight
+constexpr float kFarUp = 1048576.0f;
+
+struct Settings {
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p, *min_p, *u;
+};
+
+// What `scan` says of a slice.
+struct __align__(16) Header {
+    u64 sum;         // weights in units of 2^(exp - 43)
+    u64 best;        // the first of the order
+    uint32_t lowest, theta;  // smallest candidate's key; every element with a key of theta or more is listed
+    int exp, count, cands, pad;
+};
+
+struct Rows {
+    const uint8_t *logits;
+    long long row_bytes;
+    int vocab, slices, cap;
+    Header *head;
+    u64 *list;
+    int *deep;  // rows for the third kernel
+};
+
+// Order-preserving bits of a logit (neither NaN nor -0).
+__device__ __forceinline__ uint32_t key_of(float v)
+{
+    const uint32_t b = __float_as_uint(v);
+    return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu)); }
+// (logit, index) as one number: larger is earlier in the order, 0 is nothing.
+__device__ __forceinline__ u64 rank_of(uint32_t key, int index) { return static_cast<u64>(key) << 32 | ~static_cast<uint32_t>(index); }
+__device__ __forceinline__ int index_of(u64 rank) { return static_cast<int>(~static_cast<uint32_t>(rank)); }
+
+// ---------------------------------------------------------------- weights
+// The exponent of a logit is (l - base) * (ch + cl), ch + cl = log2(e) / T to 47
+// bits.  `base` is 0 unless the row's exponents are too large for the rounding
+// below; then it is the largest logit, next to which differences are exact.
+struct Scale {
+    float ch, cl, base;
+    bool infinite;  // the largest logit is +infinity
+};
+__device__ __forceinline__ Scale scale_of(float T)
+{
+    const float t = fmaxf(T, 7.888609052e-31f);  // 2^-100
+    const float hi = 1.44269502f, lo = 1.92596299e-8f;  // log2(e)
+    Scale s{0.f, 0.f, 0.f, false};
+    if (t < INFINITY) {
+        s.ch = __fdiv_rn(hi, t);
+        s.cl = __fdiv_rn(__fadd_rn(fmaf(-s.ch, t, hi), lo), t);
+    }
+    return s;
+}
+__device__ __forceinline__ Scale scale_of(float T, float largest)
+{
+    Scale s = scale_of(T);
+    s.infinite = largest == INFINITY;
+    if (!(fabsf(largest * s.ch) <= kFarUp)) s.base = largest;
+    return s;
+}
+
+// Exponent A (rounded) and mantissa M in [2^30.5, 2^31.5]: weight M 2^(A - 31).
+// 2^f - 1 for |f| <= 1/2 by its Taylor series (the next term is below 2^-32),
+// the leading coefficient in two parts: within 2^-25 of the weight.
+__device__ __forceinline__ void split(const Scale &s, float l, int &A, uint32_t &M)
+{
+    const float d = l - s.base;
+    const float r = fmaxf(d * s.ch, kFarDown) + kRound;
+    A = __float_as_int(r) - __float_as_int(kRound);
+    const float f = fmaf(d, s.cl, fmaf(d, s.ch, kRound - r));
+    float p = 1.32154868e-6f;             // ln2^8 / 8!
+    p = fmaf(p, f, 1.52527338e-5f);       // ln2^7 / 7!
+    p = fmaf(p, f, 1.54035304e-4f);
+    p = fmaf(p, f, 1.33335581e-3f);
+    p = fmaf(p, f, 9.61812911e-3f);
+    p = fmaf(p, f, 5.55041087e-2f);
+    p = fmaf(p, f, 2.40226507e-1f);       // ln2^2 / 2!
+    p = fmaf(p, f, -1.90465421e-9f);      // ln2 - its f32
+    const float e = fmaf(f, 6.93147182e-1f, f * p);
+    M = 0x80000000u + static_cast<uint32_t>(__float2int_rn(e * 2147483648.0f));
+}
+// Weight in units of 2^(top - 43).
+__device__ __forceinline__ u64 weight(const Scale &s, float l, int top)
+{
+    int A;
+    uint32_t M;
+    split(s, l, A, M);
+    const unsigned sh = static_cast<unsigned>(top - A);
+    return sh < 64 ? (static_cast<u64>(M) << 12) >> sh : 0ull;
+}
+__device__ __forceinline__ int exponent(const Scale &s, float l)
+{
+    int A;
+    uint32_t M;
+    split(s, l, A, M);
+    return A;
+}
+// The same for a row whose largest logit may be infinite: those share the weight.
+__device__ __forceinline__ u64 row_weight(const Scale &s, float l, int top)
+{
+    if (s.infinite) return l == INFINITY ? 1ull << 43 : 0ull;
+    return weight(s, l, top);
+}
+
+// floor(f * z) for 0 <= f < 1, z < 2^64, and whether something was cut off.
+__device__ __forceinline__ u64 part_of(float f, u64 z, bool &rest)
+{
+    const uint32_t b = __float_as_uint(f);
+    const int ex = b >> 23;
+    const u64 m = ex ? (b & 0x7FFFFFu) | 0x800000u : b & 0x7FFFFFu;
+    const int s = ex ? 150 - ex : 149;  // f = m 2^-s, s >= 24
+    const u64 hi = __umul64hi(z, m), lo = z * m;
+    if (s < 64) {
+        rest = (lo << (64 - s)) != 0;
+        return (hi << (64 - s)) | (lo >> s);
+    }
+    if (s == 64) {
+        rest = lo != 0;
+        return hi;
+    }
+    if (s < 128) {
+        rest = lo != 0 || (hi << (128 - s)) != 0;
+        return hi >> (s - 64);
+    }
+    rest = (hi | lo) != 0;
+    return 0;
+}
+// The running weight that top_p asks for, and the one that the draw asks for.
+__device__ __forceinline__ u64 nucleus(float p, u64 z)
+{
+    if (!(p > 0.f)) return 1;
+    bool rest;
+    const u64 x = part_of(p, z, rest);
+    return max(x + (rest ? 1 : 0), 1ull);
+}
+__device__ __forceinline__ u64 drawn(float u, u64 z)
+{
+    const float f = fmaxf(u, 0.f);  // NaN: 0
+    if (f >= 1.f) return z;
+    bool rest;
+    return min(part_of(f, z, rest) + 1, z);
+}
+__device__ __forceinline__ float ratio(u64 w, u64 z) { return __fdiv_rn(__ull2float_rn(w), __ull2float_rn(z)); }
+
+// ---------------------------------------------------------------- reading a row
+// A row begins anywhere: 16-byte units from the boundary at or below it, the
+// first and the last read element by element.
+template <int TYPE>
+struct Reader {
+    static constexpr int kVec = TYPE == GQ_TYPE_F32 ? 4 : 8;
+    const uint8_t *base;
+    int shift, vocab, units;
+    __device__ __forceinline__ Reader(const uint8_t *row, int n)
+    {
+        const int size = kv::type_size(TYPE);
+        shift = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / size);
+        base = row - shift * size;
+        vocab = n;
+        units = (n + shift + kVec - 1) / kVec;
+    }
+    __device__ __forceinline__ int index(int unit, int i) const { return unit * kVec + i - shift; }
+    // Candidates as they are, -0 as 0, NaN and what lies outside as -infinity.
+    __device__ __forceinline__ void load(int unit, float (&v)[kVec]) const
+    {
+        const uint8_t *p = base + static_cast<long long>(unit) * 16;
+        const int first = index(unit, 0);
+        if (unit < units && first >= 0 && first + kVec <= vocab) {
+            if (TYPE == GQ_TYPE_F32) {
+                const float4 a = kv::load4<TYPE>(p);
+                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+            } else {
+                float4 a, b;
+                kv::load8<TYPE>(p, a, b);
+                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+                v[kVec - 4] = b.x, v[kVec - 3] = b.y, v[kVec - 2] = b.z, v[kVec - 1] = b.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                v[i] = -INFINITY;
+                if (unit < units && first + i >= 0 && first + i < vocab) {
+                    if (TYPE == GQ_TYPE_F32)
+                        v[i] = __ldg(reinterpret_cast<const float *>(p) + i);
+                    else if (TYPE == GQ_TYPE_F16)
+                        v[i] = __half2float(__ushort_as_half(__ldg(reinterpret_cast<const uint16_t *>(p) + i)));
+                    else
+                        v[i] = __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(p) + i)) << 16);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] = fmaxf(v[i] + 0.f, -INFINITY);
+    }
+};
+
+__device__ __forceinline__ float temperature(const Settings &s, int row) { return s.temperature ? __ldg(s.temperature + row) : 1.f; }
+__device__ __forceinline__ int top_k(const Settings &s, int row, int vocab)
+{
+    const int k = s.top_k ? __ldg(s.top_k + row) : 0;
+    return k > 0 && k < vocab ? k : 0;
+}
+
+__device__ __forceinline__ u64 warp_sum(u64 v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// Sum over the CTA, in every thread.  `sh` has one word per warp; a barrier on both sides.
+template <int THREADS>
+__device__ __forceinline__ u64 cta_sum(u64 v, u64 *sh)
+{
+    v = warp_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    u64 s = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) s += sh[w];
+    return s;
+}
+template <int THREADS>
+__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t *sh)
+{
+    v = __reduce_max_sync(0xffffffffu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    uint32_t m = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) m = max(m, sh[w]);
+    return m;
+}
+
+// ---------------------------------------------------------------- scan
+template <int TYPE, int EPT>
+__global__ void __launch_bounds__(kScanThreads) k_sample_scan(Rows R, Settings S, int want)
+{
+    constexpr int kVec = Reader<TYPE>::kVec, kUnits = EPT / kVec;
+    __shared__ u64 sh64[kScanThreads / 32];
+    __shared__ uint32_t sh32[kScanThreads / 32];
+    __shared__ int s_count;
+    const int tid = threadIdx.x, row = blockIdx.y, slice = blockIdx.x;
+    if (tid == 0) s_count = 0;
+    pdl_wait();
+    pdl_launch_dependents();
+    const Reader<TYPE> in(R.logits + row * R.row_bytes, R.vocab);
+    const int u0 = slice * kScanThreads * kUnits + tid;
+    float v[kUnits][kVec];
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) in.load(u0 + j * kScanThreads, v[j]);
+    const float T = temperature(S, row);
+    const int k = top_k(S, row, R.vocab);
+    float hi = -INFINITY, lo = INFINITY;
+    int cands = 0;
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            hi = fmaxf(hi, v[j][i]);
+            const bool c = v[j][i] > -INFINITY;
+            lo = c ? fminf(lo, v[j][i]) : lo;
+            cands += c ? 1 : 0;
+        }
+    const uint32_t mine = key_of(hi), top = cta_max<kScanThreads>(mine, sh32);
+    const float best = value_of(top);
+    Header h{};
+    // the slice's first of the order: the lowest index among its largest
+    uint32_t at = 0;
+    if (mine == top) {
+#pragma unroll
+        for (int j = kUnits - 1; j >= 0; --j)
+#pragma unroll
+            for (int i = kVec - 1; i >= 0; --i)
+                if (v[j][i] == best) at = ~static_cast<uint32_t>(in.index(u0 + j * kScanThreads, i));
+    }
+    at = cta_max<kScanThreads>(at, sh32);
+    h.best = top > kNone ? static_cast<u64>(top) << 32 | at : 0ull;
+    h.lowest = ~cta_max<kScanThreads>(lo < INFINITY ? ~key_of(lo) : 0u, sh32);
+    h.cands = static_cast<int>(cta_sum<kScanThreads>(static_cast<u64>(cands), sh64));
+    h.theta = kUnknown;
+    if (T > 0.f && top > kNone) {  // otherwise the first of the order is all that is asked for
+        const Scale sc = scale_of(T);
+        if (k == 0) {
+            h.exp = exponent(sc, best);
+            u64 sum = 0;
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) sum += weight(sc, v[j][i], h.exp);
+            h.sum = cta_sum<kScanThreads>(sum, sh64);
+        }
+        if (h.cands <= R.cap) {
+            h.theta = kNone + 1;
+            h.count = h.cands;
+        } else {
+            // a threshold that `w` threads reach and few elements more
+            const int threads = __syncthreads_count(mine > kNone);
+            const int w = max(1, min(k > 0 ? min(want, 2 * k / static_cast<int>(gridDim.x) + 8) : want, threads / 2));
+            uint32_t a = kNone + 1, b = top;  // w threads reach a; look in a .. b
+            while (a < b) {
+                const uint32_t mid = a + (b - a) / 2 + 1;
+                const int n = __syncthreads_count(mine >= mid);
+                if (n >= w)
+                    a = mid;
+                else
+                    b = mid - 1;
+                if (n >= w && n <= w + w / 4) break;
+            }
+            u64 counts = 0;  // elements at a or above, and above a
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    const uint32_t x = key_of(v[j][i]);
+                    counts += (x >= a ? 1ull : 0ull) + (x > a ? 1ull << 32 : 0ull);
+                }
+            counts = cta_sum<kScanThreads>(counts, sh64);
+            const int ge = static_cast<int>(counts & 0xFFFFFFFFu), gt = static_cast<int>(counts >> 32);
+            if (ge <= R.cap) {
+                h.theta = a;
+                h.count = ge;
+            } else if (gt <= R.cap) {  // many equal ones at the threshold: leave them out
+                h.theta = a + 1;
+                h.count = gt;
+            }
+        }
+        if (h.theta != kUnknown && mine >= h.theta) {
+            u64 *list = R.list + (static_cast<long long>(row) * R.slices + slice) * R.cap;
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    const uint32_t x = key_of(v[j][i]);
+                    if (x >= h.theta) list[atomicAdd(&s_count, 1)] = rank_of(x, in.index(u0 + j * kScanThreads, i));
+                }
+        }
+    }
+    if (tid == 0) R.head[static_cast<long long>(row) * R.slices + slice] = h;
+}
+
+// ---------------------------------------------------------------- sorted lists
+// Falling bitonic sort of n (a power of two, 64 .. kList) numbers.  Steps of 32
+// or less stay within a warp's own 64 numbers.
+template <int THREADS>
+__device__ __forceinline__ void sort_down(u64 *a, int n)
+{
+    for (int size = 2; size <= n; size <<= 1)
+        for (int step = size >> 1; step > 0; step >>= 1) {
+            for (int t = threadIdx.x; t < n / 2; t += THREADS) {
+                const int i = 2 * t - (t & (step - 1)), j = i + step;
+                const u64 x = a[i], y = a[j];
+                const bool down = (i & size) == 0;
+                if ((x < y) == down) {
+                    a[i] = y;
+                    a[j] = x;
+                }
+            }
+            if (step > 32 || (step == 1 && size >= 64))
+                __syncthreads();
+            else
+                __syncwarp();
+        }
+    __syncthreads();
+}
+__device__ __forceinline__ int padded(int n)
+{
+    int p = 64;
+    while (p < n) p <<= 1;
+    return p;
+}
+
+// F[i] = before + the weights of list[0 .. i], for the n sorted numbers.
+template <int THREADS>
+__device__ __forceinline__ void running_weights(const u64 *list, u64 *F, int n, u64 before, const Scale &sc, int top, u64 *sh)
+{
+    constexpr int kPer = kList / THREADS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i0 = threadIdx.x * kPer;
+    u64 w[kPer], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        w[i] = i0 + i < n ? row_weight(sc, value_of(static_cast<uint32_t>(list[i0 + i] >> 32)), top) : 0ull;
+        mine += w[i];
+    }
+    u64 incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    __syncthreads();
+    if (lane == 31) sh[warp] = incl;
+    __syncthreads();
+    u64 at = before + incl - mine;
+    for (int x = 0; x < warp; ++x) at += sh[x];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        at += w[i];
+        if (i0 + i < n) F[i0 + i] = at;
+    }
+    __syncthreads();
+}
+// First i with F[i] >= x (n if there is none); every thread searches.
+__device__ __forceinline__ int reach(const u64 *F, int n, u64 x)
+{
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (F[mid] >= x)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo;
+}
+
+// What the slices' headers say of a row; warp 0 reads them.
+struct RowHead {
+    u64 best;
+    uint32_t lowest, theta;
+    int cands;
+};
+__device__ __forceinline__ RowHead row_head(const Header *head, int slices)
+{
+    const int lane = threadIdx.x & 31;
+    RowHead r{0ull, kUnknown, 0u, 0};
+    for (int s = lane; s < slices; s += 32) {
+        const Header &h = head[s];
+        r.best = max(r.best, h.best);
+        r.lowest = min(r.lowest, h.lowest);
+        r.theta = max(r.theta, h.cands > 0 ? h.theta : 0u);
+        r.cands += h.cands;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) r.best = max(r.best, __shfl_xor_sync(0xffffffffu, r.best, o));
+    r.lowest = __reduce_min_sync(0xffffffffu, r.lowest);
+    r.theta = __reduce_max_sync(0xffffffffu, r.theta);
+    r.cands = __reduce_add_sync(0xffffffffu, r.cands);
+    return r;
+}
+
+// ---------------------------------------------------------------- pick
+__global__ void __launch_bounds__(kPickThreads)
+    k_sample_pick(Rows R, Settings S, int32_t *token, float *prob, int *status)
+{
+    __shared__ u64 list[kList], F[kList], sh[kPickThreads / 32];
+    __shared__ RowHead s_head;
+    __shared__ u64 s_sum;
+    __shared__ int s_count;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.x;
+    const Header *head = R.head + static_cast<long long>(row) * R.slices;
+    pdl_wait();
+    pdl_launch_dependents();
+    const float T = temperature(S, row), p = S.top_p ? __ldg(S.top_p + row) : 1.f, mp = S.min_p ? __ldg(S.min_p + row) : 0.f,
+                u = __ldg(S.u + row);
+    const int k = top_k(S, row, R.vocab);
+    if (warp == 0) {
+        const RowHead r = row_head(head, R.slices);
+        // the row's weight from the slices', each in units of its own largest
+        u64 sum = 0;
+        if (r.best != 0 && T > 0.f && k == 0) {
+            const Scale sc = scale_of(T);
+            const int top = exponent(sc, value_of(static_cast<uint32_t>(r.best >> 32)));
+            for (int s = lane; s < R.slices; s += 32) {
+                const unsigned shift = static_cast<unsigned>(top - head[s].exp);
+                if (head[s].cands > 0 && shift < 64) sum += head[s].sum >> shift;
+            }
+        }
+        sum = warp_sum(sum);
+        if (lane == 0) {
+            s_head = r;
+            s_sum = sum;
+            s_count = 0;
+        }
+    }
+    __syncthreads();
+    const RowHead h = s_head;
+    auto answer = [&](int tok, float pr) {
+        if (tid == 0) {
+            token[row] = tok;
+            if (prob) prob[row] = pr;
+            R.deep[row] = 0;
+        }
+    };
+    if (isnan(T) || isnan(p) || isnan(mp)) {
+        if (tid == 0 && status) atomicExch(status, GQ_ERR_SHAPE);
+        return answer(-1, 0.f);
+    }
+    if (h.best == 0) return answer(-1, 0.f);
+    if (!(T > 0.f)) return answer(index_of(h.best), 1.f);
+
+    for (int s = warp; s < R.slices; s += kPickThreads / 32) {
+        const u64 *from = R.list + (static_cast<long long>(row) * R.slices + s) * R.cap;
+        const int n = head[s].cands > 0 ? head[s].count : 0;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const u64 x = i0 + lane < n ? __ldcg(from + i0 + lane) : 0ull;
+            const bool take = static_cast<uint32_t>(x >> 32) >= h.theta;
+            const unsigned who = __ballot_sync(0xffffffffu, take);
+            int at = 0;
+            if (lane == 0 && who) at = atomicAdd(&s_count, __popc(who));
+            at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
+            if (take && at < kList) list[at] = x;
+        }
+    }
+    __syncthreads();
+    const int n = s_count;
+    const bool all = n == h.cands;  // every candidate is in the list
+    bool done = h.theta != kUnknown && n > 0 && n <= kList;
+    if (done) {
+        const int P = padded(n);
+        for (int i = n + tid; i < P; i += kPickThreads) list[i] = 0ull;
+        __syncthreads();
+        sort_down<kPickThreads>(list, P);
+        const float largest = value_of(static_cast<uint32_t>(h.best >> 32));
+        const Scale sc = scale_of(T, largest);
+        const int top = exponent(sc, largest);
+        running_weights<kPickThreads>(list, F, n, 0ull, sc, top, sh);
+        const u64 listed = F[n - 1], last = n > 1 ? listed - F[n - 2] : listed;
+        // the weight of what top_k keeps
+        u64 z = 0;
+        bool known = true;
+        if (k > 0 && k <= n)
+            z = F[k - 1];
+        else if (all || last == 0)  // nothing of weight lies beyond the list
+            z = listed;
+        else if (k == 0 && sc.base == 0.f && !sc.infinite)
+            z = max(s_sum, listed);
+        else
+            known = false;
+        if (known) {
+            u64 kept = z;
+            if (p < 1.f) {
+                const int j = reach(F, n, nucleus(p, z));
+                if (j < n)
+                    kept = min(kept, F[j]);
+                else
+                    known = all || last == 0;
+            }
+            if (mp > 0.f) {
+                bool rest = false;
+                const u64 thr = mp < 1.f ? part_of(mp, F[0], rest) + (rest ? 1 : 0) : F[0];
+                // first of the list below the threshold; the list falls
+                int lo = 0, hi = n;
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (F[mid] - (mid ? F[mid - 1] : 0ull) < thr)
+                        hi = mid;
+                    else
+                        lo = mid + 1;
+                }
+                if (lo < n)
+                    kept = min(kept, F[max(lo, 1) - 1]);
+                else if (!all && kept > listed)
+                    known = false;
+            }
+            const int j = known ? reach(F, n, drawn(u, kept)) : n;
+            if (j < n) return answer(index_of(list[j]), ratio(j ? F[j] - F[j - 1] : F[0], kept));
+        }
+        done = false;
+    }
+    if (tid == 0) R.deep[row] = 1;
+}
+
+// ---------------------------------------------------------------- deep
+struct __align__(16) Part {  // one CTA's part of a pass over the row
+    u64 before, inside, lowest, highest;
+    unsigned count, pad;
+};
+struct DeepShared {
+    u64 list[kList], F[kList];
+    unsigned hist[kBins], coarse[kBins], fine[kBins];  // fine, coarse: running counts
+    float est[kBins];                                  // running estimate of the weight, in units of the largest
+    Part part[kDeepCtas];
+    u64 sh[kDeepThreads / 32];
+    unsigned sh32[kDeepThreads / 32];
+    float shf[kDeepThreads / 32];
+    RowHead head;
+    int found;
+};
+
+template <int TYPE>
+__global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1)
+    k_sample_deep(Rows R, Settings S, int32_t *token, float *prob)
+{
+    extern __shared__ __align__(16) unsigned char raw[];
+    DeepShared &D = *reinterpret_cast<DeepShared *>(raw);
+    constexpr int kVec = Reader<TYPE>::kVec, kPer = kBins / kDeepThreads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (R.deep[row] == 0) return;  // the whole cluster
+    auto cluster = cg::this_cluster();
+    const int me = static_cast<int>(cluster.block_rank());
+    const float T = temperature(S, row), p = S.top_p ? __ldg(S.top_p + row) : 1.f, mp = S.min_p ? __ldg(S.min_p + row) : 0.f,
+                u = __ldg(S.u + row);
+    const int k = top_k(S, row, R.vocab);
+    if (warp == 0) {
+        const RowHead r = row_head(R.head + static_cast<long long>(row) * R.slices, R.slices);
+        if (lane == 0) D.head = r;
+    }
+    for (int i = tid; i < kBins; i += kDeepThreads) D.hist[i] = 0;
+    __syncthreads();
+    const RowHead h = D.head;
+    const float largest = value_of(static_cast<uint32_t>(h.best >> 32));
+    const Scale sc = scale_of(T, largest);
+    const int top = exponent(sc, largest);
+    // steps of the exponent; everything 50 octaves down is one step
+    const float t_top = (largest - sc.base) * sc.ch, t_low = (value_of(h.lowest) - sc.base) * sc.ch;
+    const float range = fminf(fmaxf(t_top - t_low, 0.001f), 50.f), per = kBins / range;
+    auto step_of = [&](float v) { return min(kBins - 1, __float2int_rz((t_top - (v - sc.base) * sc.ch) * per)); };
+
+    const Reader<TYPE> in(R.logits + row * R.row_bytes, R.vocab);
+    const int cta_units = (in.units + kDeepCtas - 1) / kDeepCtas, first = me * cta_units, end = min(first + cta_units, in.units);
+    auto each = [&](auto &&f) {  // every candidate of this CTA's part of the row
+        for (int q = first + tid; q < end; q += kDeepThreads) {
+            float v[kVec];
+            in.load(q, v);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                if (v[i] > -INFINITY) f(v[i], in.index(q, i));
+        }
+    };
+    // The CTAs' parts, added up in every CTA.
+    auto exchange = [&](Part x) {
+        __syncthreads();
+        x.before = cta_sum<kDeepThreads>(x.before, D.sh);
+        x.inside = cta_sum<kDeepThreads>(x.inside, D.sh);
+        cluster.sync();
+        if (tid < kDeepCtas) *cluster.map_shared_rank(&D.part[me], tid) = x;
+        cluster.sync();
+        Part s{0, 0, ~0ull, 0, 0, 0};
+        for (int c = 0; c < kDeepCtas; ++c) {
+            s.before += D.part[c].before;
+            s.inside += D.part[c].inside;
+            s.lowest = min(s.lowest, D.part[c].lowest);
+            s.highest = max(s.highest, D.part[c].highest);
+            s.count += D.part[c].count;
+        }
+        return s;
+    };
+    // The CTAs' histograms, added up and summed over the steps, in `out` of every CTA.
+    auto merge = [&](unsigned *out) {
+        cluster.sync();
+        constexpr int kShare = kBins / kDeepCtas;
+        for (int i = tid; i < kShare; i += kDeepThreads) {
+            unsigned s = 0;
+            for (int c = 0; c < kDeepCtas; ++c) s += cluster.map_shared_rank(D.hist, c)[me * kShare + i];
+            for (int c = 0; c < kDeepCtas; ++c) cluster.map_shared_rank(out, c)[me * kShare + i] = s;
+        }
+        cluster.sync();
+        unsigned n[kPer], mine = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) mine += n[i] = out[tid * kPer + i];
+        unsigned incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31) D.sh32[warp] = incl;
+        __syncthreads();
+        unsigned at = incl - mine;
+        for (int w = 0; w < warp; ++w) at += D.sh32[w];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) out[tid * kPer + i] = at += n[i];
+        __syncthreads();
+    };
+    // First step for which `ok` holds (it holds from some step on), else the last.
+    auto first_step = [&](auto &&ok) {
+        if (tid == 0) D.found = kBins - 1;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int b = tid * kPer + i;
+            if (ok(b) && (b == 0 || !ok(b - 1))) atomicMin(&D.found, b);
+        }
+        __syncthreads();
+        const int b = D.found;
+        __syncthreads();
+        return b;
+    };
+
+    // ---- the row's weight, and the histogram
+    bool rest = false;
+    const u64 w0 = row_weight(sc, largest, top);
+    const u64 thr = mp < 1.f ? (mp > 0.f ? part_of(mp, w0, rest) + (rest ? 1 : 0) : 0ull) : w0;
+    Part x{0, 0, 0, 0, 0, 0};
+    each([&](float v, int) {
+        atomicAdd(&D.hist[step_of(v)], 1u);
+        const u64 w = row_weight(sc, v, top);
+        x.before += w;
+        x.inside += w >= thr ? w : 0ull;
+    });
+    const Part sums = exchange(x);
+    merge(D.coarse);
+    {
+        float e[kPer], mine = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int b = tid * kPer + i;
+            mine += static_cast<float>(D.coarse[b] - (b ? D.coarse[b - 1] : 0u)) * exp2f(-(b + 0.5f) / per);
+            e[i] = mine;
+        }
+        float incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31) D.shf[warp] = incl;
+        __syncthreads();
+        float at = incl - mine;
+        for (int w = 0; w < warp; ++w) at += D.shf[w];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) D.est[tid * kPer + i] = at + e[i];
+        __syncthreads();
+    }
+
+    // ---- the first element at which the running count (by_count) or weight reaches X: its place in the sorted
+    // list, with the running weights in F
+    auto find = [&](u64 X, bool by_count) {
+        bool nested = false;
+        u64 high = 0, low = 0;  // nested: the elements between
+        int shift = 0;
+        u64 base = 0;           // weight in front of the steps
+        const unsigned *C = D.coarse;
+        const float target = __ull2float_rn(X) * (D.est[kBins - 1] / __ull2float_rn(max(sums.before, 1ull)));
+        int b = by_count ? first_step([&](int i) { return C[i] >= X; }) : first_step([&](int i) { return D.est[i] >= target; });
+        int lo = 0, hi = kBins - 1;
+        for (int tries = 0;; ++tries) {
+            const unsigned in_step = C[b] - (b ? C[b - 1] : 0u);
+            // -1: in front of the step, 0: in it, 1: behind
+            auto side = [&](float v, int e) {
+                int s;
+                if (!nested) {
+                    s = step_of(v);
+                } else {
+                    const u64 r = rank_of(key_of(v), e);
+                    if (r > high || r < low) return 1;  // in front of all steps: in `base`
+                    s = static_cast<int>((high - r) >> shift);
+                }
+                return s < b ? -1 : (s > b ? 1 : 0);
+            };
+            Part y{0, 0, ~0ull, 0, 0, 0};
+            const bool listable = in_step <= kList;
+            u64 *mine = D.F;  // this CTA's part of the list
+            __syncthreads();
+            if (tid == 0) D.found = 0;
+            __syncthreads();
+            u64 least = ~0ull, most = 0;
+            each([&](float v, int e) {
+                const int s = side(v, e);
+                if (s > 0) return;
+                const u64 w = row_weight(sc, v, top);
+                if (s < 0) {
+                    y.before += w;
+                    return;
+                }
+                y.inside += w;
+                const u64 r = rank_of(key_of(v), e);
+                if (listable)
+                    mine[atomicAdd(&D.found, 1)] = r;
+                least = min(least, r);
+                most = max(most, r);
+            });
+            // the CTA's lowest and highest
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+                most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+            }
+            __syncthreads();
+            const int mine_n = D.found;
+            if (lane == 0) D.sh[warp] = least;
+            __syncthreads();
+            for (int w = 0; w < kDeepThreads / 32; ++w) least = min(least, D.sh[w]);
+            __syncthreads();
+            if (lane == 0) D.sh[warp] = most;
+            __syncthreads();
+            for (int w = 0; w < kDeepThreads / 32; ++w) most = max(most, D.sh[w]);
+            y.lowest = least;
+            y.highest = most;
+            y.count = listable ? static_cast<unsigned>(mine_n) : 0u;
+            const Part all = exchange(y);
+            const u64 before = base + all.before;
+            if (!by_count) {  // was the estimate right?
+                int move = before >= X ? -1 : (before + all.inside < X ? 1 : 0);
+                if (move < 0) hi = b - 1;
+                if (move > 0) lo = b + 1;
+                if (move != 0 && lo <= hi) {
+                    b = tries < 4 ? b + move : (lo + hi) / 2;
+                    continue;
+                }
+            }
+            if (listable) {
+                int at = 0;
+                for (int c = 0; c < me; ++c) at += static_cast<int>(D.part[c].count);
+                for (int i = tid; i < mine_n; i += kDeepThreads) {
+                    const u64 r = mine[i];
+                    for (int c = 0; c < kDeepCtas; ++c) cluster.map_shared_rank(D.list, c)[at + i] = r;
+                }
+                cluster.sync();
+                const int n = static_cast<int>(all.count), P = padded(n);
+                for (int i = n + tid; i < P; i += kDeepThreads) D.list[i] = 0ull;
+                __syncthreads();
+                sort_down<kDeepThreads>(D.list, P);
+                running_weights<kDeepThreads>(D.list, D.F, n, before, sc, top, D.sh);
+                const int j = by_count ? static_cast<int>(X - (b ? C[b - 1] : 0u)) - 1 : reach(D.F, n, X);
+                return max(min(j, n - 1), 0);
+            }
+            // too many for the list: divide the step by the bits of its elements
+            if (by_count) X -= b ? C[b - 1] : 0u;
+            base = before;
+            high = all.highest;
+            low = all.lowest;
+            shift = max(0, 53 - __clzll(static_cast<long long>(high - low)));
+            nested = true;
+            __syncthreads();
+            for (int i = tid; i < kBins; i += kDeepThreads) D.hist[i] = 0;
+            __syncthreads();
+            each([&](float v, int e) {
+                const u64 r = rank_of(key_of(v), e);
+                if (r <= high && r >= low) atomicAdd(&D.hist[(high - r) >> shift], 1u);
+            });
+            merge(D.fine);
+            C = D.fine;
+            // the step's weights are nearly equal
+            const float want = by_count ? 0.f
+                                        : __ull2float_rn(X - before) / fmaxf(__ull2float_rn(all.inside), 1.f) * static_cast<float>(in_step);
+            b = by_count ? first_step([&](int i) { return C[i] >= X; })
+                         : first_step([&](int i) { return static_cast<float>(C[i]) >= want; });
+            lo = 0;
+            hi = kBins - 1;
+            tries = -1;
+        }
+    };
+
+    u64 kept = sums.before;
+    if (k > 0 && k < h.cands) {
+        const int j = find(static_cast<u64>(k), true);
+        kept = D.F[j];
+    }
+    const u64 z = kept;
+    if (mp > 0.f) kept = min(kept, sums.inside);
+    if (p < 1.f) {
+        const int j = find(nucleus(p, z), false);
+        kept = min(kept, D.F[j]);
+    }
+    const u64 X = drawn(u, kept);
+    const int j = find(X, false);
+    if (me == 0 && tid == 0) {
+        // the weight of the drawn one: `find` left its list and the running weights
+        token[row] = index_of(D.list[j]);
+        if (prob) prob[row] = ratio(row_weight(sc, value_of(static_cast<uint32_t>(D.list[j] >> 32)), top), kept);
+    }
+    cluster.sync();  // no CTA leaves while another reads its memory
+}
+
+// ---------------------------------------------------------------- host
+// Slices of 4096 elements while they all fit the GPU at once, of 16384 else: a
+// small batch is latency, and a large one wants long streams per CTA.
+struct Plan {
+    int ept, slices, cap, want;
+};
+Plan plan_for(int vocab, int n_rows)
+{
+    Plan p;
+    const long long fine = (vocab + 7 + 4095) / 4096;
+    p.ept = fine * n_rows <= 608 ? 8 : 32;
+    const int per = kScanThreads * p.ept;
+    p.slices = (vocab + 7 + per - 1) / per;
+    // lists of some 1024 elements a row in all, with room for four times as many
+    const int cap = 4096 / p.slices;
+    p.cap = cap < 64 ? 64 : (cap > kList ? kList : cap);
+    const int want = 1024 / p.slices;
+    p.want = want < 4 ? 4 : (want > 256 ? 256 : want);
+    return p;
+}
+size_t up16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
+
+template <int TYPE>
+cudaError_t launch(Rows R, const Settings &S, const Plan &p, int n_rows, int32_t *token, float *prob, cudaStream_t s)
+{
+    auto deep = k_sample_deep<TYPE>;
+    if (ctas_per_sm(reinterpret_cast<const void *>(deep), kDeepThreads, sizeof(DeepShared)) < 1) return cudaErrorInvalidConfiguration;
+    const dim3 grid(p.slices, n_rows);
+    cudaError_t e = p.ept == 8 ? launch_pdl(k_sample_scan<TYPE, 8>, grid, dim3(kScanThreads), 0, s, R, S, p.want)
+                               : launch_pdl(k_sample_scan<TYPE, 32>, grid, dim3(kScanThreads), 0, s, R, S, p.want);
+    if (e == cudaSuccess) e = launch_pdl(k_sample_pick, dim3(n_rows), dim3(kPickThreads), 0, s, R, S, token, prob, status_word());
+    if (e == cudaSuccess) e = launch_pdl(deep, dim3(kDeepCtas, n_rows), dim3(kDeepThreads), sizeof(DeepShared), s, R, S, token, prob);
+    return e;
+}
+
+inline bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+}  // namespace
+}  // namespace gq
+
+using namespace gq;
+
+extern "C" {
+
+size_t gq_sample_workspace_bytes(int vocab, int n_rows)
+{
+    if (vocab < 1 || vocab > GQ_MAX_VOCAB || n_rows < 1 || n_rows > 65535) return 0;
+    const Plan p = plan_for(vocab, n_rows);
+    const size_t slices = static_cast<size_t>(p.slices) * n_rows;
+    return slices * sizeof(Header) + slices * p.cap * sizeof(u64) + up16(static_cast<size_t>(n_rows) * sizeof(int));
+}
+
+int gq_sample(const void *logits, long long ldl, int type, const float *temperature, const int32_t *top_k,
+              const float *top_p, const float *min_p, const float *u, int32_t *token, float *prob_or_null,
+              void *workspace, size_t workspace_bytes, int vocab, int n_rows, gq_stream_t stream)
+{
+    if (type != GQ_TYPE_F32 && type != GQ_TYPE_F16 && type != GQ_TYPE_BF16) return GQ_ERR_FORMAT;
+    if (vocab < 1 || vocab > GQ_MAX_VOCAB || n_rows < 0 || n_rows > 65535 || ldl < vocab || ldl > (1ll << 40)) return GQ_ERR_SHAPE;
+    if (n_rows == 0) return GQ_OK;
+    if (!logits || !u || !token) return GQ_ERR_NULL;
+    if (!aligned_to(logits, kv::type_size(type)) || !aligned_to(temperature, 4) || !aligned_to(top_k, 4) || !aligned_to(top_p, 4) ||
+        !aligned_to(min_p, 4) || !aligned_to(u, 4) || !aligned_to(token, 4) || !aligned_to(prob_or_null, 4))
+        return GQ_ERR_ALIGN;
+    if (!workspace || workspace_bytes < gq_sample_workspace_bytes(vocab, n_rows)) return GQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return GQ_ERR_ALIGN;
+    const Plan p = plan_for(vocab, n_rows);
+    const size_t slices = static_cast<size_t>(p.slices) * n_rows;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const Rows R{static_cast<const uint8_t *>(logits),
+                 ldl * kv::type_size(type),
+                 vocab,
+                 p.slices,
+                 p.cap,
+                 reinterpret_cast<Header *>(ws),
+                 reinterpret_cast<u64 *>(ws + slices * sizeof(Header)),
+                 reinterpret_cast<int *>(ws + slices * sizeof(Header) + slices * p.cap * sizeof(u64))};
+    const Settings S{temperature, top_k, top_p, min_p, u};
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    switch (type) {
+    case GQ_TYPE_F32: return status_from(launch<GQ_TYPE_F32>(R, S, p, n_rows, token, prob_or_null, s));
+    case GQ_TYPE_F16: return status_from(launch<GQ_TYPE_F16>(R, S, p, n_rows, token, prob_or_null, s));
+    default: return status_from(launch<GQ_TYPE_BF16>(R, S, p, n_rows, token, prob_or_null, s));
+    }
+}
+
+}  // extern "C"
