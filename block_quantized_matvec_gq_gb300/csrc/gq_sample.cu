@@ -663,9 +663,11 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
     const Scale sc = scale_of(T, largest);
     const int top = exponent(sc, largest);
     // steps of the exponent; everything 50 octaves down is one step
-    const float t_top = (largest - sc.base) * sc.ch, t_low = (value_of(h.lowest) - sc.base) * sc.ch;
-    const float range = fminf(fmaxf(t_top - t_low, 0.001f), 50.f), per = kBins / range;
-    auto step_of = [&](float v) { return min(kBins - 1, __float2int_rz((t_top - (v - sc.base) * sc.ch) * per)); };
+    // (the products rounded alike: fused with the difference they would leave the largest's rounding, of either sign)
+    auto exponent_of = [&](float v) { return __fmul_rn(v - sc.base, sc.ch); };
+    const float t_top = exponent_of(largest);
+    const float range = fminf(fmaxf(t_top - exponent_of(value_of(h.lowest)), 0.001f), 50.f), per = kBins / range;
+    auto step_of = [&](float v) { return max(0, min(kBins - 1, __float2int_rz((t_top - exponent_of(v)) * per))); };
 
     const Reader<TYPE> in(R.logits + row * R.row_bytes, R.vocab);
     const int cta_units = (in.units + kDeepCtas - 1) / kDeepCtas, first = me * cta_units, end = min(first + cta_units, in.units);

@@ -45,10 +45,11 @@ extern "C" {
  * more, counts as none, and the device status (gq_device_status) becomes
  * GQ_ERR_SHAPE.
  *
- * Accuracy: sums are f32.  With v = A_a x, |error| <= 2^-24 |Y| +
- *   |scale| sum_j |B_ij| (2^-19 sum_k |A_jk x_k|)
- * (operands of 22 bits or more; the f32 sums of the tensor cores are
- * truncated), and within 1e-6 of the added term in the 2-norm.  A non-finite
+ * Accuracy: |error| <= 2^-24 |Y| +
+ *   (2^-17 + 2^-32 K) |scale| sum_j |B_ij| sum_k |A_jk x_k|
+ * (operands of 22 bits or more, f32 sums, those of the tensor cores truncated;
+ * this is every rounding at its worst), and within 1e-6 of the added term in
+ * the 2-norm.  A non-finite
  * x, A or B gives non-finite sums where the definition's are (NaN possibly for
  * an infinity), for the tokens of that adapter and that row alone.
  * Deterministic for the same arguments.

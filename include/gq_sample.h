@@ -35,7 +35,7 @@ extern "C" {
  * gives token -1 and prob 0.  u counts as brought into [0, 1]: a u of 1 or more
  * gives the last kept, a NaN or a negative one the first.  T below 2^-100
  * counts as 2^-100; an infinite T gives equal weights.  If the largest logit
- * is +infinity the infinite ones share the weight.  A NaN among T, top_p or
+ * is +infinity the infinite ones share the weight, whatever T is.  A NaN among T, top_p or
  * min_p gives token -1, prob 0 and GQ_ERR_SHAPE in the device status
  * (gq_device_status).
  *   logits  n_rows rows of vocab elements of `type` (GQ_TYPE_*), ldl elements
