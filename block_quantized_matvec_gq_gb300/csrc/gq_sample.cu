@@ -31,6 +31,7 @@
 // What bounds it: the one pass over the logits, and for small batches the
 // latency of the three kernels.
 #include <cooperative_groups.h>
+#include <limits.h>
 #include <math.h>
 
 #include "gq_host.h"
@@ -44,11 +45,12 @@ namespace {
 namespace cg = cooperative_groups;
 using u64 = unsigned long long;
 
-constexpr int kScanThreads = 512;
+constexpr int kScanThreads = 256;
 constexpr int kPickThreads = 1024;
 constexpr int kDeepThreads = 512;
 constexpr int kDeepCtas = 8;
 constexpr int kList = 2048;  // elements that are sorted at once
+constexpr int kMaxSlices = 640;
 constexpr int kBins = 2048;
 constexpr uint32_t kNone = 0x007FFFFFu;        // key of -infinity: no candidate
 constexpr uint32_t kUnknown = 0xFFFFFFFFu;     // threshold of a slice whose list is empty
@@ -73,16 +75,16 @@ struct __align__(16) Header {
 struct Rows {
     const uint8_t *logits;
     long long row_bytes;
-    int vocab, slices, cap;
+    int vocab, slices, cap, cap_log2;
     Header *head;
     u64 *list;
     int *deep;  // rows for the third kernel
 };
 
-// Order-preserving bits of a logit (neither NaN nor -0).
+// Order-preserving bits of a logit that is not a NaN; -0 is 0.
 __device__ __forceinline__ uint32_t key_of(float v)
 {
-    const uint32_t b = __float_as_uint(v);
+    const uint32_t b = __float_as_uint(v + 0.f);
     return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu)); }
@@ -118,24 +120,45 @@ __device__ __forceinline__ Scale scale_of(float T, float largest)
 }
 
 // Exponent A (rounded) and mantissa M in [2^30.5, 2^31.5]: weight M 2^(A - 31).
-// 2^f - 1 for |f| <= 1/2 by its Taylor series (the next term is below 2^-32),
-// the leading coefficient in two parts: within 2^-25 of the weight.
+// 2^f - 1 = f P(f) for |f| <= 1/2, P of degree 5 through the values at the six
+// Chebyshev points of the interval (2^-27.5 from it), its leading coefficient
+// in two parts: M is within 2^-24.9 of the weight, 2^-33 on average.
+constexpr float kP5 = 1.545316336e-04f, kP4 = 1.339086331e-03f, kP3 = 9.618083015e-03f, kP2 = 5.550356954e-02f,
+                kP1 = 2.402265072e-01f, kP0 = 6.931471825e-01f, kP0Low = 5.561629e-09f;
 __device__ __forceinline__ void split(const Scale &s, float l, int &A, uint32_t &M)
 {
     const float d = l - s.base;
     const float r = fmaxf(d * s.ch, kFarDown) + kRound;
     A = __float_as_int(r) - __float_as_int(kRound);
     const float f = fmaf(d, s.cl, fmaf(d, s.ch, kRound - r));
-    float p = 1.32154868e-6f;             // ln2^8 / 8!
-    p = fmaf(p, f, 1.52527338e-5f);       // ln2^7 / 7!
-    p = fmaf(p, f, 1.54035304e-4f);
-    p = fmaf(p, f, 1.33335581e-3f);
-    p = fmaf(p, f, 9.61812911e-3f);
-    p = fmaf(p, f, 5.55041087e-2f);
-    p = fmaf(p, f, 2.40226507e-1f);       // ln2^2 / 2!
-    p = fmaf(p, f, -1.90465421e-9f);      // ln2 - its f32
-    const float e = fmaf(f, 6.93147182e-1f, f * p);
+    float p = fmaf(kP5, f, kP4);
+    p = fmaf(p, f, kP3);
+    p = fmaf(p, f, kP2);
+    p = fmaf(p, f, kP1);
+    p = fmaf(p, f, kP0Low);
+    const float e = fmaf(f, kP0, f * p);
     M = 0x80000000u + static_cast<uint32_t>(__float2int_rn(e * 2147483648.0f));
+}
+__device__ __forceinline__ u64 shifted(uint32_t M, unsigned sh) { return sh < 64 ? (static_cast<u64>(M) << 12) >> sh : 0ull; }
+// Sum of two weights for base = 0, the same operations in pairs.
+__device__ __forceinline__ u64 weights2(const Scale &s, float a, float b, int top)
+{
+    const float2 ch = make_float2(s.ch, s.ch), cl = make_float2(s.cl, s.cl), l = make_float2(a, b),
+                 round = make_float2(kRound, kRound);
+    float2 r = __fmul2_rn(l, ch);
+    r = __fadd2_rn(make_float2(fmaxf(r.x, kFarDown), fmaxf(r.y, kFarDown)), round);
+    const int A0 = __float_as_int(r.x) - __float_as_int(kRound), A1 = __float_as_int(r.y) - __float_as_int(kRound);
+    const float2 n = __ffma2_rn(r, make_float2(-1.f, -1.f), round);
+    const float2 f = __ffma2_rn(l, cl, __ffma2_rn(l, ch, n));
+    float2 p = __ffma2_rn(make_float2(kP5, kP5), f, make_float2(kP4, kP4));
+    p = __ffma2_rn(p, f, make_float2(kP3, kP3));
+    p = __ffma2_rn(p, f, make_float2(kP2, kP2));
+    p = __ffma2_rn(p, f, make_float2(kP1, kP1));
+    p = __ffma2_rn(p, f, make_float2(kP0Low, kP0Low));
+    const float2 e = __ffma2_rn(f, make_float2(kP0, kP0), __fmul2_rn(f, p));
+    const float2 x = __fmul2_rn(e, make_float2(2147483648.0f, 2147483648.0f));
+    return shifted(0x80000000u + static_cast<uint32_t>(__float2int_rn(x.x)), static_cast<unsigned>(top - A0)) +
+           shifted(0x80000000u + static_cast<uint32_t>(__float2int_rn(x.y)), static_cast<unsigned>(top - A1));
 }
 // Weight in units of 2^(top - 43).
 __device__ __forceinline__ u64 weight(const Scale &s, float l, int top)
@@ -143,8 +166,7 @@ __device__ __forceinline__ u64 weight(const Scale &s, float l, int top)
     int A;
     uint32_t M;
     split(s, l, A, M);
-    const unsigned sh = static_cast<unsigned>(top - A);
-    return sh < 64 ? (static_cast<u64>(M) << 12) >> sh : 0ull;
+    return shifted(M, static_cast<unsigned>(top - A));
 }
 __device__ __forceinline__ int exponent(const Scale &s, float l)
 {
@@ -217,7 +239,7 @@ struct Reader {
         units = (n + shift + kVec - 1) / kVec;
     }
     __device__ __forceinline__ int index(int unit, int i) const { return unit * kVec + i - shift; }
-    // Candidates as they are, -0 as 0, NaN and what lies outside as -infinity.
+    // Candidates as they are, NaN and what lies outside as -infinity.
     __device__ __forceinline__ void load(int unit, float (&v)[kVec]) const
     {
         const uint8_t *p = base + static_cast<long long>(unit) * 16;
@@ -247,7 +269,7 @@ struct Reader {
             }
         }
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) v[i] = fmaxf(v[i] + 0.f, -INFINITY);
+        for (int i = 0; i < kVec; ++i) v[i] = fmaxf(v[i], -INFINITY);
     }
 };
 
@@ -277,29 +299,20 @@ __device__ __forceinline__ u64 cta_sum(u64 v, u64 *sh)
     for (int w = 0; w < THREADS / 32; ++w) s += sh[w];
     return s;
 }
-template <int THREADS>
-__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t *sh)
-{
-    v = __reduce_max_sync(0xffffffffu, v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    uint32_t m = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) m = max(m, sh[w]);
-    return m;
-}
 
 // ---------------------------------------------------------------- scan
 template <int TYPE, int EPT>
 __global__ void __launch_bounds__(kScanThreads) k_sample_scan(Rows R, Settings S, int want)
 {
-    constexpr int kVec = Reader<TYPE>::kVec, kUnits = EPT / kVec;
-    __shared__ u64 sh64[kScanThreads / 32];
-    __shared__ uint32_t sh32[kScanThreads / 32];
-    __shared__ int s_count;
-    const int tid = threadIdx.x, row = blockIdx.y, slice = blockIdx.x;
-    if (tid == 0) s_count = 0;
+    constexpr int kVec = Reader<TYPE>::kVec, kUnits = EPT / kVec, kWarps = kScanThreads / 32;
+    __shared__ u64 s_sum[kWarps];
+    __shared__ uint32_t s_hi[kWarps], s_lo[kWarps];
+    __shared__ int s_cands[kWarps], s_count, s_first;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y, slice = blockIdx.x;
+    if (tid == 0) {
+        s_count = 0;
+        s_first = INT_MAX;
+    }
     pdl_wait();
     pdl_launch_dependents();
     const Reader<TYPE> in(R.logits + row * R.row_bytes, R.vocab);
@@ -310,32 +323,56 @@ __global__ void __launch_bounds__(kScanThreads) k_sample_scan(Rows R, Settings S
     const float T = temperature(S, row);
     const int k = top_k(S, row, R.vocab);
     float hi = -INFINITY, lo = INFINITY;
-    int cands = 0;
 #pragma unroll
     for (int j = 0; j < kUnits; ++j)
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             hi = fmaxf(hi, v[j][i]);
-            const bool c = v[j][i] > -INFINITY;
-            lo = c ? fminf(lo, v[j][i]) : lo;
-            cands += c ? 1 : 0;
+            lo = fminf(lo, v[j][i]);
         }
-    const uint32_t mine = key_of(hi), top = cta_max<kScanThreads>(mine, sh32);
-    const float best = value_of(top);
+    int cands = EPT;
+    if (lo == -INFINITY) {  // masked tokens, or the row's ends
+        lo = INFINITY;
+        cands = 0;
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                if (v[j][i] > -INFINITY) {
+                    lo = fminf(lo, v[j][i]);
+                    ++cands;
+                }
+    }
+    const uint32_t mine = key_of(hi);
+    {
+        const uint32_t a = __reduce_max_sync(0xffffffffu, mine), b = __reduce_min_sync(0xffffffffu, lo < INFINITY ? key_of(lo) : kUnknown);
+        const int c = __reduce_add_sync(0xffffffffu, cands);
+        if (lane == 0) {
+            s_hi[warp] = a;
+            s_lo[warp] = b;
+            s_cands[warp] = c;
+        }
+    }
+    __syncthreads();
     Header h{};
-    // the slice's first of the order: the lowest index among its largest
-    uint32_t at = 0;
-    if (mine == top) {
+    uint32_t top = 0;
+    h.lowest = kUnknown;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        top = max(top, s_hi[w]);
+        h.lowest = min(h.lowest, s_lo[w]);
+        h.cands += s_cands[w];
+    }
+    const float best = value_of(top);
+    if (mine == top) {  // the slice's first of the order: the lowest index among its largest
+        int first = INT_MAX;
 #pragma unroll
         for (int j = kUnits - 1; j >= 0; --j)
 #pragma unroll
             for (int i = kVec - 1; i >= 0; --i)
-                if (v[j][i] == best) at = ~static_cast<uint32_t>(in.index(u0 + j * kScanThreads, i));
+                if (v[j][i] == best) first = in.index(u0 + j * kScanThreads, i);
+        atomicMin(&s_first, first);
     }
-    at = cta_max<kScanThreads>(at, sh32);
-    h.best = top > kNone ? static_cast<u64>(top) << 32 | at : 0ull;
-    h.lowest = ~cta_max<kScanThreads>(lo < INFINITY ? ~key_of(lo) : 0u, sh32);
-    h.cands = static_cast<int>(cta_sum<kScanThreads>(static_cast<u64>(cands), sh64));
     h.theta = kUnknown;
     if (T > 0.f && top > kNone) {  // otherwise the first of the order is all that is asked for
         const Scale sc = scale_of(T);
@@ -345,17 +382,24 @@ __global__ void __launch_bounds__(kScanThreads) k_sample_scan(Rows R, Settings S
 #pragma unroll
             for (int j = 0; j < kUnits; ++j)
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) sum += weight(sc, v[j][i], h.exp);
-            h.sum = cta_sum<kScanThreads>(sum, sh64);
+                for (int i = 0; i < kVec; i += 2) sum += weights2(sc, v[j][i], v[j][i + 1], h.exp);
+            sum = warp_sum(sum);
+            if (lane == 0) s_sum[warp] = sum;
         }
-        if (h.cands <= R.cap) {
-            h.theta = kNone + 1;
-            h.count = h.cands;
-        } else {
+        uint32_t a = kNone + 1;
+        if (h.cands > R.cap) {
             // a threshold that `w` threads reach and few elements more
             const int threads = __syncthreads_count(mine > kNone);
             const int w = max(1, min(k > 0 ? min(want, 2 * k / static_cast<int>(gridDim.x) + 8) : want, threads / 2));
-            uint32_t a = kNone + 1, b = top;  // w threads reach a; look in a .. b
+            uint32_t b = top;  // w threads reach a; look in a .. b
+            if (threads == kScanThreads) {  // all threads reach the least of their maxima
+                uint32_t m = __reduce_min_sync(0xffffffffu, mine);
+                if (lane == 0) s_lo[warp] = m;
+                __syncthreads();
+                a = b;
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) a = min(a, s_lo[x]);
+            }
             while (a < b) {
                 const uint32_t mid = a + (b - a) / 2 + 1;
                 const int n = __syncthreads_count(mine >= mid);
@@ -365,43 +409,53 @@ __global__ void __launch_bounds__(kScanThreads) k_sample_scan(Rows R, Settings S
                     b = mid - 1;
                 if (n >= w && n <= w + w / 4) break;
             }
-            u64 counts = 0;  // elements at a or above, and above a
+        }
+        u64 *list = R.list + (static_cast<long long>(row) * R.slices + slice) * R.cap;
+        auto put = [&](uint32_t least) {  // the elements from `least` on, as far as there is room
+            if (mine < least) return;
+            const float from = value_of(least);
 #pragma unroll
             for (int j = 0; j < kUnits; ++j)
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) {
-                    const uint32_t x = key_of(v[j][i]);
-                    counts += (x >= a ? 1ull : 0ull) + (x > a ? 1ull << 32 : 0ull);
-                }
-            counts = cta_sum<kScanThreads>(counts, sh64);
-            const int ge = static_cast<int>(counts & 0xFFFFFFFFu), gt = static_cast<int>(counts >> 32);
-            if (ge <= R.cap) {
-                h.theta = a;
-                h.count = ge;
-            } else if (gt <= R.cap) {  // many equal ones at the threshold: leave them out
+                for (int i = 0; i < kVec; ++i)
+                    if (v[j][i] >= from) {
+                        const int at = atomicAdd(&s_count, 1);
+                        if (at < R.cap) list[at] = rank_of(key_of(v[j][i]), in.index(u0 + j * kScanThreads, i));
+                    }
+        };
+        put(a);
+        __syncthreads();
+        h.count = s_count;
+        if (h.count <= R.cap) {
+            h.theta = a;
+        } else {  // many equal ones at the threshold: leave them out
+            __syncthreads();
+            if (tid == 0) s_count = 0;
+            __syncthreads();
+            if (a < top) put(a + 1);
+            __syncthreads();
+            h.count = s_count;
+            if (a < top && h.count <= R.cap)
                 h.theta = a + 1;
-                h.count = gt;
-            }
+            else
+                h.count = 0;
         }
-        if (h.theta != kUnknown && mine >= h.theta) {
-            u64 *list = R.list + (static_cast<long long>(row) * R.slices + slice) * R.cap;
+        if (k == 0)
 #pragma unroll
-            for (int j = 0; j < kUnits; ++j)
-#pragma unroll
-                for (int i = 0; i < kVec; ++i) {
-                    const uint32_t x = key_of(v[j][i]);
-                    if (x >= h.theta) list[atomicAdd(&s_count, 1)] = rank_of(x, in.index(u0 + j * kScanThreads, i));
-                }
-        }
+            for (int w = 0; w < kWarps; ++w) h.sum += s_sum[w];
     }
-    if (tid == 0) R.head[static_cast<long long>(row) * R.slices + slice] = h;
+    __syncthreads();
+    if (tid == 0) {
+        h.best = top > kNone ? rank_of(top, s_first) : 0ull;
+        R.head[static_cast<long long>(row) * R.slices + slice] = h;
+    }
 }
 
 // ---------------------------------------------------------------- sorted lists
 // Falling bitonic sort of n (a power of two, 64 .. kList) numbers.  Steps of 32
 // or less stay within a warp's own 64 numbers.
 template <int THREADS>
-__device__ __forceinline__ void sort_down(u64 *a, int n)
+__device__ __forceinline__ void bitonic_down(u64 *a, int n)
 {
     for (int size = 2; size <= n; size <<= 1)
         for (int step = size >> 1; step > 0; step >>= 1) {
@@ -421,11 +475,80 @@ __device__ __forceinline__ void sort_down(u64 *a, int n)
         }
     __syncthreads();
 }
-__device__ __forceinline__ int padded(int n)
+// Falling sort of the n numbers of `list` (distinct, values between those of
+// `high` and `low`), with `tmp` as long and kList counters: dealt into kList
+// equal steps of the value, then every number finds its place among its step's
+// few.  2048 numbers: 1.5 us, against 7 of the bitonic sort, which remains for
+// lists with more than kCrowd in one step (ties, far outliers).
+constexpr int kCrowd = 96;
+template <int THREADS>
+__device__ __forceinline__ void sort_down(u64 *list, u64 *tmp, unsigned *count, int n, float high, float low, unsigned *sh)
 {
-    int p = 64;
-    while (p < n) p <<= 1;
-    return p;
+    constexpr int kPer = kList / THREADS;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const float per = (kList - 1) / fmaxf(high - low, 1e-30f);
+    auto step_of = [&](u64 r) {
+        const float x = (high - value_of(static_cast<uint32_t>(r >> 32))) * per;
+        return max(0, min(kList - 1, __float2int_rz(x)));
+    };
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) count[tid + i * THREADS] = 0;
+    __syncthreads();
+    u64 r[kPer];
+    int step[kPer];
+    unsigned pos[kPer], most = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int x = tid + i * THREADS;
+        if (x < n) {
+            r[i] = list[x];
+            step[i] = step_of(r[i]);
+            pos[i] = atomicAdd(&count[step[i]], 1u);
+            most = max(most, pos[i] + 1);
+        }
+    }
+    __syncthreads();
+    // running counts, in place: count[s] = numbers in front of step s
+    unsigned c[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += c[i] = count[tid * kPer + i];
+    unsigned incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) sh[warp] = incl;
+    const bool crowded = __syncthreads_or(most > kCrowd);
+    if (crowded) {
+        int P = 64;
+        while (P < n) P <<= 1;
+        for (int i = n + tid; i < P; i += THREADS) list[i] = 0ull;
+        __syncthreads();
+        bitonic_down<THREADS>(list, P);
+        return;
+    }
+    unsigned at = incl - sum;
+    for (int w = 0; w < warp; ++w) at += sh[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        count[tid * kPer + i] = at;
+        at += c[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (tid + i * THREADS < n) tmp[count[step[i]] + pos[i]] = r[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (tid + i * THREADS < n) {
+            const int from = count[step[i]], to = step[i] + 1 < kList ? count[step[i] + 1] : n;
+            int place = from;
+            for (int j = from; j < to; ++j) place += tmp[j] > r[i] ? 1 : 0;
+            list[place] = r[i];
+        }
+    __syncthreads();
 }
 
 // F[i] = before + the weights of list[0 .. i], for the n sorted numbers.
@@ -502,6 +625,8 @@ __global__ void __launch_bounds__(kPickThreads)
     k_sample_pick(Rows R, Settings S, int32_t *token, float *prob, int *status)
 {
     __shared__ u64 list[kList], F[kList], sh[kPickThreads / 32];
+    __shared__ unsigned steps[kList], sh32[kPickThreads / 32];
+    __shared__ short s_listed[kMaxSlices];
     __shared__ RowHead s_head;
     __shared__ u64 s_sum;
     __shared__ int s_count;
@@ -509,6 +634,7 @@ __global__ void __launch_bounds__(kPickThreads)
     const Header *head = R.head + static_cast<long long>(row) * R.slices;
     pdl_wait();
     pdl_launch_dependents();
+    for (int s = tid; s < R.slices; s += kPickThreads) s_listed[s] = static_cast<short>(head[s].cands > 0 ? head[s].count : 0);
     const float T = temperature(S, row), p = S.top_p ? __ldg(S.top_p + row) : 1.f, mp = S.min_p ? __ldg(S.min_p + row) : 0.f,
                 u = __ldg(S.u + row);
     const int k = top_k(S, row, R.vocab);
@@ -547,17 +673,24 @@ __global__ void __launch_bounds__(kPickThreads)
     if (h.best == 0) return answer(-1, 0.f);
     if (!(T > 0.f)) return answer(index_of(h.best), 1.f);
 
-    for (int s = warp; s < R.slices; s += kPickThreads / 32) {
-        const u64 *from = R.list + (static_cast<long long>(row) * R.slices + s) * R.cap;
-        const int n = head[s].cands > 0 ? head[s].count : 0;
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const u64 x = i0 + lane < n ? __ldcg(from + i0 + lane) : 0ull;
-            const bool take = static_cast<uint32_t>(x >> 32) >= h.theta;
+    // the slices' lists as one row of entries, most of them empty
+    const u64 *lists = R.list + (static_cast<long long>(row) * R.slices << R.cap_log2);
+    constexpr int kBatch = 4;
+    for (int i0 = 0; i0 < R.slices << R.cap_log2; i0 += kBatch * kPickThreads) {
+        u64 x[kBatch];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int i = i0 + q * kPickThreads + tid, s = i >> R.cap_log2;
+            x[q] = s < R.slices && (i & (R.cap - 1)) < s_listed[s] ? __ldcg(lists + i) : 0ull;
+        }
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const bool take = static_cast<uint32_t>(x[q] >> 32) >= h.theta;
             const unsigned who = __ballot_sync(0xffffffffu, take);
             int at = 0;
             if (lane == 0 && who) at = atomicAdd(&s_count, __popc(who));
             at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
-            if (take && at < kList) list[at] = x;
+            if (take && at < kList) list[at] = x[q];
         }
     }
     __syncthreads();
@@ -565,11 +698,8 @@ __global__ void __launch_bounds__(kPickThreads)
     const bool all = n == h.cands;  // every candidate is in the list
     bool done = h.theta != kUnknown && n > 0 && n <= kList;
     if (done) {
-        const int P = padded(n);
-        for (int i = n + tid; i < P; i += kPickThreads) list[i] = 0ull;
-        __syncthreads();
-        sort_down<kPickThreads>(list, P);
         const float largest = value_of(static_cast<uint32_t>(h.best >> 32));
+        sort_down<kPickThreads>(list, F, steps, n, largest, value_of(max(h.theta, h.lowest)), sh32);
         const Scale sc = scale_of(T, largest);
         const int top = exponent(sc, largest);
         running_weights<kPickThreads>(list, F, n, 0ull, sc, top, sh);
@@ -626,6 +756,7 @@ struct __align__(16) Part {  // one CTA's part of a pass over the row
 };
 struct DeepShared {
     u64 list[kList], F[kList];
+    unsigned steps[kList];
     unsigned hist[kBins], coarse[kBins], fine[kBins];  // fine, coarse: running counts
     float est[kBins];                                  // running estimate of the weight, in units of the largest
     Part part[kDeepCtas];
@@ -860,10 +991,9 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
                     for (int c = 0; c < kDeepCtas; ++c) cluster.map_shared_rank(D.list, c)[at + i] = r;
                 }
                 cluster.sync();
-                const int n = static_cast<int>(all.count), P = padded(n);
-                for (int i = n + tid; i < P; i += kDeepThreads) D.list[i] = 0ull;
-                __syncthreads();
-                sort_down<kDeepThreads>(D.list, P);
+                const int n = static_cast<int>(all.count);
+                sort_down<kDeepThreads>(D.list, D.F, D.steps, n, value_of(static_cast<uint32_t>(all.highest >> 32)),
+                                        value_of(static_cast<uint32_t>(all.lowest >> 32)), D.sh32);
                 running_weights<kDeepThreads>(D.list, D.F, n, before, sc, top, D.sh);
                 const int j = by_count ? static_cast<int>(X - (b ? C[b - 1] : 0u)) - 1 : reach(D.F, n, X);
                 return max(min(j, n - 1), 0);
@@ -917,23 +1047,23 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
 }
 
 // ---------------------------------------------------------------- host
-// Slices of 4096 elements while they all fit the GPU at once, of 16384 else: a
+// Slices of 2048 elements while they all fit the GPU at once, of 8192 else: a
 // small batch is latency, and a large one wants long streams per CTA.
 struct Plan {
-    int ept, slices, cap, want;
+    int ept, slices, cap_log2, want;
 };
 Plan plan_for(int vocab, int n_rows)
 {
     Plan p;
-    const long long fine = (vocab + 7 + 4095) / 4096;
+    const long long fine = (vocab + 7 + 2047) / 2048;
     p.ept = fine * n_rows <= 608 ? 8 : 32;
     const int per = kScanThreads * p.ept;
     p.slices = (vocab + 7 + per - 1) / per;
-    // lists of some 1024 elements a row in all, with room for four times as many
-    const int cap = 4096 / p.slices;
-    p.cap = cap < 64 ? 64 : (cap > kList ? kList : cap);
+    // lists of some 1024 elements a row in all, with room for two to four times as many
+    p.cap_log2 = 5;
+    while (p.cap_log2 < 11 && (p.slices << (p.cap_log2 + 1)) <= 4096) ++p.cap_log2;
     const int want = 1024 / p.slices;
-    p.want = want < 4 ? 4 : (want > 256 ? 256 : want);
+    p.want = want < 4 ? 4 : (want > kScanThreads / 2 ? kScanThreads / 2 : want);
     return p;
 }
 size_t up16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
@@ -965,7 +1095,7 @@ size_t gq_sample_workspace_bytes(int vocab, int n_rows)
     if (vocab < 1 || vocab > GQ_MAX_VOCAB || n_rows < 1 || n_rows > 65535) return 0;
     const Plan p = plan_for(vocab, n_rows);
     const size_t slices = static_cast<size_t>(p.slices) * n_rows;
-    return slices * sizeof(Header) + slices * p.cap * sizeof(u64) + up16(static_cast<size_t>(n_rows) * sizeof(int));
+    return slices * sizeof(Header) + (slices << p.cap_log2) * sizeof(u64) + up16(static_cast<size_t>(n_rows) * sizeof(int));
 }
 
 int gq_sample(const void *logits, long long ldl, int type, const float *temperature, const int32_t *top_k,
@@ -988,10 +1118,11 @@ int gq_sample(const void *logits, long long ldl, int type, const float *temperat
                  ldl * kv::type_size(type),
                  vocab,
                  p.slices,
-                 p.cap,
+                 1 << p.cap_log2,
+                 p.cap_log2,
                  reinterpret_cast<Header *>(ws),
                  reinterpret_cast<u64 *>(ws + slices * sizeof(Header)),
-                 reinterpret_cast<int *>(ws + slices * sizeof(Header) + slices * p.cap * sizeof(u64))};
+                 reinterpret_cast<int *>(ws + slices * sizeof(Header) + (slices << p.cap_log2) * sizeof(u64))};
     const Settings S{temperature, top_k, top_p, min_p, u};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (type) {
