@@ -28,6 +28,7 @@ GQ_MAX_TOPK = 64
 GQ_MAX_PLAN_SEQ = 8192
 GQ_MAX_LORA_RANK = 128
 GQ_MAX_VOCAB = 1048576
+GQ_MAX_SAMPLE_ROWS = 16384
 
 GQ_OK = 0
 GQ_ERR_NULL = -1

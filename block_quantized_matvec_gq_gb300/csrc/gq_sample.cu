@@ -16,20 +16,20 @@
 //          The list's threshold is the want-th largest of the threads' own
 //          maxima, found by bisection with a vote of the CTA per step: at least
 //          `want` elements reach it, and few more.
-//   pick   one CTA per row: lists above the slices' highest threshold hold every
-//          element above it, some hundreds.  They are sorted, and where the
-//          limits and the draw fall among them, which they do for a language
-//          model's usual rows, the row is done.
+//          The CTA that finishes a row's last slice goes on to pick the token:
+//          the lists above the slices' highest threshold hold every element above
+//          it, some hundreds.  They are sorted, and where the limits and the draw
+//          fall among them, which they do for a language model's usual rows, the
+//          row is done.
 //   deep   the other rows (flat ones, a large top_k), a cluster of CTAs each: a
-//          histogram of the row over 2048 equal steps of the exponent gives the
-//          step in which X is reached, exactly for counts, by an estimate for
-//          weights; the step's elements are collected and sorted, with the exact
-//          weight in front of them, which also shows whether the estimate was
-//          right.  A step with too many elements is divided further, by the bits
-//          of (logit, index), which no two elements share.
+//          histogram of the row over 2048 equal steps of the exponent, counts and
+//          exact weights, gives the step in which X is reached; the step's
+//          elements are collected and sorted.  A step with too many elements is
+//          divided further, by the bits of (logit, index), which no two elements
+//          share.
 //
 // What bounds it: the one pass over the logits, and for small batches the
-// latency of the three kernels.
+// latency of the two kernels.
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
@@ -46,11 +46,12 @@ namespace cg = cooperative_groups;
 using u64 = unsigned long long;
 
 constexpr int kScanThreads = 256;
-constexpr int kPickThreads = 1024;
-constexpr int kDeepThreads = 512;
+constexpr int kDeepThreads = 1024;
 constexpr int kDeepCtas = 8;
+constexpr int kDeepClusters = 64;
 constexpr int kList = 2048;  // elements that are sorted at once
 constexpr int kMaxSlices = 640;
+constexpr int kSumFrom = 512;  // a top_k from here on may lie behind the list: the slices' sums bound its weight
 constexpr int kBins = 2048;
 constexpr uint32_t kNone = 0x007FFFFFu;        // key of -infinity: no candidate
 constexpr uint32_t kUnknown = 0xFFFFFFFFu;     // threshold of a slice whose list is empty
@@ -69,8 +70,9 @@ struct __align__(16) Header {
     u64 sum;         // weights in units of 2^(exp - 43)
     u64 best;        // the first of the order
     uint32_t lowest, theta;  // smallest candidate's key; every element with a key of theta or more is listed
-    int exp, count, cands, pad;
+    int exp, count, cands, pad[3];
 };
+static_assert(sizeof(Header) == 48, "read as three 16-byte words");
 
 struct Rows {
     const uint8_t *logits;
@@ -78,7 +80,8 @@ struct Rows {
     int vocab, slices, cap, cap_log2;
     Header *head;
     u64 *list;
-    int *deep;  // rows for the third kernel
+    unsigned *done;  // finished slices of every row, 0 before and after a call
+    int *deep;       // rows for the second kernel
 };
 
 // Order-preserving bits of a logit that is not a NaN; -0 is 0.
@@ -239,37 +242,46 @@ struct Reader {
         units = (n + shift + kVec - 1) / kVec;
     }
     __device__ __forceinline__ int index(int unit, int i) const { return unit * kVec + i - shift; }
-    // Candidates as they are, NaN and what lies outside as -infinity.
-    __device__ __forceinline__ void load(int unit, float (&v)[kVec]) const
+    __device__ __forceinline__ bool inside(int unit) const { return index(unit, 0) >= 0 && index(unit, kVec) <= vocab; }
+    __device__ __forceinline__ uint4 word(int unit) const
     {
-        const uint8_t *p = base + static_cast<long long>(unit) * 16;
-        const int first = index(unit, 0);
-        if (unit < units && first >= 0 && first + kVec <= vocab) {
-            if (TYPE == GQ_TYPE_F32) {
-                const float4 a = kv::load4<TYPE>(p);
-                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            } else {
-                float4 a, b;
-                kv::load8<TYPE>(p, a, b);
-                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-                v[kVec - 4] = b.x, v[kVec - 3] = b.y, v[kVec - 2] = b.z, v[kVec - 1] = b.w;
-            }
-        } else {
+        return __ldg(reinterpret_cast<const uint4 *>(base + static_cast<long long>(unit) * 16));
+    }
+    // Candidates as they are, NaN and what lies outside as -infinity.
+    __device__ __forceinline__ void values(uint4 w, float (&v)[kVec]) const
+    {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                v[i] = -INFINITY;
-                if (unit < units && first + i >= 0 && first + i < vocab) {
-                    if (TYPE == GQ_TYPE_F32)
-                        v[i] = __ldg(reinterpret_cast<const float *>(p) + i);
-                    else if (TYPE == GQ_TYPE_F16)
-                        v[i] = __half2float(__ushort_as_half(__ldg(reinterpret_cast<const uint16_t *>(p) + i)));
-                    else
-                        v[i] = __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(p) + i)) << 16);
-                }
+        for (int i = 0; i < 4; ++i) {
+            if (TYPE == GQ_TYPE_F32) {
+                v[i] = __uint_as_float(x[i]);
+            } else {
+                const float2 f = TYPE == GQ_TYPE_F16 ? kv::half2_f2(x[i]) : make_float2(kv::bf16_lo(x[i]), kv::bf16_hi(x[i]));
+                v[2 * i % kVec] = f.x;
+                v[(2 * i + 1) % kVec] = f.y;
             }
         }
 #pragma unroll
         for (int i = 0; i < kVec; ++i) v[i] = fmaxf(v[i], -INFINITY);
+    }
+    __device__ __forceinline__ void load(int unit, float (&v)[kVec]) const
+    {
+        if (unit < units && inside(unit)) return values(word(unit), v);
+        const uint8_t *p = base + static_cast<long long>(unit) * 16;
+        const int first = index(unit, 0);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            v[i] = -INFINITY;
+            if (unit < units && first + i >= 0 && first + i < vocab) {
+                if (TYPE == GQ_TYPE_F32)
+                    v[i] = __ldg(reinterpret_cast<const float *>(p) + i);
+                else if (TYPE == GQ_TYPE_F16)
+                    v[i] = __half2float(__ushort_as_half(__ldg(reinterpret_cast<const uint16_t *>(p) + i)));
+                else
+                    v[i] = __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(p) + i)) << 16);
+                v[i] = fmaxf(v[i], -INFINITY);
+            }
+        }
     }
 };
 
@@ -300,157 +312,6 @@ __device__ __forceinline__ u64 cta_sum(u64 v, u64 *sh)
     return s;
 }
 
-// ---------------------------------------------------------------- scan
-template <int TYPE, int EPT>
-__global__ void __launch_bounds__(kScanThreads) k_sample_scan(Rows R, Settings S, int want)
-{
-    constexpr int kVec = Reader<TYPE>::kVec, kUnits = EPT / kVec, kWarps = kScanThreads / 32;
-    __shared__ u64 s_sum[kWarps];
-    __shared__ uint32_t s_hi[kWarps], s_lo[kWarps];
-    __shared__ int s_cands[kWarps], s_count, s_first;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y, slice = blockIdx.x;
-    if (tid == 0) {
-        s_count = 0;
-        s_first = INT_MAX;
-    }
-    pdl_wait();
-    pdl_launch_dependents();
-    const Reader<TYPE> in(R.logits + row * R.row_bytes, R.vocab);
-    const int u0 = slice * kScanThreads * kUnits + tid;
-    float v[kUnits][kVec];
-#pragma unroll
-    for (int j = 0; j < kUnits; ++j) in.load(u0 + j * kScanThreads, v[j]);
-    const float T = temperature(S, row);
-    const int k = top_k(S, row, R.vocab);
-    float hi = -INFINITY, lo = INFINITY;
-#pragma unroll
-    for (int j = 0; j < kUnits; ++j)
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            hi = fmaxf(hi, v[j][i]);
-            lo = fminf(lo, v[j][i]);
-        }
-    int cands = EPT;
-    if (lo == -INFINITY) {  // masked tokens, or the row's ends
-        lo = INFINITY;
-        cands = 0;
-#pragma unroll
-        for (int j = 0; j < kUnits; ++j)
-#pragma unroll
-            for (int i = 0; i < kVec; ++i)
-                if (v[j][i] > -INFINITY) {
-                    lo = fminf(lo, v[j][i]);
-                    ++cands;
-                }
-    }
-    const uint32_t mine = key_of(hi);
-    {
-        const uint32_t a = __reduce_max_sync(0xffffffffu, mine), b = __reduce_min_sync(0xffffffffu, lo < INFINITY ? key_of(lo) : kUnknown);
-        const int c = __reduce_add_sync(0xffffffffu, cands);
-        if (lane == 0) {
-            s_hi[warp] = a;
-            s_lo[warp] = b;
-            s_cands[warp] = c;
-        }
-    }
-    __syncthreads();
-    Header h{};
-    uint32_t top = 0;
-    h.lowest = kUnknown;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        top = max(top, s_hi[w]);
-        h.lowest = min(h.lowest, s_lo[w]);
-        h.cands += s_cands[w];
-    }
-    const float best = value_of(top);
-    if (mine == top) {  // the slice's first of the order: the lowest index among its largest
-        int first = INT_MAX;
-#pragma unroll
-        for (int j = kUnits - 1; j >= 0; --j)
-#pragma unroll
-            for (int i = kVec - 1; i >= 0; --i)
-                if (v[j][i] == best) first = in.index(u0 + j * kScanThreads, i);
-        atomicMin(&s_first, first);
-    }
-    h.theta = kUnknown;
-    if (T > 0.f && top > kNone) {  // otherwise the first of the order is all that is asked for
-        const Scale sc = scale_of(T);
-        if (k == 0) {
-            h.exp = exponent(sc, best);
-            u64 sum = 0;
-#pragma unroll
-            for (int j = 0; j < kUnits; ++j)
-#pragma unroll
-                for (int i = 0; i < kVec; i += 2) sum += weights2(sc, v[j][i], v[j][i + 1], h.exp);
-            sum = warp_sum(sum);
-            if (lane == 0) s_sum[warp] = sum;
-        }
-        uint32_t a = kNone + 1;
-        if (h.cands > R.cap) {
-            // a threshold that `w` threads reach and few elements more
-            const int threads = __syncthreads_count(mine > kNone);
-            const int w = max(1, min(k > 0 ? min(want, 2 * k / static_cast<int>(gridDim.x) + 8) : want, threads / 2));
-            uint32_t b = top;  // w threads reach a; look in a .. b
-            if (threads == kScanThreads) {  // all threads reach the least of their maxima
-                uint32_t m = __reduce_min_sync(0xffffffffu, mine);
-                if (lane == 0) s_lo[warp] = m;
-                __syncthreads();
-                a = b;
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) a = min(a, s_lo[x]);
-            }
-            while (a < b) {
-                const uint32_t mid = a + (b - a) / 2 + 1;
-                const int n = __syncthreads_count(mine >= mid);
-                if (n >= w)
-                    a = mid;
-                else
-                    b = mid - 1;
-                if (n >= w && n <= w + w / 4) break;
-            }
-        }
-        u64 *list = R.list + (static_cast<long long>(row) * R.slices + slice) * R.cap;
-        auto put = [&](uint32_t least) {  // the elements from `least` on, as far as there is room
-            if (mine < least) return;
-            const float from = value_of(least);
-#pragma unroll
-            for (int j = 0; j < kUnits; ++j)
-#pragma unroll
-                for (int i = 0; i < kVec; ++i)
-                    if (v[j][i] >= from) {
-                        const int at = atomicAdd(&s_count, 1);
-                        if (at < R.cap) list[at] = rank_of(key_of(v[j][i]), in.index(u0 + j * kScanThreads, i));
-                    }
-        };
-        put(a);
-        __syncthreads();
-        h.count = s_count;
-        if (h.count <= R.cap) {
-            h.theta = a;
-        } else {  // many equal ones at the threshold: leave them out
-            __syncthreads();
-            if (tid == 0) s_count = 0;
-            __syncthreads();
-            if (a < top) put(a + 1);
-            __syncthreads();
-            h.count = s_count;
-            if (a < top && h.count <= R.cap)
-                h.theta = a + 1;
-            else
-                h.count = 0;
-        }
-        if (k == 0)
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) h.sum += s_sum[w];
-    }
-    __syncthreads();
-    if (tid == 0) {
-        h.best = top > kNone ? rank_of(top, s_first) : 0ull;
-        R.head[static_cast<long long>(row) * R.slices + slice] = h;
-    }
-}
-
 // ---------------------------------------------------------------- sorted lists
 // Falling bitonic sort of n (a power of two, 64 .. kList) numbers.  Steps of 32
 // or less stay within a warp's own 64 numbers.
@@ -475,19 +336,33 @@ __device__ __forceinline__ void bitonic_down(u64 *a, int n)
         }
     __syncthreads();
 }
-// Falling sort of the n numbers of `list` (distinct, values between those of
-// `high` and `low`), with `tmp` as long and kList counters: dealt into kList
+// Falling sort of the n numbers of `list` (distinct, none above `first` or below
+// `last`), with `tmp` as long and kList counters: dealt into kList
 // equal steps of the value, then every number finds its place among its step's
-// few.  2048 numbers: 1.5 us, against 7 of the bitonic sort, which remains for
-// lists with more than kCrowd in one step (ties, far outliers).
-constexpr int kCrowd = 96;
+// few.  Numbers of one value are dealt by their bits.  The bitonic sort remains
+// for lists with more than kCrowd in one step (ties, far outliers).
+constexpr int kCrowd = 256, kFew = 96;
 template <int THREADS>
-__device__ __forceinline__ void sort_down(u64 *list, u64 *tmp, unsigned *count, int n, float high, float low, unsigned *sh)
+__device__ __forceinline__ void sort_down(u64 *list, u64 *tmp, unsigned *count, int n, u64 first, u64 last, unsigned *sh)
 {
     constexpr int kPer = kList / THREADS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (n <= kFew) {  // every number finds its place among all
+        const u64 x = tid < n ? list[tid] : 0ull;
+        int place = 0;
+        if (tid < n)
+            for (int j = 0; j < n; ++j) place += list[j] > x ? 1 : 0;
+        __syncthreads();
+        if (tid < n) list[place] = x;
+        __syncthreads();
+        return;
+    }
+    const float high = value_of(static_cast<uint32_t>(first >> 32)), low = value_of(static_cast<uint32_t>(last >> 32));
     const float per = (kList - 1) / fmaxf(high - low, 1e-30f);
+    const bool ties = !(high > low);
+    const int shift = max(0, 53 - __clzll(static_cast<long long>(first - last)));
     auto step_of = [&](u64 r) {
+        if (ties) return static_cast<int>((first - r) >> shift);
         const float x = (high - value_of(static_cast<uint32_t>(r >> 32))) * per;
         return max(0, min(kList - 1, __float2int_rz(x)));
     };
@@ -595,455 +470,696 @@ __device__ __forceinline__ int reach(const u64 *F, int n, u64 x)
     return lo;
 }
 
-// What the slices' headers say of a row; warp 0 reads them.
+// What the slices' headers say of a row.
 struct RowHead {
     u64 best;
     uint32_t lowest, theta;
     int cands;
 };
-__device__ __forceinline__ RowHead row_head(const Header *head, int slices)
+__device__ __forceinline__ Header load_header(const Header *h)
 {
-    const int lane = threadIdx.x & 31;
-    RowHead r{0ull, kUnknown, 0u, 0};
-    for (int s = lane; s < slices; s += 32) {
-        const Header &h = head[s];
-        r.best = max(r.best, h.best);
-        r.lowest = min(r.lowest, h.lowest);
-        r.theta = max(r.theta, h.cands > 0 ? h.theta : 0u);
-        r.cands += h.cands;
-    }
+    Header r;
+    const uint4 *p = reinterpret_cast<const uint4 *>(h);
+    uint4 *q = reinterpret_cast<uint4 *>(&r);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(Header) / 16); ++i) q[i] = __ldcg(p + i);
+    return r;
+}
+// The CTA's rows of headers, joined in every thread; `sh` has one entry per warp.
+template <int THREADS>
+__device__ __forceinline__ RowHead join_heads(RowHead r, RowHead *sh)
+{
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) r.best = max(r.best, __shfl_xor_sync(0xffffffffu, r.best, o));
     r.lowest = __reduce_min_sync(0xffffffffu, r.lowest);
     r.theta = __reduce_max_sync(0xffffffffu, r.theta);
     r.cands = __reduce_add_sync(0xffffffffu, r.cands);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = r;
+    __syncthreads();
+    r = sh[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 32; ++w) {
+        r.best = max(r.best, sh[w].best);
+        r.lowest = min(r.lowest, sh[w].lowest);
+        r.theta = max(r.theta, sh[w].theta);
+        r.cands += sh[w].cands;
+    }
     return r;
+}
+__device__ __forceinline__ void add_head(RowHead &r, const Header &h)
+{
+    if (h.cands == 0) return;
+    r.best = max(r.best, h.best);
+    r.lowest = min(r.lowest, h.lowest);
+    r.theta = max(r.theta, h.theta);
+    r.cands += h.cands;
 }
 
 // ---------------------------------------------------------------- pick
-__global__ void __launch_bounds__(kPickThreads)
-    k_sample_pick(Rows R, Settings S, int32_t *token, float *prob, int *status)
+struct PickShared {
+    u64 list[kList], F[kList], sh[kScanThreads / 32];
+    unsigned steps[kList], sh32[kScanThreads / 32];
+    unsigned short start[kMaxSlices + 1];  // listed entries in front of every slice's
+    RowHead heads[kScanThreads / 32];
+    int count;
+};
+
+// The row from its slices' headers and lists; false where they do not settle it.
+__device__ __forceinline__ bool pick(const Rows &R, const Settings &S, int row, float T, int k, PickShared &P, int &tok, float &pr,
+                                     bool &refused)
 {
-    __shared__ u64 list[kList], F[kList], sh[kPickThreads / 32];
-    __shared__ unsigned steps[kList], sh32[kPickThreads / 32];
-    __shared__ short s_listed[kMaxSlices];
-    __shared__ RowHead s_head;
-    __shared__ u64 s_sum;
-    __shared__ int s_count;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.x;
+    constexpr int kThreads = kScanThreads, kHeads = (kMaxSlices + kThreads - 1) / kThreads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Header *head = R.head + static_cast<long long>(row) * R.slices;
-    pdl_wait();
-    pdl_launch_dependents();
-    for (int s = tid; s < R.slices; s += kPickThreads) s_listed[s] = static_cast<short>(head[s].cands > 0 ? head[s].count : 0);
-    const float T = temperature(S, row), p = S.top_p ? __ldg(S.top_p + row) : 1.f, mp = S.min_p ? __ldg(S.min_p + row) : 0.f,
-                u = __ldg(S.u + row);
-    const int k = top_k(S, row, R.vocab);
-    if (warp == 0) {
-        const RowHead r = row_head(head, R.slices);
-        // the row's weight from the slices', each in units of its own largest
-        u64 sum = 0;
-        if (r.best != 0 && T > 0.f && k == 0) {
-            const Scale sc = scale_of(T);
-            const int top = exponent(sc, value_of(static_cast<uint32_t>(r.best >> 32)));
-            for (int s = lane; s < R.slices; s += 32) {
-                const unsigned shift = static_cast<unsigned>(top - head[s].exp);
-                if (head[s].cands > 0 && shift < 64) sum += head[s].sum >> shift;
-            }
+    const float p = S.top_p ? __ldg(S.top_p + row) : 1.f, mp = S.min_p ? __ldg(S.min_p + row) : 0.f, u = __ldg(S.u + row);
+    tok = -1;
+    pr = 0.f;
+    refused = isnan(T) || isnan(p) || isnan(mp);
+    if (refused) return true;
+    // a thread takes consecutive slices
+    const int per = (R.slices + kThreads - 1) / kThreads, s0 = tid * per;
+    RowHead h{0ull, kUnknown, 0u, 0};
+    u64 sum[kHeads];
+    int exp[kHeads], count[kHeads], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        sum[i] = 0;
+        exp[i] = count[i] = 0;
+        if (i < per && s0 + i < R.slices) {
+            const Header x = load_header(head + s0 + i);
+            add_head(h, x);
+            sum[i] = x.cands > 0 ? x.sum : 0ull;
+            exp[i] = x.exp;
+            count[i] = x.count;
         }
-        sum = warp_sum(sum);
-        if (lane == 0) {
-            s_head = r;
-            s_sum = sum;
-            s_count = 0;
-        }
+        mine += count[i];
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) P.sh32[warp] = incl;
+    if (tid == 0) P.count = 0;
+    h = join_heads<kThreads>(h, P.heads);  // (a barrier in it)
+    if (h.best == 0) return true;
+    const float largest = value_of(static_cast<uint32_t>(h.best >> 32));
+    if (!(T > 0.f)) {
+        tok = index_of(h.best);
+        pr = 1.f;
+        return true;
+    }
+    if (h.theta == kUnknown) return false;
+    const Scale sc = scale_of(T, largest);
+    const int top = exponent(sc, largest);
+    const bool summed = (k == 0 || k >= kSumFrom) && sc.base == 0.f && !sc.infinite;
+    // the row's weight from the slices', each in units of its own largest
+    u64 total = 0;
+    int at = incl - mine, listed_all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        at += w < warp ? static_cast<int>(P.sh32[w]) : 0;
+        listed_all += static_cast<int>(P.sh32[w]);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        const unsigned shift = static_cast<unsigned>(top - exp[i]);
+        if (summed && shift < 64) total += sum[i] >> shift;
+        if (i < per && s0 + i < R.slices) P.start[s0 + i] = static_cast<unsigned short>(at);
+        at += count[i];
     }
     __syncthreads();
-    const RowHead h = s_head;
-    auto answer = [&](int tok, float pr) {
-        if (tid == 0) {
-            token[row] = tok;
-            if (prob) prob[row] = pr;
-            R.deep[row] = 0;
-        }
-    };
-    if (isnan(T) || isnan(p) || isnan(mp)) {
-        if (tid == 0 && status) atomicExch(status, GQ_ERR_SHAPE);
-        return answer(-1, 0.f);
-    }
-    if (h.best == 0) return answer(-1, 0.f);
-    if (!(T > 0.f)) return answer(index_of(h.best), 1.f);
-
-    // the slices' lists as one row of entries, most of them empty
+    // all listed entries, a few loads of every thread in flight
     const u64 *lists = R.list + (static_cast<long long>(row) * R.slices << R.cap_log2);
     constexpr int kBatch = 4;
-    for (int i0 = 0; i0 < R.slices << R.cap_log2; i0 += kBatch * kPickThreads) {
+    for (int i0 = 0; i0 < listed_all; i0 += kBatch * kThreads) {
         u64 x[kBatch];
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
-            const int i = i0 + q * kPickThreads + tid, s = i >> R.cap_log2;
-            x[q] = s < R.slices && (i & (R.cap - 1)) < s_listed[s] ? __ldcg(lists + i) : 0ull;
+            const int i = i0 + q * kThreads + tid;
+            x[q] = 0;
+            if (i < listed_all) {
+                int lo = 0, hi = R.slices;  // the last slice that starts at i or before: empty ones start where the next does
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (P.start[mid] <= i)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                x[q] = __ldcg(lists + (static_cast<long long>(lo) << R.cap_log2) + (i - P.start[lo]));
+            }
         }
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
             const bool take = static_cast<uint32_t>(x[q] >> 32) >= h.theta;
             const unsigned who = __ballot_sync(0xffffffffu, take);
-            int at = 0;
-            if (lane == 0 && who) at = atomicAdd(&s_count, __popc(who));
-            at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
-            if (take && at < kList) list[at] = x[q];
+            int to = 0;
+            if (lane == 0 && who) to = atomicAdd(&P.count, __popc(who));
+            to = __shfl_sync(0xffffffffu, to, 0) + __popc(who & ((1u << lane) - 1u));
+            if (take && to < kList) P.list[to] = x[q];
+        }
+    }
+    total = cta_sum<kThreads>(total, P.sh);
+    const int n = P.count;
+    if (n == 0 || n > kList) return false;
+    const bool all = n == h.cands;  // every candidate is in the list
+    sort_down<kThreads>(P.list, P.F, P.steps, n, h.best, rank_of(max(h.theta, h.lowest), R.vocab - 1), P.sh32);
+    running_weights<kThreads>(P.list, P.F, n, 0ull, sc, top, P.sh);
+    const u64 *F = P.F;
+    const u64 listed = F[n - 1], last = n > 1 ? listed - F[n - 2] : listed;
+    // the weight of what top_k keeps, between z and most
+    u64 z, most;
+    if (k > 0 && k <= n) {
+        z = most = F[k - 1];
+    } else if (all || last == 0) {  // nothing of weight lies beyond the list
+        z = most = listed;
+    } else if (k == 0) {
+        if (!summed) return false;
+        z = most = max(total, listed);
+    } else {
+        z = listed;
+        most = summed ? max(total, listed) : ~0ull;
+        if (last < (1ull << 43)) most = min(most, listed + static_cast<u64>(k - n) * last);
+    }
+    // the first element where top_p is reached, and the weight that min_p keeps, where they are in the list
+    const int from = p < 1.f ? reach(F, n, nucleus(p, z)) : n, to = p < 1.f ? (most == z ? from : reach(F, n, nucleus(p, most))) : n;
+    u64 least = ~0ull;
+    if (mp > 0.f) {
+        bool rest = false;
+        const u64 thr = mp < 1.f ? part_of(mp, F[0], rest) + (rest ? 1 : 0) : F[0];
+        int lo = 0, hi = n;  // first of the list below the threshold; the list falls
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (F[mid] - (mid ? F[mid - 1] : 0ull) < thr)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        if (lo < n)
+            least = F[max(lo, 1) - 1];
+        else if (all)
+            least = listed;
+    }
+    u64 kept;
+    if (least != ~0ull && (from == n || least <= F[from]))
+        kept = least;
+    else if (from < n && from == to)
+        kept = F[from];
+    else if (p < 1.f || mp > 0.f || most != z)
+        return false;
+    else
+        kept = z;
+    kept = min(kept, z);
+    const int j = reach(F, n, drawn(u, kept));
+    if (j == n) return false;
+    tok = index_of(P.list[j]);
+    pr = ratio(j ? F[j] - F[j - 1] : F[0], kept);
+    return true;
+}
+
+// ---------------------------------------------------------------- scan
+template <int TYPE, int EPT>
+__global__ void __launch_bounds__(kScanThreads, 4)
+    k_sample_scan(Rows R, Settings S, int want, int32_t *token, float *prob, int *status)
+{
+    constexpr int kVec = Reader<TYPE>::kVec, kUnits = EPT / kVec, kWarps = kScanThreads / 32;
+    __shared__ u64 s_sum[kWarps];
+    __shared__ uint32_t s_hi[kWarps], s_lo[kWarps];
+    __shared__ int s_cands[kWarps], s_count, s_first;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y, slice = blockIdx.x;
+    if (tid == 0) {
+        s_count = 0;
+        s_first = INT_MAX;
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    const Reader<TYPE> in(R.logits + row * R.row_bytes, R.vocab);
+    const int u0 = slice * kScanThreads * kUnits + tid;
+    float v[kUnits][kVec];
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) in.load(u0 + j * kScanThreads, v[j]);
+    const float T = temperature(S, row);
+    const int k = top_k(S, row, R.vocab);
+    float hi = -INFINITY, lo = INFINITY;
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            hi = fmaxf(hi, v[j][i]);
+            lo = fminf(lo, v[j][i]);
+        }
+    int cands = EPT;
+    if (lo == -INFINITY) {  // masked tokens, or the row's ends
+        lo = INFINITY;
+        cands = 0;
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                if (v[j][i] > -INFINITY) {
+                    lo = fminf(lo, v[j][i]);
+                    ++cands;
+                }
+    }
+    const uint32_t mine = key_of(hi);
+    {
+        const uint32_t a = __reduce_max_sync(0xffffffffu, mine), b = __reduce_min_sync(0xffffffffu, lo < INFINITY ? key_of(lo) : kUnknown);
+        const int c = __reduce_add_sync(0xffffffffu, cands);
+        if (lane == 0) {
+            s_hi[warp] = a;
+            s_lo[warp] = b;
+            s_cands[warp] = c;
         }
     }
     __syncthreads();
-    const int n = s_count;
-    const bool all = n == h.cands;  // every candidate is in the list
-    bool done = h.theta != kUnknown && n > 0 && n <= kList;
-    if (done) {
-        const float largest = value_of(static_cast<uint32_t>(h.best >> 32));
-        sort_down<kPickThreads>(list, F, steps, n, largest, value_of(max(h.theta, h.lowest)), sh32);
-        const Scale sc = scale_of(T, largest);
-        const int top = exponent(sc, largest);
-        running_weights<kPickThreads>(list, F, n, 0ull, sc, top, sh);
-        const u64 listed = F[n - 1], last = n > 1 ? listed - F[n - 2] : listed;
-        // the weight of what top_k keeps
-        u64 z = 0;
-        bool known = true;
-        if (k > 0 && k <= n)
-            z = F[k - 1];
-        else if (all || last == 0)  // nothing of weight lies beyond the list
-            z = listed;
-        else if (k == 0 && sc.base == 0.f && !sc.infinite)
-            z = max(s_sum, listed);
-        else
-            known = false;
-        if (known) {
-            u64 kept = z;
-            if (p < 1.f) {
-                const int j = reach(F, n, nucleus(p, z));
-                if (j < n)
-                    kept = min(kept, F[j]);
-                else
-                    known = all || last == 0;
-            }
-            if (mp > 0.f) {
-                bool rest = false;
-                const u64 thr = mp < 1.f ? part_of(mp, F[0], rest) + (rest ? 1 : 0) : F[0];
-                // first of the list below the threshold; the list falls
-                int lo = 0, hi = n;
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (F[mid] - (mid ? F[mid - 1] : 0ull) < thr)
-                        hi = mid;
-                    else
-                        lo = mid + 1;
-                }
-                if (lo < n)
-                    kept = min(kept, F[max(lo, 1) - 1]);
-                else if (!all && kept > listed)
-                    known = false;
-            }
-            const int j = known ? reach(F, n, drawn(u, kept)) : n;
-            if (j < n) return answer(index_of(list[j]), ratio(j ? F[j] - F[j - 1] : F[0], kept));
-        }
-        done = false;
+    Header h{};
+    uint32_t top = 0;
+    h.lowest = kUnknown;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        top = max(top, s_hi[w]);
+        h.lowest = min(h.lowest, s_lo[w]);
+        h.cands += s_cands[w];
     }
-    if (tid == 0) R.deep[row] = 1;
+    const float best = value_of(top);
+    if (mine == top) {  // the slice's first of the order: the lowest index among its largest
+        int first = INT_MAX;
+#pragma unroll
+        for (int j = kUnits - 1; j >= 0; --j)
+#pragma unroll
+            for (int i = kVec - 1; i >= 0; --i)
+                if (v[j][i] == best) first = in.index(u0 + j * kScanThreads, i);
+        atomicMin(&s_first, first);
+    }
+    h.theta = kUnknown;
+    if (T > 0.f && top > kNone) {  // otherwise the first of the order is all that is asked for
+        const Scale sc = scale_of(T);
+        if (k == 0 || k >= kSumFrom) {
+            h.exp = exponent(sc, best);
+            u64 sum = 0;
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+                for (int i = 0; i < kVec; i += 2) sum += weights2(sc, v[j][i], v[j][i + 1], h.exp);
+            sum = warp_sum(sum);
+            if (lane == 0) s_sum[warp] = sum;
+        }
+        uint32_t a = kNone + 1;
+        if (h.cands > R.cap) {
+            // a threshold that `w` threads reach and few elements more
+            const int threads = __syncthreads_count(mine > kNone);
+            const int w = max(1, min(k > 0 ? min(want, 2 * k / static_cast<int>(gridDim.x) + 8) : want, threads / 2));
+            uint32_t b = top;  // w threads reach a; look in a .. b
+            if (threads == kScanThreads) {  // all threads reach the least of their maxima
+                uint32_t m = __reduce_min_sync(0xffffffffu, mine);
+                if (lane == 0) s_lo[warp] = m;
+                __syncthreads();
+                a = b;
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) a = min(a, s_lo[x]);
+            }
+            while (a < b) {
+                const uint32_t mid = a + (b - a) / 2 + 1;
+                const int n = __syncthreads_count(mine >= mid);
+                if (n >= w)
+                    a = mid;
+                else
+                    b = mid - 1;
+                if (n >= w && n <= w + w / 4) break;
+            }
+        }
+        u64 *list = R.list + (static_cast<long long>(row) * R.slices + slice) * R.cap;
+        auto put = [&](uint32_t least) {  // the elements from `least` on, as far as there is room
+            if (mine < least) return;
+            const float from = value_of(least);
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+                for (int i = 0; i < kVec; ++i)
+                    if (v[j][i] >= from) {
+                        const int at = atomicAdd(&s_count, 1);
+                        if (at < R.cap) list[at] = rank_of(key_of(v[j][i]), in.index(u0 + j * kScanThreads, i));
+                    }
+        };
+        put(a);
+        __syncthreads();
+        h.count = s_count;
+        if (h.count <= R.cap) {
+            h.theta = a;
+        } else {  // many equal ones at the threshold: leave them out
+            __syncthreads();
+            if (tid == 0) s_count = 0;
+            __syncthreads();
+            if (a < top) put(a + 1);
+            __syncthreads();
+            h.count = s_count;
+            if (a < top && h.count <= R.cap)
+                h.theta = a + 1;
+            else
+                h.count = 0;
+        }
+        if (k == 0 || k >= kSumFrom)
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) h.sum += s_sum[w];
+    }
+    // the CTA's writes are visible device-wide before the slice counts as finished
+    __syncthreads();
+    if (tid == 0) {
+        h.best = top > kNone ? rank_of(top, s_first) : 0ull;
+        R.head[static_cast<long long>(row) * R.slices + slice] = h;
+        __threadfence();
+        s_count = atomicInc(R.done + row, R.slices - 1) == static_cast<unsigned>(R.slices - 1);
+        __threadfence();
+    }
+    __syncthreads();
+    if (!s_count) return;
+    // the row's last slice
+    __shared__ PickShared P;
+    int tok;
+    float pr;
+    bool refused;
+    const bool settled = pick(R, S, row, T, k, P, tok, pr, refused);
+    if (tid == 0) {
+        if (settled) {
+            token[row] = tok;
+            if (prob) prob[row] = pr;
+        }
+        R.deep[row] = settled ? 0 : 1;
+        if (refused && status) atomicExch(status, GQ_ERR_SHAPE);
+    }
 }
 
 // ---------------------------------------------------------------- deep
-struct __align__(16) Part {  // one CTA's part of a pass over the row
-    u64 before, inside, lowest, highest;
-    unsigned count, pad;
+// What stands in all steps up to each, and its weight with that in front of the first.
+struct Level {
+    unsigned count[kBins];
+    u64 weight[kBins];
 };
 struct DeepShared {
     u64 list[kList], F[kList];
     unsigned steps[kList];
-    unsigned hist[kBins], coarse[kBins], fine[kBins];  // fine, coarse: running counts
-    float est[kBins];                                  // running estimate of the weight, in units of the largest
-    Part part[kDeepCtas];
-    u64 sh[kDeepThreads / 32];
+    unsigned hist[kBins], low[kBins], high[kBins];  // this CTA's counts, and weights as two words
+    Level coarse, fine;
+    u64 sh[kDeepThreads / 32], sh2[kDeepThreads / 32];
     unsigned sh32[kDeepThreads / 32];
-    float shf[kDeepThreads / 32];
-    RowHead head;
+    RowHead heads[kDeepThreads / 32];
+    u64 least[kDeepCtas];  // weights that min_p keeps
+    u64 rank, reached;          // what a search found: the element, and the running weight at it
     int found;
+    unsigned listed;
 };
 
 template <int TYPE>
 __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1)
-    k_sample_deep(Rows R, Settings S, int32_t *token, float *prob)
+    k_sample_deep(Rows R, Settings S, int n_rows, int32_t *token, float *prob)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     DeepShared &D = *reinterpret_cast<DeepShared *>(raw);
     constexpr int kVec = Reader<TYPE>::kVec, kPer = kBins / kDeepThreads;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y;
-    pdl_launch_dependents();
-    pdl_wait();
-    if (R.deep[row] == 0) return;  // the whole cluster
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto cluster = cg::this_cluster();
     const int me = static_cast<int>(cluster.block_rank());
-    const float T = temperature(S, row), p = S.top_p ? __ldg(S.top_p + row) : 1.f, mp = S.min_p ? __ldg(S.min_p + row) : 0.f,
-                u = __ldg(S.u + row);
-    const int k = top_k(S, row, R.vocab);
-    if (warp == 0) {
-        const RowHead r = row_head(R.head + static_cast<long long>(row) * R.slices, R.slices);
-        if (lane == 0) D.head = r;
-    }
-    for (int i = tid; i < kBins; i += kDeepThreads) D.hist[i] = 0;
-    __syncthreads();
-    const RowHead h = D.head;
-    const float largest = value_of(static_cast<uint32_t>(h.best >> 32));
-    const Scale sc = scale_of(T, largest);
-    const int top = exponent(sc, largest);
-    // steps of the exponent; everything 50 octaves down is one step
-    // (the products rounded alike: fused with the difference they would leave the largest's rounding, of either sign)
-    auto exponent_of = [&](float v) { return __fmul_rn(v - sc.base, sc.ch); };
-    const float t_top = exponent_of(largest);
-    const float range = fminf(fmaxf(t_top - exponent_of(value_of(h.lowest)), 0.001f), 50.f), per = kBins / range;
-    auto step_of = [&](float v) { return max(0, min(kBins - 1, __float2int_rz((t_top - exponent_of(v)) * per))); };
+    pdl_launch_dependents();
+    pdl_wait();
+#pragma unroll 1
+    for (int row = blockIdx.y; row < n_rows; row += gridDim.y) {
+        if (R.deep[row] == 0) continue;  // the whole cluster
+        const float T = temperature(S, row), p = S.top_p ? __ldg(S.top_p + row) : 1.f, mp = S.min_p ? __ldg(S.min_p + row) : 0.f,
+                    u = __ldg(S.u + row);
+        const int k = top_k(S, row, R.vocab);
+        RowHead h{0ull, kUnknown, 0u, 0};
+        for (int i = tid; i < R.slices; i += kDeepThreads) add_head(h, load_header(R.head + static_cast<long long>(row) * R.slices + i));
+        h = join_heads<kDeepThreads>(h, D.heads);
+        const float largest = value_of(static_cast<uint32_t>(h.best >> 32));
+        const Scale sc = scale_of(T, largest);
+        const int top = exponent(sc, largest);
+        // equal steps of the exponent; everything 50 octaves down is one step
+        // (the products rounded alike: fused with the difference they would leave the largest's rounding, of either sign)
+        auto exponent_of = [&](float v) { return __fmul_rn(v - sc.base, sc.ch); };
+        const float t_top = exponent_of(largest);
+        const float range = fminf(fmaxf(t_top - exponent_of(value_of(h.lowest)), 0.001f), 50.f), per = kBins / range;
+        auto step_of = [&](float v) { return max(0, min(kBins - 1, __float2int_rz((t_top - exponent_of(v)) * per))); };
 
-    const Reader<TYPE> in(R.logits + row * R.row_bytes, R.vocab);
-    const int cta_units = (in.units + kDeepCtas - 1) / kDeepCtas, first = me * cta_units, end = min(first + cta_units, in.units);
-    auto each = [&](auto &&f) {  // every candidate of this CTA's part of the row
-        for (int q = first + tid; q < end; q += kDeepThreads) {
-            float v[kVec];
-            in.load(q, v);
+        const Reader<TYPE> in(R.logits + row * R.row_bytes, R.vocab);
+        const int cta_units = (in.units + kDeepCtas - 1) / kDeepCtas, first = me * cta_units, end = min(first + cta_units, in.units);
+        auto each = [&](auto &&f) {  // this CTA's part of the row, a 16-byte unit at a time, four loads in flight
+            constexpr int kBatch = 4;
+#pragma unroll 1
+            for (int q0 = first + tid; q0 < end; q0 += kBatch * kDeepThreads) {
+                uint4 w[kBatch];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int q = q0 + j * kDeepThreads;
+                    if (q < end && in.inside(q)) w[j] = in.word(q);
+                }
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int q = q0 + j * kDeepThreads;
+                    if (q >= end) break;
+                    float v[kVec];
+                    if (in.inside(q))
+                        in.values(w[j], v);
+                    else
+                        in.load(q, v);
+                    f(v, in.index(q, 0));
+                }
+            }
+        };
+        auto clear = [&] {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) D.hist[tid + i * kDeepThreads] = D.low[tid + i * kDeepThreads] = D.high[tid + i * kDeepThreads] = 0;
+            __syncthreads();
+        };
+        // One element in step b.  Its weight is added to two words, the carry found from the word's old value.
+        auto add = [&](int b, u64 w) {
+            atomicAdd(&D.hist[b], 1u);
+            const unsigned lo = static_cast<unsigned>(w), old = atomicAdd(&D.low[b], lo);
+            const unsigned hi = static_cast<unsigned>(w >> 32) + (old + lo < old ? 1u : 0u);
+            if (hi) atomicAdd(&D.high[b], hi);
+        };
+        // The CTAs' histograms, added up and summed over the steps, in every CTA's L; `base` in front.
+        auto merge = [&](Level &L, u64 base) {
+            constexpr int kShare = kBins / kDeepCtas;
+            cluster.sync();
+            for (int i = tid; i < kShare; i += kDeepThreads) {
+                const int b = me * kShare + i;
+                unsigned n = 0;
+                u64 w = 0;
+#pragma unroll 2
+                for (int c = 0; c < kDeepCtas; ++c) {
+                    n += cluster.map_shared_rank(D.hist, c)[b];
+                    w += static_cast<u64>(cluster.map_shared_rank(D.high, c)[b]) << 32;
+                    w += cluster.map_shared_rank(D.low, c)[b];
+                }
+#pragma unroll 2
+                for (int c = 0; c < kDeepCtas; ++c) {
+                    Level *to = cluster.map_shared_rank(&L, c);
+                    to->count[b] = n;
+                    to->weight[b] = w;
+                }
+            }
+            cluster.sync();
+            unsigned n[kPer], ns = 0;
+            u64 w[kPer], ws = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                ns += n[i] = L.count[tid * kPer + i];
+                ws += w[i] = L.weight[tid * kPer + i];
+            }
+            unsigned ni = ns;
+            u64 wi = ws;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned a = __shfl_up_sync(0xffffffffu, ni, o);
+                const u64 b = __shfl_up_sync(0xffffffffu, wi, o);
+                if (lane >= o) {
+                    ni += a;
+                    wi += b;
+                }
+            }
+            if (lane == 31) {
+                D.sh32[warp] = ni;
+                D.sh2[warp] = wi;
+            }
+            __syncthreads();
+            ni -= ns;
+            wi += base - ws;
+            for (int x = 0; x < warp; ++x) {
+                ni += D.sh32[x];
+                wi += D.sh2[x];
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                L.count[tid * kPer + i] = ni += n[i];
+                L.weight[tid * kPer + i] = wi += w[i];
+            }
+            __syncthreads();
+        };
+
+        // ---- the row's steps
+        bool rest = false;
+        const u64 w0 = row_weight(sc, largest, top);
+        const u64 thr = mp < 1.f ? (mp > 0.f ? part_of(mp, w0, rest) + (rest ? 1 : 0) : 0ull) : w0;
+        u64 least = 0;
+        if (tid == 0) D.listed = 0;
+        clear();
+        each([&](const float (&v)[kVec], int) {
 #pragma unroll
             for (int i = 0; i < kVec; ++i)
-                if (v[i] > -INFINITY) f(v[i], in.index(q, i));
-        }
-    };
-    // The CTAs' parts, added up in every CTA.
-    auto exchange = [&](Part x) {
-        __syncthreads();
-        x.before = cta_sum<kDeepThreads>(x.before, D.sh);
-        x.inside = cta_sum<kDeepThreads>(x.inside, D.sh);
-        cluster.sync();
-        if (tid < kDeepCtas) *cluster.map_shared_rank(&D.part[me], tid) = x;
-        cluster.sync();
-        Part s{0, 0, ~0ull, 0, 0, 0};
-        for (int c = 0; c < kDeepCtas; ++c) {
-            s.before += D.part[c].before;
-            s.inside += D.part[c].inside;
-            s.lowest = min(s.lowest, D.part[c].lowest);
-            s.highest = max(s.highest, D.part[c].highest);
-            s.count += D.part[c].count;
-        }
-        return s;
-    };
-    // The CTAs' histograms, added up and summed over the steps, in `out` of every CTA.
-    auto merge = [&](unsigned *out) {
-        cluster.sync();
-        constexpr int kShare = kBins / kDeepCtas;
-        for (int i = tid; i < kShare; i += kDeepThreads) {
-            unsigned s = 0;
-            for (int c = 0; c < kDeepCtas; ++c) s += cluster.map_shared_rank(D.hist, c)[me * kShare + i];
-            for (int c = 0; c < kDeepCtas; ++c) cluster.map_shared_rank(out, c)[me * kShare + i] = s;
-        }
-        cluster.sync();
-        unsigned n[kPer], mine = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) mine += n[i] = out[tid * kPer + i];
-        unsigned incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned up = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += up;
-        }
-        if (lane == 31) D.sh32[warp] = incl;
-        __syncthreads();
-        unsigned at = incl - mine;
-        for (int w = 0; w < warp; ++w) at += D.sh32[w];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) out[tid * kPer + i] = at += n[i];
-        __syncthreads();
-    };
-    // First step for which `ok` holds (it holds from some step on), else the last.
-    auto first_step = [&](auto &&ok) {
-        if (tid == 0) D.found = kBins - 1;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int b = tid * kPer + i;
-            if (ok(b) && (b == 0 || !ok(b - 1))) atomicMin(&D.found, b);
-        }
-        __syncthreads();
-        const int b = D.found;
-        __syncthreads();
-        return b;
-    };
+                if (v[i] > -INFINITY) {
+                    const u64 w = row_weight(sc, v[i], top);
+                    add(step_of(v[i]), w);
+                    least += w >= thr ? w : 0ull;
+                }
+        });
+        least = cta_sum<kDeepThreads>(least, D.sh);
+        if (tid < kDeepCtas) cluster.map_shared_rank(D.least, tid)[me] = least;
+        merge(D.coarse, 0ull);  // (the barriers that `least` needs in it)
+        least = 0;
+        for (int c = 0; c < kDeepCtas; ++c) least += D.least[c];
 
-    // ---- the row's weight, and the histogram
-    bool rest = false;
-    const u64 w0 = row_weight(sc, largest, top);
-    const u64 thr = mp < 1.f ? (mp > 0.f ? part_of(mp, w0, rest) + (rest ? 1 : 0) : 0ull) : w0;
-    Part x{0, 0, 0, 0, 0, 0};
-    each([&](float v, int) {
-        atomicAdd(&D.hist[step_of(v)], 1u);
-        const u64 w = row_weight(sc, v, top);
-        x.before += w;
-        x.inside += w >= thr ? w : 0ull;
-    });
-    const Part sums = exchange(x);
-    merge(D.coarse);
-    {
-        float e[kPer], mine = 0.f;
+        // ---- three times the first element at which a running count or weight reaches X: the last that top_k keeps,
+        // the last that top_p keeps, the drawn one
+        u64 z = D.coarse.weight[kBins - 1], kept = z;
+#pragma unroll 1
+        for (int phase = 0; phase < 3; ++phase) {
+            const bool by_count = phase == 0;
+            u64 X;
+            if (phase == 0) {
+                if (k == 0 || static_cast<unsigned>(k) >= D.coarse.count[kBins - 1]) continue;
+                X = static_cast<u64>(k);
+            } else if (phase == 1) {
+                if (mp > 0.f) kept = min(kept, least);
+                if (!(p < 1.f)) continue;
+                X = nucleus(p, z);
+            } else {
+                X = drawn(u, kept);
+            }
+            const Level *L = &D.coarse;
+            unsigned skip = 0;      // elements in front of the level's first step
+            u64 base = 0;           // and their weight
+            u64 high = 0, low = 0;  // ranks that the level divides (below the first level)
+            int shift = 0;
+#pragma unroll 1
+            while (true) {
+                // the first step in which X is reached; it holds an element
+                if (tid == 0) D.found = kBins - 1;
+                __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int b = tid * kPer + i;
-            mine += static_cast<float>(D.coarse[b] - (b ? D.coarse[b - 1] : 0u)) * exp2f(-(b + 0.5f) / per);
-            e[i] = mine;
-        }
-        float incl = mine;
+                for (int i = 0; i < kPer; ++i) {
+                    const int b = tid * kPer + i;
+                    auto reaches = [&](int x) { return by_count ? L->count[x] + skip >= X : L->weight[x] >= X; };
+                    if (reaches(b) && !(b > 0 && reaches(b - 1))) atomicMin(&D.found, b);
+                }
+                __syncthreads();
+                const int b = D.found;
+                const unsigned in_front = b ? L->count[b - 1] : 0u, in_step = L->count[b] - in_front;
+                const u64 weight_in_front = b ? L->weight[b - 1] : base;
+                const bool divided = L != &D.coarse;
+                if (in_step <= kList) {
+                    // its elements, to the first CTA, which sorts them
+                    unsigned *counter = cluster.map_shared_rank(&D.listed, 0);
+                    u64 *list = cluster.map_shared_rank(D.list, 0);
+                    each([&](const float (&v)[kVec], int index) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float up = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += up;
-        }
-        if (lane == 31) D.shf[warp] = incl;
-        __syncthreads();
-        float at = incl - mine;
-        for (int w = 0; w < warp; ++w) at += D.shf[w];
+                        for (int i = 0; i < kVec; ++i) {
+                            if (!(v[i] > -INFINITY)) continue;
+                            const u64 r = rank_of(key_of(v[i]), index + i);
+                            const bool here = divided ? r <= high && r >= low && static_cast<int>((high - r) >> shift) == b : step_of(v[i]) == b;
+                            if (here) {
+                                const unsigned at = atomicAdd(counter, 1u);
+                                if (at < kList) list[at] = r;
+                            }
+                        }
+                    });
+                    cluster.sync();
+                    if (me == 0) {
+                        const int n = min(static_cast<int>(D.listed), kList);
+                        u64 most = 0, fewest = ~0ull;
+                        for (int i = tid; i < n; i += kDeepThreads) {
+                            most = max(most, D.list[i]);
+                            fewest = min(fewest, D.list[i]);
+                        }
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) D.est[tid * kPer + i] = at + e[i];
-        __syncthreads();
-    }
-
-    // ---- the first element at which the running count (by_count) or weight reaches X: its place in the sorted
-    // list, with the running weights in F
-    auto find = [&](u64 X, bool by_count) {
-        bool nested = false;
-        u64 high = 0, low = 0;  // nested: the elements between
-        int shift = 0;
-        u64 base = 0;           // weight in front of the steps
-        const unsigned *C = D.coarse;
-        const float target = __ull2float_rn(X) * (D.est[kBins - 1] / __ull2float_rn(max(sums.before, 1ull)));
-        int b = by_count ? first_step([&](int i) { return C[i] >= X; }) : first_step([&](int i) { return D.est[i] >= target; });
-        int lo = 0, hi = kBins - 1;
-        for (int tries = 0;; ++tries) {
-            const unsigned in_step = C[b] - (b ? C[b - 1] : 0u);
-            // -1: in front of the step, 0: in it, 1: behind
-            auto side = [&](float v, int e) {
-                int s;
-                if (!nested) {
-                    s = step_of(v);
+                        for (int o = 16; o > 0; o >>= 1) {
+                            most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                            fewest = min(fewest, __shfl_xor_sync(0xffffffffu, fewest, o));
+                        }
+                        if (lane == 0) {
+                            D.sh[warp] = most;
+                            D.sh2[warp] = fewest;
+                        }
+                        __syncthreads();
+                        for (int w = 0; w < kDeepThreads / 32; ++w) {
+                            most = max(most, D.sh[w]);
+                            fewest = min(fewest, D.sh2[w]);
+                        }
+                        sort_down<kDeepThreads>(D.list, D.F, D.steps, n, most, fewest, D.sh32);
+                        running_weights<kDeepThreads>(D.list, D.F, n, weight_in_front, sc, top, D.sh);
+                        int at = by_count ? static_cast<int>(X - skip - in_front) - 1 : reach(D.F, n, X);
+                        at = max(min(at, n - 1), 0);
+                        if (tid < kDeepCtas) {
+                            *cluster.map_shared_rank(&D.rank, tid) = D.list[at];
+                            *cluster.map_shared_rank(&D.reached, tid) = D.F[at];
+                        }
+                        if (tid == 0) D.listed = 0;
+                    }
+                    cluster.sync();
+                    break;
+                }
+                // too many: divide it by the bits of (logit, index), which no two elements share
+                if (!divided) {
+                    // the smallest number in the step and the largest, by bisection of all numbers in their order
+                    uint32_t lo = kNone + 1, hi = static_cast<uint32_t>(h.best >> 32);
+                    while (lo < hi) {
+                        const uint32_t mid = lo + (hi - lo) / 2;
+                        if (step_of(value_of(mid)) <= b)
+                            hi = mid;
+                        else
+                            lo = mid + 1;
+                    }
+                    low = rank_of(lo, R.vocab - 1);
+                    hi = static_cast<uint32_t>(h.best >> 32);
+                    while (lo < hi) {
+                        const uint32_t mid = hi - (hi - lo) / 2;
+                        if (step_of(value_of(mid)) >= b)
+                            lo = mid;
+                        else
+                            hi = mid - 1;
+                    }
+                    high = rank_of(lo, 0);
                 } else {
-                    const u64 r = rank_of(key_of(v), e);
-                    if (r > high || r < low) return 1;  // in front of all steps: in `base`
-                    s = static_cast<int>((high - r) >> shift);
+                    high -= static_cast<u64>(b) << shift;
+                    low = max(low, high - ((1ull << shift) - 1));
                 }
-                return s < b ? -1 : (s > b ? 1 : 0);
-            };
-            Part y{0, 0, ~0ull, 0, 0, 0};
-            const bool listable = in_step <= kList;
-            u64 *mine = D.F;  // this CTA's part of the list
-            __syncthreads();
-            if (tid == 0) D.found = 0;
-            __syncthreads();
-            u64 least = ~0ull, most = 0;
-            each([&](float v, int e) {
-                const int s = side(v, e);
-                if (s > 0) return;
-                const u64 w = row_weight(sc, v, top);
-                if (s < 0) {
-                    y.before += w;
-                    return;
-                }
-                y.inside += w;
-                const u64 r = rank_of(key_of(v), e);
-                if (listable)
-                    mine[atomicAdd(&D.found, 1)] = r;
-                least = min(least, r);
-                most = max(most, r);
-            });
-            // the CTA's lowest and highest
+                skip += in_front;
+                base = weight_in_front;
+                shift = max(0, 53 - __clzll(static_cast<long long>(high - low)));
+                clear();
+                each([&](const float (&v)[kVec], int index) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-                most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                    for (int i = 0; i < kVec; ++i) {
+                        if (!(v[i] > -INFINITY)) continue;
+                        const u64 r = rank_of(key_of(v[i]), index + i);
+                        if (r <= high && r >= low) add(static_cast<int>((high - r) >> shift), row_weight(sc, v[i], top));
+                    }
+                });
+                merge(D.fine, base);
+                L = &D.fine;
             }
-            __syncthreads();
-            const int mine_n = D.found;
-            if (lane == 0) D.sh[warp] = least;
-            __syncthreads();
-            for (int w = 0; w < kDeepThreads / 32; ++w) least = min(least, D.sh[w]);
-            __syncthreads();
-            if (lane == 0) D.sh[warp] = most;
-            __syncthreads();
-            for (int w = 0; w < kDeepThreads / 32; ++w) most = max(most, D.sh[w]);
-            y.lowest = least;
-            y.highest = most;
-            y.count = listable ? static_cast<unsigned>(mine_n) : 0u;
-            const Part all = exchange(y);
-            const u64 before = base + all.before;
-            if (!by_count) {  // was the estimate right?
-                int move = before >= X ? -1 : (before + all.inside < X ? 1 : 0);
-                if (move < 0) hi = b - 1;
-                if (move > 0) lo = b + 1;
-                if (move != 0 && lo <= hi) {
-                    b = tries < 4 ? b + move : (lo + hi) / 2;
-                    continue;
-                }
+            if (phase == 0)
+                z = kept = D.reached;
+            else if (phase == 1)
+                kept = min(kept, D.reached);
+            else if (me == 0 && tid == 0) {
+                token[row] = index_of(D.rank);
+                if (prob) prob[row] = ratio(row_weight(sc, value_of(static_cast<uint32_t>(D.rank >> 32)), top), kept);
             }
-            if (listable) {
-                int at = 0;
-                for (int c = 0; c < me; ++c) at += static_cast<int>(D.part[c].count);
-                for (int i = tid; i < mine_n; i += kDeepThreads) {
-                    const u64 r = mine[i];
-                    for (int c = 0; c < kDeepCtas; ++c) cluster.map_shared_rank(D.list, c)[at + i] = r;
-                }
-                cluster.sync();
-                const int n = static_cast<int>(all.count);
-                sort_down<kDeepThreads>(D.list, D.F, D.steps, n, value_of(static_cast<uint32_t>(all.highest >> 32)),
-                                        value_of(static_cast<uint32_t>(all.lowest >> 32)), D.sh32);
-                running_weights<kDeepThreads>(D.list, D.F, n, before, sc, top, D.sh);
-                const int j = by_count ? static_cast<int>(X - (b ? C[b - 1] : 0u)) - 1 : reach(D.F, n, X);
-                return max(min(j, n - 1), 0);
-            }
-            // too many for the list: divide the step by the bits of its elements
-            if (by_count) X -= b ? C[b - 1] : 0u;
-            base = before;
-            high = all.highest;
-            low = all.lowest;
-            shift = max(0, 53 - __clzll(static_cast<long long>(high - low)));
-            nested = true;
-            __syncthreads();
-            for (int i = tid; i < kBins; i += kDeepThreads) D.hist[i] = 0;
-            __syncthreads();
-            each([&](float v, int e) {
-                const u64 r = rank_of(key_of(v), e);
-                if (r <= high && r >= low) atomicAdd(&D.hist[(high - r) >> shift], 1u);
-            });
-            merge(D.fine);
-            C = D.fine;
-            // the step's weights are nearly equal
-            const float want = by_count ? 0.f
-                                        : __ull2float_rn(X - before) / fmaxf(__ull2float_rn(all.inside), 1.f) * static_cast<float>(in_step);
-            b = by_count ? first_step([&](int i) { return C[i] >= X; })
-                         : first_step([&](int i) { return static_cast<float>(C[i]) >= want; });
-            lo = 0;
-            hi = kBins - 1;
-            tries = -1;
         }
-    };
-
-    u64 kept = sums.before;
-    if (k > 0 && k < h.cands) {
-        const int j = find(static_cast<u64>(k), true);
-        kept = D.F[j];
+        cluster.sync();  // no CTA goes on while another reads its memory
     }
-    const u64 z = kept;
-    if (mp > 0.f) kept = min(kept, sums.inside);
-    if (p < 1.f) {
-        const int j = find(nucleus(p, z), false);
-        kept = min(kept, D.F[j]);
-    }
-    const u64 X = drawn(u, kept);
-    const int j = find(X, false);
-    if (me == 0 && tid == 0) {
-        // the weight of the drawn one: `find` left its list and the running weights
-        token[row] = index_of(D.list[j]);
-        if (prob) prob[row] = ratio(row_weight(sc, value_of(static_cast<uint32_t>(D.list[j] >> 32)), top), kept);
-    }
-    cluster.sync();  // no CTA leaves while another reads its memory
 }
 
 // ---------------------------------------------------------------- host
@@ -1066,6 +1182,8 @@ Plan plan_for(int vocab, int n_rows)
     p.want = want < 4 ? 4 : (want > kScanThreads / 2 ? kScanThreads / 2 : want);
     return p;
 }
+// The counters stand in front, the same for every call, so that a workspace serves calls of any size.
+constexpr size_t kCounterBytes = GQ_MAX_SAMPLE_ROWS * sizeof(unsigned);
 size_t up16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
 template <int TYPE>
@@ -1074,10 +1192,12 @@ cudaError_t launch(Rows R, const Settings &S, const Plan &p, int n_rows, int32_t
     auto deep = k_sample_deep<TYPE>;
     if (ctas_per_sm(reinterpret_cast<const void *>(deep), kDeepThreads, sizeof(DeepShared)) < 1) return cudaErrorInvalidConfiguration;
     const dim3 grid(p.slices, n_rows);
-    cudaError_t e = p.ept == 8 ? launch_pdl(k_sample_scan<TYPE, 8>, grid, dim3(kScanThreads), 0, s, R, S, p.want)
-                               : launch_pdl(k_sample_scan<TYPE, 32>, grid, dim3(kScanThreads), 0, s, R, S, p.want);
-    if (e == cudaSuccess) e = launch_pdl(k_sample_pick, dim3(n_rows), dim3(kPickThreads), 0, s, R, S, token, prob, status_word());
-    if (e == cudaSuccess) e = launch_pdl(deep, dim3(kDeepCtas, n_rows), dim3(kDeepThreads), sizeof(DeepShared), s, R, S, token, prob);
+    int *status = status_word();
+    cudaError_t e = p.ept == 8 ? launch_pdl(k_sample_scan<TYPE, 8>, grid, dim3(kScanThreads), 0, s, R, S, p.want, token, prob, status)
+                               : launch_pdl(k_sample_scan<TYPE, 32>, grid, dim3(kScanThreads), 0, s, R, S, p.want, token, prob, status);
+    if (e == cudaSuccess)
+        e = launch_pdl(deep, dim3(kDeepCtas, n_rows < kDeepClusters ? n_rows : kDeepClusters), dim3(kDeepThreads), sizeof(DeepShared), s, R,
+                       S, n_rows, token, prob);
     return e;
 }
 
@@ -1092,10 +1212,10 @@ extern "C" {
 
 size_t gq_sample_workspace_bytes(int vocab, int n_rows)
 {
-    if (vocab < 1 || vocab > GQ_MAX_VOCAB || n_rows < 1 || n_rows > 65535) return 0;
+    if (vocab < 1 || vocab > GQ_MAX_VOCAB || n_rows < 1 || n_rows > GQ_MAX_SAMPLE_ROWS) return 0;
     const Plan p = plan_for(vocab, n_rows);
     const size_t slices = static_cast<size_t>(p.slices) * n_rows;
-    return slices * sizeof(Header) + (slices << p.cap_log2) * sizeof(u64) + up16(static_cast<size_t>(n_rows) * sizeof(int));
+    return kCounterBytes + slices * sizeof(Header) + (slices << p.cap_log2) * sizeof(u64) + up16(static_cast<size_t>(n_rows) * sizeof(int));
 }
 
 int gq_sample(const void *logits, long long ldl, int type, const float *temperature, const int32_t *top_k,
@@ -1103,7 +1223,7 @@ int gq_sample(const void *logits, long long ldl, int type, const float *temperat
               void *workspace, size_t workspace_bytes, int vocab, int n_rows, gq_stream_t stream)
 {
     if (type != GQ_TYPE_F32 && type != GQ_TYPE_F16 && type != GQ_TYPE_BF16) return GQ_ERR_FORMAT;
-    if (vocab < 1 || vocab > GQ_MAX_VOCAB || n_rows < 0 || n_rows > 65535 || ldl < vocab || ldl > (1ll << 40)) return GQ_ERR_SHAPE;
+    if (vocab < 1 || vocab > GQ_MAX_VOCAB || n_rows < 0 || n_rows > GQ_MAX_SAMPLE_ROWS || ldl < vocab || ldl > (1ll << 40)) return GQ_ERR_SHAPE;
     if (n_rows == 0) return GQ_OK;
     if (!logits || !u || !token) return GQ_ERR_NULL;
     if (!aligned_to(logits, kv::type_size(type)) || !aligned_to(temperature, 4) || !aligned_to(top_k, 4) || !aligned_to(top_p, 4) ||
@@ -1114,15 +1234,17 @@ int gq_sample(const void *logits, long long ldl, int type, const float *temperat
     const Plan p = plan_for(vocab, n_rows);
     const size_t slices = static_cast<size_t>(p.slices) * n_rows;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
+    uint8_t *const heads = ws + kCounterBytes, *const lists = heads + slices * sizeof(Header);
     const Rows R{static_cast<const uint8_t *>(logits),
                  ldl * kv::type_size(type),
                  vocab,
                  p.slices,
                  1 << p.cap_log2,
                  p.cap_log2,
-                 reinterpret_cast<Header *>(ws),
-                 reinterpret_cast<u64 *>(ws + slices * sizeof(Header)),
-                 reinterpret_cast<int *>(ws + slices * sizeof(Header) + (slices << p.cap_log2) * sizeof(u64))};
+                 reinterpret_cast<Header *>(heads),
+                 reinterpret_cast<u64 *>(lists),
+                 reinterpret_cast<unsigned *>(ws),
+                 reinterpret_cast<int *>(lists + (slices << p.cap_log2) * sizeof(u64))};
     const Settings S{temperature, top_k, top_p, min_p, u};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (type) {

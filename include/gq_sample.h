@@ -16,8 +16,9 @@
 extern "C" {
 #endif
 
-/* Largest vocab of gq_sample. */
+/* Largest vocab and n_rows of gq_sample. */
 #define GQ_MAX_VOCAB 1048576
+#define GQ_MAX_SAMPLE_ROWS 16384
 
 /* ---------------------------------------------------------------------------
  * For every row l of the logits, with temperature T, top_k, top_p, min_p and u:
@@ -45,14 +46,16 @@ extern "C" {
  *           limit, no limit, no limit.
  *   token   int32[n_rows]; prob f32[n_rows] or NULL.
  *   workspace  device memory, 16-byte aligned, at least
- *           gq_sample_workspace_bytes bytes, scratch before and after the call.
- *           Two calls that may run concurrently must not share it.
+ *           gq_sample_workspace_bytes bytes.  ZERO-FILL IT ONCE before its first
+ *           use; every completed call leaves it ready for the next, of any size
+ *           that fits.  Two calls that may run concurrently must not share it.
  * Arithmetic: weights are whole numbers of 2^-43 of about the largest weight, each within
  * 2^-23 of itself and 2^-42 of the largest; their sums are exact.  So the
  * result does not depend on how the row was split, the same inputs give the
  * same token, and a token differs from that of exact weights only where
  * u (or top_p, min_p) lies within rounding of a boundary.
- * Range: 1 <= vocab <= GQ_MAX_VOCAB, 0 <= n_rows <= 65535 (0: nothing to do).
+ * Range: 1 <= vocab <= GQ_MAX_VOCAB, 0 <= n_rows <= GQ_MAX_SAMPLE_ROWS (0:
+ * nothing to do).
  * Errors before the launches: GQ_ERR_FORMAT (type), GQ_ERR_NULL, GQ_ERR_ALIGN,
  * GQ_ERR_SHAPE, GQ_ERR_WORKSPACE; after them GQ_ERR_CUDA.
  * ------------------------------------------------------------------------ */

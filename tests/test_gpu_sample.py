@@ -66,7 +66,7 @@ def sample(x, typ, T=None, k=None, p=None, m=None, u=0.5, with_prob=True, ws=Non
     token = t.full((n + 2,), -77, dtype=t.int32, device="cuda")
     prob = t.full((n + 2,), -77.0, device="cuda")
     if ws is None:
-        ws = t.full((gq.gq_sample_workspace_bytes(vocab, n),), 0xA5, dtype=t.uint8, device="cuda")
+        ws = t.zeros(gq.gq_sample_workspace_bytes(vocab, n), dtype=t.uint8, device="cuda")
     gq.gq_sample(x, x.stride(0), TYPES[typ], arr(T, np.float32), arr(k, np.int32), arr(p, np.float32), arr(m, np.float32),
                  arr(u, np.float32), token, prob if with_prob else None, ws, ws.numel(), vocab, n)
     token, prob = token.cpu().numpy(), prob.cpu().numpy()
@@ -235,7 +235,7 @@ def test_captured_and_replayed_with_other_logits_and_settings():
     t = torch()
     g = np.random.default_rng(12)
     n, vocab = 6, 20011
-    ws = t.empty(gq.gq_sample_workspace_bytes(vocab, n), dtype=t.uint8, device="cuda")
+    ws = t.zeros(gq.gq_sample_workspace_bytes(vocab, n), dtype=t.uint8, device="cuda")
     x, T, u = t.zeros(n, vocab, device="cuda"), t.ones(n, device="cuda"), t.zeros(n, device="cuda")
     k = t.zeros(n, dtype=t.int32, device="cuda")
     token, prob = t.zeros(n, dtype=t.int32, device="cuda"), t.zeros(n, device="cuda")
@@ -271,6 +271,25 @@ def test_two_streams_with_a_workspace_each():
             with t.cuda.stream(streams[i]):
                 got = sample(x, "f32", u=u, p=0.9)
             assert np.array_equal(got[0], alone[i][0]) and np.array_equal(got[1], alone[i][1])
+
+
+def test_one_workspace_for_calls_of_any_size():
+    t = torch()
+    g = np.random.default_rng(15)
+    ws = t.zeros(max(gq.gq_sample_workspace_bytes(*s) for s in ((60000, 30), (300, 700), (200000, 1))), dtype=t.uint8, device="cuda")
+    for vocab, n in ((60000, 30), (300, 700), (200000, 1), (300, 2), (60000, 29), (5, 1)):
+        x, s = logits(g, n, vocab, vocab % 1000 == 0), settings(g, n, vocab)
+        got, want = sample(x, "f32", **s, ws=ws), sample(x, "f32", **s)
+        assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("limit", [dict(m=0.3), dict(m=0.02, p=0.9), dict(p=0.2), dict(p=0.5), {}])
+def test_a_top_k_beyond_the_list(limit):
+    """Whether the list settles it depends on the other limits; sharp and flat rows."""
+    g = np.random.default_rng(16)
+    n, vocab = 30, 50000
+    x = logits(g, n, vocab, True) * np.linspace(0.3, 2.0, n)[:, None]
+    check(x, "f32", u=g.random(n), k=g.choice([1500, 4000, 20000, 49999], n), **limit)
 
 
 def test_the_largest_vocabulary():

@@ -96,12 +96,12 @@ def test_sample():
     refuses(name, SAMPLE, gq.GQ_ERR_FORMAT, type=[-1, 3])
     refuses(name, SAMPLE, gq.GQ_ERR_NULL, logits=[None], u=[None], token=[None])
     refuses(name, SAMPLE, gq.GQ_ERR_ALIGN, **{p: [A + 2] for p in ("t", "k", "p", "m", "u", "token", "prob")}, logits=[A + 2], ws=[U])
-    refuses(name, SAMPLE, gq.GQ_ERR_SHAPE, vocab=[0, gq.GQ_MAX_VOCAB + 1], n=[-1, 65536], ldl=[99])
+    refuses(name, SAMPLE, gq.GQ_ERR_SHAPE, vocab=[0, gq.GQ_MAX_VOCAB + 1], n=[-1, gq.GQ_MAX_SAMPLE_ROWS + 1], ldl=[99])
     need = gq.gq_sample_workspace_bytes(100, 3)
     assert need > 0
     refuses(name, SAMPLE, gq.GQ_ERR_WORKSPACE, ws=[None], ws_bytes=[need - 1])
     assert call(name, SAMPLE, n=0) == gq.GQ_OK
-    for bad in ((0, 1), (gq.GQ_MAX_VOCAB + 1, 1), (10, 0), (10, 65536)):
+    for bad in ((0, 1), (gq.GQ_MAX_VOCAB + 1, 1), (10, 0), (10, gq.GQ_MAX_SAMPLE_ROWS + 1)):
         assert gq.gq_sample_workspace_bytes(*bad) == 0
 
 
