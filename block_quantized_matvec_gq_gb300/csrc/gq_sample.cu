@@ -45,12 +45,11 @@ namespace {
 namespace cg = cooperative_groups;
 using u64 = unsigned long long;
 
-constexpr int kScanThreads = 256;
+constexpr int kScanThreads = 256, kSmallThreads = 512;  // of a slice of 8192 and of 4096 elements
 constexpr int kDeepThreads = 1024;
 constexpr int kDeepCtas = 8;
 constexpr int kDeepClusters = 64;
 constexpr int kList = 2048;  // elements that are sorted at once
-constexpr int kMaxSlices = 640;
 constexpr int kSumFrom = 512;  // a top_k from here on may lie behind the list: the slices' sums bound its weight
 constexpr int kBins = 2048;
 constexpr uint32_t kNone = 0x007FFFFFu;        // key of -infinity: no candidate
@@ -337,20 +336,27 @@ __device__ __forceinline__ void bitonic_down(u64 *a, int n)
     __syncthreads();
 }
 // Falling sort of the n numbers of `list` (distinct, none above `first` or below
-// `last`), with `tmp` as long and kList counters: dealt into kList
-// equal steps of the value, then every number finds its place among its step's
-// few.  Numbers of one value are dealt by their bits.  The bitonic sort remains
-// for lists with more than kCrowd in one step (ties, far outliers).
-constexpr int kCrowd = 256, kFew = 96;
+// `last`), with `tmp` as long: dealt into kSteps equal steps of the value, then
+// every number finds its place among its step's few.  Numbers of one value are
+// dealt by their bits.  The bitonic sort remains for lists with more than kCrowd
+// in one step (ties, far outliers).  Loops are not unrolled: this code runs once
+// in a kernel, and what it costs is latency and fetching instructions.
+constexpr int kSteps = 1024, kCrowd = 256, kFew = 96;
+struct SortShared {
+    unsigned count[kSteps + 1];
+    unsigned short pos[kList];
+    unsigned sh[32];
+};
 template <int THREADS>
-__device__ __forceinline__ void sort_down(u64 *list, u64 *tmp, unsigned *count, int n, u64 first, u64 last, unsigned *sh)
+__device__ __forceinline__ void sort_down(u64 *list, u64 *tmp, SortShared &Q, int n, u64 first, u64 last)
 {
-    constexpr int kPer = kList / THREADS;
+    constexpr int kPer = kSteps / THREADS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (n <= kFew) {  // every number finds its place among all
         const u64 x = tid < n ? list[tid] : 0ull;
         int place = 0;
         if (tid < n)
+#pragma unroll 4
             for (int j = 0; j < n; ++j) place += list[j] > x ? 1 : 0;
         __syncthreads();
         if (tid < n) list[place] = x;
@@ -358,42 +364,36 @@ __device__ __forceinline__ void sort_down(u64 *list, u64 *tmp, unsigned *count, 
         return;
     }
     const float high = value_of(static_cast<uint32_t>(first >> 32)), low = value_of(static_cast<uint32_t>(last >> 32));
-    const float per = (kList - 1) / fmaxf(high - low, 1e-30f);
+    const float per = (kSteps - 1) / fmaxf(high - low, 1e-30f);
     const bool ties = !(high > low);
-    const int shift = max(0, 53 - __clzll(static_cast<long long>(first - last)));
+    const int shift = max(0, 54 - __clzll(static_cast<long long>(first - last)));
     auto step_of = [&](u64 r) {
         if (ties) return static_cast<int>((first - r) >> shift);
         const float x = (high - value_of(static_cast<uint32_t>(r >> 32))) * per;
-        return max(0, min(kList - 1, __float2int_rz(x)));
+        return max(0, min(kSteps - 1, __float2int_rz(x)));
     };
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) count[tid + i * THREADS] = 0;
+    for (int i = 0; i < kPer; ++i) Q.count[tid + i * THREADS] = 0;
     __syncthreads();
-    u64 r[kPer];
-    int step[kPer];
-    unsigned pos[kPer], most = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int x = tid + i * THREADS;
-        if (x < n) {
-            r[i] = list[x];
-            step[i] = step_of(r[i]);
-            pos[i] = atomicAdd(&count[step[i]], 1u);
-            most = max(most, pos[i] + 1);
-        }
+    unsigned most = 0;
+#pragma unroll 1
+    for (int x = tid; x < n; x += THREADS) {
+        const unsigned pos = atomicAdd(&Q.count[step_of(list[x])], 1u);
+        Q.pos[x] = static_cast<unsigned short>(pos);
+        most = max(most, pos + 1);
     }
     __syncthreads();
     // running counts, in place: count[s] = numbers in front of step s
     unsigned c[kPer], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += c[i] = count[tid * kPer + i];
+    for (int i = 0; i < kPer; ++i) sum += c[i] = Q.count[tid * kPer + i];
     unsigned incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const unsigned up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
     }
-    if (lane == 31) sh[warp] = incl;
+    if (lane == 31) Q.sh[warp] = incl;
     const bool crowded = __syncthreads_or(most > kCrowd);
     if (crowded) {
         int P = 64;
@@ -403,40 +403,44 @@ __device__ __forceinline__ void sort_down(u64 *list, u64 *tmp, unsigned *count, 
         bitonic_down<THREADS>(list, P);
         return;
     }
-    unsigned at = incl - sum;
-    for (int w = 0; w < warp; ++w) at += sh[w];
+    unsigned at = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? Q.sh[lane] : 0u);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        count[tid * kPer + i] = at;
+        Q.count[tid * kPer + i] = at;
         at += c[i];
     }
+    if (tid == 0) Q.count[kSteps] = n;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        if (tid + i * THREADS < n) tmp[count[step[i]] + pos[i]] = r[i];
+#pragma unroll 1
+    for (int x = tid; x < n; x += THREADS) {
+        const u64 r = list[x];
+        tmp[Q.count[step_of(r)] + Q.pos[x]] = r;
+    }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        if (tid + i * THREADS < n) {
-            const int from = count[step[i]], to = step[i] + 1 < kList ? count[step[i] + 1] : n;
-            int place = from;
-            for (int j = from; j < to; ++j) place += tmp[j] > r[i] ? 1 : 0;
-            list[place] = r[i];
-        }
+#pragma unroll 1
+    for (int x = tid; x < n; x += THREADS) {
+        const u64 r = tmp[x];
+        const int s = step_of(r);
+        int place = Q.count[s];
+        const int to = Q.count[s + 1];
+        for (int j = place; j < to; ++j) place += tmp[j] > r ? 1 : 0;
+        list[place] = r;
+    }
     __syncthreads();
 }
 
-// F[i] = before + the weights of list[0 .. i], for the n sorted numbers.
+// F[i] = before + the weights of list[0 .. i], for the n sorted numbers; a thread
+// takes consecutive ones.
 template <int THREADS>
 __device__ __forceinline__ void running_weights(const u64 *list, u64 *F, int n, u64 before, const Scale &sc, int top, u64 *sh)
 {
-    constexpr int kPer = kList / THREADS;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i0 = threadIdx.x * kPer;
-    u64 w[kPer], mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        w[i] = i0 + i < n ? row_weight(sc, value_of(static_cast<uint32_t>(list[i0 + i] >> 32)), top) : 0ull;
-        mine += w[i];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = (n + THREADS - 1) / THREADS, i0 = threadIdx.x * per,
+              i1 = min(i0 + per, n);
+    u64 mine = 0;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+        mine += row_weight(sc, value_of(static_cast<uint32_t>(list[i] >> 32)), top);
+        F[i] = mine;
     }
     u64 incl = mine;
 #pragma unroll
@@ -444,37 +448,38 @@ __device__ __forceinline__ void running_weights(const u64 *list, u64 *F, int n, 
         const u64 up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
     }
-    __syncthreads();
     if (lane == 31) sh[warp] = incl;
     __syncthreads();
-    u64 at = before + incl - mine;
-    for (int x = 0; x < warp; ++x) at += sh[x];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        at += w[i];
-        if (i0 + i < n) F[i0 + i] = at;
-    }
+    const u64 at = before + incl - mine + warp_sum(lane < warp ? sh[lane] : 0ull);
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) F[i] += at;
     __syncthreads();
 }
-// First i with F[i] >= x (n if there is none); every thread searches.
-__device__ __forceinline__ int reach(const u64 *F, int n, u64 x)
+// First i < n for which `here` holds, in every thread (n if there is none; it may hold for one only).
+template <int THREADS, class Here>
+__device__ __forceinline__ int only(int n, int &found, Here &&here)
 {
-    int lo = 0, hi = n;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (F[mid] >= x)
-            hi = mid;
-        else
-            lo = mid + 1;
-    }
-    return lo;
+    __syncthreads();
+    if (threadIdx.x == 0) found = n;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n; i += THREADS)
+        if (here(i)) found = i;
+    __syncthreads();
+    return found;
+}
+// First i with F[i] >= x, n if there is none.
+template <int THREADS>
+__device__ __forceinline__ int reach(const u64 *F, int n, u64 x, int &found)
+{
+    return only<THREADS>(n, found, [&](int i) { return F[i] >= x && (i == 0 || F[i - 1] < x); });
 }
 
 // What the slices' headers say of a row.
 struct RowHead {
     u64 best;
     uint32_t lowest, theta;
-    int cands;
+    int cands, most;  // most: the longest list
 };
 __device__ __forceinline__ Header load_header(const Header *h)
 {
@@ -494,6 +499,7 @@ __device__ __forceinline__ RowHead join_heads(RowHead r, RowHead *sh)
     r.lowest = __reduce_min_sync(0xffffffffu, r.lowest);
     r.theta = __reduce_max_sync(0xffffffffu, r.theta);
     r.cands = __reduce_add_sync(0xffffffffu, r.cands);
+    r.most = __reduce_max_sync(0xffffffffu, r.most);
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = r;
     __syncthreads();
     r = sh[0];
@@ -503,6 +509,7 @@ __device__ __forceinline__ RowHead join_heads(RowHead r, RowHead *sh)
         r.lowest = min(r.lowest, sh[w].lowest);
         r.theta = max(r.theta, sh[w].theta);
         r.cands += sh[w].cands;
+        r.most = max(r.most, sh[w].most);
     }
     return r;
 }
@@ -513,56 +520,34 @@ __device__ __forceinline__ void add_head(RowHead &r, const Header &h)
     r.lowest = min(r.lowest, h.lowest);
     r.theta = max(r.theta, h.theta);
     r.cands += h.cands;
+    r.most = max(r.most, h.count);
 }
 
 // ---------------------------------------------------------------- pick
 struct PickShared {
-    u64 list[kList], F[kList], sh[kScanThreads / 32];
-    unsigned steps[kList], sh32[kScanThreads / 32];
-    unsigned short start[kMaxSlices + 1];  // listed entries in front of every slice's
-    RowHead heads[kScanThreads / 32];
-    int count;
+    u64 list[kList], F[kList], sh[32];
+    SortShared sort;
+    RowHead heads[32];
+    int count, found;
 };
 
 // The row from its slices' headers and lists; false where they do not settle it.
+template <int THREADS>
 __device__ __forceinline__ bool pick(const Rows &R, const Settings &S, int row, float T, int k, PickShared &P, int &tok, float &pr,
                                      bool &refused)
 {
-    constexpr int kThreads = kScanThreads, kHeads = (kMaxSlices + kThreads - 1) / kThreads;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
     const Header *head = R.head + static_cast<long long>(row) * R.slices;
     const float p = S.top_p ? __ldg(S.top_p + row) : 1.f, mp = S.min_p ? __ldg(S.min_p + row) : 0.f, u = __ldg(S.u + row);
     tok = -1;
     pr = 0.f;
     refused = isnan(T) || isnan(p) || isnan(mp);
     if (refused) return true;
-    // a thread takes consecutive slices
-    const int per = (R.slices + kThreads - 1) / kThreads, s0 = tid * per;
-    RowHead h{0ull, kUnknown, 0u, 0};
-    u64 sum[kHeads];
-    int exp[kHeads], count[kHeads], mine = 0;
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        sum[i] = 0;
-        exp[i] = count[i] = 0;
-        if (i < per && s0 + i < R.slices) {
-            const Header x = load_header(head + s0 + i);
-            add_head(h, x);
-            sum[i] = x.cands > 0 ? x.sum : 0ull;
-            exp[i] = x.exp;
-            count[i] = x.count;
-        }
-        mine += count[i];
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
-    }
-    if (lane == 31) P.sh32[warp] = incl;
+    RowHead h{0ull, kUnknown, 0u, 0, 0};
+#pragma unroll 1
+    for (int s = tid; s < R.slices; s += THREADS) add_head(h, load_header(head + s));
     if (tid == 0) P.count = 0;
-    h = join_heads<kThreads>(h, P.heads);  // (a barrier in it)
+    h = join_heads<THREADS>(h, P.heads);  // (a barrier in it)
     if (h.best == 0) return true;
     const float largest = value_of(static_cast<uint32_t>(h.best >> 32));
     if (!(T > 0.f)) {
@@ -574,59 +559,56 @@ __device__ __forceinline__ bool pick(const Rows &R, const Settings &S, int row, 
     const Scale sc = scale_of(T, largest);
     const int top = exponent(sc, largest);
     const bool summed = (k == 0 || k >= kSumFrom) && sc.base == 0.f && !sc.infinite;
-    // the row's weight from the slices', each in units of its own largest
+    // the row's weight from the slices', each in units of its own largest; and their lists, 2^g threads a slice
     u64 total = 0;
-    int at = incl - mine, listed_all = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        at += w < warp ? static_cast<int>(P.sh32[w]) : 0;
-        listed_all += static_cast<int>(P.sh32[w]);
-    }
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        const unsigned shift = static_cast<unsigned>(top - exp[i]);
-        if (summed && shift < 64) total += sum[i] >> shift;
-        if (i < per && s0 + i < R.slices) P.start[s0 + i] = static_cast<unsigned short>(at);
-        at += count[i];
-    }
-    __syncthreads();
-    // all listed entries, a few loads of every thread in flight
     const u64 *lists = R.list + (static_cast<long long>(row) * R.slices << R.cap_log2);
-    constexpr int kBatch = 4;
-    for (int i0 = 0; i0 < listed_all; i0 += kBatch * kThreads) {
-        u64 x[kBatch];
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            const int i = i0 + q * kThreads + tid;
-            x[q] = 0;
-            if (i < listed_all) {
-                int lo = 0, hi = R.slices;  // the last slice that starts at i or before: empty ones start where the next does
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (P.start[mid] <= i)
-                        lo = mid;
-                    else
-                        hi = mid;
-                }
-                x[q] = __ldcg(lists + (static_cast<long long>(lo) << R.cap_log2) + (i - P.start[lo]));
-            }
+    int g = 0;
+    while ((R.slices << (g + 1)) <= THREADS) ++g;
+    constexpr int kBatch = 8;
+#pragma unroll 1
+    for (int s0 = 0; s0 < R.slices; s0 += THREADS >> g) {
+        const int s = s0 + (tid >> g), e0 = tid & ((1 << g) - 1);
+        int n = 0;
+        if (s < R.slices) {
+            const Header x = load_header(head + s);
+            n = x.count;
+            const unsigned shift = static_cast<unsigned>(top - x.exp);
+            if (summed && e0 == 0 && x.cands > 0 && shift < 64) total += x.sum >> shift;
         }
+#pragma unroll 1
+        for (int e = 0; e < h.most; e += kBatch << g) {
+            u64 x[kBatch];
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            const bool take = static_cast<uint32_t>(x[q] >> 32) >= h.theta;
-            const unsigned who = __ballot_sync(0xffffffffu, take);
+            for (int q = 0; q < kBatch; ++q) {
+                const int i = e + e0 + (q << g);
+                x[q] = i < n ? __ldcg(lists + (static_cast<long long>(s) << R.cap_log2) + i) : 0ull;
+            }
+            unsigned mine = 0;
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) mine += static_cast<uint32_t>(x[q] >> 32) >= h.theta ? 1u : 0u;
+            unsigned incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned up = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += up;
+            }
             int to = 0;
-            if (lane == 0 && who) to = atomicAdd(&P.count, __popc(who));
-            to = __shfl_sync(0xffffffffu, to, 0) + __popc(who & ((1u << lane) - 1u));
-            if (take && to < kList) P.list[to] = x[q];
+            if (lane == 31 && incl) to = atomicAdd(&P.count, static_cast<int>(incl));
+            to = __shfl_sync(0xffffffffu, to, 31) + static_cast<int>(incl - mine);
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q)
+                if (static_cast<uint32_t>(x[q] >> 32) >= h.theta) {
+                    if (to < kList) P.list[to] = x[q];
+                    ++to;
+                }
         }
     }
-    total = cta_sum<kThreads>(total, P.sh);
+    total = cta_sum<THREADS>(total, P.sh);
     const int n = P.count;
     if (n == 0 || n > kList) return false;
     const bool all = n == h.cands;  // every candidate is in the list
-    sort_down<kThreads>(P.list, P.F, P.steps, n, h.best, rank_of(max(h.theta, h.lowest), R.vocab - 1), P.sh32);
-    running_weights<kThreads>(P.list, P.F, n, 0ull, sc, top, P.sh);
+    sort_down<THREADS>(P.list, P.F, P.sort, n, h.best, rank_of(max(h.theta, h.lowest), R.vocab - 1));
+    running_weights<THREADS>(P.list, P.F, n, 0ull, sc, top, P.sh);
     const u64 *F = P.F;
     const u64 listed = F[n - 1], last = n > 1 ? listed - F[n - 2] : listed;
     // the weight of what top_k keeps, between z and most
@@ -644,19 +626,18 @@ __device__ __forceinline__ bool pick(const Rows &R, const Settings &S, int row, 
         if (last < (1ull << 43)) most = min(most, listed + static_cast<u64>(k - n) * last);
     }
     // the first element where top_p is reached, and the weight that min_p keeps, where they are in the list
-    const int from = p < 1.f ? reach(F, n, nucleus(p, z)) : n, to = p < 1.f ? (most == z ? from : reach(F, n, nucleus(p, most))) : n;
+    int from = n, to = n;
+    if (p < 1.f) {
+        from = to = reach<THREADS>(F, n, nucleus(p, z), P.found);
+        if (most != z) to = reach<THREADS>(F, n, nucleus(p, most), P.found);
+    }
     u64 least = ~0ull;
     if (mp > 0.f) {
         bool rest = false;
         const u64 thr = mp < 1.f ? part_of(mp, F[0], rest) + (rest ? 1 : 0) : F[0];
-        int lo = 0, hi = n;  // first of the list below the threshold; the list falls
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (F[mid] - (mid ? F[mid - 1] : 0ull) < thr)
-                hi = mid;
-            else
-                lo = mid + 1;
-        }
+        // first of the list below the threshold; the list falls
+        auto w = [&](int i) { return F[i] - (i ? F[i - 1] : 0ull); };
+        const int lo = only<THREADS>(n, P.found, [&](int i) { return w(i) < thr && (i == 0 || w(i - 1) >= thr); });
         if (lo < n)
             least = F[max(lo, 1) - 1];
         else if (all)
@@ -672,7 +653,7 @@ __device__ __forceinline__ bool pick(const Rows &R, const Settings &S, int row, 
     else
         kept = z;
     kept = min(kept, z);
-    const int j = reach(F, n, drawn(u, kept));
+    const int j = reach<THREADS>(F, n, drawn(u, kept), P.found);
     if (j == n) return false;
     tok = index_of(P.list[j]);
     pr = ratio(j ? F[j] - F[j - 1] : F[0], kept);
@@ -680,11 +661,11 @@ __device__ __forceinline__ bool pick(const Rows &R, const Settings &S, int row, 
 }
 
 // ---------------------------------------------------------------- scan
-template <int TYPE, int EPT>
-__global__ void __launch_bounds__(kScanThreads, 4)
+template <int TYPE, int EPT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     k_sample_scan(Rows R, Settings S, int want, int32_t *token, float *prob, int *status)
 {
-    constexpr int kVec = Reader<TYPE>::kVec, kUnits = EPT / kVec, kWarps = kScanThreads / 32;
+    constexpr int kVec = Reader<TYPE>::kVec, kUnits = EPT / kVec, kWarps = THREADS / 32;
     __shared__ u64 s_sum[kWarps];
     __shared__ uint32_t s_hi[kWarps], s_lo[kWarps];
     __shared__ int s_cands[kWarps], s_count, s_first;
@@ -696,10 +677,10 @@ __global__ void __launch_bounds__(kScanThreads, 4)
     pdl_wait();
     pdl_launch_dependents();
     const Reader<TYPE> in(R.logits + row * R.row_bytes, R.vocab);
-    const int u0 = slice * kScanThreads * kUnits + tid;
+    const int u0 = slice * THREADS * kUnits + tid;
     float v[kUnits][kVec];
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) in.load(u0 + j * kScanThreads, v[j]);
+    for (int j = 0; j < kUnits; ++j) in.load(u0 + j * THREADS, v[j]);
     const float T = temperature(S, row);
     const int k = top_k(S, row, R.vocab);
     float hi = -INFINITY, lo = INFINITY;
@@ -750,7 +731,7 @@ __global__ void __launch_bounds__(kScanThreads, 4)
         for (int j = kUnits - 1; j >= 0; --j)
 #pragma unroll
             for (int i = kVec - 1; i >= 0; --i)
-                if (v[j][i] == best) first = in.index(u0 + j * kScanThreads, i);
+                if (v[j][i] == best) first = in.index(u0 + j * THREADS, i);
         atomicMin(&s_first, first);
     }
     h.theta = kUnknown;
@@ -772,7 +753,7 @@ __global__ void __launch_bounds__(kScanThreads, 4)
             const int threads = __syncthreads_count(mine > kNone);
             const int w = max(1, min(k > 0 ? min(want, 2 * k / static_cast<int>(gridDim.x) + 8) : want, threads / 2));
             uint32_t b = top;  // w threads reach a; look in a .. b
-            if (threads == kScanThreads) {  // all threads reach the least of their maxima
+            if (threads == THREADS) {  // all threads reach the least of their maxima
                 uint32_t m = __reduce_min_sync(0xffffffffu, mine);
                 if (lane == 0) s_lo[warp] = m;
                 __syncthreads();
@@ -800,7 +781,7 @@ __global__ void __launch_bounds__(kScanThreads, 4)
                 for (int i = 0; i < kVec; ++i)
                     if (v[j][i] >= from) {
                         const int at = atomicAdd(&s_count, 1);
-                        if (at < R.cap) list[at] = rank_of(key_of(v[j][i]), in.index(u0 + j * kScanThreads, i));
+                        if (at < R.cap) list[at] = rank_of(key_of(v[j][i]), in.index(u0 + j * THREADS, i));
                     }
         };
         put(a);
@@ -840,7 +821,7 @@ __global__ void __launch_bounds__(kScanThreads, 4)
     int tok;
     float pr;
     bool refused;
-    const bool settled = pick(R, S, row, T, k, P, tok, pr, refused);
+    const bool settled = pick<THREADS>(R, S, row, T, k, P, tok, pr, refused);
     if (tid == 0) {
         if (settled) {
             token[row] = tok;
@@ -859,7 +840,7 @@ struct Level {
 };
 struct DeepShared {
     u64 list[kList], F[kList];
-    unsigned steps[kList];
+    SortShared sort;
     unsigned hist[kBins], low[kBins], high[kBins];  // this CTA's counts, and weights as two words
     Level coarse, fine;
     u64 sh[kDeepThreads / 32], sh2[kDeepThreads / 32];
@@ -889,7 +870,7 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
         const float T = temperature(S, row), p = S.top_p ? __ldg(S.top_p + row) : 1.f, mp = S.min_p ? __ldg(S.min_p + row) : 0.f,
                     u = __ldg(S.u + row);
         const int k = top_k(S, row, R.vocab);
-        RowHead h{0ull, kUnknown, 0u, 0};
+        RowHead h{0ull, kUnknown, 0u, 0, 0};
         for (int i = tid; i < R.slices; i += kDeepThreads) add_head(h, load_header(R.head + static_cast<long long>(row) * R.slices + i));
         h = join_heads<kDeepThreads>(h, D.heads);
         const float largest = value_of(static_cast<uint32_t>(h.best >> 32));
@@ -1096,9 +1077,9 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
                             most = max(most, D.sh[w]);
                             fewest = min(fewest, D.sh2[w]);
                         }
-                        sort_down<kDeepThreads>(D.list, D.F, D.steps, n, most, fewest, D.sh32);
+                        sort_down<kDeepThreads>(D.list, D.F, D.sort, n, most, fewest);
                         running_weights<kDeepThreads>(D.list, D.F, n, weight_in_front, sc, top, D.sh);
-                        int at = by_count ? static_cast<int>(X - skip - in_front) - 1 : reach(D.F, n, X);
+                        int at = by_count ? static_cast<int>(X - skip - in_front) - 1 : reach<kDeepThreads>(D.F, n, X, D.found);
                         at = max(min(at, n - 1), 0);
                         if (tid < kDeepCtas) {
                             *cluster.map_shared_rank(&D.rank, tid) = D.list[at];
@@ -1163,7 +1144,7 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
 }
 
 // ---------------------------------------------------------------- host
-// Slices of 2048 elements while they all fit the GPU at once, of 8192 else: a
+// Slices of 4096 elements while they all fit the GPU at once, of 8192 else: a
 // small batch is latency, and a large one wants long streams per CTA.
 struct Plan {
     int ept, slices, cap_log2, want;
@@ -1171,15 +1152,15 @@ struct Plan {
 Plan plan_for(int vocab, int n_rows)
 {
     Plan p;
-    const long long fine = (vocab + 7 + 2047) / 2048;
-    p.ept = fine * n_rows <= 608 ? 8 : 32;
-    const int per = kScanThreads * p.ept;
+    const long long fine = (vocab + 7 + 4095) / 4096;
+    p.ept = fine * n_rows <= 304 ? 8 : 32;
+    const int threads = p.ept == 8 ? kSmallThreads : kScanThreads, per = threads * p.ept;
     p.slices = (vocab + 7 + per - 1) / per;
     // lists of some 1024 elements a row in all, with room for two to four times as many
     p.cap_log2 = 5;
     while (p.cap_log2 < 11 && (p.slices << (p.cap_log2 + 1)) <= 4096) ++p.cap_log2;
     const int want = 1024 / p.slices;
-    p.want = want < 4 ? 4 : (want > kScanThreads / 2 ? kScanThreads / 2 : want);
+    p.want = want < 4 ? 4 : (want > threads / 2 ? threads / 2 : want);
     return p;
 }
 // The counters stand in front, the same for every call, so that a workspace serves calls of any size.
@@ -1193,8 +1174,8 @@ cudaError_t launch(Rows R, const Settings &S, const Plan &p, int n_rows, int32_t
     if (ctas_per_sm(reinterpret_cast<const void *>(deep), kDeepThreads, sizeof(DeepShared)) < 1) return cudaErrorInvalidConfiguration;
     const dim3 grid(p.slices, n_rows);
     int *status = status_word();
-    cudaError_t e = p.ept == 8 ? launch_pdl(k_sample_scan<TYPE, 8>, grid, dim3(kScanThreads), 0, s, R, S, p.want, token, prob, status)
-                               : launch_pdl(k_sample_scan<TYPE, 32>, grid, dim3(kScanThreads), 0, s, R, S, p.want, token, prob, status);
+    cudaError_t e = p.ept == 8 ? launch_pdl(k_sample_scan<TYPE, 8, kSmallThreads>, grid, dim3(kSmallThreads), 0, s, R, S, p.want, token, prob, status)
+                               : launch_pdl(k_sample_scan<TYPE, 32, kScanThreads>, grid, dim3(kScanThreads), 0, s, R, S, p.want, token, prob, status);
     if (e == cudaSuccess)
         e = launch_pdl(deep, dim3(kDeepCtas, n_rows < kDeepClusters ? n_rows : kDeepClusters), dim3(kDeepThreads), sizeof(DeepShared), s, R,
                        S, n_rows, token, prob);
