@@ -116,44 +116,60 @@ __global__ void __launch_bounds__(kThreads)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-        bool in[NT];  // lane's token (column g) of every n-tile
+        bool in[NT], col_in[NT][2];  // whether the lane's tokens belong to the group: as operand (column g), as results
 #pragma unroll
-        for (int n = 0; n < NT; ++n) in[n] = tile.group[8 * n + g] == j;
-#pragma unroll 2
-        for (int c = c0 + warp; c < c1; c += kWarps) {
+        for (int n = 0; n < NT; ++n) {
+            in[n] = tile.group[8 * n + g] == j;
+            col_in[n][0] = tile.group[8 * n + 2 * t] == j;
+            col_in[n][1] = tile.group[8 * n + 2 * t + 1] == j;
+        }
+        // a chunk as it is loaded; the next one is on its way while one is multiplied
+        struct Raw {
+            uint4 a[MT][2];
+            uint2 q[NT];
+            float4 x[NT][2];
+            float d[NT][2];
+        };
+        auto load = [&](Raw &w, int c) {
             const int k = 32 * c + 8 * t;
-            uint4 aw[MT][2];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int r = 16 * m + 8 * h + g;
-                    aw[m][h] = r < rank ? __ldg(reinterpret_cast<const uint4 *>(a + static_cast<long long>(r) * K + k))
-                                        : make_uint4(0, 0, 0, 0);
+                    w.a[m][h] = r < rank ? __ldg(reinterpret_cast<const uint4 *>(a + static_cast<long long>(r) * K + k))
+                                         : make_uint4(0, 0, 0, 0);
                 }
-            float x[NT][8], dt[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const long long tok = t0 + 8 * n + g;
                 if (Q8) {
-                    const uint2 q = in[n] ? __ldg(reinterpret_cast<const uint2 *>(Xq + tok * K + k)) : make_uint2(0, 0);
+                    w.q[n] = in[n] ? __ldg(reinterpret_cast<const uint2 *>(Xq + tok * K + k)) : make_uint2(0, 0);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        // a code's byte + 128 as the low bits of 2^23
-                        const uint32_t w = (i < 4 ? q.x : q.y) ^ 0x80808080u;
-                        x[n][i] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 | (i & 3))) - 8388736.0f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int col = 8 * n + 2 * t + i;
-                        dt[n][i] = tile.group[col] == j ? __ldg(dx + static_cast<long long>(t0 + col) * chunks + c) : 0.f;
-                    }
+                    for (int i = 0; i < 2; ++i)
+                        w.d[n][i] = col_in[n][i] ? __ldg(dx + static_cast<long long>(t0 + 8 * n + 2 * t + i) * chunks + c) : 0.f;
                 } else {
                     const float4 *p = reinterpret_cast<const float4 *>(X + tok * ldx + k);
                     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const float4 u = in[n] ? __ldg(p) : zero, v = in[n] ? __ldg(p + 1) : zero;
-                    x[n][0] = u.x, x[n][1] = u.y, x[n][2] = u.z, x[n][3] = u.w;
-                    x[n][4] = v.x, x[n][5] = v.y, x[n][6] = v.z, x[n][7] = v.w;
+                    w.x[n][0] = in[n] ? __ldg(p) : zero;
+                    w.x[n][1] = in[n] ? __ldg(p + 1) : zero;
+                }
+            }
+        };
+        auto multiply = [&](const Raw &w) {
+            float x[NT][8];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (Q8) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        // a code's byte + 128 as the low bits of 2^23
+                        const uint32_t v = (i < 4 ? w.q[n].x : w.q[n].y) ^ 0x80808080u;
+                        x[n][i] = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7440 | (i & 3))) - 8388736.0f;
+                    }
+                } else {
+                    x[n][0] = w.x[n][0].x, x[n][1] = w.x[n][0].y, x[n][2] = w.x[n][0].z, x[n][3] = w.x[n][0].w;
+                    x[n][4] = w.x[n][1].x, x[n][5] = w.x[n][1].y, x[n][6] = w.x[n][1].z, x[n][7] = w.x[n][1].w;
                 }
             }
 #pragma unroll
@@ -161,7 +177,7 @@ __global__ void __launch_bounds__(kThreads)
                 float af[4][4];
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    const float2 lo = weights2<BF16>((&aw[m][0].x)[s]), hi = weights2<BF16>((&aw[m][1].x)[s]);
+                    const float2 lo = weights2<BF16>((&w.a[m][0].x)[s]), hi = weights2<BF16>((&w.a[m][1].x)[s]);
                     af[s][0] = lo.x, af[s][1] = hi.x, af[s][2] = lo.y, af[s][3] = hi.y;
                 }
 #pragma unroll
@@ -175,9 +191,20 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
                     for (int s = 0; s < 4; ++s) mma_tf32(d, af[s], head(x[n][2 * s]), head(x[n][2 * s + 1]));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[m][n][i] = Q8 ? fmaf(dt[n][i & 1], d[i], acc[m][n][i]) : acc[m][n][i] + d[i];
+                    for (int i = 0; i < 4; ++i) acc[m][n][i] = Q8 ? fmaf(w.d[n][i & 1], d[i], acc[m][n][i]) : acc[m][n][i] + d[i];
                 }
             }
+        };
+        int c = c0 + warp;
+        if (c < c1) {
+            Raw now, next;
+            load(now, c);
+            for (; c + kWarps < c1; c += kWarps) {
+                load(next, c + kWarps);
+                multiply(now);
+                now = next;
+            }
+            multiply(now);
         }
         float *mine = red + warp * kOut;
 #pragma unroll
@@ -203,23 +230,37 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ---------------------------------------------------------------- Y = Y0 + scale B v
+constexpr int kStages = 3;
+// Four rows of weights (16 bytes a lane, 8 where a chunk is 16 deep) and the lane's results of 8 NT tokens.
+__host__ __device__ constexpr int expand_stage(int kc, int nt) { return 64 * kc + 1024 * nt; }
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void *to, const void *from)
+{
+    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(s), "l"(from) : "memory");
+}
 // CTA: a tile of 8 NT tokens and a range of row blocks, which its warps take in
 // turn.  Row slots are dealt so that a lane's four results of a token are four
 // consecutive rows: slot g (+ 8) of instruction m is row 4 g + 2 m (+ 1).
 // KC = 16: a rank of up to 16, where a lane's chunk is four elements.
 template <int KC, int NT, bool BF16>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     k_lora_expand(const uint16_t *__restrict__ W, Batch B, const float *__restrict__ V, const float *Y0, long long ldy0,
                   float *Y, long long ldy, int rank, int rows, int slices, int row_groups, int group_blocks)
 {
-    extern __shared__ __align__(16) float vs[];  // [8 NT][stride]
+    extern __shared__ __align__(16) char raw[];
     __shared__ Tile tile;
     constexpr int TT = 8 * NT, E = KC / 4;  // elements of a lane's chunk
+    constexpr int kStageBytes = expand_stage(KC, NT);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    char *const ring = raw + warp * kStages * kStageBytes;  // the lane's parts: 2 E or 16 bytes of every 64 E or 512
+    float *const vs = reinterpret_cast<float *>(raw + kWarps * kStages * kStageBytes);  // [8 NT][stride]
     const int tile_no = blockIdx.x / row_groups, rg = blockIdx.x - tile_no * row_groups;
     const int t0 = tile_no * TT;
-    const int blocks = (rows + kRowBlock - 1) / kRowBlock;
-    const int rb0 = rg * group_blocks, rb1 = min(rb0 + group_blocks, blocks);
+    const int rb0 = rg * group_blocks, rb1 = min(rb0 + group_blocks, (rows + kRowBlock - 1) / kRowBlock);
     const int depth = (rank + KC - 1) / KC * KC, stride = depth + 4;
     pdl_launch_dependents();
     // the lists, Y0 and the weights were complete before `shrink` let this
@@ -258,87 +299,112 @@ __global__ void __launch_bounds__(kThreads)
                 put[n][i] = add[n][i] || (j == 0 && tile.group[tok] < 0 && t0 + tok < B.M && Y != Y0);
             }
         const uint16_t *w = W + static_cast<long long>(product ? tile.adapter[j] : 0) * rows * rank;
-        for (int rb = rb0 + warp; rb < rb1; rb += kWarps) {
-            const int row = rb * kRowBlock + 4 * g;
-            const bool in = row < rows;
-            float4 y[NT][2];
+        // Steps: a warp's row blocks, each in nk chunks of the rank.  A step's weights, and with a block's last chunk its
+        // part of Y0, come through a ring of kStages steps in shared memory; every lane copies what it reads itself, so
+        // that nothing but its own copies' arrival has to be waited for.
+        const int nk = depth / KC, blocks = rb0 + warp < rb1 ? (rb1 - rb0 - warp + kWarps - 1) / kWarps : 0, steps = blocks * nk;
+        int fetch_row = (rb0 + warp) * kRowBlock + 4 * g, fetch_k = 0;
+        auto fetch = [&](int step) {
+            if (step < steps) {
+                char *to = ring + (step % kStages) * kStageBytes;
+                if (product && fetch_row < rows && fetch_k * KC + E * t < rank) {
+                    const uint16_t *from = w + static_cast<long long>(fetch_row) * rank + fetch_k * KC + E * t;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                    for (int r = 0; r < 4; ++r) cp_async<2 * E>(to + r * 64 * E + lane * 2 * E, from + static_cast<long long>(r) * rank);
+                }
+                if (++fetch_k == nk) {
+                    if (fetch_row < rows) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (in && put[n][i])
-                        y[n][i] = *reinterpret_cast<const float4 *>(Y0 + static_cast<long long>(t0 + 8 * n + 2 * t + i) * ldy0 + row);
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (put[n][i])
+                                    cp_async<16>(to + 256 * E + (2 * n + i) * 512 + lane * 16,
+                                                 Y0 + static_cast<long long>(t0 + 8 * n + 2 * t + i) * ldy0 + fetch_row);
+                    }
+                    fetch_k = 0;
+                    fetch_row += kWarps * kRowBlock;
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) fetch(i);
+        int row = (rb0 + warp) * kRowBlock + 4 * g, kc = 0;
+        float acc[NT][2][4];
+        for (int step = 0; step < steps; ++step) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            const char *from = ring + (step % kStages) * kStageBytes;
             if (product) {
-                float acc[NT][2][4];
-                for (int k0 = 0; k0 < depth; k0 += KC) {
-                    const int k = k0 + E * t;
-                    uint32_t aw[2][2][E / 2];
+                const int k = kc * KC + E * t;
+                const bool have = row < rows && k < rank;
+                float af[2][E / 2][4];
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
+                for (int m = 0; m < 2; ++m) {
+                    uint32_t x[2][E / 2];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint16_t *p = w + static_cast<long long>(row + 2 * m + h) * rank + k;
-                            const bool have = in && k < rank;
-                            if (E == 8) {
-                                const uint4 v = have ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0, 0, 0, 0);
-                                aw[m][h][0] = v.x, aw[m][h][1] = v.y, aw[m][h][E / 2 - 2] = v.z, aw[m][h][E / 2 - 1] = v.w;
-                            } else {
-                                const uint2 v = have ? __ldg(reinterpret_cast<const uint2 *>(p)) : make_uint2(0, 0);
-                                aw[m][h][0] = v.x, aw[m][h][1] = v.y;
-                            }
-                        }
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t *q = reinterpret_cast<const uint32_t *>(from + (2 * m + h) * 64 * E + lane * 2 * E);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float v[E];
+                        for (int i = 0; i < E / 2; ++i) x[h][i] = have ? q[i] : 0u;
+                    }
 #pragma unroll
-                        for (int q = 0; q < E / 4; ++q) {
-                            const float4 u = *reinterpret_cast<const float4 *>(vs + (8 * n + g) * stride + k + 4 * q);
-                            v[4 * q] = u.x, v[4 * q + 1] = u.y, v[4 * q + 2] = u.z, v[4 * q + 3] = u.w;
-                        }
-#pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            float d[4] = {0.f, 0.f, 0.f, 0.f};
-                            float af[E / 2][4];
-#pragma unroll
-                            for (int s = 0; s < E / 2; ++s) {
-                                const float2 lo = weights2<BF16>(aw[m][0][s]), hi = weights2<BF16>(aw[m][1][s]);
-                                af[s][0] = lo.x, af[s][1] = hi.x, af[s][2] = lo.y, af[s][3] = hi.y;
-                            }
-#pragma unroll
-                            for (int s = 0; s < E / 2; ++s)
-                                mma_tf32(d, af[s], v[2 * s] - head(v[2 * s]), v[2 * s + 1] - head(v[2 * s + 1]));
-#pragma unroll
-                            for (int s = 0; s < E / 2; ++s) mma_tf32(d, af[s], head(v[2 * s]), head(v[2 * s + 1]));
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[n][m][i] = k0 == 0 ? d[i] : acc[n][m][i] + d[i];
-                        }
+                    for (int s = 0; s < E / 2; ++s) {
+                        const float2 lo = weights2<BF16>(x[0][s]), hi = weights2<BF16>(x[1][s]);
+                        af[m][s][0] = lo.x, af[m][s][1] = hi.x, af[m][s][2] = lo.y, af[m][s][3] = hi.y;
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
+                    float v[E];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (add[n][i]) {
-                            y[n][i].x += acc[n][0][i];
-                            y[n][i].y += acc[n][0][2 + i];
-                            y[n][i].z += acc[n][1][i];
-                            y[n][i].w += acc[n][1][2 + i];
-                        }
+                    for (int q = 0; q < E / 4; ++q) {
+                        const float4 u = *reinterpret_cast<const float4 *>(vs + (8 * n + g) * stride + k + 4 * q);
+                        v[4 * q] = u.x, v[4 * q + 1] = u.y, v[4 * q + 2] = u.z, v[4 * q + 3] = u.w;
+                    }
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int s = 0; s < E / 2; ++s)
+                            mma_tf32(d, af[m][s], v[2 * s] - head(v[2 * s]), v[2 * s + 1] - head(v[2 * s + 1]));
+#pragma unroll
+                        for (int s = 0; s < E / 2; ++s) mma_tf32(d, af[m][s], head(v[2 * s]), head(v[2 * s + 1]));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[n][m][i] = kc == 0 ? d[i] : acc[n][m][i] + d[i];
+                    }
+                }
             }
+            if (++kc == nk) {
+                if (row < rows) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (in && put[n][i])
-                        *reinterpret_cast<float4 *>(Y + static_cast<long long>(t0 + 8 * n + 2 * t + i) * ldy + row) = y[n][i];
+                        for (int i = 0; i < 2; ++i)
+                            if (put[n][i]) {
+                                float4 y = *reinterpret_cast<const float4 *>(from + 256 * E + (2 * n + i) * 512 + lane * 16);
+                                if (add[n][i]) {
+                                    y.x += acc[n][0][i];
+                                    y.y += acc[n][0][2 + i];
+                                    y.z += acc[n][1][i];
+                                    y.w += acc[n][1][2 + i];
+                                }
+                                *reinterpret_cast<float4 *>(Y + static_cast<long long>(t0 + 8 * n + 2 * t + i) * ldy + row) = y;
+                            }
+                }
+                kc = 0;
+                row += kWarps * kRowBlock;
+            }
+            fetch(step + kStages - 1);
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
     }
 }
 
 // ---------------------------------------------------------------- host
 // Slices of K: enough CTAs for two per SM, at least one chunk for every warp.
-constexpr int kWantCtas = 304;
+constexpr int kWantCtas = 912, kExpandCtas = 608;
 int most_slices(int K, int M)
 {
     const int tiles = (M + 7) / 8, by_k = (K / 32 + kWarps - 1) / kWarps;
@@ -394,13 +460,11 @@ cudaError_t expand(const Call &c, int tiles, int groups, int slices)
 {
     auto kern = k_lora_expand<KC, NT, BF16>;
     const int depth = (c.rank + KC - 1) / KC * KC;
-    const size_t smem = sizeof(float) * 8 * NT * (depth + 4);
+    const size_t smem = sizeof(float) * 8 * NT * (depth + 4) + kWarps * kStages * expand_stage(KC, NT);
     if (ctas_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
-    // four row blocks a warp, fewer where that leaves SMs without a CTA
     const int blocks = (c.rows + kRowBlock - 1) / kRowBlock, most = (blocks + kWarps - 1) / kWarps;
     const long long have = static_cast<long long>(tiles) * groups;
-    long long rg = (kWantCtas + have - 1) / have;
-    if (rg < (most + 3) / 4) rg = (most + 3) / 4;
+    long long rg = (kExpandCtas + have - 1) / have;
     if (rg > most) rg = most;
     const int group_blocks = static_cast<int>((blocks + rg - 1) / rg);
     const int row_groups = (blocks + group_blocks - 1) / group_blocks;
@@ -423,7 +487,7 @@ int run(const Call &c, int type)
     // Neighbouring tokens of one request share their adapter: tiles of 32 where
     // requests have 16 tokens or more on average.
     const bool long_runs = c.B.sequence != nullptr && c.B.M / 16 >= c.B.n_seq;
-    const int tt = long_runs ? 32 : 8, st = long_runs ? 16 : 8;  // tokens of an expand and of a shrink tile
+    const int tt = long_runs ? 16 : 8, st = long_runs ? 16 : 8;  // tokens of an expand and of a shrink tile
     const int distinct = long_runs ? 1 : (c.B.n_adapters < tt ? c.B.n_adapters : tt);
     const int tiles = (c.B.M + tt - 1) / tt, shrink_tiles = (c.B.M + st - 1) / st, chunks = c.K / 32;
     int slices = most_slices(c.K, c.B.M);
@@ -435,7 +499,7 @@ int run(const Call &c, int type)
     cudaError_t e = long_runs ? shrink_rank<2>(c, bf16, shrink_tiles, distinct, slices, slice_chunks)
                               : shrink_rank<1>(c, bf16, shrink_tiles, distinct, slices, slice_chunks);
     if (e == cudaSuccess)
-        e = long_runs ? expand_rank<4>(c, bf16, tiles, distinct, slices) : expand_rank<1>(c, bf16, tiles, distinct, slices);
+        e = long_runs ? expand_rank<2>(c, bf16, tiles, distinct, slices) : expand_rank<1>(c, bf16, tiles, distinct, slices);
     return status_from(e);
 }
 
