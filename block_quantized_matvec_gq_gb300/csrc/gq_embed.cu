@@ -1,10 +1,10 @@
 // gq_embed.cu -- rows of a packed table by token id (include/gq_embed.h).
 //
-// A warp decodes 256 consecutive weights of one token's row, eight per lane: a
-// lane's codes are one load of 4 or 8 bytes, its scales one or two short ones
-// that its neighbours share, its result one or two 16-byte stores.  The rows
-// are independent; a warp takes its tasks one after the other and the loads of
-// one do not wait for the stores of another.
+// A warp takes a token's row, or a part of it where there are fewer tokens than
+// warps: 256 consecutive weights at a time, eight per lane.  A lane's codes are
+// one load of 4 or 8 bytes, its scales one or two short ones that its neighbours
+// share, its result one or two 16-byte stores; four such pieces are loaded before
+// the first is stored.
 //
 // What bounds it: the writes.
 #include <math.h>
@@ -75,29 +75,39 @@ __device__ __forceinline__ void decode8(const uint8_t *__restrict__ W, long long
 template <int FORMAT, int TYPE>
 __global__ void __launch_bounds__(kThreads)
     k_embed(const uint8_t *__restrict__ W, const int32_t *__restrict__ ids, float scale, uint8_t *__restrict__ Y,
-            long long row_bytes, int rows, int K, long long tasks, int per_row, int *status)
+            long long row_bytes, int rows, int K, int M, int parts, int part_elems, int *status)
 {
+    constexpr int kBatch = 4;
     const int lane = threadIdx.x & 31;
-    const long long step = static_cast<long long>(gridDim.x) * (kThreads / 32);
+    const unsigned warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int t = static_cast<int>(warp / static_cast<unsigned>(parts)), part = static_cast<int>(warp - t * static_cast<unsigned>(parts));
     pdl_launch_dependents();
     pdl_wait();
-    for (long long task = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); task < tasks; task += step) {
-        const long long t = task / per_row;
-        const int e0 = static_cast<int>(task - t * per_row) * 256 + 8 * lane;
-        const int id = __ldg(ids + t);
-        if (e0 >= K) continue;
-        float w[8];
-        if (id >= 0 && id < rows) {
-            decode8<FORMAT>(W, rows, K, id, e0, w);
+    if (t >= M) return;
+    const int id = __ldg(ids + t);
+    const int end = min(K, (part + 1) * part_elems);
+    const bool have = id >= 0 && id < rows;
+    if (id >= rows && part == 0 && lane == 0 && status) atomicExch(status, GQ_ERR_SHAPE);
+    uint8_t *y = Y + t * row_bytes;
+    for (int e0 = part * part_elems + 8 * lane; e0 < end; e0 += kBatch * 256) {
+        float w[kBatch][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] *= scale;
-        } else {
+        for (int q = 0; q < kBatch; ++q) {
+            if (have && e0 + 256 * q < end) {
+                decode8<FORMAT>(W, rows, K, id, e0 + 256 * q, w[q]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = 0.f;
-            if (id >= rows && e0 == 0 && status) atomicExch(status, GQ_ERR_SHAPE);
+                for (int i = 0; i < 8; ++i) w[q][i] = 0.f;
+            }
         }
-        kv::store8<TYPE>(Y + t * row_bytes + static_cast<long long>(e0) * kv::type_size(TYPE),
-                         make_float4(w[0], w[1], w[2], w[3]), make_float4(w[4], w[5], w[6], w[7]));
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            if (e0 + 256 * q >= end) continue;
+            const float *x = w[q];
+            kv::store8<TYPE>(y + static_cast<long long>(e0 + 256 * q) * kv::type_size(TYPE),
+                             make_float4(x[0] * scale, x[1] * scale, x[2] * scale, x[3] * scale),
+                             make_float4(x[4] * scale, x[5] * scale, x[6] * scale, x[7] * scale));
+        }
     }
 }
 
@@ -105,22 +115,27 @@ template <int FORMAT>
 cudaError_t launch(const uint8_t *W, const int32_t *ids, float scale, void *Y, long long ldy, int type, int rows, int K,
                    int M, cudaStream_t s)
 {
-    const int per_row = (K + 255) / 256;
-    const long long tasks = static_cast<long long>(M) * per_row;
-    const long long want = (tasks + kThreads / 32 - 1) / (kThreads / 32), cap = static_cast<long long>(sm_count()) * 8;
-    const dim3 grid(static_cast<unsigned>(want < cap ? want : cap)), block(kThreads);
+    // six times the warps that an SM holds, so that the last ones to finish are a small part
+    const int pieces = (K + 255) / 256, warps = sm_count() * 48 * 6;
+    int parts = (warps + M - 1) / M;
+    if (parts > pieces) parts = pieces;
+    const int part_elems = (pieces + parts - 1) / parts * 256;
+    parts = (K + part_elems - 1) / part_elems;
+    const long long ctas = (static_cast<long long>(M) * parts + kThreads / 32 - 1) / (kThreads / 32);
+    if (ctas > 0x7FFFFFFF || static_cast<long long>(M) * parts > 0xFFFFFF00ll) return cudaErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(ctas)), block(kThreads);
     uint8_t *y = static_cast<uint8_t *>(Y);
     const long long row_bytes = ldy * kv::type_size(type);
     switch (type) {
     case GQ_TYPE_F32:
-        return launch_pdl(k_embed<FORMAT, GQ_TYPE_F32>, grid, block, 0, s, W, ids, scale, y, row_bytes, rows, K, tasks,
-                          per_row, status_word());
+        return launch_pdl(k_embed<FORMAT, GQ_TYPE_F32>, grid, block, 0, s, W, ids, scale, y, row_bytes, rows, K, M,
+                          parts, part_elems, status_word());
     case GQ_TYPE_F16:
-        return launch_pdl(k_embed<FORMAT, GQ_TYPE_F16>, grid, block, 0, s, W, ids, scale, y, row_bytes, rows, K, tasks,
-                          per_row, status_word());
+        return launch_pdl(k_embed<FORMAT, GQ_TYPE_F16>, grid, block, 0, s, W, ids, scale, y, row_bytes, rows, K, M,
+                          parts, part_elems, status_word());
     default:
-        return launch_pdl(k_embed<FORMAT, GQ_TYPE_BF16>, grid, block, 0, s, W, ids, scale, y, row_bytes, rows, K, tasks,
-                          per_row, status_word());
+        return launch_pdl(k_embed<FORMAT, GQ_TYPE_BF16>, grid, block, 0, s, W, ids, scale, y, row_bytes, rows, K, M,
+                          parts, part_elems, status_word());
     }
 }
 

@@ -87,7 +87,26 @@ __device__ __forceinline__ void find_groups(Tile &tile, const Batch &B, int t0)
     __syncthreads();
 }
 
+// Asynchronous copy of 16, 8 or 4 bytes to shared memory.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void *to, const void *from)
+{
+    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(from), "n"(BYTES) : "memory");
+}
+
 // ---------------------------------------------------------------- v = A x
+// A chunk of 32 elements: a warp's weights, and activations (f32, or codes and scales).  Stages: what two CTAs per SM
+// have room for, at least two.
+__host__ __device__ constexpr int shrink_stage(int mt, int nt, bool q8) { return 1024 * mt + (q8 ? 512 : 1024) * nt; }
+__host__ __device__ constexpr int shrink_stages(int mt, int nt, bool q8)
+{
+    const int n = (108 << 10) / (8 * shrink_stage(mt, nt, q8));
+    return n > 6 ? 6 : (n < 2 ? 2 : n);
+}
 // CTA: a tile of 8 NT tokens, one slice of K.  The warps take the slice's
 // 32-element chunks in turn, each for all of rank (16 MT), and add up in
 // shared memory; the slices' sums are added by `expand`.
@@ -97,11 +116,18 @@ __global__ void __launch_bounds__(kThreads)
                   const int8_t *__restrict__ Xq, const float *__restrict__ dx, float *__restrict__ V, int rank, int K,
                   int slice_chunks)
 {
-    extern __shared__ __align__(16) float red[];  // [kWarps][16 MT][8 NT]
+    extern __shared__ __align__(16) float red[];  // [kWarps][16 MT][8 NT], and before that the warps' rings
     __shared__ Tile tile;
-    constexpr int TT = 8 * NT, kOut = 16 * MT * TT;
+    constexpr int TT = 8 * NT, kOut = 16 * MT * TT, kStage = shrink_stage(MT, NT, Q8), kStages = shrink_stages(MT, NT, Q8);
+    struct Raw {  // the lane's part of a chunk
+        uint4 a[MT][2];
+        uint2 q[NT];
+        float4 x[NT][2];
+        float d[NT][2];
+    };
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int t0 = blockIdx.x * TT, chunks = K / 32;
+    char *const ring = reinterpret_cast<char *>(red) + (threadIdx.x >> 5) * kStages * kStage;
     const int c0 = blockIdx.y * slice_chunks, c1 = min(c0 + slice_chunks, chunks);
     pdl_wait();
     // only now: what the next kernel reads before its own wait is complete then
@@ -123,36 +149,64 @@ __global__ void __launch_bounds__(kThreads)
             col_in[n][0] = tile.group[8 * n + 2 * t] == j;
             col_in[n][1] = tile.group[8 * n + 2 * t + 1] == j;
         }
-        // a chunk as it is loaded; the next one is on its way while one is multiplied
-        struct Raw {
-            uint4 a[MT][2];
-            uint2 q[NT];
-            float4 x[NT][2];
-            float d[NT][2];
+        // Chunks come through a ring in shared memory; every lane copies what it reads itself.
+        auto fetch = [&](int i) {
+            const int c = c0 + warp + kWarps * i;
+            if (c < c1) {
+                char *to = ring + (i % kStages) * kStage + lane * 16;
+                const int k = 32 * c + 8 * t;
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = 16 * m + 8 * h + g;
+                        if (r < rank) cp_async<16>(to + (2 * m + h) * 512, a + static_cast<long long>(r) * K + k);
+                    }
+                to += 1024 * MT;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const long long tok = t0 + 8 * n + g;
+                    if (Q8) {
+                        if (in[n]) cp_async<8>(to + n * 512 - lane * 8, Xq + tok * K + k);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            if (col_in[n][x])
+                                cp_async<4>(to + n * 512 + 256 + x * 128 - lane * 12, dx + static_cast<long long>(t0 + 8 * n + 2 * t + x) * chunks + c);
+                    } else if (in[n]) {
+                        cp_async<16>(to + n * 1024, X + tok * ldx + k);
+                        cp_async<16>(to + n * 1024 + 512, X + tok * ldx + k + 4);
+                    }
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        auto load = [&](Raw &w, int c) {
-            const int k = 32 * c + 8 * t;
+        auto load = [&](Raw &w, int i) {
+            const char *from = ring + (i % kStages) * kStage + lane * 16;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int r = 16 * m + 8 * h + g;
-                    w.a[m][h] = r < rank ? __ldg(reinterpret_cast<const uint4 *>(a + static_cast<long long>(r) * K + k))
-                                         : make_uint4(0, 0, 0, 0);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(from + (2 * m + h) * 512);
+                    w.a[m][h] = 16 * m + 8 * h + g < rank ? v : make_uint4(0, 0, 0, 0);
                 }
+            from += 1024 * MT;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const long long tok = t0 + 8 * n + g;
                 if (Q8) {
-                    w.q[n] = in[n] ? __ldg(reinterpret_cast<const uint2 *>(Xq + tok * K + k)) : make_uint2(0, 0);
+                    const uint2 v = *reinterpret_cast<const uint2 *>(from + n * 512 - lane * 8);
+                    w.q[n] = in[n] ? v : make_uint2(0, 0);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        w.d[n][i] = col_in[n][i] ? __ldg(dx + static_cast<long long>(t0 + 8 * n + 2 * t + i) * chunks + c) : 0.f;
+                    for (int x = 0; x < 2; ++x) {
+                        const float d = *reinterpret_cast<const float *>(from + n * 512 + 256 + x * 128 - lane * 12);
+                        w.d[n][x] = col_in[n][x] ? d : 0.f;
+                    }
                 } else {
-                    const float4 *p = reinterpret_cast<const float4 *>(X + tok * ldx + k);
                     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-                    w.x[n][0] = in[n] ? __ldg(p) : zero;
-                    w.x[n][1] = in[n] ? __ldg(p + 1) : zero;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float4 v = *reinterpret_cast<const float4 *>(from + n * 1024 + x * 512);
+                        w.x[n][x] = in[n] ? v : zero;
+                    }
                 }
             }
         };
@@ -195,17 +249,19 @@ __global__ void __launch_bounds__(kThreads)
                 }
             }
         };
-        int c = c0 + warp;
-        if (c < c1) {
-            Raw now, next;
-            load(now, c);
-            for (; c + kWarps < c1; c += kWarps) {
-                load(next, c + kWarps);
-                multiply(now);
-                now = next;
-            }
+        const int mine_n = c0 + warp < c1 ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) fetch(i);
+#pragma unroll 1
+        for (int i = 0; i < mine_n; ++i) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            Raw now;
+            load(now, i);
             multiply(now);
+            fetch(i + kStages - 1);
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // the sums take the rings' place
         float *mine = red + warp * kOut;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -233,20 +289,12 @@ __global__ void __launch_bounds__(kThreads)
 constexpr int kStages = 3;
 // Four rows of weights (16 bytes a lane, 8 where a chunk is 16 deep) and the lane's results of 8 NT tokens.
 __host__ __device__ constexpr int expand_stage(int kc, int nt) { return 64 * kc + 1024 * nt; }
-template <int BYTES>
-__device__ __forceinline__ void cp_async(void *to, const void *from)
-{
-    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(to));
-    if (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(s), "l"(from) : "memory");
-}
 // CTA: a tile of 8 NT tokens and a range of row blocks, which its warps take in
 // turn.  Row slots are dealt so that a lane's four results of a token are four
 // consecutive rows: slot g (+ 8) of instruction m is row 4 g + 2 m (+ 1).
 // KC = 16: a rank of up to 16, where a lane's chunk is four elements.
-template <int KC, int NT, bool BF16>
+// kOne: the rank is one chunk, whose v then stays in registers.
+template <int KC, bool kOne, int NT, bool BF16>
 __global__ void __launch_bounds__(kThreads, 2)
     k_lora_expand(const uint16_t *__restrict__ W, Batch B, const float *__restrict__ V, const float *Y0, long long ldy0,
                   float *Y, long long ldy, int rank, int rows, int slices, int row_groups, int group_blocks)
@@ -256,12 +304,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr int TT = 8 * NT, E = KC / 4;  // elements of a lane's chunk
     constexpr int kStageBytes = expand_stage(KC, NT);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    char *const ring = raw + warp * kStages * kStageBytes;  // the lane's parts: 2 E or 16 bytes of every 64 E or 512
+    constexpr int kRowPieces = KC / 8, kPieces = kRowPieces;  // 16-byte pieces of a row's chunk, and of a lane
+    // where piece c of row r lies: the pieces of a 128-byte line turned by the row group 4 g that reads it
+    auto place = [](int r, int c) { return (r * kRowPieces + c) ^ (kRowPieces == 2 ? (r >> 2 & 3) * 2 : (r >> 2 & 1) * 4); };
+    char *const ring = raw + warp * kStages * kStageBytes;
     float *const vs = reinterpret_cast<float *>(raw + kWarps * kStages * kStageBytes);  // [8 NT][stride]
     const int tile_no = blockIdx.x / row_groups, rg = blockIdx.x - tile_no * row_groups;
     const int t0 = tile_no * TT;
     const int rb0 = rg * group_blocks, rb1 = min(rb0 + group_blocks, (rows + kRowBlock - 1) / kRowBlock);
-    const int depth = (rank + KC - 1) / KC * KC, stride = depth + 4;
+    const int depth = (rank + KC - 1) / KC * KC, stride = KC == 16 ? depth : depth + 4;  // (no two lanes of a load on one bank)
     pdl_launch_dependents();
     // the lists, Y0 and the weights were complete before `shrink` let this
     // kernel begin; v is complete after the wait
@@ -274,19 +325,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     bool waited = false;
     for (int j = blockIdx.z; j < max(groups, 1); j += gridDim.z) {
         const bool product = j < groups;
-        if (!waited) pdl_wait();
-        waited = true;
-        const float scale = product ? __ldg(B.scale + tile.adapter[j]) : 0.f;
-        for (int i = threadIdx.x; i < TT * depth; i += kThreads) {
-            const int tok = i / depth, r = i - tok * depth;
-            float s = 0.f;
-            if (r < rank && tile.group[tok] == j) {
-                const float *p = V + static_cast<long long>(t0 + tok) * rank + r;
-                for (int c = 0; c < slices; ++c) s += __ldcg(p + static_cast<long long>(c) * B.M * rank);
-            }
-            vs[tok * stride + r] = s * scale;
-        }
-        __syncthreads();
         // tokens whose rows this pass writes: the group's, and with the first group those without an adapter, if
         // their rows have to be copied
         bool put[NT][2], add[NT][2];
@@ -300,17 +338,21 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         const uint16_t *w = W + static_cast<long long>(product ? tile.adapter[j] : 0) * rows * rank;
         // Steps: a warp's row blocks, each in nk chunks of the rank.  A step's weights, and with a block's last chunk its
-        // part of Y0, come through a ring of kStages steps in shared memory; every lane copies what it reads itself, so
-        // that nothing but its own copies' arrival has to be waited for.
+        // part of Y0, come through a ring of kStages steps in shared memory.  Of Y0 every lane copies what it reads itself;
+        // the weights are copied as they lie (a rank of 16 or 32: 1 or 2 KB without a gap; copied by the lanes that read
+        // them they cost three times their bytes), the 16-byte pieces placed so that no two lanes meet on a bank.
         const int nk = depth / KC, blocks = rb0 + warp < rb1 ? (rb1 - rb0 - warp + kWarps - 1) / kWarps : 0, steps = blocks * nk;
         int fetch_row = (rb0 + warp) * kRowBlock + 4 * g, fetch_k = 0;
         auto fetch = [&](int step) {
             if (step < steps) {
                 char *to = ring + (step % kStages) * kStageBytes;
-                if (product && fetch_row < rows && fetch_k * KC + E * t < rank) {
-                    const uint16_t *from = w + static_cast<long long>(fetch_row) * rank + fetch_k * KC + E * t;
+                if (product) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) cp_async<2 * E>(to + r * 64 * E + lane * 2 * E, from + static_cast<long long>(r) * rank);
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int r = (lane + 32 * i) / kRowPieces, c = (lane + 32 * i) % kRowPieces;
+                        const int at = fetch_row - 4 * g + r, k = fetch_k * KC + 8 * c;
+                        if (at < rows && k < rank) cp_async<16>(to + 16 * place(r, c), w + static_cast<long long>(at) * rank + k);
+                    }
                 }
                 if (++fetch_k == nk) {
                     if (fetch_row < rows) {
@@ -330,10 +372,36 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) fetch(i);
+        // v is complete after the wait; the copies above were let go before
+        if (!waited) pdl_wait();
+        waited = true;
+        const float scale = product ? __ldg(B.scale + tile.adapter[j]) : 0.f;
+        for (int i = threadIdx.x; i < TT * depth; i += kThreads) {
+            const int tok = i / depth, r = i - tok * depth;
+            float s = 0.f;
+            if (r < rank && tile.group[tok] == j) {
+                const float *p = V + static_cast<long long>(t0 + tok) * rank + r;
+#pragma unroll 8
+                for (int c = 0; c < slices; ++c) s += __ldcg(p + static_cast<long long>(c) * B.M * rank);
+            }
+            vs[tok * stride + r] = s * scale;
+        }
+        __syncthreads();
+        float2 vr[kOne ? NT : 1][E];  // leading bits and rest
+        if (kOne && product) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    const float v = vs[(8 * n + g) * stride + E * t + i];
+                    vr[n][i] = make_float2(head(v), v - head(v));
+                }
+        }
         int row = (rb0 + warp) * kRowBlock + 4 * g, kc = 0;
         float acc[NT][2][4];
         for (int step = 0; step < steps; ++step) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            __syncwarp();  // the other lanes' copies as well; and they have read the step before, whose place is next
             const char *from = ring + (step % kStages) * kStageBytes;
             if (product) {
                 const int k = kc * KC + E * t;
@@ -344,9 +412,16 @@ __global__ void __launch_bounds__(kThreads, 2)
                     uint32_t x[2][E / 2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t *q = reinterpret_cast<const uint32_t *>(from + (2 * m + h) * 64 * E + lane * 2 * E);
+                        const char *q = from + 16 * place(4 * g + 2 * m + h, E * t / 8) + (E * t % 8) * 2;
+                        if (E == 8) {
+                            const uint4 y = *reinterpret_cast<const uint4 *>(q);
+                            x[h][0] = y.x, x[h][1] = y.y, x[h][E / 2 - 2] = y.z, x[h][E / 2 - 1] = y.w;
+                        } else {
+                            const uint2 y = *reinterpret_cast<const uint2 *>(q);
+                            x[h][0] = y.x, x[h][1] = y.y;
+                        }
 #pragma unroll
-                        for (int i = 0; i < E / 2; ++i) x[h][i] = have ? q[i] : 0u;
+                        for (int i = 0; i < E / 2; ++i) x[h][i] = have ? x[h][i] : 0u;
                     }
 #pragma unroll
                     for (int s = 0; s < E / 2; ++s) {
@@ -356,22 +431,28 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    float v[E];
+                    float2 v[E];
+                    if (kOne) {
 #pragma unroll
-                    for (int q = 0; q < E / 4; ++q) {
-                        const float4 u = *reinterpret_cast<const float4 *>(vs + (8 * n + g) * stride + k + 4 * q);
-                        v[4 * q] = u.x, v[4 * q + 1] = u.y, v[4 * q + 2] = u.z, v[4 * q + 3] = u.w;
+                        for (int i = 0; i < E; ++i) v[i] = vr[n][i];
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < E / 4; ++q) {
+                            const float4 u = *reinterpret_cast<const float4 *>(vs + (8 * n + g) * stride + k + 4 * q);
+                            const float x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[4 * q + i] = make_float2(head(x[i]), x[i] - head(x[i]));
+                        }
                     }
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int s = 0; s < E / 2; ++s)
-                            mma_tf32(d, af[m][s], v[2 * s] - head(v[2 * s]), v[2 * s + 1] - head(v[2 * s + 1]));
+                        for (int s = 0; s < E / 2; ++s) mma_tf32(d, af[m][s], v[2 * s].y, v[2 * s + 1].y);
 #pragma unroll
-                        for (int s = 0; s < E / 2; ++s) mma_tf32(d, af[m][s], head(v[2 * s]), head(v[2 * s + 1]));
+                        for (int s = 0; s < E / 2; ++s) mma_tf32(d, af[m][s], v[2 * s].x, v[2 * s + 1].x);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[n][m][i] = kc == 0 ? d[i] : acc[n][m][i] + d[i];
+                        for (int i = 0; i < 4; ++i) acc[n][m][i] = kOne || kc == 0 ? d[i] : acc[n][m][i] + d[i];
                     }
                 }
             }
@@ -432,7 +513,8 @@ template <int MT, int NT, bool BF16, bool Q8>
 cudaError_t shrink(const Call &c, int tiles, int groups, int slices, int slice_chunks)
 {
     auto kern = k_lora_shrink<MT, NT, BF16, Q8>;
-    const size_t smem = sizeof(float) * kWarps * 16 * MT * 8 * NT;
+    const size_t sums = sizeof(float) * kWarps * 16 * MT * 8 * NT, rings = kWarps * shrink_stages(MT, NT, Q8) * shrink_stage(MT, NT, Q8);
+    const size_t smem = sums > rings ? sums : rings;
     if (ctas_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
     return launch_pdl(kern, dim3(tiles, slices, groups), dim3(kThreads), smem, c.s, c.A, c.B, c.X, c.ldx, c.Xq, c.dx, c.V,
                       c.rank, c.K, slice_chunks);
@@ -455,10 +537,10 @@ cudaError_t shrink_rank(const Call &c, bool bf16, int tiles, int groups, int sli
     return shrink_typed<8, NT>(c, bf16, tiles, groups, slices, slice_chunks);
 }
 
-template <int KC, int NT, bool BF16>
+template <int KC, bool kOne, int NT, bool BF16>
 cudaError_t expand(const Call &c, int tiles, int groups, int slices)
 {
-    auto kern = k_lora_expand<KC, NT, BF16>;
+    auto kern = k_lora_expand<KC, kOne, NT, BF16>;
     const int depth = (c.rank + KC - 1) / KC * KC;
     const size_t smem = sizeof(float) * 8 * NT * (depth + 4) + kWarps * kStages * expand_stage(KC, NT);
     if (ctas_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
@@ -477,8 +559,10 @@ template <int NT>
 cudaError_t expand_rank(const Call &c, bool bf16, int tiles, int groups, int slices)
 {
     if (c.rank <= 16)
-        return bf16 ? expand<16, NT, true>(c, tiles, groups, slices) : expand<16, NT, false>(c, tiles, groups, slices);
-    return bf16 ? expand<32, NT, true>(c, tiles, groups, slices) : expand<32, NT, false>(c, tiles, groups, slices);
+        return bf16 ? expand<16, true, NT, true>(c, tiles, groups, slices) : expand<16, true, NT, false>(c, tiles, groups, slices);
+    if (c.rank <= 32)
+        return bf16 ? expand<32, true, NT, true>(c, tiles, groups, slices) : expand<32, true, NT, false>(c, tiles, groups, slices);
+    return bf16 ? expand<32, false, NT, true>(c, tiles, groups, slices) : expand<32, false, NT, false>(c, tiles, groups, slices);
 }
 
 int run(const Call &c, int type)

@@ -61,7 +61,7 @@ extern "C" {
  *
  * Range: 1 <= n_seq <= GQ_MAX_PLAN_SEQ, page_tokens a multiple of 16 up to
  * 4096, max_pages * page_tokens at most 2^28, 0 <= n_tokens <= 2^28,
- * n_pages >= 1.  Errors before the launch: GQ_ERR_NULL, GQ_ERR_ALIGN,
+ * 1 <= n_pages <= 2^28.  Errors before the launch: GQ_ERR_NULL, GQ_ERR_ALIGN,
  * GQ_ERR_SHAPE; after it GQ_ERR_CUDA.
  * ------------------------------------------------------------------------ */
 int gq_kv_plan(const int32_t *n_new, const int32_t *kv_len_in, const int32_t *ring_in, int32_t *free_pages,

@@ -48,7 +48,7 @@ def test_plan():
     lists = ("n_new", "kv_in", "ring_in", "free", "table", "kv_len", "q_start", "ring")
     refuses(name, PLAN, gq.GQ_ERR_NULL, **{p: [None] for p in lists})
     refuses(name, PLAN, gq.GQ_ERR_ALIGN, **{p: [A + 2] for p in lists + ("position", "sequence")}, slot=[A + 4])
-    refuses(name, PLAN, gq.GQ_ERR_SHAPE, n_pages=[0, -1], max_pages=[0, 1 << 25], page=[0, 8, 24, 4112],
+    refuses(name, PLAN, gq.GQ_ERR_SHAPE, n_pages=[0, -1, (1 << 28) + 1], max_pages=[0, 1 << 25], page=[0, 8, 24, 4112],
             n_seq=[0, gq.GQ_MAX_PLAN_SEQ + 1], n_tokens=[-1, (1 << 28) + 1])
 
 
