@@ -21,54 +21,77 @@ constexpr int kThreads = 256;
 
 __device__ __forceinline__ float half_f(uint16_t h) { return __half2float(__ushort_as_half(h)); }
 
-// The eight weights e0 .. e0 + 7 of row r (e0 a multiple of 8).
+// A whole number below 2^23, less `off`, as f32: put under the exponent of 2^23 it
+// needs no conversion.
+__device__ __forceinline__ float whole(uint32_t q, float off = 0.f) { return __uint_as_float(0x4B000000u | q) - (8388608.0f + off); }
+
+// Where row r's parts lie: codes, (Q6_K) top bits and sub-scales, scales or records.
+struct Row {
+    const uint8_t *codes, *top, *sub, *scales;
+};
 template <int FORMAT>
-__device__ __forceinline__ void decode8(const uint8_t *__restrict__ W, long long rows, int K, long long r, int e0,
-                                        float (&w)[8])
+__device__ __forceinline__ Row row_at(const uint8_t *W, long long rows, int K, long long r)
+{
+    const long long nb = K / 32, ns = K / 256;
+    if (FORMAT == GQ_FORMAT_Q8_0) return {W + r * nb * 32, nullptr, nullptr, W + rows * nb * 32 + r * nb * 2};
+    if (FORMAT == GQ_FORMAT_Q4_0) return {W + r * nb * 16, nullptr, nullptr, W + rows * nb * 16 + r * nb * 2};
+    if (FORMAT == GQ_FORMAT_Q4_K) return {W + r * ns * 128, nullptr, nullptr, W + (rows * 128 + r * 16) * ns};
+    return {W + r * ns * 128, W + (rows * 128 + r * 64) * ns, W + (rows * 192 + r * 16) * ns, W + (rows * 208 + r * 2) * ns};
+}
+
+// What eight weights are made of, as it is loaded; and the weights e0 .. e0 + 7 (e0 a multiple of 8) from it.
+struct Raw {
+    uint4 rec;
+    uint32_t c0, c1;
+};
+template <int FORMAT>
+__device__ __forceinline__ void load8(const Row &r, int e0, Raw &x)
+{
+    auto u16 = [&](const uint8_t *p, int i) { return static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(p) + i)); };
+    if (FORMAT == GQ_FORMAT_Q8_0) {
+        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(r.codes + e0));
+        x.c0 = c.x, x.c1 = c.y;
+        x.rec.x = u16(r.scales, e0 / 32);
+        return;
+    }
+    x.c0 = __ldg(reinterpret_cast<const uint32_t *>(r.codes + e0 / 2));
+    if (FORMAT == GQ_FORMAT_Q4_0) {
+        x.rec.x = u16(r.scales, e0 / 32);
+    } else if (FORMAT == GQ_FORMAT_Q4_K) {
+        x.rec = __ldg(reinterpret_cast<const uint4 *>(r.scales) + e0 / 256);
+    } else {
+        x.c1 = __ldg(reinterpret_cast<const uint32_t *>(r.top) + e0 / 16);
+        x.rec.x = u16(r.scales, e0 / 256);
+        x.rec.y = __ldg(r.sub + e0 / 16);
+    }
+}
+template <int FORMAT>
+__device__ __forceinline__ void decode8(const Raw &x, int e0, float (&w)[8])
 {
     if (FORMAT == GQ_FORMAT_Q8_0) {
-        const long long nb = K / 32, blk = r * nb + e0 / 32;
-        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(W + blk * 32 + (e0 & 31)));
-        const float d = half_f(__ldg(reinterpret_cast<const uint16_t *>(W + rows * nb * 32) + blk));
+        const float d = half_f(static_cast<uint16_t>(x.rec.x));
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w[i] = d * static_cast<float>(static_cast<int>((i < 4 ? c.x : c.y) >> (8 * (i & 3)) & 255u) - 128);
+        for (int i = 0; i < 8; ++i) w[i] = d * (__uint_as_float(__byte_perm(i < 4 ? x.c0 : x.c1, 0x4B000000u, 0x7440 | (i & 3))) - 8388736.0f);
     } else if (FORMAT == GQ_FORMAT_Q4_0) {
-        const long long nb = K / 32, blk = r * nb + e0 / 32;
-        const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(W + blk * 16 + (e0 & 31) / 2));
-        const float d = half_f(__ldg(reinterpret_cast<const uint16_t *>(W + rows * nb * 16) + blk));
+        const float d = half_f(static_cast<uint16_t>(x.rec.x));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = d * static_cast<float>(static_cast<int>(c >> (4 * i) & 15u) - 8);
+        for (int i = 0; i < 8; ++i) w[i] = d * whole(x.c0 >> (4 * i) & 15u, 8.f);
     } else if (FORMAT == GQ_FORMAT_Q4_K) {
-        const long long ns = K / 256, sb = r * ns + e0 / 256;
-        const int s = (e0 & 255) / 32;
-        const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(W + sb * 128 + (e0 & 255) / 2));
-        const uint4 rec = __ldg(reinterpret_cast<const uint4 *>(W + rows * ns * 128) + sb);
-        const float d = half_f(static_cast<uint16_t>(rec.x)), dmin = half_f(static_cast<uint16_t>(rec.x >> 16));
+        const float d = half_f(static_cast<uint16_t>(x.rec.x)), dmin = half_f(static_cast<uint16_t>(x.rec.x >> 16));
         // bytes 0-3: scales 0-3 in 6 bits, 4-7: minima 0-3, 8-11: the low four bits of both of 4-7, whose top two
         // bits are those of the first eight bytes
-        const int sh = 8 * (s & 3);
-        const uint32_t lo = rec.y >> sh & 255u, mi = rec.z >> sh & 255u, hi = rec.w >> sh & 255u;
-        const uint32_t sc = s < 4 ? lo & 63u : (hi & 15u) | (lo >> 6) << 4;
-        const uint32_t mn = s < 4 ? mi & 63u : hi >> 4 | (mi >> 6) << 4;
-        const float dsc = d * static_cast<float>(sc), m = dmin * static_cast<float>(mn);
+        const int s = (e0 & 255) / 32, sh = 8 * (s & 3);
+        const uint32_t lo = x.rec.y >> sh, mi = x.rec.z >> sh, hi = x.rec.w >> sh;
+        const uint32_t sc = s < 4 ? lo & 63u : (hi & 15u) | (lo >> 2 & 48u);
+        const uint32_t mn = s < 4 ? mi & 63u : (hi >> 4 & 15u) | (mi >> 2 & 48u);
+        const float dsc = d * whole(sc), m = -dmin * whole(mn);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = fmaf(dsc, static_cast<float>(c >> (4 * i) & 15u), -m);
+        for (int i = 0; i < 8; ++i) w[i] = fmaf(dsc, whole(x.c0 >> (4 * i) & 15u), m);
     } else {
-        const long long ns = K / 256, sb = r * ns + e0 / 256;
-        const int e = e0 & 255;
-        const uint8_t *top = W + rows * ns * 128, *sub = top + rows * ns * 64;
-        const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(W + sb * 128 + e / 2));
-        const uint32_t t = __ldg(reinterpret_cast<const uint32_t *>(top + sb * 64) + e / 16);
-        const float sc = static_cast<float>(static_cast<int8_t>(__ldg(sub + sb * 16 + e / 16)));
-        const float d = half_f(__ldg(reinterpret_cast<const uint16_t *>(sub + rows * ns * 16) + sb)) * sc;
-        const int a0 = (e & 8) / 4;  // elements 4 a + i of the word, a from a0
+        const float d = half_f(static_cast<uint16_t>(x.rec.x)) * static_cast<float>(static_cast<int8_t>(x.rec.y));
+        const uint32_t t = x.c1 >> ((e0 & 8) ? 16 : 0);  // elements 4 a + i of the word, a = 0, 1 or 2, 3
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int p = (a0 ? 16 : 0) + (i < 4 ? 0 : 2) + 4 * (i & 3);
-            const int q = static_cast<int>(c >> (4 * i) & 15u) + static_cast<int>((t >> p & 3u) << 4) - 32;
-            w[i] = d * static_cast<float>(q);
-        }
+        for (int i = 0; i < 8; ++i) w[i] = d * whole((x.c0 >> (4 * i) & 15u) | (t >> ((i < 4 ? 0 : 2) + 4 * (i & 3)) & 3u) << 4, 32.f);
     }
 }
 
@@ -88,22 +111,20 @@ __global__ void __launch_bounds__(kThreads)
     const int end = min(K, (part + 1) * part_elems);
     const bool have = id >= 0 && id < rows;
     if (id >= rows && part == 0 && lane == 0 && status) atomicExch(status, GQ_ERR_SHAPE);
+    const Row r = row_at<FORMAT>(W, rows, K, have ? id : 0);
     uint8_t *y = Y + t * row_bytes;
     for (int e0 = part * part_elems + 8 * lane; e0 < end; e0 += kBatch * 256) {
-        float w[kBatch][8];
+        Raw w[kBatch];
+        if (have) {
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            if (have && e0 + 256 * q < end) {
-                decode8<FORMAT>(W, rows, K, id, e0 + 256 * q, w[q]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[q][i] = 0.f;
-            }
+            for (int q = 0; q < kBatch; ++q)
+                if (e0 + 256 * q < end) load8<FORMAT>(r, e0 + 256 * q, w[q]);
         }
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
             if (e0 + 256 * q >= end) continue;
-            const float *x = w[q];
+            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (have) decode8<FORMAT>(w[q], e0, x);
             kv::store8<TYPE>(y + static_cast<long long>(e0 + 256 * q) * kv::type_size(TYPE),
                              make_float4(x[0] * scale, x[1] * scale, x[2] * scale, x[3] * scale),
                              make_float4(x[4] * scale, x[5] * scale, x[6] * scale, x[7] * scale));
