@@ -3,7 +3,7 @@
 // A warp takes a token's row, or a part of it where there are fewer tokens than
 // warps: 256 consecutive weights at a time, eight per lane.  A lane's codes are
 // one load of 4 or 8 bytes, its scales one or two short ones that its neighbours
-// share, its result one or two 16-byte stores; four such pieces are loaded before
+// share, its result one or two 16-byte stores; two such pieces are loaded before
 // the first is stored.
 //
 // What bounds it: the writes.
@@ -65,17 +65,34 @@ __device__ __forceinline__ void load8(const Row &r, int e0, Raw &x)
         x.rec.y = __ldg(r.sub + e0 / 16);
     }
 }
-template <int FORMAT>
-__device__ __forceinline__ void decode8(const Raw &x, int e0, float (&w)[8])
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Nibbles i and i + 4 of c as f32, less `off`: masked in place they are units under the exponent of 2^(23 - 4 i).
+template <int I>
+__device__ __forceinline__ float2 nibbles(uint32_t c, float off)
 {
+    constexpr uint32_t kOne = 0x4B000000u - 0x02000000u * I;  // bits of 2^(23 - 4 I)
+    const uint32_t lo = (c & 15u << (4 * I)) | kOne, hi = (c >> 16 & 15u << (4 * I)) | kOne;
+    return __fadd2_rn(make_float2(__uint_as_float(lo), __uint_as_float(hi)), both(-(static_cast<float>(1 << (23 - 4 * I)) + off)));
+}
+template <int FORMAT>
+__device__ __forceinline__ void decode8(const Raw &x, int e0, float scale, float (&y)[8])
+{
+    float2 p[4];  // weights i and i + 4
     if (FORMAT == GQ_FORMAT_Q8_0) {
-        const float d = half_f(static_cast<uint16_t>(x.rec.x));
+        const float2 d = both(half_f(static_cast<uint16_t>(x.rec.x)));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = d * (__uint_as_float(__byte_perm(i < 4 ? x.c0 : x.c1, 0x4B000000u, 0x7440 | (i & 3))) - 8388736.0f);
+        for (int i = 0; i < 4; ++i) {
+            const float2 q = make_float2(__uint_as_float(__byte_perm(x.c0, 0x4B000000u, 0x7440 | i)),
+                                         __uint_as_float(__byte_perm(x.c1, 0x4B000000u, 0x7440 | i)));
+            p[i] = __fmul2_rn(__fadd2_rn(q, both(-8388736.0f)), d);
+        }
     } else if (FORMAT == GQ_FORMAT_Q4_0) {
-        const float d = half_f(static_cast<uint16_t>(x.rec.x));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = d * whole(x.c0 >> (4 * i) & 15u, 8.f);
+        const float2 d = both(half_f(static_cast<uint16_t>(x.rec.x)));
+        p[0] = __fmul2_rn(nibbles<0>(x.c0, 8.f), d);
+        p[1] = __fmul2_rn(nibbles<1>(x.c0, 8.f), d);
+        p[2] = __fmul2_rn(nibbles<2>(x.c0, 8.f), d);
+        p[3] = __fmul2_rn(nibbles<3>(x.c0, 8.f), d);
     } else if (FORMAT == GQ_FORMAT_Q4_K) {
         const float d = half_f(static_cast<uint16_t>(x.rec.x)), dmin = half_f(static_cast<uint16_t>(x.rec.x >> 16));
         // bytes 0-3: scales 0-3 in 6 bits, 4-7: minima 0-3, 8-11: the low four bits of both of 4-7, whose top two
@@ -84,23 +101,34 @@ __device__ __forceinline__ void decode8(const Raw &x, int e0, float (&w)[8])
         const uint32_t lo = x.rec.y >> sh, mi = x.rec.z >> sh, hi = x.rec.w >> sh;
         const uint32_t sc = s < 4 ? lo & 63u : (hi & 15u) | (lo >> 2 & 48u);
         const uint32_t mn = s < 4 ? mi & 63u : (hi >> 4 & 15u) | (mi >> 2 & 48u);
-        const float dsc = d * whole(sc), m = -dmin * whole(mn);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = fmaf(dsc, whole(x.c0 >> (4 * i) & 15u), m);
+        const float2 dsc = both(d * whole(sc)), m = both(-dmin * whole(mn));
+        p[0] = __ffma2_rn(nibbles<0>(x.c0, 0.f), dsc, m);
+        p[1] = __ffma2_rn(nibbles<1>(x.c0, 0.f), dsc, m);
+        p[2] = __ffma2_rn(nibbles<2>(x.c0, 0.f), dsc, m);
+        p[3] = __ffma2_rn(nibbles<3>(x.c0, 0.f), dsc, m);
     } else {
-        const float d = half_f(static_cast<uint16_t>(x.rec.x)) * static_cast<float>(static_cast<int8_t>(x.rec.y));
+        const float2 d = both(half_f(static_cast<uint16_t>(x.rec.x)) * static_cast<float>(static_cast<int8_t>(x.rec.y)));
         const uint32_t t = x.c1 >> ((e0 & 8) ? 16 : 0);  // elements 4 a + i of the word, a = 0, 1 or 2, 3
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = d * whole((x.c0 >> (4 * i) & 15u) | (t >> ((i < 4 ? 0 : 2) + 4 * (i & 3)) & 3u) << 4, 32.f);
+        for (int i = 0; i < 4; ++i) {
+            auto q = [&](int e, int at) { return whole((x.c0 >> (4 * e) & 15u) | (t >> at & 3u) << 4, 32.f); };
+            p[i] = __fmul2_rn(make_float2(q(i, 4 * i), q(i + 4, 4 * i + 2)), d);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = __fmul2_rn(p[i], both(scale));
+        y[i] = v.x;
+        y[i + 4] = v.y;
     }
 }
 
 template <int FORMAT, int TYPE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
     k_embed(const uint8_t *__restrict__ W, const int32_t *__restrict__ ids, float scale, uint8_t *__restrict__ Y,
             long long row_bytes, int rows, int K, int M, int parts, int part_elems, int *status)
 {
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 2;
     const int lane = threadIdx.x & 31;
     const unsigned warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     const int t = static_cast<int>(warp / static_cast<unsigned>(parts)), part = static_cast<int>(warp - t * static_cast<unsigned>(parts));
@@ -124,10 +152,9 @@ __global__ void __launch_bounds__(kThreads)
         for (int q = 0; q < kBatch; ++q) {
             if (e0 + 256 * q >= end) continue;
             float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (have) decode8<FORMAT>(w[q], e0, x);
+            if (have) decode8<FORMAT>(w[q], e0, scale, x);
             kv::store8<TYPE>(y + static_cast<long long>(e0 + 256 * q) * kv::type_size(TYPE),
-                             make_float4(x[0] * scale, x[1] * scale, x[2] * scale, x[3] * scale),
-                             make_float4(x[4] * scale, x[5] * scale, x[6] * scale, x[7] * scale));
+                             make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7]));
         }
     }
 }
@@ -136,8 +163,8 @@ template <int FORMAT>
 cudaError_t launch(const uint8_t *W, const int32_t *ids, float scale, void *Y, long long ldy, int type, int rows, int K,
                    int M, cudaStream_t s)
 {
-    // six times the warps that an SM holds, so that the last ones to finish are a small part
-    const int pieces = (K + 255) / 256, warps = sm_count() * 48 * 6;
+    // three times the warps that the SMs hold, so that the last ones to finish are a small part
+    const int pieces = (K + 255) / 256, warps = sm_count() * 64 * 3;
     int parts = (warps + M - 1) / M;
     if (parts > pieces) parts = pieces;
     const int part_elems = (pieces + parts - 1) / parts * 256;
