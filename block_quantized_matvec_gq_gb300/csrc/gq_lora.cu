@@ -297,7 +297,7 @@ __host__ __device__ constexpr int expand_stage(int kc, int nt) { return 64 * kc 
 template <int KC, bool kOne, int NT, bool BF16>
 __global__ void __launch_bounds__(kThreads, 2)
     k_lora_expand(const uint16_t *__restrict__ W, Batch B, const float *__restrict__ V, const float *Y0, long long ldy0,
-                  float *Y, long long ldy, int rank, int rows, int slices, int row_groups, int group_blocks)
+                  float *Y, long long ldy, int rank, int rows, int slices, long long cta_blocks, long long total_blocks)
 {
     extern __shared__ __align__(16) char raw[];
     __shared__ Tile tile;
@@ -309,20 +309,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto place = [](int r, int c) { return (r * kRowPieces + c) ^ (kRowPieces == 2 ? (r >> 2 & 3) * 2 : (r >> 2 & 1) * 4); };
     char *const ring = raw + warp * kStages * kStageBytes;
     float *const vs = reinterpret_cast<float *>(raw + kWarps * kStages * kStageBytes);  // [8 NT][stride]
-    const int tile_no = blockIdx.x / row_groups, rg = blockIdx.x - tile_no * row_groups;
-    const int t0 = tile_no * TT;
-    const int rb0 = rg * group_blocks, rb1 = min(rb0 + group_blocks, (rows + kRowBlock - 1) / kRowBlock);
-    const int depth = (rank + KC - 1) / KC * KC, stride = KC == 16 ? depth : depth + 4;  // (no two lanes of a load on one bank)
+    const int depth = kOne ? KC : (rank + KC - 1) / KC * KC, stride = KC == 16 ? depth : depth + 4;  // (no two lanes of a load on one bank)
     pdl_launch_dependents();
+    bool waited = false;
+    // a range of all tiles' row blocks in one row
+    const int tile_blocks = (rows + kRowBlock - 1) / kRowBlock;
+    const long long last = min((blockIdx.x + 1ll) * cta_blocks, total_blocks);
+    for (long long at = blockIdx.x * cta_blocks; at < last;) {
+    const int tile_no = static_cast<int>(at / tile_blocks), rb0 = static_cast<int>(at - static_cast<long long>(tile_no) * tile_blocks);
+    const int rb1 = static_cast<int>(min(static_cast<long long>(tile_blocks), rb0 + (last - at)));
+    at += rb1 - rb0;
+    const int t0 = tile_no * TT;
     // the lists, Y0 and the weights were complete before `shrink` let this
     // kernel begin; v is complete after the wait
     find_groups<TT>(tile, B, t0);
     const int groups = tile.groups;
-    if (static_cast<int>(blockIdx.z) >= max(groups, 1)) {
-        pdl_wait();
-        return;
-    }
-    bool waited = false;
     for (int j = blockIdx.z; j < max(groups, 1); j += gridDim.z) {
         const bool product = j < groups;
         // tokens whose rows this pass writes: the group's, and with the first group those without an adapter, if
@@ -376,15 +377,18 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!waited) pdl_wait();
         waited = true;
         const float scale = product ? __ldg(B.scale + tile.adapter[j]) : 0.f;
-        for (int i = threadIdx.x; i < TT * depth; i += kThreads) {
-            const int tok = i / depth, r = i - tok * depth;
-            float s = 0.f;
+        for (int i = threadIdx.x; i < TT * depth / 4; i += kThreads) {
+            const int tok = i / (depth / 4), r = 4 * (i - tok * (depth / 4));
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rank && tile.group[tok] == j) {
                 const float *p = V + static_cast<long long>(t0 + tok) * rank + r;
 #pragma unroll 8
-                for (int c = 0; c < slices; ++c) s += __ldcg(p + static_cast<long long>(c) * B.M * rank);
+                for (int c = 0; c < slices; ++c) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(p + static_cast<long long>(c) * B.M * rank));
+                    sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+                }
             }
-            vs[tok * stride + r] = s * scale;
+            *reinterpret_cast<float4 *>(vs + tok * stride + r) = make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale);
         }
         __syncthreads();
         float2 vr[kOne ? NT : 1][E];  // leading bits and rest
@@ -481,11 +485,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
     }
+    __syncthreads();
+    }
+    if (!waited) pdl_wait();
 }
 
 // ---------------------------------------------------------------- host
 // Slices of K: enough CTAs for two per SM, at least one chunk for every warp.
-constexpr int kWantCtas = 912, kExpandCtas = 608;
+constexpr int kWantCtas = 456;
 int most_slices(int K, int M)
 {
     const int tiles = (M + 7) / 8, by_k = (K / 32 + kWarps - 1) / kWarps;
@@ -544,16 +551,13 @@ cudaError_t expand(const Call &c, int tiles, int groups, int slices)
     const int depth = (c.rank + KC - 1) / KC * KC;
     const size_t smem = sizeof(float) * 8 * NT * (depth + 4) + kWarps * kStages * expand_stage(KC, NT);
     if (ctas_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
-    const int blocks = (c.rows + kRowBlock - 1) / kRowBlock, most = (blocks + kWarps - 1) / kWarps;
-    const long long have = static_cast<long long>(tiles) * groups;
-    long long rg = (kExpandCtas + have - 1) / have;
-    if (rg > most) rg = most;
-    const int group_blocks = static_cast<int>((blocks + rg - 1) / rg);
-    const int row_groups = (blocks + group_blocks - 1) / group_blocks;
-    const long long grid = static_cast<long long>(tiles) * row_groups;
-    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    return launch_pdl(kern, dim3(static_cast<unsigned>(grid), 1, groups), dim3(kThreads), smem, c.s, c.W, c.B, c.V, c.Y0,
-                      c.ldy0, c.Y, c.ldy, c.rank, c.rows, slices, row_groups, group_blocks);
+    // two CTAs per SM at once, the row blocks of all tiles dealt out evenly: no SM is left with less at the end
+    const long long total = static_cast<long long>(tiles) * ((c.rows + kRowBlock - 1) / kRowBlock);
+    const int ctas = (2 * sm_count() + groups - 1) / groups;
+    long long per = (total + ctas - 1) / ctas;
+    if (per < kWarps) per = kWarps;
+    return launch_pdl(kern, dim3(static_cast<unsigned>((total + per - 1) / per), 1, groups), dim3(kThreads), smem, c.s, c.W, c.B, c.V,
+                      c.Y0, c.ldy0, c.Y, c.ldy, c.rank, c.rows, slices, per, total);
 }
 template <int NT>
 cudaError_t expand_rank(const Call &c, bool bf16, int tiles, int groups, int slices)
@@ -572,7 +576,9 @@ int run(const Call &c, int type)
     // requests have 16 tokens or more on average.
     const bool long_runs = c.B.sequence != nullptr && c.B.M / 16 >= c.B.n_seq;
     const int tt = long_runs ? 16 : 8, st = long_runs ? 16 : 8;  // tokens of an expand and of a shrink tile
-    const int distinct = long_runs ? 1 : (c.B.n_adapters < tt ? c.B.n_adapters : tt);
+    int distinct = long_runs ? 1 : tt;
+    if (distinct > c.B.n_adapters) distinct = c.B.n_adapters;
+    if (distinct > c.B.M) distinct = c.B.M;
     const int tiles = (c.B.M + tt - 1) / tt, shrink_tiles = (c.B.M + st - 1) / st, chunks = c.K / 32;
     int slices = most_slices(c.K, c.B.M);
     const int enough = static_cast<int>((kWantCtas + static_cast<long long>(shrink_tiles) * distinct - 1) /
