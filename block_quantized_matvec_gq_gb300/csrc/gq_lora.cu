@@ -24,6 +24,7 @@
 #include "gq_host.h"
 #include "gq_internal.cuh"
 #include "gq_lora.h"
+#include "gq_tc.cuh"
 
 namespace gq {
 namespace {
@@ -490,6 +491,239 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!waited) pdl_wait();
 }
 
+// ---------------------------------------------------------------- the same for prompts
+// Tiles of 16 tokens by 256 rows as bulk copies: a producer warp brings Y0's 16
+// stretches of 1 KB and the rows' weights into a stage, eight warps add B v in
+// place, and the producer sends the stretches to Y.  Copied by the threads that
+// hold the results, in 128-byte pieces of four tokens an instruction, the same
+// bytes took 168 us where this takes 136 (4096 tokens, 21504 rows, rank 16:
+// 705 MB); long stretches are what the memory is fast at, and the copies cost the
+// multiplying warps no instructions.
+constexpr int kBulkThreads = kThreads + 32, kBulkTokens = 16, kBulkRows = 256, kPitch = 4 * kBulkRows + 16;
+__host__ __device__ constexpr int bulk_stage(int rank) { return kBulkTokens * kPitch + 2 * kBulkRows * rank; }
+inline int bulk_stages(int rank)
+{
+    const int n = (104 << 10) / bulk_stage(rank);
+    return n > 6 ? 6 : (n < 2 ? 2 : n);
+}
+__device__ __forceinline__ void bulk_store(void *to, uint32_t from, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(from), "r"(bytes) : "memory");
+}
+
+template <int KC, bool kOne, bool BF16>
+__global__ void __launch_bounds__(kBulkThreads, 2)
+    k_lora_expand_bulk(const uint16_t *__restrict__ W, Batch B, const float *__restrict__ V, const float *Y0, long long ldy0,
+                       float *Y, long long ldy, int rank, int rows, int slices, long long cta_items, long long total_items,
+                       int stages)
+{
+    extern __shared__ __align__(16) char raw[];
+    __shared__ Tile tile;
+    __shared__ __align__(8) uint64_t bars[2 * 6];  // filled, and multiplied
+    __shared__ int abort;
+    constexpr int E = KC / 4, NT = 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int depth = kOne ? KC : (rank + KC - 1) / KC * KC, stride = KC == 16 ? depth : depth + 4;
+    const int stage_bytes = bulk_stage(rank);
+    float *const vs = reinterpret_cast<float *>(raw + stages * stage_bytes);
+    const uint32_t base = tcu::smem_u32(raw), full = tcu::smem_u32(bars), done = full + 8 * 6;
+    volatile int *const abort_flag = &abort;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            tcu::mbar_init(full + 8 * i, 1);
+            tcu::mbar_init(done + 8 * i, kWarps);
+        }
+        abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    pdl_launch_dependents();
+    bool waited = false;
+    int stage = 0, phase = 0;  // of the next item
+    auto next_stage = [&](int &s, int &ph) {
+        if (++s == stages) {
+            s = 0;
+            ph ^= 1;
+        }
+    };
+    const int tile_items = (rows + kBulkRows - 1) / kBulkRows;
+    const long long last = min((blockIdx.x + 1ll) * cta_items, total_items);
+    for (long long at = blockIdx.x * cta_items; at < last;) {
+        const int tile_no = static_cast<int>(at / tile_items), i0 = static_cast<int>(at - static_cast<long long>(tile_no) * tile_items);
+        const int n = static_cast<int>(min(static_cast<long long>(tile_items - i0), last - at));
+        at += n;
+        const int t0 = tile_no * kBulkTokens;
+        // the lists, Y0 and the weights were complete before `shrink` let this kernel begin; v is complete after the wait
+        find_groups<kBulkTokens>(tile, B, t0);
+        const int groups = tile.groups;
+        for (int j = 0; j < max(groups, 1); ++j) {
+            const bool product = j < groups;
+            unsigned add = 0, put = 0;  // tokens with a product, and tokens that are written
+            for (int i = 0; i < kBulkTokens; ++i) {
+                const int of = tile.group[i];
+                if (product && of == j) add |= 1u << i;
+                if (j == 0 && of < 0 && t0 + i < B.M && Y != Y0) put |= 1u << i;
+            }
+            put |= add;
+            if (put == 0) continue;
+            const uint16_t *w = W + static_cast<long long>(product ? tile.adapter[j] : 0) * rows * rank;
+            if (warp == kWarps) {
+                // ---- the producer: lane i < 16 copies token i, lane 16 the weights
+                const bool mine = lane < kBulkTokens && (put >> lane & 1u);
+                const float *y0 = Y0 + (t0 + lane) * ldy0;
+                float *y = Y + (t0 + lane) * ldy;
+                int ls = stage, lp = phase, issued = 0;
+                auto load = [&](int i) {
+                    const int row = (i0 + i) * kBulkRows, count = min(kBulkRows, rows - row);
+                    const uint32_t to = base + ls * stage_bytes, bar = full + 8 * ls;
+                    if (lane == 0) tcu::mbar_expect_tx(bar, __popc(put) * count * 4 + (product ? count * rank * 2 : 0));
+                    __syncwarp();
+                    if (mine) tcu::bulk_load(to + lane * kPitch, y0 + row, count * 4, bar);
+                    if (lane == kBulkTokens && product)
+                        tcu::bulk_load(to + kBulkTokens * kPitch, w + static_cast<long long>(row) * rank, count * rank * 2, bar);
+                    next_stage(ls, lp);
+                    ++issued;
+                };
+                for (int i = 0; i < stages - 1 && i < n; ++i) load(i);
+                int s = stage, ph = phase, i = 0;
+                for (; i < n; ++i) {
+                    if (i + stages - 1 < n) {
+                        // into the stage of the item before, once its results have been read
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        __syncwarp();
+                        load(i + stages - 1);
+                    }
+                    if (!tcu::wait_warp(done + 8 * s, ph, abort_flag, B.status)) break;
+                    const int row = (i0 + i) * kBulkRows, count = min(kBulkRows, rows - row);
+                    if (mine) bulk_store(y + row, base + s * stage_bytes + lane * kPitch, count * 4);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    next_stage(s, ph);
+                }
+                if (i < n) {  // gave up: its copies have to arrive before the CTA may end
+                    int ws = stage, wp = phase;
+                    for (int x = 0; x < issued; ++x, next_stage(ws, wp)) {
+                        abort = 0;
+                        tcu::wait_warp(full + 8 * ws, wp, abort_flag, B.status);
+                    }
+                    abort = 1;
+                }
+                asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            } else {
+                // ---- the multiplying warps: 32 rows each
+                if (!waited) pdl_wait();
+                const float scale = product ? __ldg(B.scale + tile.adapter[j]) : 0.f;
+                for (int i = threadIdx.x; i < kBulkTokens * depth / 4; i += kThreads) {
+                    const int tok = i / (depth / 4), r = 4 * (i - tok * (depth / 4));
+                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (r < rank && (add >> tok & 1u)) {
+                        const float *p = V + static_cast<long long>(t0 + tok) * rank + r;
+#pragma unroll 8
+                        for (int c = 0; c < slices; ++c) {
+                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(p + static_cast<long long>(c) * B.M * rank));
+                            sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+                        }
+                    }
+                    *reinterpret_cast<float4 *>(vs + tok * stride + r) =
+                        make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale);
+                }
+                asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+                float2 vr[kOne ? NT : 1][E];  // leading bits and rest
+                if (kOne) {
+#pragma unroll
+                    for (int q = 0; q < NT; ++q)
+#pragma unroll
+                        for (int i = 0; i < E; ++i) {
+                            const float v = vs[(8 * q + g) * stride + E * t + i];
+                            vr[q][i] = make_float2(head(v), v - head(v));
+                        }
+                }
+                int s = stage, ph = phase;
+                for (int i = 0; i < n; ++i) {
+                    if (!tcu::wait_warp(full + 8 * s, ph, abort_flag, B.status)) break;
+                    char *const from = raw + s * stage_bytes;
+                    if (product) {
+                        float acc[NT][2][4];
+                        for (int k0 = 0; k0 < depth; k0 += KC) {
+                            const int k = k0 + E * t;
+                            float af[2][E / 2][4];
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                uint32_t x[2][E / 2];
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const char *q = from + kBulkTokens * kPitch + ((32 * warp + 16 * m + 8 * h + g) * rank + k) * 2;
+                                    if (E == 8) {
+                                        const uint4 y = *reinterpret_cast<const uint4 *>(q);
+                                        x[h][0] = y.x, x[h][1] = y.y, x[h][E / 2 - 2] = y.z, x[h][E / 2 - 1] = y.w;
+                                    } else {
+                                        const uint2 y = *reinterpret_cast<const uint2 *>(q);
+                                        x[h][0] = y.x, x[h][1] = y.y;
+                                    }
+#pragma unroll
+                                    for (int e = 0; e < E / 2; ++e) x[h][e] = k < rank ? x[h][e] : 0u;
+                                }
+#pragma unroll
+                                for (int e = 0; e < E / 2; ++e) {
+                                    const float2 lo = weights2<BF16>(x[0][e]), hi = weights2<BF16>(x[1][e]);
+                                    af[m][e][0] = lo.x, af[m][e][1] = hi.x, af[m][e][2] = lo.y, af[m][e][3] = hi.y;
+                                }
+                            }
+#pragma unroll
+                            for (int q = 0; q < NT; ++q) {
+                                float2 v[E];
+                                if (kOne) {
+#pragma unroll
+                                    for (int e = 0; e < E; ++e) v[e] = vr[q][e];
+                                } else {
+#pragma unroll
+                                    for (int x = 0; x < E / 4; ++x) {
+                                        const float4 u = *reinterpret_cast<const float4 *>(vs + (8 * q + g) * stride + k + 4 * x);
+                                        const float y[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) v[4 * x + e] = make_float2(head(y[e]), y[e] - head(y[e]));
+                                    }
+                                }
+#pragma unroll
+                                for (int m = 0; m < 2; ++m) {
+                                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                                    for (int e = 0; e < E / 2; ++e) mma_tf32(d, af[m][e], v[2 * e].y, v[2 * e + 1].y);
+#pragma unroll
+                                    for (int e = 0; e < E / 2; ++e) mma_tf32(d, af[m][e], v[2 * e].x, v[2 * e + 1].x);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) acc[q][m][e] = kOne || k0 == 0 ? d[e] : acc[q][m][e] + d[e];
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; q < NT; ++q)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const int tok = 8 * q + 2 * t + x;
+                                float *y = reinterpret_cast<float *>(from + tok * kPitch) + 32 * warp + g;
+                                if (add >> tok & 1u) {
+#pragma unroll
+                                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                                        for (int h = 0; h < 2; ++h) y[16 * m + 8 * h] += acc[q][m][2 * h + x];
+                                }
+                            }
+                        tcu::fence_async_smem();  // before the bulk copies read it
+                    }
+                    __syncwarp();
+                    if (lane == 0) tcu::mbar_arrive(done + 8 * s);
+                    next_stage(s, ph);
+                }
+            }
+            waited = true;
+            for (int i = 0; i < n; ++i) next_stage(stage, phase);
+            __syncthreads();
+            if (*abort_flag) return;
+        }
+        __syncthreads();
+    }
+    if (!waited) pdl_wait();
+}
+
 // ---------------------------------------------------------------- host
 // Slices of K: enough CTAs for two per SM, at least one chunk for every warp.
 constexpr int kWantCtas = 456;
@@ -569,6 +803,26 @@ cudaError_t expand_rank(const Call &c, bool bf16, int tiles, int groups, int sli
     return bf16 ? expand<32, false, NT, true>(c, tiles, groups, slices) : expand<32, false, NT, false>(c, tiles, groups, slices);
 }
 
+template <int KC, bool kOne, bool BF16>
+cudaError_t expand_bulk(const Call &c, int slices)
+{
+    auto kern = k_lora_expand_bulk<KC, kOne, BF16>;
+    const int depth = (c.rank + KC - 1) / KC * KC, stages = bulk_stages(c.rank);
+    const size_t smem = sizeof(float) * kBulkTokens * (depth + 4) + static_cast<size_t>(stages) * bulk_stage(c.rank);
+    const int per_sm = ctas_per_sm(reinterpret_cast<const void *>(kern), kBulkThreads, smem);
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    const long long total = static_cast<long long>((c.B.M + kBulkTokens - 1) / kBulkTokens) * ((c.rows + kBulkRows - 1) / kBulkRows);
+    const long long ctas = static_cast<long long>(per_sm) * sm_count(), per = (total + ctas - 1) / ctas;
+    return launch_pdl(kern, dim3(static_cast<unsigned>((total + per - 1) / per)), dim3(kBulkThreads), smem, c.s, c.W, c.B, c.V, c.Y0,
+                      c.ldy0, c.Y, c.ldy, c.rank, c.rows, slices, per, total, stages);
+}
+cudaError_t expand_bulk_rank(const Call &c, bool bf16, int slices)
+{
+    if (c.rank <= 16) return bf16 ? expand_bulk<16, true, true>(c, slices) : expand_bulk<16, true, false>(c, slices);
+    if (c.rank <= 32) return bf16 ? expand_bulk<32, true, true>(c, slices) : expand_bulk<32, true, false>(c, slices);
+    return bf16 ? expand_bulk<32, false, true>(c, slices) : expand_bulk<32, false, false>(c, slices);
+}
+
 int run(const Call &c, int type)
 {
     const bool bf16 = type == GQ_TYPE_BF16;
@@ -589,7 +843,7 @@ int run(const Call &c, int type)
     cudaError_t e = long_runs ? shrink_rank<2>(c, bf16, shrink_tiles, distinct, slices, slice_chunks)
                               : shrink_rank<1>(c, bf16, shrink_tiles, distinct, slices, slice_chunks);
     if (e == cudaSuccess)
-        e = long_runs ? expand_rank<2>(c, bf16, tiles, distinct, slices) : expand_rank<1>(c, bf16, tiles, distinct, slices);
+        e = long_runs ? expand_bulk_rank(c, bf16, slices) : expand_rank<1>(c, bf16, tiles, distinct, slices);
     return status_from(e);
 }
 
@@ -614,6 +868,7 @@ int check_and_run(Call c, int type, size_t workspace_bytes)
     if (!c.V || workspace_bytes < need) return GQ_ERR_WORKSPACE;
     if (!aligned16(c.V)) return GQ_ERR_ALIGN;
     c.B.status = status_word();
+    if (!c.B.status) return GQ_ERR_CUDA;
     return run(c, type);
 }
 
