@@ -286,6 +286,186 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// ---------------------------------------------------------------- the same for prompts
+// CTA: a tile of 8 NT tokens and one slice of K, in steps of 256 elements: all
+// threads copy a step's weights and activations, and eight warps take one
+// 32-element chunk each.  Rows are padded so that the operands' loads meet no bank
+// twice.  (Bulk copies, one per row, took 58 us where this takes 25 for 4096
+// tokens of rank 16: they cost some 60 cycles each, and the rows are 256 and 512
+// bytes.)
+constexpr int kStep = 256, kStepA = 2 * kStep + 64;
+__host__ __device__ constexpr int step_x(bool q8) { return q8 ? kStep + 32 : 4 * kStep + 16; }
+__host__ __device__ constexpr int step_bytes(int rank, int tokens, bool q8) { return rank * kStepA + tokens * (step_x(q8) + (q8 ? 48 : 0)); }
+inline int step_stages(int rank, int tokens, bool q8)
+{
+    const int n = (104 << 10) / step_bytes(rank, tokens, q8);
+    return n > 4 ? 4 : (n < 2 ? 2 : n);
+}
+
+template <int MT, int NT, bool BF16, bool Q8>
+__global__ void __launch_bounds__(kThreads)
+    k_lora_shrink_tile(const uint16_t *__restrict__ A, Batch B, const float *__restrict__ X, long long ldx,
+                       const int8_t *__restrict__ Xq, const float *__restrict__ dx, float *__restrict__ V, int rank, int K,
+                       int slice_steps, int stages)
+{
+    extern __shared__ __align__(16) char raw[];  // stages; after the last step the warps' sums [kWarps][8 NT][16 MT]
+    __shared__ Tile tile;
+    constexpr int TT = 8 * NT, kOut = 16 * MT * TT, kPieces = kStep * (Q8 ? 1 : 4) / 16;  // 16-byte pieces of a token's step
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int t0 = blockIdx.x * TT, chunks = K / 32, steps = (K + kStep - 1) / kStep;
+    const int s0 = blockIdx.y * slice_steps, n = min(slice_steps, steps - s0);
+    const int stage_bytes = step_bytes(rank, TT, Q8), off_x = rank * kStepA, off_d = off_x + TT * step_x(Q8);
+    pdl_wait();
+    // only now: what the next kernel reads before its own wait is complete then
+    pdl_launch_dependents();
+    find_groups<TT>(tile, B, t0);
+    for (int j = 0; j < tile.groups; ++j) {
+        const uint16_t *a = A + static_cast<long long>(tile.adapter[j]) * rank * K;
+        auto fetch = [&](int i, int slot) {
+            if (i < n) {
+                const int k0 = (s0 + i) * kStep, count = min(kStep, K - k0);
+                char *to = raw + slot * stage_bytes;
+                {
+                    const int c = tid & 31;
+                    const uint16_t *from = a + static_cast<long long>(warp) * K + k0 + 8 * c;
+                    if (8 * c < count)
+                        for (int r = warp; r < rank; r += kWarps, from += static_cast<long long>(kWarps) * K)
+                            cp_async<16>(to + r * kStepA + 16 * c, from);
+                }
+                constexpr int kRows = kThreads / kPieces;  // tokens copied at once
+                const int c = tid % kPieces;
+                if (c * (Q8 ? 16 : 4) < count) {
+#pragma unroll
+                    for (int r0 = 0; r0 < TT; r0 += kRows) {
+                        const int r = r0 + tid / kPieces;
+                        if (tile.group[r] == j) {
+                            const void *from = Q8 ? static_cast<const void *>(Xq + static_cast<long long>(t0 + r) * K + k0 + 16 * c)
+                                                  : static_cast<const void *>(X + (t0 + r) * ldx + k0 + 4 * c);
+                            cp_async<16>(to + off_x + r * step_x(Q8) + 16 * c, from);
+                        }
+                    }
+                }
+                if (Q8) {
+                    const int r = tid >> 3, x = tid & 7, at = k0 / 32 + x;
+                    if (r < TT && at < chunks && tile.group[r] == j)
+                        cp_async<4>(to + off_d + r * 36 + 4 * x, dx + static_cast<long long>(t0 + r) * chunks + at);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        float acc[MT][NT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][q][i] = 0.f;
+        unsigned in = 0, col = 0;  // whether the lane's tokens belong to the group: as operand (column g), as results
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+            in |= (tile.group[8 * q + g] == j ? 1u : 0u) << q;
+            col |= (tile.group[8 * q + 2 * t] == j ? 1u : 0u) << (2 * q);
+            col |= (tile.group[8 * q + 2 * t + 1] == j ? 1u : 0u) << (2 * q + 1);
+        }
+        for (int i = 0; i < stages - 1; ++i) fetch(i, i);
+        int slot = 0, next = stages - 1;
+        for (int i = 0; i < n; ++i) {
+            // this step's copies; the later ones, stages - 2 of them, may be on their way
+            if (stages == 2)
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            else if (stages == 3)
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else
+                asm volatile("cp.async.wait_group 2;" ::: "memory");
+            __syncthreads();
+            fetch(i + stages - 1, next);
+            if ((s0 + i) * (kStep / 32) + warp < chunks) {
+                const char *from = raw + slot * stage_bytes + warp * 64 + t * 16;
+                const char *xs = raw + slot * stage_bytes + off_x + (warp * 32 + t * 8) * (Q8 ? 1 : 4);
+                const char *ds = raw + slot * stage_bytes + off_d + warp * 4;
+                float x[NT][8], d_now[NT][2];
+#pragma unroll
+                for (int q = 0; q < NT; ++q) {
+                    const char *p = xs + (8 * q + g) * step_x(Q8);
+                    const bool have = in >> q & 1u;
+                    if (Q8) {
+                        const uint2 c = *reinterpret_cast<const uint2 *>(p);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            // a code's byte + 128 as the low bits of 2^23
+                            const uint32_t v = have ? (e < 4 ? c.x : c.y) ^ 0x80808080u : 0x80808080u;
+                            x[q][e] = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7440 | (e & 3))) - 8388736.0f;
+                        }
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float d = *reinterpret_cast<const float *>(ds + (8 * q + 2 * t + y) * 36);
+                            d_now[q][y] = col >> (2 * q + y) & 1u ? d : 0.f;
+                        }
+                    } else {
+                        const float4 u = reinterpret_cast<const float4 *>(p)[0], v = reinterpret_cast<const float4 *>(p)[1];
+                        const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[q][e] = have ? y[e] : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    float af[4][4];
+                    uint4 w[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = 16 * m + 8 * h + g;
+                        w[h] = r < rank ? *reinterpret_cast<const uint4 *>(from + r * kStepA) : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 lo = weights2<BF16>((&w[0].x)[e]), hi = weights2<BF16>((&w[1].x)[e]);
+                        af[e][0] = lo.x, af[e][1] = hi.x, af[e][2] = lo.y, af[e][3] = hi.y;
+                    }
+#pragma unroll
+                    for (int q = 0; q < NT; ++q) {
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+                        if (!Q8) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                mma_tf32(d, af[e], x[q][2 * e] - head(x[q][2 * e]), x[q][2 * e + 1] - head(x[q][2 * e + 1]));
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mma_tf32(d, af[e], head(x[q][2 * e]), head(x[q][2 * e + 1]));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[m][q][e] = Q8 ? fmaf(d_now[q][e & 1], d[e], acc[m][q][e]) : acc[m][q][e] + d[e];
+                    }
+                }
+            }
+            if (++slot == stages) slot = 0;
+            if (++next == stages) next = 0;
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // the sums take the stages' place
+        float *mine = reinterpret_cast<float *>(raw) + warp * kOut;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mine[(8 * q + 2 * t + (i & 1)) * 16 * MT + 16 * m + g + 8 * (i >> 1)] = acc[m][q][i];
+        __syncthreads();
+        const float *sums = reinterpret_cast<const float *>(raw);
+        float *out = V + static_cast<long long>(blockIdx.y) * B.M * rank;
+        for (int i = tid; i < kOut; i += kThreads) {
+            const int tok = i / (16 * MT), r = i - tok * 16 * MT;
+            if (r < rank && tile.group[tok] == j) {
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) v += sums[w * kOut + i];
+                out[static_cast<long long>(t0 + tok) * rank + r] = v;
+            }
+        }
+        __syncthreads();
+    }
+}
+
 // ---------------------------------------------------------------- Y = Y0 + scale B v
 constexpr int kStages = 3;
 // Four rows of weights (16 bytes a lane, 8 where a chunk is 16 deep) and the lane's results of 8 NT tokens.
@@ -725,13 +905,20 @@ __global__ void __launch_bounds__(kBulkThreads, 2)
 }
 
 // ---------------------------------------------------------------- host
-// Slices of K: enough CTAs for two per SM, at least one chunk for every warp.
-constexpr int kWantCtas = 456;
+// Slices of K: some three CTAs per SM for a decode batch's tiles of 8 tokens; for a
+// prompt's, of 16 or 32, as many CTAs as run at once, at most two per SM.  A slice
+// has 256 elements or more, a chunk for every warp.
+constexpr int kWantCtas = 456, kWantTiles = 304;
+int bounded_slices(long long n, int K)
+{
+    const int by_k = (K + kStep - 1) / kStep;
+    return n < 1 ? 1 : (n < by_k ? static_cast<int>(n) : by_k);
+}
+int decode_slices(int K, long long tiles) { return bounded_slices((kWantCtas + tiles - 1) / tiles, K); }
 int most_slices(int K, int M)
 {
-    const int tiles = (M + 7) / 8, by_k = (K / 32 + kWarps - 1) / kWarps;
-    const int want = (kWantCtas + tiles - 1) / tiles;
-    return want < by_k ? want : by_k;
+    const int few = decode_slices(K, (M + 7) / 8), many = bounded_slices(kWantTiles / ((M + 31) / 32), K);
+    return few > many ? few : many;
 }
 
 struct Call {
@@ -776,6 +963,35 @@ cudaError_t shrink_rank(const Call &c, bool bf16, int tiles, int groups, int sli
     if (c.rank <= 32) return shrink_typed<2, NT>(c, bf16, tiles, groups, slices, slice_chunks);
     if (c.rank <= 64) return shrink_typed<4, NT>(c, bf16, tiles, groups, slices, slice_chunks);
     return shrink_typed<8, NT>(c, bf16, tiles, groups, slices, slice_chunks);
+}
+
+template <int MT, int NT, bool BF16, bool Q8>
+cudaError_t shrink_tile(const Call &c, int *slices)
+{
+    auto kern = k_lora_shrink_tile<MT, NT, BF16, Q8>;
+    const int tiles = (c.B.M + 8 * NT - 1) / (8 * NT), steps = (c.K + kStep - 1) / kStep, stages = step_stages(c.rank, 8 * NT, Q8);
+    const size_t rings = static_cast<size_t>(stages) * step_bytes(c.rank, 8 * NT, Q8), sums = sizeof(float) * kWarps * 16 * MT * 8 * NT;
+    const size_t smem = rings > sums ? rings : sums;
+    const int per_sm = ctas_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem);
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    const int at_once = per_sm * sm_count();
+    const int want = bounded_slices((at_once < kWantTiles ? at_once : kWantTiles) / tiles, c.K), slice_steps = (steps + want - 1) / want;
+    *slices = (steps + slice_steps - 1) / slice_steps;
+    return launch_pdl(kern, dim3(tiles, *slices), dim3(kThreads), smem, c.s, c.A, c.B, c.X, c.ldx, c.Xq, c.dx, c.V, c.rank, c.K,
+                      slice_steps, stages);
+}
+template <int MT, int NT>
+cudaError_t shrink_tile_typed(const Call &c, bool bf16, int *slices)
+{
+    if (c.Xq) return bf16 ? shrink_tile<MT, NT, true, true>(c, slices) : shrink_tile<MT, NT, false, true>(c, slices);
+    return bf16 ? shrink_tile<MT, NT, true, false>(c, slices) : shrink_tile<MT, NT, false, false>(c, slices);
+}
+cudaError_t shrink_tile_rank(const Call &c, bool bf16, int *slices)
+{
+    if (c.rank <= 16) return shrink_tile_typed<1, 4>(c, bf16, slices);
+    if (c.rank <= 32) return shrink_tile_typed<2, 4>(c, bf16, slices);
+    if (c.rank <= 64) return shrink_tile_typed<4, 4>(c, bf16, slices);
+    return shrink_tile_typed<8, 2>(c, bf16, slices);
 }
 
 template <int KC, bool kOne, int NT, bool BF16>
@@ -826,24 +1042,24 @@ cudaError_t expand_bulk_rank(const Call &c, bool bf16, int slices)
 int run(const Call &c, int type)
 {
     const bool bf16 = type == GQ_TYPE_BF16;
-    // Neighbouring tokens of one request share their adapter: tiles of 32 where
-    // requests have 16 tokens or more on average.
-    const bool long_runs = c.B.sequence != nullptr && c.B.M / 16 >= c.B.n_seq;
-    const int tt = long_runs ? 16 : 8, st = long_runs ? 16 : 8;  // tokens of an expand and of a shrink tile
-    int distinct = long_runs ? 1 : tt;
-    if (distinct > c.B.n_adapters) distinct = c.B.n_adapters;
-    if (distinct > c.B.M) distinct = c.B.M;
-    const int tiles = (c.B.M + tt - 1) / tt, shrink_tiles = (c.B.M + st - 1) / st, chunks = c.K / 32;
-    int slices = most_slices(c.K, c.B.M);
-    const int enough = static_cast<int>((kWantCtas + static_cast<long long>(shrink_tiles) * distinct - 1) /
-                                        (static_cast<long long>(shrink_tiles) * distinct));
-    if (slices > enough) slices = enough;
+    int slices = 0;
+    // Neighbouring tokens of one request share their adapter: the prompts' form where requests have 16 tokens or more
+    // on average.
+    if (c.B.sequence != nullptr && c.B.M / 16 >= c.B.n_seq) {
+        cudaError_t e = shrink_tile_rank(c, bf16, &slices);
+        if (e == cudaSuccess) e = expand_bulk_rank(c, bf16, slices);
+        return status_from(e);
+    }
+    constexpr int kTokens = 8;
+    int groups = kTokens;  // at most, in a tile
+    if (groups > c.B.n_adapters) groups = c.B.n_adapters;
+    if (groups > c.B.M) groups = c.B.M;
+    const int tiles = (c.B.M + kTokens - 1) / kTokens, chunks = c.K / 32;
+    slices = decode_slices(c.K, static_cast<long long>(tiles) * groups);
     const int slice_chunks = (chunks + slices - 1) / slices;
     slices = (chunks + slice_chunks - 1) / slice_chunks;
-    cudaError_t e = long_runs ? shrink_rank<2>(c, bf16, shrink_tiles, distinct, slices, slice_chunks)
-                              : shrink_rank<1>(c, bf16, shrink_tiles, distinct, slices, slice_chunks);
-    if (e == cudaSuccess)
-        e = long_runs ? expand_bulk_rank(c, bf16, slices) : expand_rank<1>(c, bf16, tiles, distinct, slices);
+    cudaError_t e = shrink_rank<1>(c, bf16, tiles, groups, slices, slice_chunks);
+    if (e == cudaSuccess) e = expand_rank<1>(c, bf16, tiles, groups, slices);
     return status_from(e);
 }
 
