@@ -23,6 +23,7 @@
 // bytes of Y (and, for few tokens, of the adapters), not the products.
 #include "gq_host.h"
 #include "gq_internal.cuh"
+#include "gq_kv.cuh"
 #include "gq_lora.h"
 #include "gq_tc.cuh"
 
@@ -56,8 +57,103 @@ __device__ __forceinline__ float2 weights2(uint32_t w)
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
+template <bool BF16>
+__device__ __forceinline__ void mma_16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    if (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // The 11 leading bits of x; the rest, x - head(x), is exact and tf32 keeps 11 bits of it.
 __device__ __forceinline__ float head(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFFE000u); }
+
+// A pair of numbers as 16-bit ones, and what that leaves of them (exact).
+template <bool BF16>
+__device__ __forceinline__ uint32_t round2(float &a, float &b)
+{
+    const uint32_t w = BF16 ? kv::f2_bf162(a, b) : kv::f2_half2(a, b);
+    const float2 r = weights2<BF16>(w);
+    a -= r.x;
+    b -= r.y;
+    return w;
+}
+// Pieces of 16 bits that hold an f32 number to 22 bits or more.
+template <bool BF16>
+constexpr int kPiecesOf = BF16 ? 3 : 2;
+
+// One 32-element chunk of v = A x: acc += A x for 16 MT rows and 8 NT tokens.
+// `a(m, h)` gives the lane's 8 weights of row 16 m + 8 h + g, `x(q, v)` its 8
+// activations of token 8 q + g (codes as whole numbers for Q8), `d(q, i)` the scale
+// of token 8 q + 2 t + i.  The order of the contraction is free: step s takes
+// elements 4 s .. 4 s + 3 of every lane.  16-bit weights are operands as they are;
+// codes are exact in either type, f32 numbers are three pieces of bf16.  f16 has
+// not the range for f32 numbers: there both are tf32, the numbers in two pieces.
+template <int MT, int NT, bool BF16, bool Q8, class GetA, class GetX, class GetD>
+__device__ __forceinline__ void multiply_chunk(float (&acc)[MT][NT][4], GetA &&a, GetX &&x, GetD &&d)
+{
+    constexpr bool k16 = Q8 || BF16;
+    constexpr int P = Q8 ? 1 : kPiecesOf<BF16>;
+    uint32_t b[k16 ? P : 1][NT][4];
+    float v[k16 ? 1 : NT][8];
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+        if (k16) {
+            float y[8];
+            x(q, y);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) b[p][q][e] = round2<BF16>(y[2 * e], y[2 * e + 1]);
+        } else {
+            x(q, v[q]);
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const uint4 lo4 = a(m, 0), hi4 = a(m, 1);
+        const uint32_t lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
+        float af[4][4];
+        if (!k16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 l = weights2<BF16>(lo[e]), h = weights2<BF16>(hi[e]);
+                af[e][0] = l.x, af[e][1] = h.x, af[e][2] = l.y, af[e][3] = h.y;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+            float r[4] = {0.f, 0.f, 0.f, 0.f};
+            if (k16) {
+#pragma unroll
+                for (int p = P - 1; p >= 0; --p)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        mma_16<BF16>(r, lo[2 * s], hi[2 * s], lo[2 * s + 1], hi[2 * s + 1], b[p][q][2 * s], b[p][q][2 * s + 1]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    mma_tf32(r, af[e], v[q][2 * e] - head(v[q][2 * e]), v[q][2 * e + 1] - head(v[q][2 * e + 1]));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mma_tf32(r, af[e], head(v[q][2 * e]), head(v[q][2 * e + 1]));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[m][q][e] = Q8 ? fmaf(d(q, e & 1), r[e], acc[m][q][e]) : acc[m][q][e] + r[e];
+        }
+    }
+}
+// Eight codes as whole numbers: a code's byte + 128 as the low bits of 2^23.
+__device__ __forceinline__ void codes8(uint2 c, float (&x)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        x[e] = __uint_as_float(__byte_perm((e < 4 ? c.x : c.y) ^ 0x80808080u, 0x4B000000u, 0x7440 | (e & 3))) - 8388736.0f;
+}
 
 // Tokens of a tile: which group (distinct adapter, by first appearance) each
 // belongs to, -1 for none, and the groups' adapters.  All threads take part.
@@ -212,43 +308,17 @@ __global__ void __launch_bounds__(kThreads)
             }
         };
         auto multiply = [&](const Raw &w) {
-            float x[NT][8];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (Q8) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        // a code's byte + 128 as the low bits of 2^23
-                        const uint32_t v = (i < 4 ? w.q[n].x : w.q[n].y) ^ 0x80808080u;
-                        x[n][i] = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7440 | (i & 3))) - 8388736.0f;
+            multiply_chunk<MT, NT, BF16, Q8>(
+                acc, [&](int m, int h) { return w.a[m][h]; },
+                [&](int q, float(&v)[8]) {
+                    if (Q8) {
+                        codes8(w.q[q], v);
+                    } else {
+                        v[0] = w.x[q][0].x, v[1] = w.x[q][0].y, v[2] = w.x[q][0].z, v[3] = w.x[q][0].w;
+                        v[4] = w.x[q][1].x, v[5] = w.x[q][1].y, v[6] = w.x[q][1].z, v[7] = w.x[q][1].w;
                     }
-                } else {
-                    x[n][0] = w.x[n][0].x, x[n][1] = w.x[n][0].y, x[n][2] = w.x[n][0].z, x[n][3] = w.x[n][0].w;
-                    x[n][4] = w.x[n][1].x, x[n][5] = w.x[n][1].y, x[n][6] = w.x[n][1].z, x[n][7] = w.x[n][1].w;
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                float af[4][4];
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const float2 lo = weights2<BF16>((&w.a[m][0].x)[s]), hi = weights2<BF16>((&w.a[m][1].x)[s]);
-                    af[s][0] = lo.x, af[s][1] = hi.x, af[s][2] = lo.y, af[s][3] = hi.y;
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (!Q8) {
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            mma_tf32(d, af[s], x[n][2 * s] - head(x[n][2 * s]), x[n][2 * s + 1] - head(x[n][2 * s + 1]));
-                    }
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) mma_tf32(d, af[s], head(x[n][2 * s]), head(x[n][2 * s + 1]));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[m][n][i] = Q8 ? fmaf(w.d[n][i & 1], d[i], acc[m][n][i]) : acc[m][n][i] + d[i];
-                }
-            }
+                },
+                [&](int q, int i) { return w.d[q][i]; });
         };
         const int mine_n = c0 + warp < c1 ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
 #pragma unroll
@@ -383,59 +453,26 @@ __global__ void __launch_bounds__(kThreads)
                 const char *from = raw + slot * stage_bytes + warp * 64 + t * 16;
                 const char *xs = raw + slot * stage_bytes + off_x + (warp * 32 + t * 8) * (Q8 ? 1 : 4);
                 const char *ds = raw + slot * stage_bytes + off_d + warp * 4;
-                float x[NT][8], d_now[NT][2];
-#pragma unroll
-                for (int q = 0; q < NT; ++q) {
-                    const char *p = xs + (8 * q + g) * step_x(Q8);
-                    const bool have = in >> q & 1u;
-                    if (Q8) {
-                        const uint2 c = *reinterpret_cast<const uint2 *>(p);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            // a code's byte + 128 as the low bits of 2^23
-                            const uint32_t v = have ? (e < 4 ? c.x : c.y) ^ 0x80808080u : 0x80808080u;
-                            x[q][e] = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7440 | (e & 3))) - 8388736.0f;
-                        }
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const float d = *reinterpret_cast<const float *>(ds + (8 * q + 2 * t + y) * 36);
-                            d_now[q][y] = col >> (2 * q + y) & 1u ? d : 0.f;
-                        }
-                    } else {
-                        const float4 u = reinterpret_cast<const float4 *>(p)[0], v = reinterpret_cast<const float4 *>(p)[1];
-                        const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[q][e] = have ? y[e] : 0.f;
-                    }
-                }
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    float af[4][4];
-                    uint4 w[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                multiply_chunk<MT, NT, BF16, Q8>(
+                    acc,
+                    [&](int m, int h) {
                         const int r = 16 * m + 8 * h + g;
-                        w[h] = r < rank ? *reinterpret_cast<const uint4 *>(from + r * kStepA) : make_uint4(0, 0, 0, 0);
-                    }
+                        return r < rank ? *reinterpret_cast<const uint4 *>(from + r * kStepA) : make_uint4(0, 0, 0, 0);
+                    },
+                    [&](int q, float(&v)[8]) {
+                        const char *p = xs + (8 * q + g) * step_x(Q8);
+                        const bool have = in >> q & 1u;
+                        if (Q8) {
+                            const uint2 c = *reinterpret_cast<const uint2 *>(p);
+                            codes8(have ? c : make_uint2(0, 0), v);
+                        } else {
+                            const float4 u = reinterpret_cast<const float4 *>(p)[0], w = reinterpret_cast<const float4 *>(p)[1];
+                            const float y[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 lo = weights2<BF16>((&w[0].x)[e]), hi = weights2<BF16>((&w[1].x)[e]);
-                        af[e][0] = lo.x, af[e][1] = hi.x, af[e][2] = lo.y, af[e][3] = hi.y;
-                    }
-#pragma unroll
-                    for (int q = 0; q < NT; ++q) {
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
-                        if (!Q8) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                mma_tf32(d, af[e], x[q][2 * e] - head(x[q][2 * e]), x[q][2 * e + 1] - head(x[q][2 * e + 1]));
+                            for (int e = 0; e < 8; ++e) v[e] = have ? y[e] : 0.f;
                         }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) mma_tf32(d, af[e], head(x[q][2 * e]), head(x[q][2 * e + 1]));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[m][q][e] = Q8 ? fmaf(d_now[q][e & 1], d[e], acc[m][q][e]) : acc[m][q][e] + d[e];
-                    }
-                }
+                    },
+                    [&](int q, int i) { return col >> (2 * q + i) & 1u ? *reinterpret_cast<const float *>(ds + (8 * q + 2 * t + i) * 36) : 0.f; });
             }
             if (++slot == stages) slot = 0;
             if (++next == stages) next = 0;
@@ -467,6 +504,87 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ---------------------------------------------------------------- Y = Y0 + scale B v
+// v in shared memory as pieces of 16 bits: kPiecesOf rows of TOKENS x pitch bytes,
+// then (f16) the factors that undo the scaling.  f16 has not v's range: a token's
+// v is scaled so that its largest lies in [2^13, 2^14), an exact power of two.
+__host__ __device__ constexpr int v_pitch(int depth) { return 2 * depth + (2 * depth % 128 == 0 ? 64 : 0); }  // (banks)
+__host__ __device__ constexpr int v_bytes(int depth, int tokens) { return 3 * tokens * v_pitch(depth) + 4 * tokens; }
+
+// A warp takes a token, a lane four of its numbers; slices are added up.  `member`
+// says which tokens have a v.
+template <int TOKENS, bool BF16, class Member>
+__device__ __forceinline__ void stage_v(char *vs, const float *__restrict__ V, long long t0, int M, int rank, int depth, int slices,
+                                        float scale, Member &&member)
+{
+    const int lane = threadIdx.x & 31, pitch = v_pitch(depth);
+    for (int tok = threadIdx.x >> 5; tok < TOKENS; tok += kWarps) {
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (4 * lane < rank && member(tok)) {
+            const float *p = V + (t0 + tok) * rank + 4 * lane;
+#pragma unroll 8
+            for (int c = 0; c < slices; ++c) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(p + static_cast<long long>(c) * M * rank));
+                sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+            }
+        }
+        float y[4] = {sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale};
+        if (!BF16) {
+            float most = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
+            most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+            const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;  // 128: not finite, and so v stays
+            const int k = e == 128 ? 0 : min(13 - e, 126);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] *= pow2i(k);
+            if (lane == 0) reinterpret_cast<float *>(vs + 3 * TOKENS * pitch)[tok] = pow2i(-k);
+        }
+        if (4 * lane < depth) {
+#pragma unroll
+            for (int p = 0; p < kPiecesOf<BF16>; ++p) {
+                const uint32_t a = round2<BF16>(y[0], y[1]), b = round2<BF16>(y[2], y[3]);
+                *reinterpret_cast<uint2 *>(vs + (p * TOKENS + tok) * pitch + 8 * lane) = make_uint2(a, b);
+            }
+        }
+    }
+}
+// The lane's part of a chunk of v, for 8 NT tokens; and two instructions' rows (m)
+// times that: weights are operands as they lie.
+template <int KC, int NT, bool BF16>
+struct Fragment {
+    uint32_t w[kPiecesOf<BF16>][NT][KC / 8];
+    __device__ __forceinline__ void load(const char *vs, int pitch, int k0, int g, int t)
+    {
+#pragma unroll
+        for (int p = 0; p < kPiecesOf<BF16>; ++p)
+#pragma unroll
+            for (int q = 0; q < NT; ++q) {
+                const char *from = vs + (p * 8 * NT + 8 * q + g) * pitch + 2 * k0 + KC / 2 * t;
+                if (KC == 32) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(from);
+                    w[p][q][0] = x.x, w[p][q][1] = x.y, w[p][q][KC / 8 - 2] = x.z, w[p][q][KC / 8 - 1] = x.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(from);
+                    w[p][q][0] = x.x, w[p][q][1] = x.y;
+                }
+            }
+    }
+    __device__ __forceinline__ void multiply(float (&acc)[NT][2][4], const uint32_t (&x)[2][2][KC / 8], bool first) const
+    {
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int p = kPiecesOf<BF16> - 1; p >= 0; --p)
+#pragma unroll
+                    for (int s = 0; s < KC / 16; ++s)
+                        mma_16<BF16>(d, x[m][0][2 * s], x[m][1][2 * s], x[m][0][2 * s + 1], x[m][1][2 * s + 1], w[p][q][2 * s], w[p][q][2 * s + 1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[q][m][e] = first ? d[e] : acc[q][m][e] + d[e];
+            }
+    }
+};
+
 constexpr int kStages = 3;
 // Four rows of weights (16 bytes a lane, 8 where a chunk is 16 deep) and the lane's results of 8 NT tokens.
 __host__ __device__ constexpr int expand_stage(int kc, int nt) { return 64 * kc + 1024 * nt; }
@@ -489,8 +607,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     // where piece c of row r lies: the pieces of a 128-byte line turned by the row group 4 g that reads it
     auto place = [](int r, int c) { return (r * kRowPieces + c) ^ (kRowPieces == 2 ? (r >> 2 & 3) * 2 : (r >> 2 & 1) * 4); };
     char *const ring = raw + warp * kStages * kStageBytes;
-    float *const vs = reinterpret_cast<float *>(raw + kWarps * kStages * kStageBytes);  // [8 NT][stride]
-    const int depth = kOne ? KC : (rank + KC - 1) / KC * KC, stride = KC == 16 ? depth : depth + 4;  // (no two lanes of a load on one bank)
+    char *const vs = raw + kWarps * kStages * kStageBytes;
+    const int depth = kOne ? KC : (rank + KC - 1) / KC * KC, pitch = v_pitch(depth);
     pdl_launch_dependents();
     bool waited = false;
     // a range of all tiles' row blocks in one row
@@ -558,30 +676,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!waited) pdl_wait();
         waited = true;
         const float scale = product ? __ldg(B.scale + tile.adapter[j]) : 0.f;
-        for (int i = threadIdx.x; i < TT * depth / 4; i += kThreads) {
-            const int tok = i / (depth / 4), r = 4 * (i - tok * (depth / 4));
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < rank && tile.group[tok] == j) {
-                const float *p = V + static_cast<long long>(t0 + tok) * rank + r;
-#pragma unroll 8
-                for (int c = 0; c < slices; ++c) {
-                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(p + static_cast<long long>(c) * B.M * rank));
-                    sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
-                }
-            }
-            *reinterpret_cast<float4 *>(vs + tok * stride + r) = make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale);
-        }
+        stage_v<TT, BF16>(vs, V, t0, B.M, rank, depth, slices, scale, [&](int tok) { return tile.group[tok] == j; });
         __syncthreads();
-        float2 vr[kOne ? NT : 1][E];  // leading bits and rest
-        if (kOne && product) {
+        Fragment<KC, NT, BF16> v;  // of all of the rank, where that is one chunk
+        if (kOne) v.load(vs, pitch, 0, g, t);
+        float undo[NT][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const float v = vs[(8 * n + g) * stride + E * t + i];
-                    vr[n][i] = make_float2(head(v), v - head(v));
-                }
-        }
+            for (int i = 0; i < 2; ++i) undo[n][i] = BF16 ? 1.f : reinterpret_cast<const float *>(vs + 3 * TT * pitch)[8 * n + 2 * t + i];
         int row = (rb0 + warp) * kRowBlock + 4 * g, kc = 0;
         float acc[NT][2][4];
         for (int step = 0; step < steps; ++step) {
@@ -591,55 +694,24 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (product) {
                 const int k = kc * KC + E * t;
                 const bool have = row < rows && k < rank;
-                float af[2][E / 2][4];
+                uint32_t x[2][2][E / 2];
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    uint32_t x[2][E / 2];
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const char *q = from + 16 * place(4 * g + 2 * m + h, E * t / 8) + (E * t % 8) * 2;
                         if (E == 8) {
                             const uint4 y = *reinterpret_cast<const uint4 *>(q);
-                            x[h][0] = y.x, x[h][1] = y.y, x[h][E / 2 - 2] = y.z, x[h][E / 2 - 1] = y.w;
+                            x[m][h][0] = y.x, x[m][h][1] = y.y, x[m][h][E / 2 - 2] = y.z, x[m][h][E / 2 - 1] = y.w;
                         } else {
                             const uint2 y = *reinterpret_cast<const uint2 *>(q);
-                            x[h][0] = y.x, x[h][1] = y.y;
+                            x[m][h][0] = y.x, x[m][h][1] = y.y;
                         }
 #pragma unroll
-                        for (int i = 0; i < E / 2; ++i) x[h][i] = have ? x[h][i] : 0u;
+                        for (int i = 0; i < E / 2; ++i) x[m][h][i] = have ? x[m][h][i] : 0u;
                     }
-#pragma unroll
-                    for (int s = 0; s < E / 2; ++s) {
-                        const float2 lo = weights2<BF16>(x[0][s]), hi = weights2<BF16>(x[1][s]);
-                        af[m][s][0] = lo.x, af[m][s][1] = hi.x, af[m][s][2] = lo.y, af[m][s][3] = hi.y;
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float2 v[E];
-                    if (kOne) {
-#pragma unroll
-                        for (int i = 0; i < E; ++i) v[i] = vr[n][i];
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < E / 4; ++q) {
-                            const float4 u = *reinterpret_cast<const float4 *>(vs + (8 * n + g) * stride + k + 4 * q);
-                            const float x[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) v[4 * q + i] = make_float2(head(x[i]), x[i] - head(x[i]));
-                        }
-                    }
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int s = 0; s < E / 2; ++s) mma_tf32(d, af[m][s], v[2 * s].y, v[2 * s + 1].y);
-#pragma unroll
-                        for (int s = 0; s < E / 2; ++s) mma_tf32(d, af[m][s], v[2 * s].x, v[2 * s + 1].x);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[n][m][i] = kOne || kc == 0 ? d[i] : acc[n][m][i] + d[i];
-                    }
-                }
+                if (!kOne) v.load(vs, pitch, kc * KC, g, t);
+                v.multiply(acc, x, kOne || kc == 0);
             }
             if (++kc == nk) {
                 if (row < rows) {
@@ -650,10 +722,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                             if (put[n][i]) {
                                 float4 y = *reinterpret_cast<const float4 *>(from + 256 * E + (2 * n + i) * 512 + lane * 16);
                                 if (add[n][i]) {
-                                    y.x += acc[n][0][i];
-                                    y.y += acc[n][0][2 + i];
-                                    y.z += acc[n][1][i];
-                                    y.w += acc[n][1][2 + i];
+                                    y.x = fmaf(acc[n][0][i], undo[n][i], y.x);
+                                    y.y = fmaf(acc[n][0][2 + i], undo[n][i], y.y);
+                                    y.z = fmaf(acc[n][1][i], undo[n][i], y.z);
+                                    y.w = fmaf(acc[n][1][2 + i], undo[n][i], y.w);
                                 }
                                 *reinterpret_cast<float4 *>(Y + static_cast<long long>(t0 + 8 * n + 2 * t + i) * ldy + row) = y;
                             }
@@ -703,9 +775,9 @@ __global__ void __launch_bounds__(kBulkThreads, 2)
     __shared__ int abort;
     constexpr int E = KC / 4, NT = 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int depth = kOne ? KC : (rank + KC - 1) / KC * KC, stride = KC == 16 ? depth : depth + 4;
+    const int depth = kOne ? KC : (rank + KC - 1) / KC * KC, pitch = v_pitch(depth);
     const int stage_bytes = bulk_stage(rank);
-    float *const vs = reinterpret_cast<float *>(raw + stages * stage_bytes);
+    char *const vs = raw + stages * stage_bytes;
     const uint32_t base = tcu::smem_u32(raw), full = tcu::smem_u32(bars), done = full + 8 * 6;
     volatile int *const abort_flag = &abort;
     if (threadIdx.x == 0) {
@@ -791,31 +863,16 @@ __global__ void __launch_bounds__(kBulkThreads, 2)
                 // ---- the multiplying warps: 32 rows each
                 if (!waited) pdl_wait();
                 const float scale = product ? __ldg(B.scale + tile.adapter[j]) : 0.f;
-                for (int i = threadIdx.x; i < kBulkTokens * depth / 4; i += kThreads) {
-                    const int tok = i / (depth / 4), r = 4 * (i - tok * (depth / 4));
-                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (r < rank && (add >> tok & 1u)) {
-                        const float *p = V + static_cast<long long>(t0 + tok) * rank + r;
-#pragma unroll 8
-                        for (int c = 0; c < slices; ++c) {
-                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(p + static_cast<long long>(c) * B.M * rank));
-                            sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
-                        }
-                    }
-                    *reinterpret_cast<float4 *>(vs + tok * stride + r) =
-                        make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale);
-                }
+                stage_v<kBulkTokens, BF16>(vs, V, t0, B.M, rank, depth, slices, scale, [&](int tok) { return (add >> tok & 1u) != 0; });
                 asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-                float2 vr[kOne ? NT : 1][E];  // leading bits and rest
-                if (kOne) {
+                Fragment<KC, NT, BF16> v;  // of all of the rank, where that is one chunk
+                if (kOne) v.load(vs, pitch, 0, g, t);
+                float undo[NT][2];
 #pragma unroll
-                    for (int q = 0; q < NT; ++q)
+                for (int q = 0; q < NT; ++q)
 #pragma unroll
-                        for (int i = 0; i < E; ++i) {
-                            const float v = vs[(8 * q + g) * stride + E * t + i];
-                            vr[q][i] = make_float2(head(v), v - head(v));
-                        }
-                }
+                    for (int x = 0; x < 2; ++x)
+                        undo[q][x] = BF16 ? 1.f : reinterpret_cast<const float *>(vs + 3 * kBulkTokens * pitch)[8 * q + 2 * t + x];
                 int s = stage, ph = phase;
                 for (int i = 0; i < n; ++i) {
                     if (!tcu::wait_warp(full + 8 * s, ph, abort_flag, B.status)) break;
@@ -824,55 +881,24 @@ __global__ void __launch_bounds__(kBulkThreads, 2)
                         float acc[NT][2][4];
                         for (int k0 = 0; k0 < depth; k0 += KC) {
                             const int k = k0 + E * t;
-                            float af[2][E / 2][4];
+                            uint32_t x[2][2][E / 2];
 #pragma unroll
-                            for (int m = 0; m < 2; ++m) {
-                                uint32_t x[2][E / 2];
+                            for (int m = 0; m < 2; ++m)
 #pragma unroll
                                 for (int h = 0; h < 2; ++h) {
                                     const char *q = from + kBulkTokens * kPitch + ((32 * warp + 16 * m + 8 * h + g) * rank + k) * 2;
                                     if (E == 8) {
                                         const uint4 y = *reinterpret_cast<const uint4 *>(q);
-                                        x[h][0] = y.x, x[h][1] = y.y, x[h][E / 2 - 2] = y.z, x[h][E / 2 - 1] = y.w;
+                                        x[m][h][0] = y.x, x[m][h][1] = y.y, x[m][h][E / 2 - 2] = y.z, x[m][h][E / 2 - 1] = y.w;
                                     } else {
                                         const uint2 y = *reinterpret_cast<const uint2 *>(q);
-                                        x[h][0] = y.x, x[h][1] = y.y;
+                                        x[m][h][0] = y.x, x[m][h][1] = y.y;
                                     }
 #pragma unroll
-                                    for (int e = 0; e < E / 2; ++e) x[h][e] = k < rank ? x[h][e] : 0u;
+                                    for (int e = 0; e < E / 2; ++e) x[m][h][e] = k < rank ? x[m][h][e] : 0u;
                                 }
-#pragma unroll
-                                for (int e = 0; e < E / 2; ++e) {
-                                    const float2 lo = weights2<BF16>(x[0][e]), hi = weights2<BF16>(x[1][e]);
-                                    af[m][e][0] = lo.x, af[m][e][1] = hi.x, af[m][e][2] = lo.y, af[m][e][3] = hi.y;
-                                }
-                            }
-#pragma unroll
-                            for (int q = 0; q < NT; ++q) {
-                                float2 v[E];
-                                if (kOne) {
-#pragma unroll
-                                    for (int e = 0; e < E; ++e) v[e] = vr[q][e];
-                                } else {
-#pragma unroll
-                                    for (int x = 0; x < E / 4; ++x) {
-                                        const float4 u = *reinterpret_cast<const float4 *>(vs + (8 * q + g) * stride + k + 4 * x);
-                                        const float y[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                                        for (int e = 0; e < 4; ++e) v[4 * x + e] = make_float2(head(y[e]), y[e] - head(y[e]));
-                                    }
-                                }
-#pragma unroll
-                                for (int m = 0; m < 2; ++m) {
-                                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                                    for (int e = 0; e < E / 2; ++e) mma_tf32(d, af[m][e], v[2 * e].y, v[2 * e + 1].y);
-#pragma unroll
-                                    for (int e = 0; e < E / 2; ++e) mma_tf32(d, af[m][e], v[2 * e].x, v[2 * e + 1].x);
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) acc[q][m][e] = kOne || k0 == 0 ? d[e] : acc[q][m][e] + d[e];
-                                }
-                            }
+                            if (!kOne) v.load(vs, pitch, k0, g, t);
+                            v.multiply(acc, x, kOne || k0 == 0);
                         }
 #pragma unroll
                         for (int q = 0; q < NT; ++q)
@@ -884,7 +910,7 @@ __global__ void __launch_bounds__(kBulkThreads, 2)
 #pragma unroll
                                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                                        for (int h = 0; h < 2; ++h) y[16 * m + 8 * h] += acc[q][m][2 * h + x];
+                                        for (int h = 0; h < 2; ++h) y[16 * m + 8 * h] = fmaf(acc[q][m][2 * h + x], undo[q][x], y[16 * m + 8 * h]);
                                 }
                             }
                         tcu::fence_async_smem();  // before the bulk copies read it
@@ -999,7 +1025,7 @@ cudaError_t expand(const Call &c, int tiles, int groups, int slices)
 {
     auto kern = k_lora_expand<KC, kOne, NT, BF16>;
     const int depth = (c.rank + KC - 1) / KC * KC;
-    const size_t smem = sizeof(float) * 8 * NT * (depth + 4) + kWarps * kStages * expand_stage(KC, NT);
+    const size_t smem = v_bytes(depth, 8 * NT) + kWarps * kStages * expand_stage(KC, NT);
     if (ctas_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
     // two CTAs per SM at once, the row blocks of all tiles dealt out evenly: no SM is left with less at the end
     const long long total = static_cast<long long>(tiles) * ((c.rows + kRowBlock - 1) / kRowBlock);
@@ -1024,7 +1050,7 @@ cudaError_t expand_bulk(const Call &c, int slices)
 {
     auto kern = k_lora_expand_bulk<KC, kOne, BF16>;
     const int depth = (c.rank + KC - 1) / KC * KC, stages = bulk_stages(c.rank);
-    const size_t smem = sizeof(float) * kBulkTokens * (depth + 4) + static_cast<size_t>(stages) * bulk_stage(c.rank);
+    const size_t smem = v_bytes(depth, kBulkTokens) + static_cast<size_t>(stages) * bulk_stage(c.rank);
     const int per_sm = ctas_per_sm(reinterpret_cast<const void *>(kern), kBulkThreads, smem);
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
     const long long total = static_cast<long long>((c.B.M + kBulkTokens - 1) / kBulkTokens) * ((c.rows + kBulkRows - 1) / kBulkRows);
