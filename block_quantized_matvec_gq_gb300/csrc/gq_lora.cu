@@ -373,7 +373,7 @@ inline int step_stages(int rank, int tokens, bool q8)
 }
 
 template <int MT, int NT, bool BF16, bool Q8>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     k_lora_shrink_tile(const uint16_t *__restrict__ A, Batch B, const float *__restrict__ X, long long ldx,
                        const int8_t *__restrict__ Xq, const float *__restrict__ dx, float *__restrict__ V, int rank, int K,
                        int slice_steps, int stages)
@@ -1016,7 +1016,7 @@ cudaError_t shrink_tile_rank(const Call &c, bool bf16, int *slices)
 {
     if (c.rank <= 16) return shrink_tile_typed<1, 4>(c, bf16, slices);
     if (c.rank <= 32) return shrink_tile_typed<2, 4>(c, bf16, slices);
-    if (c.rank <= 64) return shrink_tile_typed<4, 4>(c, bf16, slices);
+    if (c.rank <= 64) return shrink_tile_typed<4, 2>(c, bf16, slices);
     return shrink_tile_typed<8, 2>(c, bf16, slices);
 }
 
