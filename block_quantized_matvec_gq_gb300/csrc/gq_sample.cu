@@ -16,8 +16,7 @@
 //          The list's threshold is the want-th largest of the threads' own
 //          maxima, found by bisection with a vote of the CTA per step: at least
 //          `want` elements reach it, and few more.
-//          The CTA that finishes a row's last slice goes on to pick the token:
-//          the lists above the slices' highest threshold hold every element above
+//   pick   one CTA per row (where a row is one slice, the same CTA): the lists above the slices' highest threshold hold every element above
 //          it, some hundreds.  They are sorted, and where the limits and the draw
 //          fall among them, which they do for a language model's usual rows, the
 //          row is done.
@@ -29,7 +28,7 @@
 //          share.
 //
 // What bounds it: the one pass over the logits, and for small batches the
-// latency of the two kernels.
+// latency of the kernels.
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
@@ -46,8 +45,9 @@ namespace cg = cooperative_groups;
 using u64 = unsigned long long;
 
 constexpr int kScanThreads = 256, kSmallThreads = 512;  // of a slice of 8192 and of 4096 elements
+constexpr int kPickThreads = 512;
 constexpr int kDeepThreads = 1024;
-constexpr int kDeepCtas = 8;
+constexpr int kDeepCtas = 16;
 constexpr int kDeepClusters = 64;
 constexpr int kList = 2048;  // elements that are sorted at once
 constexpr int kSumFrom = 512;  // a top_k from here on may lie behind the list: the slices' sums bound its weight
@@ -79,8 +79,7 @@ struct Rows {
     int vocab, slices, cap, cap_log2;
     Header *head;
     u64 *list;
-    unsigned *done;  // finished slices of every row, 0 before and after a call
-    int *deep;       // rows for the second kernel
+    int *deep;  // rows for the last kernel
 };
 
 // Order-preserving bits of a logit that is not a NaN; -0 is 0.
@@ -533,12 +532,13 @@ struct PickShared {
 
 // The row from its slices' headers and lists; false where they do not settle it.
 template <int THREADS>
-__device__ __forceinline__ bool pick(const Rows &R, const Settings &S, int row, float T, int k, PickShared &P, int &tok, float &pr,
-                                     bool &refused)
+__device__ __forceinline__ bool settle(const Rows &R, const Settings &S, int row, PickShared &P, int &tok, float &pr, bool &refused)
 {
     const int tid = threadIdx.x, lane = tid & 31;
     const Header *head = R.head + static_cast<long long>(row) * R.slices;
-    const float p = S.top_p ? __ldg(S.top_p + row) : 1.f, mp = S.min_p ? __ldg(S.min_p + row) : 0.f, u = __ldg(S.u + row);
+    const float T = temperature(S, row), p = S.top_p ? __ldg(S.top_p + row) : 1.f, mp = S.min_p ? __ldg(S.min_p + row) : 0.f,
+                u = __ldg(S.u + row);
+    const int k = top_k(S, row, R.vocab);
     tok = -1;
     pr = 0.f;
     refused = isnan(T) || isnan(p) || isnan(mp);
@@ -660,8 +660,26 @@ __device__ __forceinline__ bool pick(const Rows &R, const Settings &S, int row, 
     return true;
 }
 
+template <int THREADS>
+__device__ __forceinline__ void pick(const Rows &R, const Settings &S, int row, PickShared &P, int32_t *token, float *prob, int *status)
+{
+    int tok;
+    float pr;
+    bool refused;
+    const bool settled = settle<THREADS>(R, S, row, P, tok, pr, refused);
+    if (threadIdx.x == 0) {
+        if (settled) {
+            token[row] = tok;
+            if (prob) prob[row] = pr;
+        }
+        R.deep[row] = settled ? 0 : 1;
+        if (refused && status) atomicExch(status, GQ_ERR_SHAPE);
+    }
+}
+
 // ---------------------------------------------------------------- scan
-template <int TYPE, int EPT, int THREADS>
+// kOne: a row is one slice, and the CTA goes on to pick the token.
+template <int TYPE, int EPT, int THREADS, bool kOne>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     k_sample_scan(Rows R, Settings S, int want, int32_t *token, float *prob, int *status)
 {
@@ -805,31 +823,24 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) h.sum += s_sum[w];
     }
-    // the CTA's writes are visible device-wide before the slice counts as finished
     __syncthreads();
     if (tid == 0) {
         h.best = top > kNone ? rank_of(top, s_first) : 0ull;
         R.head[static_cast<long long>(row) * R.slices + slice] = h;
-        __threadfence();
-        s_count = atomicInc(R.done + row, R.slices - 1) == static_cast<unsigned>(R.slices - 1);
-        __threadfence();
     }
-    __syncthreads();
-    if (!s_count) return;
-    // the row's last slice
+    if (kOne) {
+        __shared__ PickShared P;
+        __syncthreads();
+        pick<THREADS>(R, S, row, P, token, prob, status);
+    }
+}
+
+__global__ void __launch_bounds__(kPickThreads) k_sample_pick(Rows R, Settings S, int32_t *token, float *prob, int *status)
+{
     __shared__ PickShared P;
-    int tok;
-    float pr;
-    bool refused;
-    const bool settled = pick<THREADS>(R, S, row, T, k, P, tok, pr, refused);
-    if (tid == 0) {
-        if (settled) {
-            token[row] = tok;
-            if (prob) prob[row] = pr;
-        }
-        R.deep[row] = settled ? 0 : 1;
-        if (refused && status) atomicExch(status, GQ_ERR_SHAPE);
-    }
+    pdl_wait();
+    pdl_launch_dependents();
+    pick<kPickThreads>(R, S, blockIdx.x, P, token, prob, status);
 }
 
 // ---------------------------------------------------------------- deep
@@ -1163,8 +1174,6 @@ Plan plan_for(int vocab, int n_rows)
     p.want = want < 4 ? 4 : (want > threads / 2 ? threads / 2 : want);
     return p;
 }
-// The counters stand in front, the same for every call, so that a workspace serves calls of any size.
-constexpr size_t kCounterBytes = GQ_MAX_SAMPLE_ROWS * sizeof(unsigned);
 size_t up16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
 template <int TYPE>
@@ -1172,10 +1181,20 @@ cudaError_t launch(Rows R, const Settings &S, const Plan &p, int n_rows, int32_t
 {
     auto deep = k_sample_deep<TYPE>;
     if (ctas_per_sm(reinterpret_cast<const void *>(deep), kDeepThreads, sizeof(DeepShared)) < 1) return cudaErrorInvalidConfiguration;
+    static std::once_flag once[64];  // clusters of 16 are asked for, once a device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [&] { cudaFuncSetAttribute(deep, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
     const dim3 grid(p.slices, n_rows);
     int *status = status_word();
-    cudaError_t e = p.ept == 8 ? launch_pdl(k_sample_scan<TYPE, 8, kSmallThreads>, grid, dim3(kSmallThreads), 0, s, R, S, p.want, token, prob, status)
-                               : launch_pdl(k_sample_scan<TYPE, 32, kScanThreads>, grid, dim3(kScanThreads), 0, s, R, S, p.want, token, prob, status);
+    auto scan = [&](auto kern, int threads) { return launch_pdl(kern, grid, dim3(threads), 0, s, R, S, p.want, token, prob, status); };
+    const bool one = p.slices == 1;
+    cudaError_t e;
+    if (p.ept == 8)
+        e = one ? scan(k_sample_scan<TYPE, 8, kSmallThreads, true>, kSmallThreads) : scan(k_sample_scan<TYPE, 8, kSmallThreads, false>, kSmallThreads);
+    else
+        e = one ? scan(k_sample_scan<TYPE, 32, kScanThreads, true>, kScanThreads) : scan(k_sample_scan<TYPE, 32, kScanThreads, false>, kScanThreads);
+    if (e == cudaSuccess && !one) e = launch_pdl(k_sample_pick, dim3(n_rows), dim3(kPickThreads), 0, s, R, S, token, prob, status);
     if (e == cudaSuccess)
         e = launch_pdl(deep, dim3(kDeepCtas, n_rows < kDeepClusters ? n_rows : kDeepClusters), dim3(kDeepThreads), sizeof(DeepShared), s, R,
                        S, n_rows, token, prob);
@@ -1196,7 +1215,7 @@ size_t gq_sample_workspace_bytes(int vocab, int n_rows)
     if (vocab < 1 || vocab > GQ_MAX_VOCAB || n_rows < 1 || n_rows > GQ_MAX_SAMPLE_ROWS) return 0;
     const Plan p = plan_for(vocab, n_rows);
     const size_t slices = static_cast<size_t>(p.slices) * n_rows;
-    return kCounterBytes + slices * sizeof(Header) + (slices << p.cap_log2) * sizeof(u64) + up16(static_cast<size_t>(n_rows) * sizeof(int));
+    return slices * sizeof(Header) + (slices << p.cap_log2) * sizeof(u64) + up16(static_cast<size_t>(n_rows) * sizeof(int));
 }
 
 int gq_sample(const void *logits, long long ldl, int type, const float *temperature, const int32_t *top_k,
@@ -1215,7 +1234,7 @@ int gq_sample(const void *logits, long long ldl, int type, const float *temperat
     const Plan p = plan_for(vocab, n_rows);
     const size_t slices = static_cast<size_t>(p.slices) * n_rows;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    uint8_t *const heads = ws + kCounterBytes, *const lists = heads + slices * sizeof(Header);
+    uint8_t *const heads = ws, *const lists = heads + slices * sizeof(Header);
     const Rows R{static_cast<const uint8_t *>(logits),
                  ldl * kv::type_size(type),
                  vocab,
@@ -1224,7 +1243,6 @@ int gq_sample(const void *logits, long long ldl, int type, const float *temperat
                  p.cap_log2,
                  reinterpret_cast<Header *>(heads),
                  reinterpret_cast<u64 *>(lists),
-                 reinterpret_cast<unsigned *>(ws),
                  reinterpret_cast<int *>(lists + (slices << p.cap_log2) * sizeof(u64))};
     const Settings S{temperature, top_k, top_p, min_p, u};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

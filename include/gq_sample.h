@@ -46,9 +46,8 @@ extern "C" {
  *           limit, no limit, no limit.
  *   token   int32[n_rows]; prob f32[n_rows] or NULL.
  *   workspace  device memory, 16-byte aligned, at least
- *           gq_sample_workspace_bytes bytes.  ZERO-FILL IT ONCE before its first
- *           use; every completed call leaves it ready for the next, of any size
- *           that fits.  Two calls that may run concurrently must not share it.
+ *           gq_sample_workspace_bytes bytes, scratch before and after the call.
+ *           Two calls that may run concurrently must not share it.
  * Arithmetic: weights are whole numbers of 2^-43 of about the largest weight, each within
  * 2^-23 of itself and 2^-42 of the largest; their sums are exact.  So the
  * result does not depend on how the row was split, the same inputs give the

@@ -66,7 +66,7 @@ def sample(x, typ, T=None, k=None, p=None, m=None, u=0.5, with_prob=True, ws=Non
     token = t.full((n + 2,), -77, dtype=t.int32, device="cuda")
     prob = t.full((n + 2,), -77.0, device="cuda")
     if ws is None:
-        ws = t.zeros(gq.gq_sample_workspace_bytes(vocab, n), dtype=t.uint8, device="cuda")
+        ws = t.full((gq.gq_sample_workspace_bytes(vocab, n),), 0xA5, dtype=t.uint8, device="cuda")
     gq.gq_sample(x, x.stride(0), TYPES[typ], arr(T, np.float32), arr(k, np.int32), arr(p, np.float32), arr(m, np.float32),
                  arr(u, np.float32), token, prob if with_prob else None, ws, ws.numel(), vocab, n)
     token, prob = token.cpu().numpy(), prob.cpu().numpy()
