@@ -262,9 +262,9 @@ struct Reader {
 #pragma unroll
         for (int i = 0; i < kVec; ++i) v[i] = fmaxf(v[i], -INFINITY);
     }
-    __device__ __forceinline__ void load(int unit, float (&v)[kVec]) const
+    // A unit that the row's beginning or end cuts, element by element.
+    __device__ __forceinline__ void edge(int unit, float (&v)[kVec]) const
     {
-        if (unit < units && inside(unit)) return values(word(unit), v);
         const uint8_t *p = base + static_cast<long long>(unit) * 16;
         const int first = index(unit, 0);
 #pragma unroll
@@ -280,6 +280,13 @@ struct Reader {
                 v[i] = fmaxf(v[i], -INFINITY);
             }
         }
+    }
+    __device__ __forceinline__ void load(int unit, float (&v)[kVec]) const
+    {
+        if (unit < units && inside(unit))
+            values(word(unit), v);
+        else
+            edge(unit, v);
     }
 };
 
@@ -304,10 +311,8 @@ __device__ __forceinline__ u64 cta_sum(u64 v, u64 *sh)
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
     __syncthreads();
-    u64 s = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) s += sh[w];
-    return s;
+    const int lane = threadIdx.x & 31;
+    return warp_sum(lane < THREADS / 32 ? sh[lane] : 0ull);
 }
 
 // ---------------------------------------------------------------- sorted lists
@@ -340,7 +345,7 @@ __device__ __forceinline__ void bitonic_down(u64 *a, int n)
 // dealt by their bits.  The bitonic sort remains for lists with more than kCrowd
 // in one step (ties, far outliers).  Loops are not unrolled: this code runs once
 // in a kernel, and what it costs is latency and fetching instructions.
-constexpr int kSteps = 1024, kCrowd = 256, kFew = 96;
+constexpr int kSteps = 1024, kCrowd = 256, kFew = 256;
 struct SortShared {
     unsigned count[kSteps + 1];
     unsigned short pos[kList];
@@ -490,8 +495,7 @@ __device__ __forceinline__ Header load_header(const Header *h)
     return r;
 }
 // The CTA's rows of headers, joined in every thread; `sh` has one entry per warp.
-template <int THREADS>
-__device__ __forceinline__ RowHead join_heads(RowHead r, RowHead *sh)
+__device__ __forceinline__ RowHead warp_join(RowHead r)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) r.best = max(r.best, __shfl_xor_sync(0xffffffffu, r.best, o));
@@ -499,18 +503,17 @@ __device__ __forceinline__ RowHead join_heads(RowHead r, RowHead *sh)
     r.theta = __reduce_max_sync(0xffffffffu, r.theta);
     r.cands = __reduce_add_sync(0xffffffffu, r.cands);
     r.most = __reduce_max_sync(0xffffffffu, r.most);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = r;
-    __syncthreads();
-    r = sh[0];
-#pragma unroll
-    for (int w = 1; w < THREADS / 32; ++w) {
-        r.best = max(r.best, sh[w].best);
-        r.lowest = min(r.lowest, sh[w].lowest);
-        r.theta = max(r.theta, sh[w].theta);
-        r.cands += sh[w].cands;
-        r.most = max(r.most, sh[w].most);
-    }
     return r;
+}
+template <int THREADS>
+__device__ __forceinline__ RowHead join_heads(RowHead r, RowHead *sh)
+{
+    const int lane = threadIdx.x & 31;
+    r = warp_join(r);
+    if (lane == 0) sh[threadIdx.x >> 5] = r;
+    __syncthreads();
+    const RowHead none{0ull, kUnknown, 0u, 0, 0};
+    return warp_join(lane < THREADS / 32 ? sh[lane] : none);
 }
 __device__ __forceinline__ void add_head(RowHead &r, const Header &h)
 {
@@ -896,27 +899,22 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
 
         const Reader<TYPE> in(R.logits + row * R.row_bytes, R.vocab);
         const int cta_units = (in.units + kDeepCtas - 1) / kDeepCtas, first = me * cta_units, end = min(first + cta_units, in.units);
-        auto each = [&](auto &&f) {  // this CTA's part of the row, a 16-byte unit at a time, four loads in flight
-            constexpr int kBatch = 4;
+        // This CTA's part of the row, a 16-byte unit at a time, the next one on its way.  Not unrolled: the kernel runs
+        // once over little data, and fetching long code is what it would wait for.
+        auto each = [&](auto &&f) {
+            int q = first + tid;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (q < end && in.inside(q)) w = in.word(q);
 #pragma unroll 1
-            for (int q0 = first + tid; q0 < end; q0 += kBatch * kDeepThreads) {
-                uint4 w[kBatch];
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    const int q = q0 + j * kDeepThreads;
-                    if (q < end && in.inside(q)) w[j] = in.word(q);
-                }
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    const int q = q0 + j * kDeepThreads;
-                    if (q >= end) break;
-                    float v[kVec];
-                    if (in.inside(q))
-                        in.values(w[j], v);
-                    else
-                        in.load(q, v);
-                    f(v, in.index(q, 0));
-                }
+            for (; q < end; q += kDeepThreads) {
+                const int next = q + kDeepThreads;
+                uint4 after = make_uint4(0, 0, 0, 0);
+                if (next < end && in.inside(next)) after = in.word(next);
+                float v[kVec];
+                in.values(w, v);
+                if (!in.inside(q)) in.edge(q, v);
+                f(v, in.index(q, 0));
+                w = after;
             }
         };
         auto clear = [&] {
@@ -933,24 +931,26 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
         };
         // The CTAs' histograms, added up and summed over the steps, in every CTA's L; `base` in front.
         auto merge = [&](Level &L, u64 base) {
+            // 16 neighbouring lanes take a step of this CTA's share, one CTA's part each, and write the sum to one CTA each
             constexpr int kShare = kBins / kDeepCtas;
+            static_assert(kDeepCtas == 16, "half a warp");
             cluster.sync();
-            for (int i = tid; i < kShare; i += kDeepThreads) {
-                const int b = me * kShare + i;
-                unsigned n = 0;
-                u64 w = 0;
-#pragma unroll 2
-                for (int c = 0; c < kDeepCtas; ++c) {
-                    n += cluster.map_shared_rank(D.hist, c)[b];
-                    w += static_cast<u64>(cluster.map_shared_rank(D.high, c)[b]) << 32;
-                    w += cluster.map_shared_rank(D.low, c)[b];
+            const int c = tid & 15;
+            const unsigned *hist = cluster.map_shared_rank(D.hist, c), *lo = cluster.map_shared_rank(D.low, c),
+                           *hi = cluster.map_shared_rank(D.high, c);
+            Level *to = cluster.map_shared_rank(&L, c);
+#pragma unroll
+            for (int i = 0; i < kShare * 16 / kDeepThreads; ++i) {
+                const int b = me * kShare + i * (kDeepThreads / 16) + (tid >> 4);
+                unsigned n = hist[b];
+                u64 w = (static_cast<u64>(hi[b]) << 32) + lo[b];
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) {
+                    n += __shfl_xor_sync(0xffffffffu, n, o);
+                    w += __shfl_xor_sync(0xffffffffu, w, o);
                 }
-#pragma unroll 2
-                for (int c = 0; c < kDeepCtas; ++c) {
-                    Level *to = cluster.map_shared_rank(&L, c);
-                    to->count[b] = n;
-                    to->weight[b] = w;
-                }
+                to->count[b] = n;
+                to->weight[b] = w;
             }
             cluster.sync();
             unsigned n[kPer], ns = 0;
@@ -976,12 +976,8 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
                 D.sh2[warp] = wi;
             }
             __syncthreads();
-            ni -= ns;
-            wi += base - ws;
-            for (int x = 0; x < warp; ++x) {
-                ni += D.sh32[x];
-                wi += D.sh2[x];
-            }
+            ni += __reduce_add_sync(0xffffffffu, lane < warp ? D.sh32[lane] : 0u) - ns;
+            wi += warp_sum(lane < warp ? D.sh2[lane] : 0ull) + base - ws;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 L.count[tid * kPer + i] = ni += n[i];
@@ -1070,23 +1066,27 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
                     if (me == 0) {
                         const int n = min(static_cast<int>(D.listed), kList);
                         u64 most = 0, fewest = ~0ull;
-                        for (int i = tid; i < n; i += kDeepThreads) {
-                            most = max(most, D.list[i]);
-                            fewest = min(fewest, D.list[i]);
-                        }
+                        if (n > kFew) {
+                            for (int i = tid; i < n; i += kDeepThreads) {
+                                most = max(most, D.list[i]);
+                                fewest = min(fewest, D.list[i]);
+                            }
+                            auto extremes = [&] {
 #pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) {
-                            most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-                            fewest = min(fewest, __shfl_xor_sync(0xffffffffu, fewest, o));
-                        }
-                        if (lane == 0) {
-                            D.sh[warp] = most;
-                            D.sh2[warp] = fewest;
-                        }
-                        __syncthreads();
-                        for (int w = 0; w < kDeepThreads / 32; ++w) {
-                            most = max(most, D.sh[w]);
-                            fewest = min(fewest, D.sh2[w]);
+                                for (int o = 16; o > 0; o >>= 1) {
+                                    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                                    fewest = min(fewest, __shfl_xor_sync(0xffffffffu, fewest, o));
+                                }
+                            };
+                            extremes();
+                            if (lane == 0) {
+                                D.sh[warp] = most;
+                                D.sh2[warp] = fewest;
+                            }
+                            __syncthreads();
+                            most = D.sh[lane];  // (32 warps)
+                            fewest = D.sh2[lane];
+                            extremes();
                         }
                         sort_down<kDeepThreads>(D.list, D.F, D.sort, n, most, fewest);
                         running_weights<kDeepThreads>(D.list, D.F, n, weight_in_front, sc, top, D.sh);
