@@ -931,26 +931,50 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
         };
         // The CTAs' histograms, added up and summed over the steps, in every CTA's L; `base` in front.
         auto merge = [&](Level &L, u64 base) {
-            // 16 neighbouring lanes take a step of this CTA's share, one CTA's part each, and write the sum to one CTA each
-            constexpr int kShare = kBins / kDeepCtas;
-            static_assert(kDeepCtas == 16, "half a warp");
+            // A CTA sums a share of the steps: two warps fetch each CTA's part of it, 128 bytes an access (single words of
+            // many CTAs cost ten times that), and bring the sums to one CTA each.
+            constexpr int kShare = kBins / kDeepCtas, kHalf = kShare / 2;
+            static_assert(kDeepThreads == 64 * kDeepCtas && kShare == 128, "two warps a CTA, two steps a lane");
+            unsigned *const part = reinterpret_cast<unsigned *>(D.list);  // [3][kDeepCtas][kShare]: list and F, which are free
+            static_assert(3 * kDeepCtas * kShare * sizeof(unsigned) <= sizeof(D.list) + sizeof(D.F), "room for the parts");
             cluster.sync();
-            const int c = tid & 15;
-            const unsigned *hist = cluster.map_shared_rank(D.hist, c), *lo = cluster.map_shared_rank(D.low, c),
-                           *hi = cluster.map_shared_rank(D.high, c);
-            Level *to = cluster.map_shared_rank(&L, c);
+            {
+                const int c = warp >> 1, x = (warp & 1) * kHalf + lane;
+                const unsigned *from[3] = {cluster.map_shared_rank(D.hist, c), cluster.map_shared_rank(D.low, c),
+                                           cluster.map_shared_rank(D.high, c)};
+                unsigned v[3][2];
 #pragma unroll
-            for (int i = 0; i < kShare * 16 / kDeepThreads; ++i) {
-                const int b = me * kShare + i * (kDeepThreads / 16) + (tid >> 4);
-                unsigned n = hist[b];
-                u64 w = (static_cast<u64>(hi[b]) << 32) + lo[b];
+                for (int k = 0; k < 3; ++k)
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1) {
-                    n += __shfl_xor_sync(0xffffffffu, n, o);
-                    w += __shfl_xor_sync(0xffffffffu, w, o);
+                    for (int i = 0; i < 2; ++i) v[k][i] = from[k][me * kShare + x + 32 * i];
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) part[(k * kDeepCtas + c) * kShare + x + 32 * i] = v[k][i];
+            }
+            __syncthreads();
+            if (tid < kShare) {
+                unsigned n = 0;
+                u64 w = 0;
+#pragma unroll 4
+                for (int c = 0; c < kDeepCtas; ++c) {
+                    n += part[c * kShare + tid];
+                    w += part[(kDeepCtas + c) * kShare + tid] + (static_cast<u64>(part[(2 * kDeepCtas + c) * kShare + tid]) << 32);
                 }
-                to->count[b] = n;
-                to->weight[b] = w;
+                L.count[me * kShare + tid] = n;
+                L.weight[me * kShare + tid] = w;
+            }
+            __syncthreads();
+            {
+                Level *to = cluster.map_shared_rank(&L, warp >> 1);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int b = me * kShare + (warp & 1) * kHalf + lane + 32 * i;
+                    if ((warp >> 1) != me) {
+                        to->count[b] = L.count[b];
+                        to->weight[b] = L.weight[b];
+                    }
+                }
             }
             cluster.sync();
             unsigned n[kPer], ns = 0;
