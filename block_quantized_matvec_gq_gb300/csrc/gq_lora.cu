@@ -3,24 +3,34 @@
 //   v = A_a x (rank numbers a token), then Y = Y0 + scale_a B_a v.
 //
 // Two kernels: `shrink` writes v to the workspace, `expand` adds.  Both work on
-// tiles of 8 or 32 neighbouring tokens.  A tile's distinct adapters (its
-// groups) are found with one warp vote; each is multiplied with the whole tile
-// and kept for its own tokens, so no sorting of the batch precedes them, and an
-// adapter's weights pass only by its own tokens' results.  Decode batches,
-// whose neighbours differ, take tiles of 8 (the width of the matrix
-// instruction) with the groups in different CTAs; prompts take 32, nearly
-// always one group.
+// tiles of neighbouring tokens.  A tile's distinct adapters (its groups) are found
+// with one warp vote; each is multiplied with the whole tile and kept for its own
+// tokens, so no sorting of the batch precedes them, and an adapter's weights touch
+// only its own tokens' results.
 //
-// The products run on mma.sync with tf32 operands: 16-bit weights are exact in
-// tf32, f32 activations and v are two pieces of 11 bits, and Q8_0 codes are
-// exact, their scale applied to each block's sum.  The order of the contraction
-// is free, so a lane takes 8 consecutive elements of a row as its operands of
-// four instructions: weights and activations come in 16-byte loads straight
-// from memory, without shared memory between.  Sums of more than 32 products
-// are added in f32 registers, because the tensor core truncates its own.
+//   decode batches, whose neighbours differ: tiles of 8 tokens, the width of the
+//     matrix instruction, the groups in different CTAs; every lane copies the
+//     pieces of weights and activations that it multiplies (cp.async), so that no
+//     thread waits for another.
+//   prompts, nearly always one group a tile: tiles of 16 or 32 tokens; `shrink`
+//     shares a step's copies between its warps, `expand` moves Y by bulk copies.
+//
+// The products run on mma.sync.  Weights are operands as they are (16 bits).  So
+// are Q8_0 codes, whose scale is applied to each 32-block's sum; f32 numbers are
+// three pieces of bf16, or two of f16 where they can be scaled into its range (v),
+// or two of tf32 (activations beside f16 weights): 22 bits or more.  The order of
+// the contraction is free, so a lane takes 8 consecutive elements of a row, one
+// 16-byte load, as its operands of two instructions.  Sums of more than 32
+// products are added in f32 registers, because the tensor core truncates its own.
 //
 // tcgen05 is not used: the contraction is 8 to 128 deep, so the work is the
 // bytes of Y (and, for few tokens, of the adapters), not the products.
+//
+// What bounds them: 4096 tokens of rank 16 beside 21504 rows (732 MB) take 153 us,
+// 4.8 TB/s; without the stores 111, without the products 148: the memory.  A plain
+// copy in the same order takes 114 for Y alone.  1531 tokens of rank 64 (112 MB)
+// take 65, where the products and the two kernels' beginnings show; 64 tokens of
+// 48 adapters of rank 32 (84 MB) 27.7.  One token: 4.4, the latency of two kernels.
 #include "gq_host.h"
 #include "gq_internal.cuh"
 #include "gq_kv.cuh"
@@ -204,10 +214,10 @@ __host__ __device__ constexpr int shrink_stages(int mt, int nt, bool q8)
     const int n = (108 << 10) / (8 * shrink_stage(mt, nt, q8));
     return n > 6 ? 6 : (n < 2 ? 2 : n);
 }
-// CTA: a tile of 8 NT tokens, one slice of K.  The warps take the slice's
+// CTA: a tile of 8 tokens, one slice of K.  The warps take the slice's
 // 32-element chunks in turn, each for all of rank (16 MT), and add up in
 // shared memory; the slices' sums are added by `expand`.
-template <int MT, int NT, bool BF16, bool Q8>
+template <int MT, bool BF16, bool Q8>
 __global__ void __launch_bounds__(kThreads)
     k_lora_shrink(const uint16_t *__restrict__ A, Batch B, const float *__restrict__ X, long long ldx,
                   const int8_t *__restrict__ Xq, const float *__restrict__ dx, float *__restrict__ V, int rank, int K,
@@ -215,7 +225,7 @@ __global__ void __launch_bounds__(kThreads)
 {
     extern __shared__ __align__(16) float red[];  // [kWarps][16 MT][8 NT], and before that the warps' rings
     __shared__ Tile tile;
-    constexpr int TT = 8 * NT, kOut = 16 * MT * TT, kStage = shrink_stage(MT, NT, Q8), kStages = shrink_stages(MT, NT, Q8);
+    constexpr int NT = 1, TT = 8 * NT, kOut = 16 * MT * TT, kStage = shrink_stage(MT, NT, Q8), kStages = shrink_stages(MT, NT, Q8);
     struct Raw {  // the lane's part of a chunk
         uint4 a[MT][2];
         uint2 q[NT];
@@ -588,19 +598,19 @@ struct Fragment {
 constexpr int kStages = 3;
 // Four rows of weights (16 bytes a lane, 8 where a chunk is 16 deep) and the lane's results of 8 NT tokens.
 __host__ __device__ constexpr int expand_stage(int kc, int nt) { return 64 * kc + 1024 * nt; }
-// CTA: a tile of 8 NT tokens and a range of row blocks, which its warps take in
+// CTA: a range of row blocks of tiles of 8 tokens, which its warps take in
 // turn.  Row slots are dealt so that a lane's four results of a token are four
 // consecutive rows: slot g (+ 8) of instruction m is row 4 g + 2 m (+ 1).
 // KC = 16: a rank of up to 16, where a lane's chunk is four elements.
 // kOne: the rank is one chunk, whose v then stays in registers.
-template <int KC, bool kOne, int NT, bool BF16>
+template <int KC, bool kOne, bool BF16>
 __global__ void __launch_bounds__(kThreads, 2)
     k_lora_expand(const uint16_t *__restrict__ W, Batch B, const float *__restrict__ V, const float *Y0, long long ldy0,
                   float *Y, long long ldy, int rank, int rows, int slices, long long cta_blocks, long long total_blocks)
 {
     extern __shared__ __align__(16) char raw[];
     __shared__ Tile tile;
-    constexpr int TT = 8 * NT, E = KC / 4;  // elements of a lane's chunk
+    constexpr int NT = 1, TT = 8 * NT, E = KC / 4;  // E: elements of a lane's chunk
     constexpr int kStageBytes = expand_stage(KC, NT);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     constexpr int kRowPieces = KC / 8, kPieces = kRowPieces;  // 16-byte pieces of a row's chunk, and of a lane
@@ -615,130 +625,130 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int tile_blocks = (rows + kRowBlock - 1) / kRowBlock;
     const long long last = min((blockIdx.x + 1ll) * cta_blocks, total_blocks);
     for (long long at = blockIdx.x * cta_blocks; at < last;) {
-    const int tile_no = static_cast<int>(at / tile_blocks), rb0 = static_cast<int>(at - static_cast<long long>(tile_no) * tile_blocks);
-    const int rb1 = static_cast<int>(min(static_cast<long long>(tile_blocks), rb0 + (last - at)));
-    at += rb1 - rb0;
-    const int t0 = tile_no * TT;
-    // the lists, Y0 and the weights were complete before `shrink` let this
-    // kernel begin; v is complete after the wait
-    find_groups<TT>(tile, B, t0);
-    const int groups = tile.groups;
-    for (int j = blockIdx.z; j < max(groups, 1); j += gridDim.z) {
-        const bool product = j < groups;
-        // tokens whose rows this pass writes: the group's, and with the first group those without an adapter, if
-        // their rows have to be copied
-        bool put[NT][2], add[NT][2];
+        const int tile_no = static_cast<int>(at / tile_blocks), rb0 = static_cast<int>(at - static_cast<long long>(tile_no) * tile_blocks);
+        const int rb1 = static_cast<int>(min(static_cast<long long>(tile_blocks), rb0 + (last - at)));
+        at += rb1 - rb0;
+        const int t0 = tile_no * TT;
+        // the lists, Y0 and the weights were complete before `shrink` let this
+        // kernel begin; v is complete after the wait
+        find_groups<TT>(tile, B, t0);
+        const int groups = tile.groups;
+        for (int j = blockIdx.z; j < max(groups, 1); j += gridDim.z) {
+            const bool product = j < groups;
+            // tokens whose rows this pass writes: the group's, and with the first group those without an adapter, if
+            // their rows have to be copied
+            bool put[NT][2], add[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int tok = 8 * n + 2 * t + i;
-                add[n][i] = product && tile.group[tok] == j;
-                put[n][i] = add[n][i] || (j == 0 && tile.group[tok] < 0 && t0 + tok < B.M && Y != Y0);
-            }
-        const uint16_t *w = W + static_cast<long long>(product ? tile.adapter[j] : 0) * rows * rank;
-        // Steps: a warp's row blocks, each in nk chunks of the rank.  A step's weights, and with a block's last chunk its
-        // part of Y0, come through a ring of kStages steps in shared memory.  Of Y0 every lane copies what it reads itself;
-        // the weights are copied as they lie (a rank of 16 or 32: 1 or 2 KB without a gap; copied by the lanes that read
-        // them they cost three times their bytes), the 16-byte pieces placed so that no two lanes meet on a bank.
-        const int nk = depth / KC, blocks = rb0 + warp < rb1 ? (rb1 - rb0 - warp + kWarps - 1) / kWarps : 0, steps = blocks * nk;
-        int fetch_row = (rb0 + warp) * kRowBlock + 4 * g, fetch_k = 0;
-        auto fetch = [&](int step) {
-            if (step < steps) {
-                char *to = ring + (step % kStages) * kStageBytes;
-                if (product) {
+                for (int i = 0; i < 2; ++i) {
+                    const int tok = 8 * n + 2 * t + i;
+                    add[n][i] = product && tile.group[tok] == j;
+                    put[n][i] = add[n][i] || (j == 0 && tile.group[tok] < 0 && t0 + tok < B.M && Y != Y0);
+                }
+            const uint16_t *w = W + static_cast<long long>(product ? tile.adapter[j] : 0) * rows * rank;
+            // Steps: a warp's row blocks, each in nk chunks of the rank.  A step's weights, and with a block's last chunk its
+            // part of Y0, come through a ring of kStages steps in shared memory.  Of Y0 every lane copies what it reads itself;
+            // the weights are copied as they lie (a rank of 16 or 32: 1 or 2 KB without a gap; copied by the lanes that read
+            // them they cost three times their bytes), the 16-byte pieces placed so that no two lanes meet on a bank.
+            const int nk = depth / KC, blocks = rb0 + warp < rb1 ? (rb1 - rb0 - warp + kWarps - 1) / kWarps : 0, steps = blocks * nk;
+            int fetch_row = (rb0 + warp) * kRowBlock + 4 * g, fetch_k = 0;
+            auto fetch = [&](int step) {
+                if (step < steps) {
+                    char *to = ring + (step % kStages) * kStageBytes;
+                    if (product) {
 #pragma unroll
-                    for (int i = 0; i < kPieces; ++i) {
-                        const int r = (lane + 32 * i) / kRowPieces, c = (lane + 32 * i) % kRowPieces;
-                        const int at = fetch_row - 4 * g + r, k = fetch_k * KC + 8 * c;
-                        if (at < rows && k < rank) cp_async<16>(to + 16 * place(r, c), w + static_cast<long long>(at) * rank + k);
+                        for (int i = 0; i < kPieces; ++i) {
+                            const int r = (lane + 32 * i) / kRowPieces, c = (lane + 32 * i) % kRowPieces;
+                            const int at = fetch_row - 4 * g + r, k = fetch_k * KC + 8 * c;
+                            if (at < rows && k < rank) cp_async<16>(to + 16 * place(r, c), w + static_cast<long long>(at) * rank + k);
+                        }
+                    }
+                    if (++fetch_k == nk) {
+                        if (fetch_row < rows) {
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    if (put[n][i])
+                                        cp_async<16>(to + 256 * E + (2 * n + i) * 512 + lane * 16,
+                                                     Y0 + static_cast<long long>(t0 + 8 * n + 2 * t + i) * ldy0 + fetch_row);
+                        }
+                        fetch_k = 0;
+                        fetch_row += kWarps * kRowBlock;
                     }
                 }
-                if (++fetch_k == nk) {
-                    if (fetch_row < rows) {
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+#pragma unroll
+            for (int i = 0; i < kStages - 1; ++i) fetch(i);
+            // v is complete after the wait; the copies above were let go before
+            if (!waited) pdl_wait();
+            waited = true;
+            const float scale = product ? __ldg(B.scale + tile.adapter[j]) : 0.f;
+            stage_v<TT, BF16>(vs, V, t0, B.M, rank, depth, slices, scale, [&](int tok) { return tile.group[tok] == j; });
+            __syncthreads();
+            Fragment<KC, NT, BF16> v;  // of all of the rank, where that is one chunk
+            if (kOne) v.load(vs, pitch, 0, g, t);
+            float undo[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) undo[n][i] = BF16 ? 1.f : reinterpret_cast<const float *>(vs + 3 * TT * pitch)[8 * n + 2 * t + i];
+            int row = (rb0 + warp) * kRowBlock + 4 * g, kc = 0;
+            float acc[NT][2][4];
+            for (int step = 0; step < steps; ++step) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+                __syncwarp();  // the other lanes' copies as well; and they have read the step before, whose place is next
+                const char *from = ring + (step % kStages) * kStageBytes;
+                if (product) {
+                    const int k = kc * KC + E * t;
+                    const bool have = row < rows && k < rank;
+                    uint32_t x[2][2][E / 2];
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const char *q = from + 16 * place(4 * g + 2 * m + h, E * t / 8) + (E * t % 8) * 2;
+                            if (E == 8) {
+                                const uint4 y = *reinterpret_cast<const uint4 *>(q);
+                                x[m][h][0] = y.x, x[m][h][1] = y.y, x[m][h][E / 2 - 2] = y.z, x[m][h][E / 2 - 1] = y.w;
+                            } else {
+                                const uint2 y = *reinterpret_cast<const uint2 *>(q);
+                                x[m][h][0] = y.x, x[m][h][1] = y.y;
+                            }
+#pragma unroll
+                            for (int i = 0; i < E / 2; ++i) x[m][h][i] = have ? x[m][h][i] : 0u;
+                        }
+                    if (!kOne) v.load(vs, pitch, kc * KC, g, t);
+                    v.multiply(acc, x, kOne || kc == 0);
+                }
+                if (++kc == nk) {
+                    if (row < rows) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
-                                if (put[n][i])
-                                    cp_async<16>(to + 256 * E + (2 * n + i) * 512 + lane * 16,
-                                                 Y0 + static_cast<long long>(t0 + 8 * n + 2 * t + i) * ldy0 + fetch_row);
-                    }
-                    fetch_k = 0;
-                    fetch_row += kWarps * kRowBlock;
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) fetch(i);
-        // v is complete after the wait; the copies above were let go before
-        if (!waited) pdl_wait();
-        waited = true;
-        const float scale = product ? __ldg(B.scale + tile.adapter[j]) : 0.f;
-        stage_v<TT, BF16>(vs, V, t0, B.M, rank, depth, slices, scale, [&](int tok) { return tile.group[tok] == j; });
-        __syncthreads();
-        Fragment<KC, NT, BF16> v;  // of all of the rank, where that is one chunk
-        if (kOne) v.load(vs, pitch, 0, g, t);
-        float undo[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) undo[n][i] = BF16 ? 1.f : reinterpret_cast<const float *>(vs + 3 * TT * pitch)[8 * n + 2 * t + i];
-        int row = (rb0 + warp) * kRowBlock + 4 * g, kc = 0;
-        float acc[NT][2][4];
-        for (int step = 0; step < steps; ++step) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-            __syncwarp();  // the other lanes' copies as well; and they have read the step before, whose place is next
-            const char *from = ring + (step % kStages) * kStageBytes;
-            if (product) {
-                const int k = kc * KC + E * t;
-                const bool have = row < rows && k < rank;
-                uint32_t x[2][2][E / 2];
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const char *q = from + 16 * place(4 * g + 2 * m + h, E * t / 8) + (E * t % 8) * 2;
-                        if (E == 8) {
-                            const uint4 y = *reinterpret_cast<const uint4 *>(q);
-                            x[m][h][0] = y.x, x[m][h][1] = y.y, x[m][h][E / 2 - 2] = y.z, x[m][h][E / 2 - 1] = y.w;
-                        } else {
-                            const uint2 y = *reinterpret_cast<const uint2 *>(q);
-                            x[m][h][0] = y.x, x[m][h][1] = y.y;
-                        }
-#pragma unroll
-                        for (int i = 0; i < E / 2; ++i) x[m][h][i] = have ? x[m][h][i] : 0u;
-                    }
-                if (!kOne) v.load(vs, pitch, kc * KC, g, t);
-                v.multiply(acc, x, kOne || kc == 0);
-            }
-            if (++kc == nk) {
-                if (row < rows) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            if (put[n][i]) {
-                                float4 y = *reinterpret_cast<const float4 *>(from + 256 * E + (2 * n + i) * 512 + lane * 16);
-                                if (add[n][i]) {
-                                    y.x = fmaf(acc[n][0][i], undo[n][i], y.x);
-                                    y.y = fmaf(acc[n][0][2 + i], undo[n][i], y.y);
-                                    y.z = fmaf(acc[n][1][i], undo[n][i], y.z);
-                                    y.w = fmaf(acc[n][1][2 + i], undo[n][i], y.w);
+                                if (put[n][i]) {
+                                    float4 y = *reinterpret_cast<const float4 *>(from + 256 * E + (2 * n + i) * 512 + lane * 16);
+                                    if (add[n][i]) {
+                                        y.x = fmaf(acc[n][0][i], undo[n][i], y.x);
+                                        y.y = fmaf(acc[n][0][2 + i], undo[n][i], y.y);
+                                        y.z = fmaf(acc[n][1][i], undo[n][i], y.z);
+                                        y.w = fmaf(acc[n][1][2 + i], undo[n][i], y.w);
+                                    }
+                                    *reinterpret_cast<float4 *>(Y + static_cast<long long>(t0 + 8 * n + 2 * t + i) * ldy + row) = y;
                                 }
-                                *reinterpret_cast<float4 *>(Y + static_cast<long long>(t0 + 8 * n + 2 * t + i) * ldy + row) = y;
-                            }
+                    }
+                    kc = 0;
+                    row += kWarps * kRowBlock;
                 }
-                kc = 0;
-                row += kWarps * kRowBlock;
+                fetch(step + kStages - 1);
             }
-            fetch(step + kStages - 1);
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-    }
-    __syncthreads();
     }
     if (!waited) pdl_wait();
 }
@@ -963,32 +973,32 @@ struct Call {
     cudaStream_t s;
 };
 
-template <int MT, int NT, bool BF16, bool Q8>
+template <int MT, bool BF16, bool Q8>
 cudaError_t shrink(const Call &c, int tiles, int groups, int slices, int slice_chunks)
 {
-    auto kern = k_lora_shrink<MT, NT, BF16, Q8>;
+    constexpr int NT = 1;
+    auto kern = k_lora_shrink<MT, BF16, Q8>;
     const size_t sums = sizeof(float) * kWarps * 16 * MT * 8 * NT, rings = kWarps * shrink_stages(MT, NT, Q8) * shrink_stage(MT, NT, Q8);
     const size_t smem = sums > rings ? sums : rings;
     if (ctas_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
     return launch_pdl(kern, dim3(tiles, slices, groups), dim3(kThreads), smem, c.s, c.A, c.B, c.X, c.ldx, c.Xq, c.dx, c.V,
                       c.rank, c.K, slice_chunks);
 }
-template <int MT, int NT>
+template <int MT>
 cudaError_t shrink_typed(const Call &c, bool bf16, int tiles, int groups, int slices, int slice_chunks)
 {
     if (c.Xq)
-        return bf16 ? shrink<MT, NT, true, true>(c, tiles, groups, slices, slice_chunks)
-                    : shrink<MT, NT, false, true>(c, tiles, groups, slices, slice_chunks);
-    return bf16 ? shrink<MT, NT, true, false>(c, tiles, groups, slices, slice_chunks)
-                : shrink<MT, NT, false, false>(c, tiles, groups, slices, slice_chunks);
+        return bf16 ? shrink<MT, true, true>(c, tiles, groups, slices, slice_chunks)
+                    : shrink<MT, false, true>(c, tiles, groups, slices, slice_chunks);
+    return bf16 ? shrink<MT, true, false>(c, tiles, groups, slices, slice_chunks)
+                : shrink<MT, false, false>(c, tiles, groups, slices, slice_chunks);
 }
-template <int NT>
 cudaError_t shrink_rank(const Call &c, bool bf16, int tiles, int groups, int slices, int slice_chunks)
 {
-    if (c.rank <= 16) return shrink_typed<1, NT>(c, bf16, tiles, groups, slices, slice_chunks);
-    if (c.rank <= 32) return shrink_typed<2, NT>(c, bf16, tiles, groups, slices, slice_chunks);
-    if (c.rank <= 64) return shrink_typed<4, NT>(c, bf16, tiles, groups, slices, slice_chunks);
-    return shrink_typed<8, NT>(c, bf16, tiles, groups, slices, slice_chunks);
+    if (c.rank <= 16) return shrink_typed<1>(c, bf16, tiles, groups, slices, slice_chunks);
+    if (c.rank <= 32) return shrink_typed<2>(c, bf16, tiles, groups, slices, slice_chunks);
+    if (c.rank <= 64) return shrink_typed<4>(c, bf16, tiles, groups, slices, slice_chunks);
+    return shrink_typed<8>(c, bf16, tiles, groups, slices, slice_chunks);
 }
 
 template <int MT, int NT, bool BF16, bool Q8>
@@ -1020,10 +1030,11 @@ cudaError_t shrink_tile_rank(const Call &c, bool bf16, int *slices)
     return shrink_tile_typed<8, 2>(c, bf16, slices);
 }
 
-template <int KC, bool kOne, int NT, bool BF16>
+template <int KC, bool kOne, bool BF16>
 cudaError_t expand(const Call &c, int tiles, int groups, int slices)
 {
-    auto kern = k_lora_expand<KC, kOne, NT, BF16>;
+    constexpr int NT = 1;
+    auto kern = k_lora_expand<KC, kOne, BF16>;
     const int depth = (c.rank + KC - 1) / KC * KC;
     const size_t smem = v_bytes(depth, 8 * NT) + kWarps * kStages * expand_stage(KC, NT);
     if (ctas_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
@@ -1035,14 +1046,13 @@ cudaError_t expand(const Call &c, int tiles, int groups, int slices)
     return launch_pdl(kern, dim3(static_cast<unsigned>((total + per - 1) / per), 1, groups), dim3(kThreads), smem, c.s, c.W, c.B, c.V,
                       c.Y0, c.ldy0, c.Y, c.ldy, c.rank, c.rows, slices, per, total);
 }
-template <int NT>
 cudaError_t expand_rank(const Call &c, bool bf16, int tiles, int groups, int slices)
 {
     if (c.rank <= 16)
-        return bf16 ? expand<16, true, NT, true>(c, tiles, groups, slices) : expand<16, true, NT, false>(c, tiles, groups, slices);
+        return bf16 ? expand<16, true, true>(c, tiles, groups, slices) : expand<16, true, false>(c, tiles, groups, slices);
     if (c.rank <= 32)
-        return bf16 ? expand<32, true, NT, true>(c, tiles, groups, slices) : expand<32, true, NT, false>(c, tiles, groups, slices);
-    return bf16 ? expand<32, false, NT, true>(c, tiles, groups, slices) : expand<32, false, NT, false>(c, tiles, groups, slices);
+        return bf16 ? expand<32, true, true>(c, tiles, groups, slices) : expand<32, true, false>(c, tiles, groups, slices);
+    return bf16 ? expand<32, false, true>(c, tiles, groups, slices) : expand<32, false, false>(c, tiles, groups, slices);
 }
 
 template <int KC, bool kOne, bool BF16>
@@ -1084,8 +1094,8 @@ int run(const Call &c, int type)
     slices = decode_slices(c.K, static_cast<long long>(tiles) * groups);
     const int slice_chunks = (chunks + slices - 1) / slices;
     slices = (chunks + slice_chunks - 1) / slice_chunks;
-    cudaError_t e = shrink_rank<1>(c, bf16, tiles, groups, slices, slice_chunks);
-    if (e == cudaSuccess) e = expand_rank<1>(c, bf16, tiles, groups, slices);
+    cudaError_t e = shrink_rank(c, bf16, tiles, groups, slices, slice_chunks);
+    if (e == cudaSuccess) e = expand_rank(c, bf16, tiles, groups, slices);
     return status_from(e);
 }
 
