@@ -141,14 +141,21 @@ __device__ __forceinline__ void split(const Scale &s, float l, int &A, uint32_t 
     M = 0x80000000u + static_cast<uint32_t>(__float2int_rn(e * 2147483648.0f));
 }
 __device__ __forceinline__ u64 shifted(uint32_t M, unsigned sh) { return sh < 64 ? (static_cast<u64>(M) << 12) >> sh : 0ull; }
-// Sum of two weights for base = 0, the same operations in pairs.
-__device__ __forceinline__ u64 weights2(const Scale &s, float a, float b, int top)
+// sum += M 2^(12 - sh) cut off to a whole number, as `shifted` does: M shifted down or multiplied up, one wide
+// multiply-add.
+__device__ __forceinline__ void add_shifted(u64 &sum, uint32_t M, int sh)
+{
+    const int down = max(sh - 12, 0);
+    const uint32_t up = 1u << (12 - sh + down);  // 2^(12 - sh), or 1
+    sum += static_cast<u64>(__funnelshift_rc(M, 0u, down)) * up;
+}
+// Two weights for base = 0, the same operations in pairs.
+__device__ __forceinline__ void add_weights(u64 &sum, const Scale &s, float a, float b, int top)
 {
     const float2 ch = make_float2(s.ch, s.ch), cl = make_float2(s.cl, s.cl), l = make_float2(a, b),
                  round = make_float2(kRound, kRound);
     float2 r = __fmul2_rn(l, ch);
     r = __fadd2_rn(make_float2(fmaxf(r.x, kFarDown), fmaxf(r.y, kFarDown)), round);
-    const int A0 = __float_as_int(r.x) - __float_as_int(kRound), A1 = __float_as_int(r.y) - __float_as_int(kRound);
     const float2 n = __ffma2_rn(r, make_float2(-1.f, -1.f), round);
     const float2 f = __ffma2_rn(l, cl, __ffma2_rn(l, ch, n));
     float2 p = __ffma2_rn(make_float2(kP5, kP5), f, make_float2(kP4, kP4));
@@ -158,8 +165,9 @@ __device__ __forceinline__ u64 weights2(const Scale &s, float a, float b, int to
     p = __ffma2_rn(p, f, make_float2(kP0Low, kP0Low));
     const float2 e = __ffma2_rn(f, make_float2(kP0, kP0), __fmul2_rn(f, p));
     const float2 x = __fmul2_rn(e, make_float2(2147483648.0f, 2147483648.0f));
-    return shifted(0x80000000u + static_cast<uint32_t>(__float2int_rn(x.x)), static_cast<unsigned>(top - A0)) +
-           shifted(0x80000000u + static_cast<uint32_t>(__float2int_rn(x.y)), static_cast<unsigned>(top - A1));
+    const int from = top + __float_as_int(kRound);  // less the bits of r: the weight's distance below `top`
+    add_shifted(sum, 0x80000000u + static_cast<uint32_t>(__float2int_rn(x.x)), from - __float_as_int(r.x));
+    add_shifted(sum, 0x80000000u + static_cast<uint32_t>(__float2int_rn(x.y)), from - __float_as_int(r.y));
 }
 // Weight in units of 2^(top - 43).
 __device__ __forceinline__ u64 weight(const Scale &s, float l, int top)
@@ -245,8 +253,8 @@ struct Reader {
     {
         return __ldg(reinterpret_cast<const uint4 *>(base + static_cast<long long>(unit) * 16));
     }
-    // Candidates as they are, NaN and what lies outside as -infinity.
-    __device__ __forceinline__ void values(uint4 w, float (&v)[kVec]) const
+    // The numbers as they are.
+    __device__ __forceinline__ void raw(uint4 w, float (&v)[kVec]) const
     {
         const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -259,6 +267,11 @@ struct Reader {
                 v[(2 * i + 1) % kVec] = f.y;
             }
         }
+    }
+    // Candidates as they are, NaN and what lies outside as -infinity.
+    __device__ __forceinline__ void values(uint4 w, float (&v)[kVec]) const
+    {
+        raw(w, v);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) v[i] = fmaxf(v[i], -INFINITY);
     }
@@ -281,10 +294,11 @@ struct Reader {
             }
         }
     }
+    // NaN is left in whole units.
     __device__ __forceinline__ void load(int unit, float (&v)[kVec]) const
     {
         if (unit < units && inside(unit))
-            values(word(unit), v);
+            raw(word(unit), v);
         else
             edge(unit, v);
     }
@@ -704,26 +718,35 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     for (int j = 0; j < kUnits; ++j) in.load(u0 + j * THREADS, v[j]);
     const float T = temperature(S, row);
     const int k = top_k(S, row, R.vocab);
-    float hi = -INFINITY, lo = INFINITY;
+    // per unit the largest; of all the largest and the smallest; and whether all are finite (0 v is not a NaN)
+    float most[kUnits], hi = -INFINITY, lo = INFINITY;
+    float2 zero = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j)
+    for (int j = 0; j < kUnits; ++j) {
+        most[j] = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-            hi = fmaxf(hi, v[j][i]);
+            most[j] = fmaxf(most[j], v[j][i]);
             lo = fminf(lo, v[j][i]);
         }
+#pragma unroll
+        for (int i = 0; i < kVec; i += 2) zero = __ffma2_rn(make_float2(v[j][i], v[j][i + 1]), make_float2(0.f, 0.f), zero);
+        hi = fmaxf(hi, most[j]);
+    }
     int cands = EPT;
-    if (lo == -INFINITY) {  // masked tokens, or the row's ends
+    if (!(zero.x + zero.y == 0.f)) {  // masked tokens, or the row's ends
         lo = INFINITY;
         cands = 0;
 #pragma unroll
         for (int j = 0; j < kUnits; ++j)
 #pragma unroll
-            for (int i = 0; i < kVec; ++i)
+            for (int i = 0; i < kVec; ++i) {
+                v[j][i] = fmaxf(v[j][i], -INFINITY);  // a NaN is no candidate
                 if (v[j][i] > -INFINITY) {
                     lo = fminf(lo, v[j][i]);
                     ++cands;
                 }
+            }
     }
     const uint32_t mine = key_of(hi);
     {
@@ -764,7 +787,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 #pragma unroll
             for (int j = 0; j < kUnits; ++j)
 #pragma unroll
-                for (int i = 0; i < kVec; i += 2) sum += weights2(sc, v[j][i], v[j][i + 1], h.exp);
+                for (int i = 0; i < kVec; i += 2) add_weights(sum, sc, v[j][i], v[j][i + 1], h.exp);
             sum = warp_sum(sum);
             if (lane == 0) s_sum[warp] = sum;
         }
@@ -797,13 +820,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
             if (mine < least) return;
             const float from = value_of(least);
 #pragma unroll
-            for (int j = 0; j < kUnits; ++j)
+            for (int j = 0; j < kUnits; ++j) {
+                if (most[j] < from) continue;
 #pragma unroll
                 for (int i = 0; i < kVec; ++i)
                     if (v[j][i] >= from) {
                         const int at = atomicAdd(&s_count, 1);
                         if (at < R.cap) list[at] = rank_of(key_of(v[j][i]), in.index(u0 + j * THREADS, i));
                     }
+            }
         };
         put(a);
         __syncthreads();
