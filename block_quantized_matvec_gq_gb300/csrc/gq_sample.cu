@@ -16,19 +16,23 @@
 //          The list's threshold is the want-th largest of the threads' own
 //          maxima, found by bisection with a vote of the CTA per step: at least
 //          `want` elements reach it, and few more.
-//   pick   one CTA per row (where a row is one slice, the same CTA): the lists above the slices' highest threshold hold every element above
-//          it, some hundreds.  They are sorted, and where the limits and the draw
-//          fall among them, which they do for a language model's usual rows, the
-//          row is done.
-//   deep   the other rows (flat ones, a large top_k), a cluster of CTAs each: a
+//   pick   one CTA per row (where a row is one slice, the same CTA): the lists
+//          above the slices' highest threshold hold every element above it, some
+//          hundreds.  They are sorted, and where the limits and the draw fall
+//          among them, which they do for a language model's usual rows, the row
+//          is done.
+//   deep   the other rows (flat ones, a large top_k), a cluster of 16 CTAs each: a
 //          histogram of the row over 2048 equal steps of the exponent, counts and
 //          exact weights, gives the step in which X is reached; the step's
 //          elements are collected and sorted.  A step with too many elements is
 //          divided further, by the bits of (logit, index), which no two elements
 //          share.
 //
-// What bounds it: the one pass over the logits, and for small batches the
-// latency of the kernels.
+// What bounds it.  160 rows of 262144 f32 logits (168 MB), settings of all kinds,
+// 109 us: the scan 55 (issue; 20 instructions an element where weights are summed),
+// the pick some 13, the search of the six rows that need it some 40: dependent
+// rounds over little data, barriers of the cluster, and fetching code that runs
+// once (unrolled passes took 140 us in all instead of 124 then).
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
@@ -1244,7 +1248,8 @@ cudaError_t launch(Rows R, const Settings &S, const Plan &p, int n_rows, int32_t
     else
         e = one ? scan(k_sample_scan<TYPE, 32, kScanThreads, true>, kScanThreads) : scan(k_sample_scan<TYPE, 32, kScanThreads, false>, kScanThreads);
     if (e == cudaSuccess && !one) e = launch_pdl(k_sample_pick, dim3(n_rows), dim3(kPickThreads), 0, s, R, S, token, prob, status);
-    if (e == cudaSuccess)
+    // a row whose every candidate is in the list is always settled
+    if (e == cudaSuccess && !(one && R.vocab <= R.cap))
         e = launch_pdl(deep, dim3(kDeepCtas, n_rows < kDeepClusters ? n_rows : kDeepClusters), dim3(kDeepThreads), sizeof(DeepShared), s, R,
                        S, n_rows, token, prob);
     return e;
