@@ -652,36 +652,42 @@ __global__ void __launch_bounds__(kThreads, 2)
             // the weights are copied as they lie (a rank of 16 or 32: 1 or 2 KB without a gap; copied by the lanes that read
             // them they cost three times their bytes), the 16-byte pieces placed so that no two lanes meet on a bank.
             const int nk = depth / KC, blocks = rb0 + warp < rb1 ? (rb1 - rb0 - warp + kWarps - 1) / kWarps : 0, steps = blocks * nk;
-            int fetch_row = (rb0 + warp) * kRowBlock + 4 * g, fetch_k = 0;
-            auto fetch = [&](int step) {
-                if (step < steps) {
-                    char *to = ring + (step % kStages) * kStageBytes;
-                    if (product) {
+            const int row0 = (rb0 + warp) * kRowBlock;
+            int fetched = 0, fetch_row = row0, fetch_k = 0;
+            char *to = ring;
+            const uint16_t *from_w = w + static_cast<long long>(row0 + lane / kRowPieces) * rank + lane % kRowPieces * 8;
+            const float *from_y = Y0 + static_cast<long long>(t0 + 2 * t) * ldy0 + row0 + 4 * g;
+            auto fetch = [&] {
+                if (fetched < steps) {
+                    if (product && fetch_k + lane % kRowPieces * 8 < rank) {
 #pragma unroll
                         for (int i = 0; i < kPieces; ++i) {
-                            const int r = (lane + 32 * i) / kRowPieces, c = (lane + 32 * i) % kRowPieces;
-                            const int at = fetch_row - 4 * g + r, k = fetch_k * KC + 8 * c;
-                            if (at < rows && k < rank) cp_async<16>(to + 16 * place(r, c), w + static_cast<long long>(at) * rank + k);
+                            constexpr int kRows = 32 / kRowPieces;  // rows that the warp copies at once
+                            if (fetch_row + lane / kRowPieces + i * kRows < rows)
+                                cp_async<16>(to + 16 * place(lane / kRowPieces + i * kRows, lane % kRowPieces),
+                                             from_w + fetch_k + static_cast<long long>(i * kRows) * rank);
                         }
                     }
-                    if (++fetch_k == nk) {
-                        if (fetch_row < rows) {
+                    if ((fetch_k += KC) == depth) {
+                        if (fetch_row + 4 * g < rows) {
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
 #pragma unroll
                                 for (int i = 0; i < 2; ++i)
-                                    if (put[n][i])
-                                        cp_async<16>(to + 256 * E + (2 * n + i) * 512 + lane * 16,
-                                                     Y0 + static_cast<long long>(t0 + 8 * n + 2 * t + i) * ldy0 + fetch_row);
+                                    if (put[n][i]) cp_async<16>(to + 256 * E + (2 * n + i) * 512 + lane * 16, from_y + (8 * n + i) * ldy0);
                         }
                         fetch_k = 0;
                         fetch_row += kWarps * kRowBlock;
+                        from_w += static_cast<long long>(kWarps * kRowBlock) * rank;
+                        from_y += kWarps * kRowBlock;
                     }
+                    ++fetched;
+                    to = to == ring + (kStages - 1) * kStageBytes ? ring : to + kStageBytes;
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
 #pragma unroll
-            for (int i = 0; i < kStages - 1; ++i) fetch(i);
+            for (int i = 0; i < kStages - 1; ++i) fetch();
             // v is complete after the wait; the copies above were let go before
             if (!waited) pdl_wait();
             waited = true;
@@ -695,15 +701,15 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) undo[n][i] = BF16 ? 1.f : reinterpret_cast<const float *>(vs + 3 * TT * pitch)[8 * n + 2 * t + i];
-            int row = (rb0 + warp) * kRowBlock + 4 * g, kc = 0;
+            int row = row0 + 4 * g, k0 = 0;
+            const char *from = ring;
+            float *y_to = Y + static_cast<long long>(t0 + 2 * t) * ldy + row;
             float acc[NT][2][4];
+#pragma unroll 1
             for (int step = 0; step < steps; ++step) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
                 __syncwarp();  // the other lanes' copies as well; and they have read the step before, whose place is next
-                const char *from = ring + (step % kStages) * kStageBytes;
                 if (product) {
-                    const int k = kc * KC + E * t;
-                    const bool have = row < rows && k < rank;
                     uint32_t x[2][2][E / 2];
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
@@ -717,13 +723,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                                 const uint2 y = *reinterpret_cast<const uint2 *>(q);
                                 x[m][h][0] = y.x, x[m][h][1] = y.y;
                             }
-#pragma unroll
-                            for (int i = 0; i < E / 2; ++i) x[m][h][i] = have ? x[m][h][i] : 0u;
                         }
-                    if (!kOne) v.load(vs, pitch, kc * KC, g, t);
-                    v.multiply(acc, x, kOne || kc == 0);
+                    if (rank < depth && k0 + E * t >= rank) {  // what lies there was not copied
+#pragma unroll
+                        for (int e = 0; e < E / 2; ++e) x[0][0][e] = x[0][1][e] = x[1][0][e] = x[1][1][e] = 0u;
+                    }
+                    if (!kOne) v.load(vs, pitch, k0, g, t);
+                    v.multiply(acc, x, kOne || k0 == 0);
                 }
-                if (++kc == nk) {
+                if ((k0 += KC) == depth) {
                     if (row < rows) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
@@ -737,13 +745,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                                         y.z = fmaf(acc[n][1][i], undo[n][i], y.z);
                                         y.w = fmaf(acc[n][1][2 + i], undo[n][i], y.w);
                                     }
-                                    *reinterpret_cast<float4 *>(Y + static_cast<long long>(t0 + 8 * n + 2 * t + i) * ldy + row) = y;
+                                    *reinterpret_cast<float4 *>(y_to + (8 * n + i) * ldy) = y;
                                 }
                     }
-                    kc = 0;
+                    k0 = 0;
                     row += kWarps * kRowBlock;
+                    y_to += kWarps * kRowBlock;
                 }
-                fetch(step + kStages - 1);
+                from = from == ring + (kStages - 1) * kStageBytes ? ring : from + kStageBytes;
+                fetch();
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             __syncthreads();
