@@ -117,15 +117,13 @@ def status_string(status: int) -> str:
 
 def _ptr(t):
     """Device address of a CUDA tensor (or an int address / None)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError("libgq takes CUDA tensors (device memory)")
-    if not t.is_contiguous():
-        raise ValueError("libgq takes contiguous tensors")
-    return t.data_ptr()
+    raise ValueError("libgq takes contiguous tensors")
 
 
 def _rows(t):
