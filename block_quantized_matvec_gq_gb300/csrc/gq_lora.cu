@@ -30,7 +30,7 @@
 // 4.8 TB/s; without the stores 111, without the products 148: the memory.  A plain
 // copy in the same order takes 114 for Y alone.  1531 tokens of rank 64 (112 MB)
 // take 65, where the products and the two kernels' beginnings show; 64 tokens of
-// 48 adapters of rank 32 (84 MB) 27.7.  One token: 4.4, the latency of two kernels.
+// 48 adapters of rank 32 (84 MB) 27.1.  One token: 4.5, the latency of two kernels.
 #include "gq_host.h"
 #include "gq_internal.cuh"
 #include "gq_kv.cuh"
