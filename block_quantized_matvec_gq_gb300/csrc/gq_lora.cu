@@ -12,7 +12,7 @@
 //     matrix instruction, the groups in different CTAs; every lane copies the
 //     pieces of weights and activations that it multiplies (cp.async), so that no
 //     thread waits for another.
-//   prompts, nearly always one group a tile: tiles of 16 or 32 tokens; `shrink`
+//   prompts, nearly always one group a tile: tiles of 32 and 16 tokens; `shrink`
 //     shares a step's copies between its warps, `expand` moves Y by bulk copies.
 //
 // The products run on mma.sync.  Weights are operands as they are (16 bits).  So
@@ -367,34 +367,41 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ---------------------------------------------------------------- the same for prompts
-// CTA: a tile of 8 NT tokens and one slice of K, in steps of 256 elements: all
-// threads copy a step's weights and activations, and eight warps take one
-// 32-element chunk each.  Rows are padded so that the operands' loads meet no bank
-// twice.  (Bulk copies, one per row, took 58 us where this takes 25 for 4096
-// tokens of rank 16: they cost some 60 cycles each, and the rows are 256 and 512
-// bytes.)
-constexpr int kStep = 256, kStepA = 2 * kStep + 64;
-__host__ __device__ constexpr int step_x(bool q8) { return q8 ? kStep + 32 : 4 * kStep + 16; }
-__host__ __device__ constexpr int step_bytes(int rank, int tokens, bool q8) { return rank * kStepA + tokens * (step_x(q8) + (q8 ? 48 : 0)); }
-inline int step_stages(int rank, int tokens, bool q8)
+// CTA: a tile of 32 tokens and one slice of K, in steps: all threads copy a step's
+// weights and activations, and each warp takes one 32-element chunk of 16 MT ranks.
+// Above rank 32 the warps divide the ranks into MH parts, so that a step is 128 or
+// 64 elements instead of 256 and more steps are on their way.  Rows are padded so
+// that the operands' loads meet no bank twice.  (Bulk copies, one per row, took 58 us where this takes 25 for 4096 tokens of rank
+// 16: they cost some 60 cycles each, and the rows are 256 and 512 bytes.)
+constexpr int kTileTokens = 32;
+__host__ __device__ constexpr int step_of(int mh) { return kWarps / mh * 32; }
+__host__ __device__ constexpr int step_a(int mh) { return 2 * step_of(mh) + 64; }
+__host__ __device__ constexpr int step_x(int mh, bool q8) { return q8 ? step_of(mh) + 32 : 4 * step_of(mh) + 16; }
+__host__ __device__ constexpr int step_d(int mh) { return 4 * (kWarps / mh) + 4; }
+__host__ __device__ constexpr int step_bytes(int rank, int mh, bool q8)
 {
-    const int n = (104 << 10) / step_bytes(rank, tokens, q8);
+    return rank * step_a(mh) + kTileTokens * (step_x(mh, q8) + (q8 ? step_d(mh) : 0));
+}
+inline int step_stages(int rank, int mh, bool q8)
+{
+    const int n = (104 << 10) / step_bytes(rank, mh, q8);
     return n > 4 ? 4 : (n < 2 ? 2 : n);
 }
 
-template <int MT, int NT, bool BF16, bool Q8>
+template <int MT, int MH, bool BF16, bool Q8>
 __global__ void __launch_bounds__(kThreads, 2)
     k_lora_shrink_tile(const uint16_t *__restrict__ A, Batch B, const float *__restrict__ X, long long ldx,
                        const int8_t *__restrict__ Xq, const float *__restrict__ dx, float *__restrict__ V, int rank, int K,
                        int slice_steps, int stages)
 {
-    extern __shared__ __align__(16) char raw[];  // stages; after the last step the warps' sums [kWarps][8 NT][16 MT]
+    extern __shared__ __align__(16) char raw[];  // stages; after the last step the warps' sums [kWarps][tokens][16 MT]
     __shared__ Tile tile;
-    constexpr int TT = 8 * NT, kOut = 16 * MT * TT, kPieces = kStep * (Q8 ? 1 : 4) / 16;  // 16-byte pieces of a token's step
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    constexpr int TT = kTileTokens, NT = TT / 8, kOut = 16 * MT * TT, kChunks = kWarps / MH, kStep = 32 * kChunks;
+    constexpr int kPieces = kStep * (Q8 ? 1 : 4) / 16, kPiecesA = 2 * kStep / 16;  // 16-byte pieces of a token's step, of a rank's
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3, chunk = warp % kChunks, m0 = warp / kChunks * MT;
     const int t0 = blockIdx.x * TT, chunks = K / 32, steps = (K + kStep - 1) / kStep;
     const int s0 = blockIdx.y * slice_steps, n = min(slice_steps, steps - s0);
-    const int stage_bytes = step_bytes(rank, TT, Q8), off_x = rank * kStepA, off_d = off_x + TT * step_x(Q8);
+    const int stage_bytes = step_bytes(rank, MH, Q8), off_x = rank * step_a(MH), off_d = off_x + TT * step_x(MH, Q8);
     pdl_wait();
     // only now: what the next kernel reads before its own wait is complete then
     pdl_launch_dependents();
@@ -406,11 +413,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const int k0 = (s0 + i) * kStep, count = min(kStep, K - k0);
                 char *to = raw + slot * stage_bytes;
                 {
-                    const int c = tid & 31;
-                    const uint16_t *from = a + static_cast<long long>(warp) * K + k0 + 8 * c;
+                    constexpr int kRanks = kThreads / kPiecesA;  // ranks copied at once
+                    const int c = tid % kPiecesA;
+                    const uint16_t *from = a + static_cast<long long>(tid / kPiecesA) * K + k0 + 8 * c;
                     if (8 * c < count)
-                        for (int r = warp; r < rank; r += kWarps, from += static_cast<long long>(kWarps) * K)
-                            cp_async<16>(to + r * kStepA + 16 * c, from);
+                        for (int r = tid / kPiecesA; r < rank; r += kRanks, from += static_cast<long long>(kRanks) * K)
+                            cp_async<16>(to + r * step_a(MH) + 16 * c, from);
                 }
                 constexpr int kRows = kThreads / kPieces;  // tokens copied at once
                 const int c = tid % kPieces;
@@ -418,17 +426,17 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                     for (int r0 = 0; r0 < TT; r0 += kRows) {
                         const int r = r0 + tid / kPieces;
-                        if (tile.group[r] == j) {
+                        if (r < TT && tile.group[r] == j) {
                             const void *from = Q8 ? static_cast<const void *>(Xq + static_cast<long long>(t0 + r) * K + k0 + 16 * c)
                                                   : static_cast<const void *>(X + (t0 + r) * ldx + k0 + 4 * c);
-                            cp_async<16>(to + off_x + r * step_x(Q8) + 16 * c, from);
+                            cp_async<16>(to + off_x + r * step_x(MH, Q8) + 16 * c, from);
                         }
                     }
                 }
                 if (Q8) {
-                    const int r = tid >> 3, x = tid & 7, at = k0 / 32 + x;
+                    const int r = tid / kChunks, x = tid % kChunks, at = k0 / 32 + x;
                     if (r < TT && at < chunks && tile.group[r] == j)
-                        cp_async<4>(to + off_d + r * 36 + 4 * x, dx + static_cast<long long>(t0 + r) * chunks + at);
+                        cp_async<4>(to + off_d + r * step_d(MH) + 4 * x, dx + static_cast<long long>(t0 + r) * chunks + at);
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -459,18 +467,18 @@ __global__ void __launch_bounds__(kThreads, 2)
                 asm volatile("cp.async.wait_group 2;" ::: "memory");
             __syncthreads();
             fetch(i + stages - 1, next);
-            if ((s0 + i) * (kStep / 32) + warp < chunks) {
-                const char *from = raw + slot * stage_bytes + warp * 64 + t * 16;
-                const char *xs = raw + slot * stage_bytes + off_x + (warp * 32 + t * 8) * (Q8 ? 1 : 4);
-                const char *ds = raw + slot * stage_bytes + off_d + warp * 4;
+            if ((s0 + i) * kChunks + chunk < chunks) {
+                const char *from = raw + slot * stage_bytes + chunk * 64 + t * 16;
+                const char *xs = raw + slot * stage_bytes + off_x + (chunk * 32 + t * 8) * (Q8 ? 1 : 4);
+                const char *ds = raw + slot * stage_bytes + off_d + chunk * 4;
                 multiply_chunk<MT, NT, BF16, Q8>(
                     acc,
                     [&](int m, int h) {
-                        const int r = 16 * m + 8 * h + g;
-                        return r < rank ? *reinterpret_cast<const uint4 *>(from + r * kStepA) : make_uint4(0, 0, 0, 0);
+                        const int r = 16 * (m0 + m) + 8 * h + g;
+                        return r < rank ? *reinterpret_cast<const uint4 *>(from + r * step_a(MH)) : make_uint4(0, 0, 0, 0);
                     },
                     [&](int q, float(&v)[8]) {
-                        const char *p = xs + (8 * q + g) * step_x(Q8);
+                        const char *p = xs + (8 * q + g) * step_x(MH, Q8);
                         const bool have = in >> q & 1u;
                         if (Q8) {
                             const uint2 c = *reinterpret_cast<const uint2 *>(p);
@@ -482,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                             for (int e = 0; e < 8; ++e) v[e] = have ? y[e] : 0.f;
                         }
                     },
-                    [&](int q, int i) { return col >> (2 * q + i) & 1u ? *reinterpret_cast<const float *>(ds + (8 * q + 2 * t + i) * 36) : 0.f; });
+                    [&](int q, int i) { return col >> (2 * q + i) & 1u ? *reinterpret_cast<const float *>(ds + (8 * q + 2 * t + i) * step_d(MH)) : 0.f; });
             }
             if (++slot == stages) slot = 0;
             if (++next == stages) next = 0;
@@ -500,12 +508,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         __syncthreads();
         const float *sums = reinterpret_cast<const float *>(raw);
         float *out = V + static_cast<long long>(blockIdx.y) * B.M * rank;
-        for (int i = tid; i < kOut; i += kThreads) {
-            const int tok = i / (16 * MT), r = i - tok * 16 * MT;
+        for (int i = tid; i < MH * kOut; i += kThreads) {
+            const int tok = i / (16 * MT * MH), r = i % (16 * MT * MH);
             if (r < rank && tile.group[tok] == j) {
+                const float *part = sums + r / (16 * MT) * kChunks * kOut + tok * 16 * MT + r % (16 * MT);
                 float v = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) v += sums[w * kOut + i];
+                for (int w = 0; w < kChunks; ++w) v += part[w * kOut];
                 out[static_cast<long long>(t0 + tok) * rank + r] = v;
             }
         }
@@ -520,14 +529,16 @@ __global__ void __launch_bounds__(kThreads, 2)
 __host__ __device__ constexpr int v_pitch(int depth) { return 2 * depth + (2 * depth % 128 == 0 ? 64 : 0); }  // (banks)
 __host__ __device__ constexpr int v_bytes(int depth, int tokens) { return 3 * tokens * v_pitch(depth) + 4 * tokens; }
 
-// A warp takes a token, a lane four of its numbers; slices are added up.  `member`
-// says which tokens have a v.
+// A lane takes four numbers of a token, a warp as many tokens as that makes; slices
+// are added up.  `member` says which tokens have a v.
 template <int TOKENS, bool BF16, class Member>
 __device__ __forceinline__ void stage_v(char *vs, const float *__restrict__ V, long long t0, int M, int rank, int depth, int slices,
                                         float scale, Member &&member)
 {
-    const int lane = threadIdx.x & 31, pitch = v_pitch(depth);
-    for (int tok = threadIdx.x >> 5; tok < TOKENS; tok += kWarps) {
+    const int pitch = v_pitch(depth), shift = depth > 64 ? 5 : depth > 32 ? 4 : depth > 16 ? 3 : 2;  // lanes a token
+    const int lane = threadIdx.x & 31 & ((1 << shift) - 1);
+#pragma unroll 1
+    for (int tok = threadIdx.x >> shift; tok < TOKENS; tok += kThreads >> shift) {
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
         if (4 * lane < rank && member(tok)) {
             const float *p = V + (t0 + tok) * rank + 4 * lane;
@@ -540,7 +551,9 @@ __device__ __forceinline__ void stage_v(char *vs, const float *__restrict__ V, l
         float y[4] = {sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale};
         if (!BF16) {
             float most = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
-            most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+            uint32_t bits = __float_as_uint(most);
+            for (int o = 1 << shift >> 1; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+            most = __uint_as_float(bits);
             const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;  // 128: not finite, and so v stays
             const int k = e == 128 ? 0 : min(13 - e, 126);
 #pragma unroll
@@ -952,12 +965,12 @@ __global__ void __launch_bounds__(kBulkThreads, 2)
 
 // ---------------------------------------------------------------- host
 // Slices of K: some three CTAs per SM for a decode batch's tiles of 8 tokens; for a
-// prompt's, of 16 or 32, as many CTAs as run at once, at most two per SM.  A slice
+// prompt's, of 32, as many CTAs as run at once, at most two per SM.  A slice
 // has 256 elements or more, a chunk for every warp.
 constexpr int kWantCtas = 456, kWantTiles = 304;
 int bounded_slices(long long n, int K)
 {
-    const int by_k = (K + kStep - 1) / kStep;
+    const int by_k = (K + 255) / 256;
     return n < 1 ? 1 : (n < by_k ? static_cast<int>(n) : by_k);
 }
 int decode_slices(int K, long long tiles) { return bounded_slices((kWantCtas + tiles - 1) / tiles, K); }
@@ -1011,12 +1024,13 @@ cudaError_t shrink_rank(const Call &c, bool bf16, int tiles, int groups, int sli
     return shrink_typed<8>(c, bf16, tiles, groups, slices, slice_chunks);
 }
 
-template <int MT, int NT, bool BF16, bool Q8>
+template <int MT, int MH, bool BF16, bool Q8>
 cudaError_t shrink_tile(const Call &c, int *slices)
 {
-    auto kern = k_lora_shrink_tile<MT, NT, BF16, Q8>;
-    const int tiles = (c.B.M + 8 * NT - 1) / (8 * NT), steps = (c.K + kStep - 1) / kStep, stages = step_stages(c.rank, 8 * NT, Q8);
-    const size_t rings = static_cast<size_t>(stages) * step_bytes(c.rank, 8 * NT, Q8), sums = sizeof(float) * kWarps * 16 * MT * 8 * NT;
+    auto kern = k_lora_shrink_tile<MT, MH, BF16, Q8>;
+    const int tiles = (c.B.M + kTileTokens - 1) / kTileTokens, steps = (c.K + step_of(MH) - 1) / step_of(MH);
+    const int stages = step_stages(c.rank, MH, Q8);
+    const size_t rings = static_cast<size_t>(stages) * step_bytes(c.rank, MH, Q8), sums = sizeof(float) * kWarps * 16 * MT * kTileTokens;
     const size_t smem = rings > sums ? rings : sums;
     const int per_sm = ctas_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem);
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
@@ -1026,18 +1040,18 @@ cudaError_t shrink_tile(const Call &c, int *slices)
     return launch_pdl(kern, dim3(tiles, *slices), dim3(kThreads), smem, c.s, c.A, c.B, c.X, c.ldx, c.Xq, c.dx, c.V, c.rank, c.K,
                       slice_steps, stages);
 }
-template <int MT, int NT>
+template <int MT, int MH>
 cudaError_t shrink_tile_typed(const Call &c, bool bf16, int *slices)
 {
-    if (c.Xq) return bf16 ? shrink_tile<MT, NT, true, true>(c, slices) : shrink_tile<MT, NT, false, true>(c, slices);
-    return bf16 ? shrink_tile<MT, NT, true, false>(c, slices) : shrink_tile<MT, NT, false, false>(c, slices);
+    if (c.Xq) return bf16 ? shrink_tile<MT, MH, true, true>(c, slices) : shrink_tile<MT, MH, false, true>(c, slices);
+    return bf16 ? shrink_tile<MT, MH, true, false>(c, slices) : shrink_tile<MT, MH, false, false>(c, slices);
 }
 cudaError_t shrink_tile_rank(const Call &c, bool bf16, int *slices)
 {
-    if (c.rank <= 16) return shrink_tile_typed<1, 4>(c, bf16, slices);
-    if (c.rank <= 32) return shrink_tile_typed<2, 4>(c, bf16, slices);
-    if (c.rank <= 64) return shrink_tile_typed<4, 2>(c, bf16, slices);
-    return shrink_tile_typed<8, 2>(c, bf16, slices);
+    if (c.rank <= 16) return shrink_tile_typed<1, 1>(c, bf16, slices);
+    if (c.rank <= 32) return shrink_tile_typed<2, 1>(c, bf16, slices);
+    if (c.rank <= 64) return shrink_tile_typed<2, 2>(c, bf16, slices);
+    return shrink_tile_typed<2, 4>(c, bf16, slices);
 }
 
 template <int KC, bool kOne, bool BF16>
