@@ -3,17 +3,16 @@
 //   v = A_a x (rank numbers a token), then Y = Y0 + scale_a B_a v.
 //
 // Two kernels: `shrink` writes v to the workspace, `expand` adds.  Both work on
-// tiles of neighbouring tokens.  A tile's distinct adapters (its groups) are found
-// with one warp vote; each is multiplied with the whole tile and kept for its own
-// tokens, so no sorting of the batch precedes them, and an adapter's weights touch
-// only its own tokens' results.
+// neighbouring tokens; an adapter's weights touch only its own tokens' results.
 //
 //   decode batches, whose neighbours differ: tiles of 8 tokens, the width of the
-//     matrix instruction, the groups in different CTAs; every lane copies the
-//     pieces of weights and activations that it multiplies (cp.async), so that no
-//     thread waits for another.
-//   prompts, nearly always one group a tile: tiles of 32 and 16 tokens; `shrink`
-//     shares a step's copies between its warps, `expand` moves Y by bulk copies.
+//     matrix instruction.  A tile's distinct adapters (its groups) are found with
+//     one warp vote, each multiplied with the whole tile in a CTA of its own and
+//     kept for its own tokens; every lane copies the pieces of weights and
+//     activations that it multiplies (cp.async), so that no thread waits for another.
+//   prompts: units of up to 32 and 16 tokens of one adapter, found by a kernel in
+//     front; `shrink` shares a step's copies between its warps, `expand` moves Y by
+//     bulk copies.
 //
 // The products run on mma.sync.  Weights are operands as they are (16 bits).  So
 // are Q8_0 codes, whose scale is applied to each 32-block's sum; f32 numbers are
@@ -26,11 +25,11 @@
 // tcgen05 is not used: the contraction is 8 to 128 deep, so the work is the
 // bytes of Y (and, for few tokens, of the adapters), not the products.
 //
-// What bounds them: 4096 tokens of rank 16 beside 21504 rows (732 MB) take 153 us,
-// 4.8 TB/s; without the stores 111, without the products 148: the memory.  A plain
-// copy in the same order takes 114 for Y alone.  1531 tokens of rank 64 (112 MB)
-// take 65, where the products and the two kernels' beginnings show; 64 tokens of
-// 48 adapters of rank 32 (84 MB) 27.1.  One token: 4.5, the latency of two kernels.
+// What bounds them: 4096 tokens of rank 16 beside 21504 rows (732 MB) take 132 us,
+// 5.5 TB/s: the memory (a plain copy in the same order takes 114 for Y alone).  1531
+// tokens of rank 64 (112 MB) take 47, of which finding the units and shrink are the
+// first 20; 64 tokens of 48 adapters of rank 32 (84 MB) 26.4.  One token: 4.4, the
+// latency of two kernels.
 #include "gq_host.h"
 #include "gq_internal.cuh"
 #include "gq_kv.cuh"
@@ -367,7 +366,94 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ---------------------------------------------------------------- the same for prompts
-// CTA: a tile of 32 tokens and one slice of K, in steps: all threads copy a step's
+// Units: neighbouring tokens of one adapter (or of none), at most 32 or 16.  A tile
+// at fixed places would hold two requests' ends here and there, and its CTA would
+// take twice as long as the others and keep the call waiting (1531 tokens of seven
+// prompts: 60 us, 47 with units and the kernel that finds them; 4096 of four
+// prompts: 152 and 132).  [0] is their number, then first tokens and adapters,
+// behind the last M.
+constexpr int kUnitThreads = 1024, kUnitTokens = 4;  // tokens of a thread in a round
+__host__ __device__ constexpr long long unit_words(long long M) { return M + 2; }
+__device__ __forceinline__ int adapter_of(const Batch &B, int t)
+{
+    const int b = __ldg(B.sequence + t);
+    if (b < 0) return -1;
+    const int a = b < B.n_seq ? __ldg(B.adapter + b) : B.n_adapters;
+    if (a >= B.n_adapters) {
+        if (B.status) atomicExch(B.status, GQ_ERR_SHAPE);
+        return -1;
+    }
+    return a < 0 ? -1 : a;
+}
+__global__ void __launch_bounds__(kUnitThreads) k_lora_units(Batch B, int2 *__restrict__ of32, int2 *__restrict__ of16)
+{
+    __shared__ int starts[2][kUnitThreads / 32];
+    __shared__ unsigned counts[2][kUnitThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int n32 = 0, n16 = 0, start = 0;  // units so far, and where the last run began
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int t0 = 0, round = 0; t0 < B.M; t0 += kUnitThreads * kUnitTokens, round ^= 1) {
+        const int t = t0 + tid * kUnitTokens;
+        int a[kUnitTokens + 1];  // and the token in front
+#pragma unroll
+        for (int i = 0; i <= kUnitTokens; ++i) a[i] = t + i - 1 >= 0 && t + i - 1 < B.M ? adapter_of(B, t + i - 1) : -2;
+        // the run's first token: the greatest at or in front of the thread's
+        int from[kUnitTokens], mine = -1;
+#pragma unroll
+        for (int i = 0; i < kUnitTokens; ++i) from[i] = mine = a[i + 1] != a[i] ? t + i : mine;
+        int before = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before = max(before, up);
+        }
+        if (lane == 31) starts[round][warp] = before;
+        before = __shfl_up_sync(0xffffffffu, before, 1);
+        if (lane == 0) before = -1;
+        __syncthreads();
+        const int others = starts[round][lane];
+        before = max(max(before, start), __reduce_max_sync(0xffffffffu, lane < warp ? others : -1));
+        start = max(start, __reduce_max_sync(0xffffffffu, others));
+        unsigned is16 = 0, is32 = 0;
+#pragma unroll
+        for (int i = 0; i < kUnitTokens; ++i) {
+            const int at = t + i - max(from[i], before);
+            if (t + i < B.M) {
+                is16 |= (at % 16 == 0 ? 1u : 0u) << i;
+                is32 |= (at % 32 == 0 ? 1u : 0u) << i;
+            }
+        }
+        const unsigned own = __popc(is16) << 16 | __popc(is32);  // at most 4096 of each in a round
+        unsigned incl = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31) counts[round][warp] = incl;
+        __syncthreads();
+        const unsigned sums = counts[round][lane];
+        incl += __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0u) - own;
+        int to16 = n16 + static_cast<int>(incl >> 16), to32 = n32 + static_cast<int>(incl & 0xFFFFu);
+#pragma unroll
+        for (int i = 0; i < kUnitTokens; ++i) {
+            const int2 unit = make_int2(t + i, a[i + 1]);
+            if (is16 >> i & 1u) of16[1 + to16++] = unit;
+            if (is32 >> i & 1u) of32[1 + to32++] = unit;
+        }
+        const unsigned all = __reduce_add_sync(0xffffffffu, sums);
+        n16 += static_cast<int>(all >> 16);
+        n32 += static_cast<int>(all & 0xFFFFu);
+    }
+    if (tid == 0) {
+        of16[0] = make_int2(n16, 0);
+        of32[0] = make_int2(n32, 0);
+        of16[1 + n16] = of32[1 + n32] = make_int2(B.M, -1);
+    }
+}
+
+// CTA: a unit of up to 32 tokens and one slice of K, in steps: all threads copy a step's
 // weights and activations, and each warp takes one 32-element chunk of 16 MT ranks.
 // Above rank 32 the warps divide the ranks into MH parts, so that a step is 128 or
 // 64 elements instead of 256 and more steps are on their way.  Rows are padded so
@@ -390,24 +476,26 @@ inline int step_stages(int rank, int mh, bool q8)
 
 template <int MT, int MH, bool BF16, bool Q8>
 __global__ void __launch_bounds__(kThreads, 2)
-    k_lora_shrink_tile(const uint16_t *__restrict__ A, Batch B, const float *__restrict__ X, long long ldx,
-                       const int8_t *__restrict__ Xq, const float *__restrict__ dx, float *__restrict__ V, int rank, int K,
-                       int slice_steps, int stages)
+    k_lora_shrink_tile(const uint16_t *__restrict__ A, const int2 *__restrict__ units, int M, const float *__restrict__ X,
+                       long long ldx, const int8_t *__restrict__ Xq, const float *__restrict__ dx, float *__restrict__ V, int rank,
+                       int K, int slice_steps, int stages)
 {
     extern __shared__ __align__(16) char raw[];  // stages; after the last step the warps' sums [kWarps][tokens][16 MT]
-    __shared__ Tile tile;
     constexpr int TT = kTileTokens, NT = TT / 8, kOut = 16 * MT * TT, kChunks = kWarps / MH, kStep = 32 * kChunks;
     constexpr int kPieces = kStep * (Q8 ? 1 : 4) / 16, kPiecesA = 2 * kStep / 16;  // 16-byte pieces of a token's step, of a rank's
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3, chunk = warp % kChunks, m0 = warp / kChunks * MT;
-    const int t0 = blockIdx.x * TT, chunks = K / 32, steps = (K + kStep - 1) / kStep;
+    const int chunks = K / 32, steps = (K + kStep - 1) / kStep;
     const int s0 = blockIdx.y * slice_steps, n = min(slice_steps, steps - s0);
     const int stage_bytes = step_bytes(rank, MH, Q8), off_x = rank * step_a(MH), off_d = off_x + TT * step_x(MH, Q8);
     pdl_wait();
     // only now: what the next kernel reads before its own wait is complete then
     pdl_launch_dependents();
-    find_groups<TT>(tile, B, t0);
-    for (int j = 0; j < tile.groups; ++j) {
-        const uint16_t *a = A + static_cast<long long>(tile.adapter[j]) * rank * K;
+    const int n_units = __ldcg(units).x;
+    for (int j = blockIdx.x; j < n_units; j += gridDim.x) {
+        const int2 unit = __ldcg(units + 1 + j);
+        const int t0 = unit.x, tokens = __ldcg(units + 2 + j).x - t0;
+        if (unit.y < 0) continue;
+        const uint16_t *a = A + static_cast<long long>(unit.y) * rank * K;
         auto fetch = [&](int i, int slot) {
             if (i < n) {
                 const int k0 = (s0 + i) * kStep, count = min(kStep, K - k0);
@@ -426,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                     for (int r0 = 0; r0 < TT; r0 += kRows) {
                         const int r = r0 + tid / kPieces;
-                        if (r < TT && tile.group[r] == j) {
+                        if (r < tokens) {
                             const void *from = Q8 ? static_cast<const void *>(Xq + static_cast<long long>(t0 + r) * K + k0 + 16 * c)
                                                   : static_cast<const void *>(X + (t0 + r) * ldx + k0 + 4 * c);
                             cp_async<16>(to + off_x + r * step_x(MH, Q8) + 16 * c, from);
@@ -435,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 if (Q8) {
                     const int r = tid / kChunks, x = tid % kChunks, at = k0 / 32 + x;
-                    if (r < TT && at < chunks && tile.group[r] == j)
+                    if (r < tokens && at < chunks)
                         cp_async<4>(to + off_d + r * step_d(MH) + 4 * x, dx + static_cast<long long>(t0 + r) * chunks + at);
                 }
             }
@@ -448,12 +536,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int q = 0; q < NT; ++q)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][q][i] = 0.f;
-        unsigned in = 0, col = 0;  // whether the lane's tokens belong to the group: as operand (column g), as results
+        unsigned in = 0, col = 0;  // whether the lane's tokens belong to the unit: as operand (column g), as results
 #pragma unroll
         for (int q = 0; q < NT; ++q) {
-            in |= (tile.group[8 * q + g] == j ? 1u : 0u) << q;
-            col |= (tile.group[8 * q + 2 * t] == j ? 1u : 0u) << (2 * q);
-            col |= (tile.group[8 * q + 2 * t + 1] == j ? 1u : 0u) << (2 * q + 1);
+            in |= (8 * q + g < tokens ? 1u : 0u) << q;
+            col |= (8 * q + 2 * t < tokens ? 1u : 0u) << (2 * q);
+            col |= (8 * q + 2 * t + 1 < tokens ? 1u : 0u) << (2 * q + 1);
         }
         for (int i = 0; i < stages - 1; ++i) fetch(i, i);
         int slot = 0, next = stages - 1;
@@ -507,10 +595,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     mine[(8 * q + 2 * t + (i & 1)) * 16 * MT + 16 * m + g + 8 * (i >> 1)] = acc[m][q][i];
         __syncthreads();
         const float *sums = reinterpret_cast<const float *>(raw);
-        float *out = V + static_cast<long long>(blockIdx.y) * B.M * rank;
+        float *out = V + static_cast<long long>(blockIdx.y) * M * rank;
         for (int i = tid; i < MH * kOut; i += kThreads) {
             const int tok = i / (16 * MT * MH), r = i % (16 * MT * MH);
-            if (r < rank && tile.group[tok] == j) {
+            if (r < rank && tok < tokens) {
                 const float *part = sums + r / (16 * MT) * kChunks * kOut + tok * 16 * MT + r % (16 * MT);
                 float v = 0.f;
 #pragma unroll
@@ -798,12 +886,11 @@ __device__ __forceinline__ void bulk_store(void *to, uint32_t from, uint32_t byt
 
 template <int KC, bool kOne, bool BF16>
 __global__ void __launch_bounds__(kBulkThreads, 2)
-    k_lora_expand_bulk(const uint16_t *__restrict__ W, Batch B, const float *__restrict__ V, const float *Y0, long long ldy0,
-                       float *Y, long long ldy, int rank, int rows, int slices, long long cta_items, long long total_items,
-                       int stages)
+    k_lora_expand_bulk(const uint16_t *__restrict__ W, const int2 *__restrict__ units, const float *__restrict__ scales, int M,
+                       int *status, const float *__restrict__ V, const float *Y0, long long ldy0, float *Y, long long ldy, int rank,
+                       int rows, int slices, int stages)
 {
     extern __shared__ __align__(16) char raw[];
-    __shared__ Tile tile;
     __shared__ __align__(8) uint64_t bars[2 * 6];  // filled, and multiplied
     __shared__ int abort;
     constexpr int E = KC / 4, NT = 2;
@@ -821,6 +908,7 @@ __global__ void __launch_bounds__(kBulkThreads, 2)
         abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    __syncthreads();
     pdl_launch_dependents();
     bool waited = false;
     int stage = 0, phase = 0;  // of the next item
@@ -831,134 +919,127 @@ __global__ void __launch_bounds__(kBulkThreads, 2)
         }
     };
     const int tile_items = (rows + kBulkRows - 1) / kBulkRows;
+    // The items of all units in one row, dealt out evenly.  The units, Y0 and the weights were complete before `shrink`
+    // let this kernel begin; v is complete after the wait.
+    const long long total_items = static_cast<long long>(__ldcg(units).x) * tile_items;
+    const long long cta_items = (total_items + gridDim.x - 1) / gridDim.x;
     const long long last = min((blockIdx.x + 1ll) * cta_items, total_items);
     for (long long at = blockIdx.x * cta_items; at < last;) {
-        const int tile_no = static_cast<int>(at / tile_items), i0 = static_cast<int>(at - static_cast<long long>(tile_no) * tile_items);
+        const int unit_no = static_cast<int>(at / tile_items), i0 = static_cast<int>(at - static_cast<long long>(unit_no) * tile_items);
         const int n = static_cast<int>(min(static_cast<long long>(tile_items - i0), last - at));
         at += n;
-        const int t0 = tile_no * kBulkTokens;
-        // the lists, Y0 and the weights were complete before `shrink` let this kernel begin; v is complete after the wait
-        find_groups<kBulkTokens>(tile, B, t0);
-        const int groups = tile.groups;
-        for (int j = 0; j < max(groups, 1); ++j) {
-            const bool product = j < groups;
-            unsigned add = 0, put = 0;  // tokens with a product, and tokens that are written
-            for (int i = 0; i < kBulkTokens; ++i) {
-                const int of = tile.group[i];
-                if (product && of == j) add |= 1u << i;
-                if (j == 0 && of < 0 && t0 + i < B.M && Y != Y0) put |= 1u << i;
-            }
-            put |= add;
-            if (put == 0) continue;
-            const uint16_t *w = W + static_cast<long long>(product ? tile.adapter[j] : 0) * rows * rank;
-            if (warp == kWarps) {
-                // ---- the producer: lane i < 16 copies token i, lane 16 the weights
-                const bool mine = lane < kBulkTokens && (put >> lane & 1u);
-                const float *y0 = Y0 + (t0 + lane) * ldy0;
-                float *y = Y + (t0 + lane) * ldy;
-                int ls = stage, lp = phase, issued = 0;
-                auto load = [&](int i) {
-                    const int row = (i0 + i) * kBulkRows, count = min(kBulkRows, rows - row);
-                    const uint32_t to = base + ls * stage_bytes, bar = full + 8 * ls;
-                    if (lane == 0) tcu::mbar_expect_tx(bar, __popc(put) * count * 4 + (product ? count * rank * 2 : 0));
+        const int2 unit = __ldcg(units + 1 + unit_no);
+        const int t0 = unit.x, tokens = __ldcg(units + 2 + unit_no).x - t0;
+        const bool product = unit.y >= 0;
+        if (!product && Y == Y0) continue;
+        const uint16_t *w = W + static_cast<long long>(product ? unit.y : 0) * rows * rank;
+        if (warp == kWarps) {
+            // ---- the producer: lane i < 16 copies token i, lane 16 the weights
+            const bool mine = lane < tokens;
+            const float *y0 = Y0 + (t0 + lane) * ldy0;
+            float *y = Y + (t0 + lane) * ldy;
+            int ls = stage, lp = phase, issued = 0;
+            auto load = [&](int i) {
+                const int row = (i0 + i) * kBulkRows, count = min(kBulkRows, rows - row);
+                const uint32_t to = base + ls * stage_bytes, bar = full + 8 * ls;
+                if (lane == 0) tcu::mbar_expect_tx(bar, tokens * count * 4 + (product ? count * rank * 2 : 0));
+                __syncwarp();
+                if (mine) tcu::bulk_load(to + lane * kPitch, y0 + row, count * 4, bar);
+                if (lane == kBulkTokens && product)
+                    tcu::bulk_load(to + kBulkTokens * kPitch, w + static_cast<long long>(row) * rank, count * rank * 2, bar);
+                next_stage(ls, lp);
+                ++issued;
+            };
+            for (int i = 0; i < stages - 1 && i < n; ++i) load(i);
+            int s = stage, ph = phase, i = 0;
+            for (; i < n; ++i) {
+                if (i + stages - 1 < n) {
+                    // into the stage of the item before, once its results have been read
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     __syncwarp();
-                    if (mine) tcu::bulk_load(to + lane * kPitch, y0 + row, count * 4, bar);
-                    if (lane == kBulkTokens && product)
-                        tcu::bulk_load(to + kBulkTokens * kPitch, w + static_cast<long long>(row) * rank, count * rank * 2, bar);
-                    next_stage(ls, lp);
-                    ++issued;
-                };
-                for (int i = 0; i < stages - 1 && i < n; ++i) load(i);
-                int s = stage, ph = phase, i = 0;
-                for (; i < n; ++i) {
-                    if (i + stages - 1 < n) {
-                        // into the stage of the item before, once its results have been read
-                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                        __syncwarp();
-                        load(i + stages - 1);
-                    }
-                    if (!tcu::wait_warp(done + 8 * s, ph, abort_flag, B.status)) break;
-                    const int row = (i0 + i) * kBulkRows, count = min(kBulkRows, rows - row);
-                    if (mine) bulk_store(y + row, base + s * stage_bytes + lane * kPitch, count * 4);
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    next_stage(s, ph);
+                    load(i + stages - 1);
                 }
-                if (i < n) {  // gave up: its copies have to arrive before the CTA may end
-                    int ws = stage, wp = phase;
-                    for (int x = 0; x < issued; ++x, next_stage(ws, wp)) {
-                        abort = 0;
-                        tcu::wait_warp(full + 8 * ws, wp, abort_flag, B.status);
-                    }
-                    abort = 1;
+                if (!tcu::wait_warp(done + 8 * s, ph, abort_flag, status)) break;
+                const int row = (i0 + i) * kBulkRows, count = min(kBulkRows, rows - row);
+                if (mine) bulk_store(y + row, base + s * stage_bytes + lane * kPitch, count * 4);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                next_stage(s, ph);
+            }
+            if (i < n) {  // gave up: its copies have to arrive before the CTA may end
+                int ws = stage, wp = phase;
+                for (int x = 0; x < issued; ++x, next_stage(ws, wp)) {
+                    abort = 0;
+                    tcu::wait_warp(full + 8 * ws, wp, abort_flag, status);
                 }
-                asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-            } else {
-                // ---- the multiplying warps: 32 rows each
-                if (!waited) pdl_wait();
-                const float scale = product ? __ldg(B.scale + tile.adapter[j]) : 0.f;
-                stage_v<kBulkTokens, BF16>(vs, V, t0, B.M, rank, depth, slices, scale, [&](int tok) { return (add >> tok & 1u) != 0; });
-                asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-                Fragment<KC, NT, BF16> v;  // of all of the rank, where that is one chunk
-                if (kOne) v.load(vs, pitch, 0, g, t);
-                float undo[NT][2];
+                abort = 1;
+            }
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        } else {
+            // ---- the multiplying warps: 32 rows each
+            if (!waited) pdl_wait();
+            const float scale = product ? __ldg(scales + unit.y) : 0.f;
+            if (product)
+                stage_v<kBulkTokens, BF16>(vs, V, t0, M, rank, depth, slices, scale, [&](int tok) { return tok < tokens; });
+            asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+            Fragment<KC, NT, BF16> v;  // of all of the rank, where that is one chunk
+            if (kOne) v.load(vs, pitch, 0, g, t);
+            float undo[NT][2];
 #pragma unroll
-                for (int q = 0; q < NT; ++q)
+            for (int q = 0; q < NT; ++q)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        undo[q][x] = BF16 ? 1.f : reinterpret_cast<const float *>(vs + 3 * kBulkTokens * pitch)[8 * q + 2 * t + x];
-                int s = stage, ph = phase;
-                for (int i = 0; i < n; ++i) {
-                    if (!tcu::wait_warp(full + 8 * s, ph, abort_flag, B.status)) break;
-                    char *const from = raw + s * stage_bytes;
-                    if (product) {
-                        float acc[NT][2][4];
-                        for (int k0 = 0; k0 < depth; k0 += KC) {
-                            const int k = k0 + E * t;
-                            uint32_t x[2][2][E / 2];
+                for (int x = 0; x < 2; ++x)
+                    undo[q][x] = BF16 ? 1.f : reinterpret_cast<const float *>(vs + 3 * kBulkTokens * pitch)[8 * q + 2 * t + x];
+            int s = stage, ph = phase;
+            for (int i = 0; i < n; ++i) {
+                if (!tcu::wait_warp(full + 8 * s, ph, abort_flag, status)) break;
+                char *const from = raw + s * stage_bytes;
+                if (product) {
+                    float acc[NT][2][4];
+                    for (int k0 = 0; k0 < depth; k0 += KC) {
+                        const int k = k0 + E * t;
+                        uint32_t x[2][2][E / 2];
 #pragma unroll
-                            for (int m = 0; m < 2; ++m)
+                        for (int m = 0; m < 2; ++m)
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    const char *q = from + kBulkTokens * kPitch + ((32 * warp + 16 * m + 8 * h + g) * rank + k) * 2;
-                                    if (E == 8) {
-                                        const uint4 y = *reinterpret_cast<const uint4 *>(q);
-                                        x[m][h][0] = y.x, x[m][h][1] = y.y, x[m][h][E / 2 - 2] = y.z, x[m][h][E / 2 - 1] = y.w;
-                                    } else {
-                                        const uint2 y = *reinterpret_cast<const uint2 *>(q);
-                                        x[m][h][0] = y.x, x[m][h][1] = y.y;
-                                    }
-#pragma unroll
-                                    for (int e = 0; e < E / 2; ++e) x[m][h][e] = k < rank ? x[m][h][e] : 0u;
+                            for (int h = 0; h < 2; ++h) {
+                                const char *q = from + kBulkTokens * kPitch + ((32 * warp + 16 * m + 8 * h + g) * rank + k) * 2;
+                                if (E == 8) {
+                                    const uint4 y = *reinterpret_cast<const uint4 *>(q);
+                                    x[m][h][0] = y.x, x[m][h][1] = y.y, x[m][h][E / 2 - 2] = y.z, x[m][h][E / 2 - 1] = y.w;
+                                } else {
+                                    const uint2 y = *reinterpret_cast<const uint2 *>(q);
+                                    x[m][h][0] = y.x, x[m][h][1] = y.y;
                                 }
-                            if (!kOne) v.load(vs, pitch, k0, g, t);
-                            v.multiply(acc, x, kOne || k0 == 0);
-                        }
 #pragma unroll
-                        for (int q = 0; q < NT; ++q)
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const int tok = 8 * q + 2 * t + x;
-                                float *y = reinterpret_cast<float *>(from + tok * kPitch) + 32 * warp + g;
-                                if (add >> tok & 1u) {
-#pragma unroll
-                                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                                        for (int h = 0; h < 2; ++h) y[16 * m + 8 * h] = fmaf(acc[q][m][2 * h + x], undo[q][x], y[16 * m + 8 * h]);
-                                }
+                                for (int e = 0; e < E / 2; ++e) x[m][h][e] = k < rank ? x[m][h][e] : 0u;
                             }
-                        tcu::fence_async_smem();  // before the bulk copies read it
+                        if (!kOne) v.load(vs, pitch, k0, g, t);
+                        v.multiply(acc, x, kOne || k0 == 0);
                     }
-                    __syncwarp();
-                    if (lane == 0) tcu::mbar_arrive(done + 8 * s);
-                    next_stage(s, ph);
+#pragma unroll
+                    for (int q = 0; q < NT; ++q)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int tok = 8 * q + 2 * t + x;
+                            float *y = reinterpret_cast<float *>(from + tok * kPitch) + 32 * warp + g;
+                            if (tok < tokens) {
+#pragma unroll
+                                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h) y[16 * m + 8 * h] = fmaf(acc[q][m][2 * h + x], undo[q][x], y[16 * m + 8 * h]);
+                            }
+                        }
+                    tcu::fence_async_smem();  // before the bulk copies read it
                 }
+                __syncwarp();
+                if (lane == 0) tcu::mbar_arrive(done + 8 * s);
+                next_stage(s, ph);
             }
-            waited = true;
-            for (int i = 0; i < n; ++i) next_stage(stage, phase);
-            __syncthreads();
-            if (*abort_flag) return;
         }
+        waited = true;
+        for (int i = 0; i < n; ++i) next_stage(stage, phase);
         __syncthreads();
+        if (*abort_flag) return;
     }
     if (!waited) pdl_wait();
 }
@@ -994,6 +1075,7 @@ struct Call {
     float *V;
     int rank, rows, K;
     cudaStream_t s;
+    int2 *of32 = nullptr, *of16 = nullptr;
 };
 
 template <int MT, bool BF16, bool Q8>
@@ -1028,7 +1110,8 @@ template <int MT, int MH, bool BF16, bool Q8>
 cudaError_t shrink_tile(const Call &c, int *slices)
 {
     auto kern = k_lora_shrink_tile<MT, MH, BF16, Q8>;
-    const int tiles = (c.B.M + kTileTokens - 1) / kTileTokens, steps = (c.K + step_of(MH) - 1) / step_of(MH);
+    // as many CTAs as there can be units, if every request's tokens lie together
+    const int tiles = (c.B.M + kTileTokens - 1) / kTileTokens + c.B.n_seq, steps = (c.K + step_of(MH) - 1) / step_of(MH);
     const int stages = step_stages(c.rank, MH, Q8);
     const size_t rings = static_cast<size_t>(stages) * step_bytes(c.rank, MH, Q8), sums = sizeof(float) * kWarps * 16 * MT * kTileTokens;
     const size_t smem = rings > sums ? rings : sums;
@@ -1037,7 +1120,7 @@ cudaError_t shrink_tile(const Call &c, int *slices)
     const int at_once = per_sm * sm_count();
     const int want = bounded_slices((at_once < kWantTiles ? at_once : kWantTiles) / tiles, c.K), slice_steps = (steps + want - 1) / want;
     *slices = (steps + slice_steps - 1) / slice_steps;
-    return launch_pdl(kern, dim3(tiles, *slices), dim3(kThreads), smem, c.s, c.A, c.B, c.X, c.ldx, c.Xq, c.dx, c.V, c.rank, c.K,
+    return launch_pdl(kern, dim3(tiles, *slices), dim3(kThreads), smem, c.s, c.A, static_cast<const int2 *>(c.of32), c.B.M, c.X, c.ldx, c.Xq, c.dx, c.V, c.rank, c.K,
                       slice_steps, stages);
 }
 template <int MT, int MH>
@@ -1087,10 +1170,11 @@ cudaError_t expand_bulk(const Call &c, int slices)
     const size_t smem = v_bytes(depth, kBulkTokens) + static_cast<size_t>(stages) * bulk_stage(c.rank);
     const int per_sm = ctas_per_sm(reinterpret_cast<const void *>(kern), kBulkThreads, smem);
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
-    const long long total = static_cast<long long>((c.B.M + kBulkTokens - 1) / kBulkTokens) * ((c.rows + kBulkRows - 1) / kBulkRows);
-    const long long ctas = static_cast<long long>(per_sm) * sm_count(), per = (total + ctas - 1) / ctas;
-    return launch_pdl(kern, dim3(static_cast<unsigned>((total + per - 1) / per)), dim3(kBulkThreads), smem, c.s, c.W, c.B, c.V, c.Y0,
-                      c.ldy0, c.Y, c.ldy, c.rank, c.rows, slices, per, total, stages);
+    const long long most = ((c.B.M + kBulkTokens - 1ll) / kBulkTokens + c.B.n_seq) * ((c.rows + kBulkRows - 1) / kBulkRows);
+    const long long ctas = static_cast<long long>(per_sm) * sm_count();
+    return launch_pdl(kern, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(kBulkThreads), smem, c.s, c.W,
+                      static_cast<const int2 *>(c.of16), c.B.scale, c.B.M, c.B.status, c.V, c.Y0, c.ldy0, c.Y, c.ldy, c.rank, c.rows,
+                      slices, stages);
 }
 cudaError_t expand_bulk_rank(const Call &c, bool bf16, int slices)
 {
@@ -1099,14 +1183,17 @@ cudaError_t expand_bulk_rank(const Call &c, bool bf16, int slices)
     return bf16 ? expand_bulk<32, false, true>(c, slices) : expand_bulk<32, false, false>(c, slices);
 }
 
-int run(const Call &c, int type)
+int run(Call c, int type)
 {
     const bool bf16 = type == GQ_TYPE_BF16;
     int slices = 0;
     // Neighbouring tokens of one request share their adapter: the prompts' form where requests have 16 tokens or more
     // on average.
     if (c.B.sequence != nullptr && c.B.M / 16 >= c.B.n_seq) {
-        cudaError_t e = shrink_tile_rank(c, bf16, &slices);
+        c.of32 = reinterpret_cast<int2 *>(c.V + static_cast<long long>(most_slices(c.K, c.B.M)) * c.B.M * c.rank);
+        c.of16 = c.of32 + unit_words(c.B.M);
+        cudaError_t e = launch_pdl(k_lora_units, dim3(1), dim3(kUnitThreads), 0, c.s, c.B, c.of32, c.of16);
+        if (e == cudaSuccess) e = shrink_tile_rank(c, bf16, &slices);
         if (e == cudaSuccess) e = expand_bulk_rank(c, bf16, slices);
         return status_from(e);
     }
@@ -1159,7 +1246,8 @@ size_t gq_lora_workspace_bytes(int rank, int K, int M)
 {
     if (rank < 8 || rank % 8 != 0 || rank > GQ_MAX_LORA_RANK || K < 32 || K % 32 != 0 || K > (1 << 24) || M < 1 || M > (1 << 28))
         return 0;
-    return static_cast<size_t>(most_slices(K, M)) * M * rank * sizeof(float);
+    // A x of every slice; and for prompts (16 tokens a request or more) the units
+    return static_cast<size_t>(most_slices(K, M)) * M * rank * sizeof(float) + (M < 16 ? 0 : 2 * unit_words(M) * sizeof(int2));
 }
 
 int gq_lora_add(const void *A, const void *B, int type, const float *scale, const int32_t *adapter,

@@ -211,3 +211,35 @@ def test_weights_beyond_32_bits_of_elements():
     gq.gq_lora_add(A, B, gq.GQ_TYPE_BF16, t.ones(n, device="cuda"), t.tensor([n - 1], dtype=t.int32, device="cuda"), None, x, K,
                    y, rows, y, rows, ws, ws.numel(), n, rank, rows, K, 1, 1)
     assert float(y[0, rows - 1]) == 6.0 and float(y.abs().sum()) == 6.0
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_prompts_whose_tokens_lie_anywhere(q8):
+    """Runs of one token, of a multiple of 16 or 32 and one more or less, over more than one round of 4096 tokens."""
+    g = np.random.default_rng(5)
+    sequence = g.integers(-1, 6, 700)  # nearly every token begins a run
+    Case(700, 64, 36, 8, 4, [0, 3, -1, 1, 1, 2], sequence, "bf16", q8, pad=4).check()
+    lengths = [1, 31, 32, 33, 1, 16, 15, 17, 64, 0, 65, 127, 3000, 1, 1024, 4096, 2]
+    adapter = g.integers(-1, 3, len(lengths))
+    Case(sum(lengths), 32, 20, 16, 3, adapter, runs(lengths), "f16", q8).check()
+    Case(sum(lengths), 32, 20, 16, 3, adapter, runs(lengths), "f16", q8).check(in_place=True)
+
+
+def test_prompts_in_a_graph_with_other_lists():
+    t = torch()
+    M, K, rows, rank, n_seq = 600, 256, 96, 40, 8
+    c = Case(M, K, rows, rank, 3, [0, 1, -1, 2, 2, 0, 1, -1], runs([75] * 8), "bf16", False)
+    ws = t.empty(gq.gq_lora_workspace_bytes(rank, K, M), dtype=t.uint8, device="cuda")
+    x, y0, y, adapter, scale, sequence = dev(c.x), dev(c.y0), t.empty(M, rows, device="cuda"), dev(c.adapter), dev(c.scale), dev(c.sequence)
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        for _ in range(2):
+            gq.gq_lora_add(c.A, c.B, TYPES["bf16"], scale, adapter, sequence, x, K, y0, rows, y, rows, ws, ws.numel(), 3, rank, rows, K,
+                           n_seq, M)
+    for lengths in ([75] * 8, [1, 2, 3, 4, 90, 0, 200, 300], [593, 1, 1, 1, 1, 1, 1, 1]):
+        c.sequence = runs(lengths).astype(c.sequence.dtype)
+        sequence.copy_(dev(c.sequence))
+        y.fill_(float("nan"))
+        graph.replay()
+        assert np.array_equal(y.cpu().numpy(), c.run())
+        c.check()
