@@ -36,6 +36,7 @@
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
+#include <stddef.h>
 
 #include "gq_host.h"
 #include "gq_internal.cuh"
@@ -477,24 +478,24 @@ __device__ __forceinline__ void running_weights(const u64 *list, u64 *F, int n, 
     for (int i = i0; i < i1; ++i) F[i] += at;
     __syncthreads();
 }
-// First i < n for which `here` holds, in every thread (n if there is none; it may hold for one only).
-template <int THREADS, class Here>
-__device__ __forceinline__ int only(int n, int &found, Here &&here)
+// The first i < kList from which on `reaches` holds, the last i if it nowhere does.
+// One warp's work, a look at every 64th and at those of one such part (a CTA's look
+// at all, with its barriers, took 0.65 us, all warps at a binary search 0.9).
+template <class Reaches>
+__device__ __forceinline__ int search(Reaches &&reaches)
 {
-    __syncthreads();
-    if (threadIdx.x == 0) found = n;
-    __syncthreads();
-#pragma unroll 1
-    for (int i = threadIdx.x; i < n; i += THREADS)
-        if (here(i)) found = i;
-    __syncthreads();
-    return found;
+    static_assert(kList == 64 * 32, "a lane a part");
+    const int lane = threadIdx.x & 31;
+    auto vote = [&](int i) { return __ballot_sync(0xffffffffu, reaches(i)); };
+    const unsigned part = vote(64 * lane + 63);
+    const int i = 64 * (part ? __ffs(part) - 1 : 31);
+    const unsigned lo = vote(i + lane), hi = vote(i + 32 + lane);
+    return i + (lo ? __ffs(lo) - 1 : hi ? 31 + __ffs(hi) : 63);
 }
-// First i with F[i] >= x, n if there is none.
-template <int THREADS>
-__device__ __forceinline__ int reach(const u64 *F, int n, u64 x, int &found)
+// First i with F[i] >= x, n if there is none; a warp's.
+__device__ __forceinline__ int reach(const u64 *F, int n, u64 x)
 {
-    return only<THREADS>(n, found, [&](int i) { return F[i] >= x && (i == 0 || F[i - 1] < x); });
+    return F[n - 1] >= x ? search([&](int i) { return i >= n - 1 || F[i] >= x; }) : n;
 }
 
 // What the slices' headers say of a row.
@@ -548,10 +549,11 @@ struct PickShared {
     u64 list[kList], F[kList], sh[32];
     SortShared sort;
     RowHead heads[32];
-    int count, found;
+    int count;
 };
 
-// The row from its slices' headers and lists; false where they do not settle it.
+// The row from its slices' headers and lists; false where they do not settle it.  Of
+// use in the first warp.
 template <int THREADS>
 __device__ __forceinline__ bool settle(const Rows &R, const Settings &S, int row, PickShared &P, int &tok, float &pr, bool &refused)
 {
@@ -630,6 +632,7 @@ __device__ __forceinline__ bool settle(const Rows &R, const Settings &S, int row
     const bool all = n == h.cands;  // every candidate is in the list
     sort_down<THREADS>(P.list, P.F, P.sort, n, h.best, rank_of(max(h.theta, h.lowest), R.vocab - 1));
     running_weights<THREADS>(P.list, P.F, n, 0ull, sc, top, P.sh);
+    if (threadIdx.x >= 32) return false;  // the first warp has the rest to itself
     const u64 *F = P.F;
     const u64 listed = F[n - 1], last = n > 1 ? listed - F[n - 2] : listed;
     // the weight of what top_k keeps, between z and most
@@ -649,8 +652,8 @@ __device__ __forceinline__ bool settle(const Rows &R, const Settings &S, int row
     // the first element where top_p is reached, and the weight that min_p keeps, where they are in the list
     int from = n, to = n;
     if (p < 1.f) {
-        from = to = reach<THREADS>(F, n, nucleus(p, z), P.found);
-        if (most != z) to = reach<THREADS>(F, n, nucleus(p, most), P.found);
+        from = to = reach(F, n, nucleus(p, z));
+        if (most != z) to = reach(F, n, nucleus(p, most));
     }
     u64 least = ~0ull;
     if (mp > 0.f) {
@@ -658,7 +661,7 @@ __device__ __forceinline__ bool settle(const Rows &R, const Settings &S, int row
         const u64 thr = mp < 1.f ? part_of(mp, F[0], rest) + (rest ? 1 : 0) : F[0];
         // first of the list below the threshold; the list falls
         auto w = [&](int i) { return F[i] - (i ? F[i - 1] : 0ull); };
-        const int lo = only<THREADS>(n, P.found, [&](int i) { return w(i) < thr && (i == 0 || w(i - 1) >= thr); });
+        const int lo = w(n - 1) < thr ? search([&](int i) { return i >= n - 1 || w(i) < thr; }) : n;
         if (lo < n)
             least = F[max(lo, 1) - 1];
         else if (all)
@@ -674,7 +677,7 @@ __device__ __forceinline__ bool settle(const Rows &R, const Settings &S, int row
     else
         kept = z;
     kept = min(kept, z);
-    const int j = reach<THREADS>(F, n, drawn(u, kept), P.found);
+    const int j = reach(F, n, drawn(u, kept));
     if (j == n) return false;
     tok = index_of(P.list[j]);
     pr = ratio(j ? F[j] - F[j - 1] : F[0], kept);
@@ -884,15 +887,17 @@ struct Level {
 struct DeepShared {
     u64 list[kList], F[kList];
     SortShared sort;
-    unsigned hist[kBins], low[kBins], high[kBins];  // this CTA's counts, and weights as two words
-    Level coarse, fine;
+    alignas(16) unsigned hist[kBins], low[kBins], high[kBins];  // this CTA's counts, and weights as two words
+    Level fine, coarse;
     u64 sh[kDeepThreads / 32], sh2[kDeepThreads / 32];
     unsigned sh32[kDeepThreads / 32];
     RowHead heads[kDeepThreads / 32];
     u64 least[kDeepCtas];  // weights that min_p keeps
     u64 rank, reached;          // what a search found: the element, and the running weight at it
-    int found;
-    unsigned listed;
+    u64 limits[2];              // the running weights where top_k ends, and top_p
+    int from[3], to[3];         // the steps that are collected for top_k, top_p and the draw
+    int found, fit;
+    unsigned listed, local;
 };
 
 template <int TYPE>
@@ -1061,15 +1066,174 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
         least = 0;
         for (int c = 0; c < kDeepCtas; ++c) least += D.least[c];
 
+        // The first step in which a running weight or count reaches X; it holds an element.
+        static_assert(kBins == kList, "as `search` looks");
+        auto first_step = [&](const Level &L, bool by_count, u64 X, unsigned skip) {
+            return search([&](int b) { return by_count ? L.count[b] + skip >= X : L.weight[b] >= X; });
+        };
+        // This CTA's list sorted, and its running weights with `front` in front; how many they are.
+        auto sort_list = [&](u64 front) {
+            const int n = min(static_cast<int>(D.listed), kList);
+            u64 most = 0, fewest = ~0ull;
+            if (n > kFew) {
+#pragma unroll 1
+                for (int i = tid; i < n; i += kDeepThreads) {
+                    most = max(most, D.list[i]);
+                    fewest = min(fewest, D.list[i]);
+                }
+                auto extremes = [&] {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) {
+                        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                        fewest = min(fewest, __shfl_xor_sync(0xffffffffu, fewest, o));
+                    }
+                };
+                extremes();
+                if (lane == 0) {
+                    D.sh[warp] = most;
+                    D.sh2[warp] = fewest;
+                }
+                __syncthreads();
+                most = D.sh[lane];  // (32 warps)
+                fewest = D.sh2[lane];
+                extremes();
+            }
+            sort_down<kDeepThreads>(D.list, D.F, D.sort, n, most, fewest);
+            running_weights<kDeepThreads>(D.list, D.F, n, front, sc, top, D.sh);
+            return n;
+        };
+        auto finish = [&](u64 rank, u64 kept) {
+            token[row] = index_of(rank);
+            if (prob) prob[row] = ratio(row_weight(sc, value_of(static_cast<uint32_t>(rank >> 32)), top), kept);
+        };
+
         // ---- three times the first element at which a running count or weight reaches X: the last that top_k keeps,
-        // the last that top_p keeps, the drawn one
-        u64 z = D.coarse.weight[kBins - 1], kept = z;
+        // the last that top_p keeps, the drawn one.  Each X follows from the one before, but the step that holds that
+        // bounds it: the steps between the bounds are collected for all three at once and sorted by a CTA each, which
+        // leaves a look-up to be done in turn (160 rows of 262144: 102 us, one after the other 109).
+        const u64 total = D.coarse.weight[kBins - 1];
+        const bool limited = k > 0 && static_cast<unsigned>(k) < D.coarse.count[kBins - 1];
+        auto front_of = [&](int b) { return b ? D.coarse.weight[b - 1] : 0ull; };
+        auto count_in_front = [&](int b) { return b ? D.coarse.count[b - 1] : 0u; };
+        if (warp == 0) {
+            int from[3] = {kBins, kBins, kBins}, to[3] = {-1, -1, -1};  // none if there is no such limit
+            u64 lo = total, hi = total;  // bounds of the weight kept so far
+            if (limited) {
+                from[0] = to[0] = first_step(D.coarse, true, static_cast<u64>(k), 0u);
+                lo = front_of(to[0]);
+                hi = D.coarse.weight[to[0]];
+            }
+            if (p < 1.f) {
+                from[1] = first_step(D.coarse, false, nucleus(p, lo), 0u);
+                to[1] = first_step(D.coarse, false, nucleus(p, hi), 0u);
+                lo = min(lo, front_of(from[1]));
+                hi = min(hi, D.coarse.weight[to[1]]);
+            }
+            if (mp > 0.f) {
+                lo = min(lo, least);
+                hi = min(hi, least);
+            }
+            from[2] = first_step(D.coarse, false, drawn(u, lo), 0u);
+            to[2] = first_step(D.coarse, false, drawn(u, hi), 0u);
+            bool fit = true;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                fit &= to[i] < 0 || D.coarse.count[to[i]] - count_in_front(from[i]) <= kList;
+                if (lane == i) {
+                    D.from[i] = from[i];
+                    D.to[i] = to[i];
+                }
+            }
+            if (lane == 0) {
+                D.fit = fit ? 1 : 0;
+                D.local = 0;
+            }
+        }
+        __syncthreads();
+        if (D.fit != 0) {  // the whole cluster
+            const int from[3] = {D.from[0], D.from[1], D.from[2]}, to[3] = {D.to[0], D.to[1], D.to[2]};
+            // Here first, then to the CTAs that sort them: a count in another CTA's memory takes a microsecond.  Which
+            // lists an element belongs to stands above its index.
+            static_assert(GQ_MAX_VOCAB <= 1 << 28, "room above the index");
+            constexpr unsigned kLocal = 3 * kList;
+            u64 *const local = reinterpret_cast<u64 *>(D.hist);  // and `fine`, which are free
+            static_assert(offsetof(DeepShared, coarse) - offsetof(DeepShared, hist) >= kLocal * sizeof(u64), "room for all three");
+            u64 *const list[3] = {cluster.map_shared_rank(D.list, 0), cluster.map_shared_rank(D.list, 1), cluster.map_shared_rank(D.list, 2)};
+            unsigned *const listed[3] = {cluster.map_shared_rank(&D.listed, 0), cluster.map_shared_rank(&D.listed, 1),
+                                         cluster.map_shared_rank(&D.listed, 2)};
+            auto send = [&](bool have, u64 r, unsigned in) {  // a warp's
+                unsigned mask[3], at[3];
+#pragma unroll
+                for (int c = 0; c < 3; ++c) {
+                    mask[c] = __ballot_sync(0xffffffffu, have && (in >> c & 1u));
+                    at[c] = 0;
+                    if (lane == 0 && mask[c]) at[c] = atomicAdd(listed[c], static_cast<unsigned>(__popc(mask[c])));
+                }
+#pragma unroll
+                for (int c = 0; c < 3; ++c) {
+                    const unsigned place = __shfl_sync(0xffffffffu, at[c], 0) + __popc(mask[c] & ((1u << lane) - 1u));
+                    if (mask[c] >> lane & 1u && place < kList) list[c][place] = r;
+                }
+            };
+            each([&](const float (&v)[kVec], int index) {
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    if (!(v[i] > -INFINITY)) continue;
+                    const int b = step_of(v[i]);
+                    const unsigned in = (b >= from[0] && b <= to[0] ? 1u : 0u) | (b >= from[1] && b <= to[1] ? 2u : 0u) |
+                                        (b >= from[2] && b <= to[2] ? 4u : 0u);
+                    if (in) {
+                        const unsigned at = atomicAdd(&D.local, 1u);
+                        if (at < kLocal) local[at] = rank_of(key_of(v[i]), index + i) ^ in << 28;
+                    }
+                }
+            });
+            __syncthreads();
+#pragma unroll 1
+            for (unsigned x = warp * 32; x < D.local; x += kDeepThreads) {
+                const u64 r = x + lane < D.local ? local[x + lane] : 0ull;
+                const unsigned in = ~static_cast<uint32_t>(r) >> 28;
+                send(x + lane < D.local, r | 0xF0000000ull, in);
+            }
+            cluster.sync();
+            int n = 0;
+            const int mine = me < 3 ? D.from[me] : kBins;
+            if (mine < kBins) n = sort_list(front_of(mine));
+            // the first of the list whose running weight reaches X
+            auto first_of = [&](u64 X) { return n > 0 ? min(reach(D.F, n, X), n - 1) : 0; };
+            u64 kept = total;
+            if (limited) {
+                if (me == 0) {
+                    const int at = max(min(k - static_cast<int>(count_in_front(mine)), n) - 1, 0);
+                    if (tid > 0 && tid < 3) cluster.map_shared_rank(D.limits, tid)[0] = D.F[at];
+                }
+                cluster.sync();
+                kept = D.limits[0];
+            }
+            if (p < 1.f) {
+                if (me == 1 && warp == 0) {
+                    const int at = first_of(nucleus(p, kept));
+                    if (lane == 0) cluster.map_shared_rank(D.limits, 2)[1] = D.F[at];
+                }
+                cluster.sync();
+                kept = min(kept, D.limits[1]);
+            }
+            if (mp > 0.f) kept = min(kept, least);
+            if (me == 2 && warp == 0) {
+                const int at = first_of(drawn(u, kept));
+                if (lane == 0) finish(D.list[at], kept);
+            }
+            cluster.sync();  // no CTA goes on while another reads its memory
+            continue;
+        }
+        // ---- a step with too many elements: one after the other, dividing such steps further
+        u64 z = total, kept = z;
 #pragma unroll 1
         for (int phase = 0; phase < 3; ++phase) {
             const bool by_count = phase == 0;
             u64 X;
             if (phase == 0) {
-                if (k == 0 || static_cast<unsigned>(k) >= D.coarse.count[kBins - 1]) continue;
+                if (!limited) continue;
                 X = static_cast<u64>(k);
             } else if (phase == 1) {
                 if (mp > 0.f) kept = min(kept, least);
@@ -1085,14 +1249,9 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
             int shift = 0;
 #pragma unroll 1
             while (true) {
-                // the first step in which X is reached; it holds an element
-                if (tid == 0) D.found = kBins - 1;
-                __syncthreads();
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int b = tid * kPer + i;
-                    auto reaches = [&](int x) { return by_count ? L->count[x] + skip >= X : L->weight[x] >= X; };
-                    if (reaches(b) && !(b > 0 && reaches(b - 1))) atomicMin(&D.found, b);
+                if (warp == 0) {
+                    const int x = first_step(*L, by_count, X, skip);
+                    if (lane == 0) D.found = x;
                 }
                 __syncthreads();
                 const int b = D.found;
@@ -1117,37 +1276,14 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
                     });
                     cluster.sync();
                     if (me == 0) {
-                        const int n = min(static_cast<int>(D.listed), kList);
-                        u64 most = 0, fewest = ~0ull;
-                        if (n > kFew) {
-                            for (int i = tid; i < n; i += kDeepThreads) {
-                                most = max(most, D.list[i]);
-                                fewest = min(fewest, D.list[i]);
+                        const int n = sort_list(weight_in_front);
+                        if (warp == 0) {
+                            int at = by_count ? static_cast<int>(X - skip - in_front) - 1 : n > 0 ? reach(D.F, n, X) : 0;
+                            at = max(min(at, n - 1), 0);
+                            if (lane < kDeepCtas) {
+                                *cluster.map_shared_rank(&D.rank, lane) = D.list[at];
+                                *cluster.map_shared_rank(&D.reached, lane) = D.F[at];
                             }
-                            auto extremes = [&] {
-#pragma unroll
-                                for (int o = 16; o > 0; o >>= 1) {
-                                    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-                                    fewest = min(fewest, __shfl_xor_sync(0xffffffffu, fewest, o));
-                                }
-                            };
-                            extremes();
-                            if (lane == 0) {
-                                D.sh[warp] = most;
-                                D.sh2[warp] = fewest;
-                            }
-                            __syncthreads();
-                            most = D.sh[lane];  // (32 warps)
-                            fewest = D.sh2[lane];
-                            extremes();
-                        }
-                        sort_down<kDeepThreads>(D.list, D.F, D.sort, n, most, fewest);
-                        running_weights<kDeepThreads>(D.list, D.F, n, weight_in_front, sc, top, D.sh);
-                        int at = by_count ? static_cast<int>(X - skip - in_front) - 1 : reach<kDeepThreads>(D.F, n, X, D.found);
-                        at = max(min(at, n - 1), 0);
-                        if (tid < kDeepCtas) {
-                            *cluster.map_shared_rank(&D.rank, tid) = D.list[at];
-                            *cluster.map_shared_rank(&D.reached, tid) = D.F[at];
                         }
                         if (tid == 0) D.listed = 0;
                     }
@@ -1198,10 +1334,8 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
                 z = kept = D.reached;
             else if (phase == 1)
                 kept = min(kept, D.reached);
-            else if (me == 0 && tid == 0) {
-                token[row] = index_of(D.rank);
-                if (prob) prob[row] = ratio(row_weight(sc, value_of(static_cast<uint32_t>(D.rank >> 32)), top), kept);
-            }
+            else if (me == 0 && tid == 0)
+                finish(D.rank, kept);
         }
         cluster.sync();  // no CTA goes on while another reads its memory
     }
