@@ -29,10 +29,11 @@
 //          share.
 //
 // What bounds it.  160 rows of 262144 f32 logits (168 MB), settings of all kinds,
-// 109 us: the scan 55 (issue; 20 instructions an element where weights are summed),
-// the pick some 13, the search of the six rows that need it some 40: dependent
-// rounds over little data, barriers of the cluster, and fetching code that runs
-// once (unrolled passes took 140 us in all instead of 124 then).
+// 101 us: the scan 55 (issue; 20 instructions an element where weights are summed),
+// the pick some 13, the search of the four to seven rows that need it 25: the pass
+// over the row 6, joining the histograms 4.6, and rounds over little data, barriers
+// of the cluster, and fetching code that runs once (unrolled passes took 16 us more
+// in all).
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
