@@ -25,10 +25,10 @@
 // tcgen05 is not used: the contraction is 8 to 128 deep, so the work is the
 // bytes of Y (and, for few tokens, of the adapters), not the products.
 //
-// What bounds them: 4096 tokens of rank 16 beside 21504 rows (732 MB) take 132 us,
-// 5.5 TB/s: the memory (a plain copy in the same order takes 114 for Y alone).  1531
-// tokens of rank 64 (112 MB) take 47, of which finding the units and shrink are the
-// first 20; 64 tokens of 48 adapters of rank 32 (84 MB) 26.4.  One token: 4.4, the
+// What bounds them: 4096 tokens of rank 16 beside 21504 rows (732 MB) take 126 us,
+// 5.8 TB/s: the memory (a plain copy in the same order takes 114 for Y alone).  1531
+// tokens of rank 64 (112 MB) take 46, of which finding the units and shrink are the
+// first 20; 64 tokens of 48 adapters of rank 32 (84 MB) 25.2.  One token: 4.5, the
 // latency of two kernels.
 #include "gq_host.h"
 #include "gq_internal.cuh"
@@ -699,6 +699,10 @@ struct Fragment {
 constexpr int kStages = 3;
 // Four rows of weights (16 bytes a lane, 8 where a chunk is 16 deep) and the lane's results of 8 NT tokens.
 __host__ __device__ constexpr int expand_stage(int kc, int nt) { return 64 * kc + 1024 * nt; }
+// What a CTA does in the time that a tile's beginning takes (groups, v, the first
+// copies: some 4 us), in row blocks.  CTAs that pass from one tile to the next get
+// so much less (64 tokens of rank 32: 26.4 us, 25.2 with it).
+__host__ __device__ constexpr int tile_start(int rank) { return (128 << 10) / (64 * rank + 512); }
 // CTA: a range of row blocks of tiles of 8 tokens, which its warps take in
 // turn.  Row slots are dealt so that a lane's four results of a token are four
 // consecutive rows: slot g (+ 8) of instruction m is row 4 g + 2 m (+ 1).
@@ -722,13 +726,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int depth = kOne ? KC : (rank + KC - 1) / KC * KC, pitch = v_pitch(depth);
     pdl_launch_dependents();
     bool waited = false;
-    // a range of all tiles' row blocks in one row
-    const int tile_blocks = (rows + kRowBlock - 1) / kRowBlock;
-    const long long last = min((blockIdx.x + 1ll) * cta_blocks, total_blocks);
-    for (long long at = blockIdx.x * cta_blocks; at < last;) {
-        const int tile_no = static_cast<int>(at / tile_blocks), rb0 = static_cast<int>(at - static_cast<long long>(tile_no) * tile_blocks);
-        const int rb1 = static_cast<int>(min(static_cast<long long>(tile_blocks), rb0 + (last - at)));
-        at += rb1 - rb0;
+    // a range of all tiles' row blocks in one row, `start` in front of every tile's standing for what beginning it costs
+    const int start = tile_start(rank), tile_blocks = start + (rows + kRowBlock - 1) / kRowBlock;
+    long long at = start + blockIdx.x * cta_blocks;
+    const long long last = min(at + cta_blocks, total_blocks);
+    while (at < last) {
+        const int tile_no = static_cast<int>(at / tile_blocks), from = static_cast<int>(at - static_cast<long long>(tile_no) * tile_blocks);
+        const int to = static_cast<int>(min(static_cast<long long>(tile_blocks), from + (last - at)));
+        at += to - from;
+        const int rb0 = max(from - start, 0), rb1 = to - start;
+        if (rb1 <= rb0) continue;
         const int t0 = tile_no * TT;
         // the lists, Y0 and the weights were complete before `shrink` let this
         // kernel begin; v is complete after the wait
@@ -874,6 +881,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // multiplying warps no instructions.
 constexpr int kBulkThreads = kThreads + 32, kBulkTokens = 16, kBulkRows = 256, kPitch = 4 * kBulkRows + 16;
 __host__ __device__ constexpr int bulk_stage(int rank) { return kBulkTokens * kPitch + 2 * kBulkRows * rank; }
+__host__ __device__ constexpr int unit_start(int rank) { return (128 << 10) / (2 * kBulkRows * rank + 2048 * kBulkTokens); }
 inline int bulk_stages(int rank)
 {
     const int n = (104 << 10) / bulk_stage(rank);
@@ -918,16 +926,19 @@ __global__ void __launch_bounds__(kBulkThreads, 2)
             ph ^= 1;
         }
     };
-    const int tile_items = (rows + kBulkRows - 1) / kBulkRows;
-    // The items of all units in one row, dealt out evenly.  The units, Y0 and the weights were complete before `shrink`
-    // let this kernel begin; v is complete after the wait.
-    const long long total_items = static_cast<long long>(__ldcg(units).x) * tile_items;
-    const long long cta_items = (total_items + gridDim.x - 1) / gridDim.x;
-    const long long last = min((blockIdx.x + 1ll) * cta_items, total_items);
-    for (long long at = blockIdx.x * cta_items; at < last;) {
-        const int unit_no = static_cast<int>(at / tile_items), i0 = static_cast<int>(at - static_cast<long long>(unit_no) * tile_items);
-        const int n = static_cast<int>(min(static_cast<long long>(tile_items - i0), last - at));
-        at += n;
+    // The items of all units in one row, `start` in front of every unit's as in the other form, dealt out evenly.  The
+    // units, Y0 and the weights were complete before `shrink` let this kernel begin; v is complete after the wait.
+    const int start = unit_start(rank), unit_items = start + (rows + kBulkRows - 1) / kBulkRows;
+    const long long total_items = static_cast<long long>(__ldcg(units).x) * unit_items;
+    const long long cta_items = (total_items - start + gridDim.x - 1) / gridDim.x;
+    long long at = start + blockIdx.x * cta_items;
+    const long long last = min(at + cta_items, total_items);
+    while (at < last) {
+        const int unit_no = static_cast<int>(at / unit_items), from = static_cast<int>(at - static_cast<long long>(unit_no) * unit_items);
+        const int to = static_cast<int>(min(static_cast<long long>(unit_items), from + (last - at)));
+        at += to - from;
+        const int i0 = max(from - start, 0), n = to - start - i0;
+        if (n <= 0) continue;
         const int2 unit = __ldcg(units + 1 + unit_no);
         const int t0 = unit.x, tokens = __ldcg(units + 2 + unit_no).x - t0;
         const bool product = unit.y >= 0;
@@ -1146,11 +1157,12 @@ cudaError_t expand(const Call &c, int tiles, int groups, int slices)
     const size_t smem = v_bytes(depth, 8 * NT) + kWarps * kStages * expand_stage(KC, NT);
     if (ctas_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
     // two CTAs per SM at once, the row blocks of all tiles dealt out evenly: no SM is left with less at the end
-    const long long total = static_cast<long long>(tiles) * ((c.rows + kRowBlock - 1) / kRowBlock);
+    const long long total = static_cast<long long>(tiles) * (tile_start(c.rank) + (c.rows + kRowBlock - 1) / kRowBlock);
     const int ctas = (2 * sm_count() + groups - 1) / groups;
-    long long per = (total + ctas - 1) / ctas;
+    const long long work = total - tile_start(c.rank);  // the first tile's beginning is every CTA's own
+    long long per = (work + ctas - 1) / ctas;
     if (per < kWarps) per = kWarps;
-    return launch_pdl(kern, dim3(static_cast<unsigned>((total + per - 1) / per), 1, groups), dim3(kThreads), smem, c.s, c.W, c.B, c.V,
+    return launch_pdl(kern, dim3(static_cast<unsigned>((work + per - 1) / per), 1, groups), dim3(kThreads), smem, c.s, c.W, c.B, c.V,
                       c.Y0, c.ldy0, c.Y, c.ldy, c.rank, c.rows, slices, per, total);
 }
 cudaError_t expand_rank(const Call &c, bool bf16, int tiles, int groups, int slices)
