@@ -307,3 +307,28 @@ def test_frequencies_follow_the_probabilities():
     token, prob = sample(x, "f32", u=(np.arange(800) + 0.5) / 800)
     assert list(np.bincount(token, minlength=4)) == [400, 100, 200, 100]
     assert np.allclose(prob, np.array([0.5, 0.125, 0.25, 0.125])[token], rtol=2.0 ** -20)
+
+
+@pytest.mark.parametrize("typ", list(TYPES))
+@pytest.mark.parametrize("vocab", [2047, 2048, 2049, 4089, 4090])
+def test_rows_about_as_long_as_the_list_or_a_slice(vocab, typ):
+    g = np.random.default_rng(vocab)
+    for sharp in (True, False):
+        check(logits(g, 12, vocab, sharp), typ, **settings(g, 12, vocab))
+    token, prob = sample(np.zeros((3, vocab)), typ, u=np.array([0.0, 0.5, 1.0]), k=vocab - 1)
+    assert token.tolist() == [0, (vocab - 1) // 2, vocab - 2]
+    assert np.all(np.abs(prob * (vocab - 1) - 1) < 2.0 ** -21)
+
+
+def test_limits_that_fall_into_one_crowded_step_and_others_that_do_not():
+    """Searched rows: thousands of equal logits where one of top_k, top_p and the draw ends, a smooth slope at the others."""
+    g = np.random.default_rng(12)
+    vocab = 60013
+    x = np.tile(np.sort(g.standard_normal(vocab) * 0.4)[::-1], (9, 1))
+    for r in range(9):
+        a = [3000, 9000, 30000][r % 3]
+        x[r, a:a + 5000] = x[r, a]
+        x[r] = x[r, g.permutation(vocab)]
+    k = np.repeat([0, 10000, 40000], 3)
+    for p, m in ((1.0, 0.0), (0.2, 0.0), (0.7, 0.3), (0.999, 0.9)):
+        check(x, "f32", k=k, p=p, m=m, u=g.random(9))
