@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kUnitThreads) k_lora_units(Batch B, int2 *__re
 // weights and activations, and each warp takes one 32-element chunk of 16 MT ranks.
 // Above rank 32 the warps divide the ranks into MH parts, so that a step is 128 or
 // 64 elements instead of 256 and more steps are on their way.  Rows are padded so
-// that the operands' loads meet no bank twice.  (Bulk copies, one per row, took 58 us where this takes 25 for 4096 tokens of rank
+// that the operands' loads meet no bank twice.  (Bulk copies, one per row, took 58 us where this then took 25 for 4096 tokens of rank
 // 16: they cost some 60 cycles each, and the rows are 256 and 512 bytes.)
 constexpr int kTileTokens = 32;
 __host__ __device__ constexpr int step_of(int mh) { return kWarps / mh * 32; }
@@ -876,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // stretches of 1 KB and the rows' weights into a stage, eight warps add B v in
 // place, and the producer sends the stretches to Y.  Copied by the threads that
 // hold the results, in 128-byte pieces of four tokens an instruction, the same
-// bytes took 168 us where this takes 136 (4096 tokens, 21504 rows, rank 16:
+// bytes took 168 us where this then took 136 (4096 tokens, 21504 rows, rank 16:
 // 705 MB); long stretches are what the memory is fast at, and the copies cost the
 // multiplying warps no instructions.
 constexpr int kBulkThreads = kThreads + 32, kBulkTokens = 16, kBulkRows = 256, kPitch = 4 * kBulkRows + 16;
@@ -1199,9 +1199,11 @@ int run(Call c, int type)
 {
     const bool bf16 = type == GQ_TYPE_BF16;
     int slices = 0;
-    // Neighbouring tokens of one request share their adapter: the prompts' form where requests have 16 tokens or more
-    // on average.
-    if (c.B.sequence != nullptr && c.B.M / 16 >= c.B.n_seq) {
+    // Neighbouring tokens of one request share their adapter: the prompts' form where requests have 8 tokens or more on
+    // average, or 4 in a large batch.  5376 x 5376, us in this form and in the other: 8 requests of 4, 8 and 16 tokens,
+    // rank 16: 11.1 and 8.3, 11.2 and 9.8, 12.0 and 17.3; rank 64: 16.4 and 13.0, 16.7 and 17.7, 17.4 and 36.0; 64
+    // requests of 2, 4 and 8, rank 16: 20.4 and 14.6, 20.5 and 24.5, 22.9 and 50.9.
+    if (c.B.sequence != nullptr && c.B.M / (c.B.M < 256 ? 8 : 4) >= c.B.n_seq) {
         c.of32 = reinterpret_cast<int2 *>(c.V + static_cast<long long>(most_slices(c.K, c.B.M)) * c.B.M * c.rank);
         c.of16 = c.of32 + unit_words(c.B.M);
         cudaError_t e = launch_pdl(k_lora_units, dim3(1), dim3(kUnitThreads), 0, c.s, c.B, c.of32, c.of16);
@@ -1258,8 +1260,8 @@ size_t gq_lora_workspace_bytes(int rank, int K, int M)
 {
     if (rank < 8 || rank % 8 != 0 || rank > GQ_MAX_LORA_RANK || K < 32 || K % 32 != 0 || K > (1 << 24) || M < 1 || M > (1 << 28))
         return 0;
-    // A x of every slice; and for prompts (16 tokens a request or more) the units
-    return static_cast<size_t>(most_slices(K, M)) * M * rank * sizeof(float) + (M < 16 ? 0 : 2 * unit_words(M) * sizeof(int2));
+    // A x of every slice; and the units, from the fewest tokens on that take the prompts' form
+    return static_cast<size_t>(most_slices(K, M)) * M * rank * sizeof(float) + (M < 8 ? 0 : 2 * unit_words(M) * sizeof(int2));
 }
 
 int gq_lora_add(const void *A, const void *B, int type, const float *scale, const int32_t *adapter,

@@ -61,7 +61,7 @@ extern "C" {
  * Errors before the launches: GQ_ERR_FORMAT (type), GQ_ERR_NULL, GQ_ERR_ALIGN,
  * GQ_ERR_SHAPE, GQ_ERR_WORKSPACE; after them GQ_ERR_CUDA.
  * Two kernels are launched on `stream`, three for prompts (a sequence list and
- * 16 tokens or more a request on average).
+ * 8 tokens or more a request on average, or 4 from 256 tokens on).
  * ------------------------------------------------------------------------ */
 size_t gq_lora_workspace_bytes(int rank, int K, int M); /* 0 if out of range */
 int gq_lora_add(const void *A, const void *B, int type, const float *scale, const int32_t *adapter,

@@ -243,3 +243,12 @@ def test_prompts_in_a_graph_with_other_lists():
         graph.replay()
         assert np.array_equal(y.cpu().numpy(), c.run())
         c.check()
+
+
+@pytest.mark.parametrize("M,n_seq", [(7, 1), (8, 1), (9, 1), (15, 2), (16, 2), (255, 31), (255, 32), (255, 60), (256, 64), (256, 65), (260, 65)])
+@pytest.mark.parametrize("q8", [False, True])
+def test_both_sides_of_the_rule_for_prompts(M, n_seq, q8):
+    """Few tokens a request, with a workspace of exactly the bytes asked for."""
+    g = np.random.default_rng(M + n_seq)
+    sequence = np.sort(g.integers(0, n_seq, M))
+    Case(M, 96, 40, 24, 5, g.integers(-1, 5, n_seq), sequence, "bf16", q8, seed=n_seq).check()
