@@ -964,8 +964,10 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
             const unsigned hi = static_cast<unsigned>(w >> 32) + (old + lo < old ? 1u : 0u);
             if (hi) atomicAdd(&D.high[b], hi);
         };
-        // The CTAs' histograms, added up and summed over the steps, in every CTA's L; `base` in front.
-        auto merge = [&](Level &L, u64 base) {
+        // The CTAs' histograms, added up and summed over the steps, in every CTA's L; `base` in front.  `between` is done
+        // between the two barriers of the cluster: the first is also the one that says that all its CTAs run, before
+        // which none may touch another's memory.
+        auto merge = [&](Level &L, u64 base, auto &&between) {
             // A CTA sums a share of the steps: two warps fetch each CTA's part of it, 128 bytes an access (single words of
             // many CTAs cost ten times that), and bring the sums to one CTA each.
             constexpr int kShare = kBins / kDeepCtas, kHalf = kShare / 2;
@@ -973,6 +975,7 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
             unsigned *const part = reinterpret_cast<unsigned *>(D.list);  // [3][kDeepCtas][kShare]: list and F, which are free
             static_assert(3 * kDeepCtas * kShare * sizeof(unsigned) <= sizeof(D.list) + sizeof(D.F), "room for the parts");
             cluster.sync();
+            between();
             {
                 const int c = warp >> 1, x = (warp & 1) * kHalf + lane;
                 const unsigned *from[3] = {cluster.map_shared_rank(D.hist, c), cluster.map_shared_rank(D.low, c),
@@ -1062,8 +1065,9 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
                 }
         });
         least = cta_sum<kDeepThreads>(least, D.sh);
-        if (tid < kDeepCtas) cluster.map_shared_rank(D.least, tid)[me] = least;
-        merge(D.coarse, 0ull);  // (the barriers that `least` needs in it)
+        merge(D.coarse, 0ull, [&] {
+            if (tid < kDeepCtas) cluster.map_shared_rank(D.least, tid)[me] = least;
+        });
         least = 0;
         for (int c = 0; c < kDeepCtas; ++c) least += D.least[c];
 
@@ -1328,7 +1332,7 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
                         if (r <= high && r >= low) add(static_cast<int>((high - r) >> shift), row_weight(sc, v[i], top));
                     }
                 });
-                merge(D.fine, base);
+                merge(D.fine, base, [] {});
                 L = &D.fine;
             }
             if (phase == 0)
