@@ -165,8 +165,9 @@ cudaError_t launch(const uint8_t *W, const int32_t *ids, float scale, void *Y, l
                    int M, cudaStream_t s)
 {
     // three times the warps that the SMs hold, so that the last ones to finish are a small part
-    const int pieces = (K + 255) / 256, warps = sm_count() * 64 * 3;
-    int parts = (warps + M - 1) / M;
+    const int pieces = (K + 255) / 256;
+    const long long warps = sm_count() * 64 * 3;
+    int parts = static_cast<int>((warps + M - 1) / M);  // (the sum of two ints may pass 31 bits)
     if (parts > pieces) parts = pieces;
     const int part_elems = (pieces + parts - 1) / parts * 256;
     parts = (K + part_elems - 1) / part_elems;
