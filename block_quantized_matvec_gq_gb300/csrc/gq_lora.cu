@@ -1066,10 +1066,14 @@ int bounded_slices(long long n, int K)
     return n < 1 ? 1 : (n < by_k ? static_cast<int>(n) : by_k);
 }
 int decode_slices(int K, long long tiles) { return bounded_slices((kWantCtas + tiles - 1) / tiles, K); }
-int most_slices(int K, int M)
+// Rows of slices' sums that calls of up to M tokens write: the most of slices x tokens, so that the workspace of the
+// largest batch serves the smaller ones.  A decode batch has at most ceil(kWantCtas / tiles of 8) slices, which times
+// its tokens is at most 8 (kWantCtas - 1) + M; a prompt's at most kWantTiles / (tiles of 32), or one.
+long long sum_rows(int K, int M)
 {
-    const int few = decode_slices(K, (M + 7) / 8), many = bounded_slices(kWantTiles / ((M + 31) / 32), K);
-    return few > many ? few : many;
+    const long long by_k = static_cast<long long>((K + 255) / 256) * M, few = 8ll * (kWantCtas - 1) + M,
+                    many = M > 32 * kWantTiles ? M : 32 * kWantTiles, most = few > many ? few : many;
+    return by_k < most ? by_k : most;
 }
 
 struct Call {
@@ -1204,7 +1208,7 @@ int run(Call c, int type)
     // rank 16: 11.1 and 8.3, 11.2 and 9.8, 12.0 and 17.3; rank 64: 16.4 and 13.0, 16.7 and 17.7, 17.4 and 36.0; 64
     // requests of 2, 4 and 8, rank 16: 20.4 and 14.6, 20.5 and 24.5, 22.9 and 50.9.
     if (c.B.sequence != nullptr && c.B.M / (c.B.M < 256 ? 8 : 4) >= c.B.n_seq) {
-        c.of32 = reinterpret_cast<int2 *>(c.V + static_cast<long long>(most_slices(c.K, c.B.M)) * c.B.M * c.rank);
+        c.of32 = reinterpret_cast<int2 *>(c.V + sum_rows(c.K, c.B.M) * c.rank);
         c.of16 = c.of32 + unit_words(c.B.M);
         cudaError_t e = launch_pdl(k_lora_units, dim3(1), dim3(kUnitThreads), 0, c.s, c.B, c.of32, c.of16);
         if (e == cudaSuccess) e = shrink_tile_rank(c, bf16, &slices);
@@ -1261,7 +1265,7 @@ size_t gq_lora_workspace_bytes(int rank, int K, int M)
     if (rank < 8 || rank % 8 != 0 || rank > GQ_MAX_LORA_RANK || K < 32 || K % 32 != 0 || K > (1 << 24) || M < 1 || M > (1 << 28))
         return 0;
     // A x of every slice; and the units, from the fewest tokens on that take the prompts' form
-    return static_cast<size_t>(most_slices(K, M)) * M * rank * sizeof(float) + (M < 8 ? 0 : 2 * unit_words(M) * sizeof(int2));
+    return static_cast<size_t>(sum_rows(K, M)) * rank * sizeof(float) + (M < 8 ? 0 : 2 * unit_words(M) * sizeof(int2));
 }
 
 int gq_lora_add(const void *A, const void *B, int type, const float *scale, const int32_t *adapter,

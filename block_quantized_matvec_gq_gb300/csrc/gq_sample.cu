@@ -1352,11 +1352,12 @@ __global__ void __launch_bounds__(kDeepThreads) __cluster_dims__(kDeepCtas, 1, 1
 struct Plan {
     int ept, slices, cap_log2, want;
 };
+constexpr int kFineSlices = 304;
+int fine_slices(int vocab) { return (vocab + 7 + 4095) / 4096; }
 Plan plan_for(int vocab, int n_rows)
 {
     Plan p;
-    const long long fine = (vocab + 7 + 4095) / 4096;
-    p.ept = fine * n_rows <= 304 ? 8 : 32;
+    p.ept = static_cast<long long>(fine_slices(vocab)) * n_rows <= kFineSlices ? 8 : 32;
     const int threads = p.ept == 8 ? kSmallThreads : kScanThreads, per = threads * p.ept;
     p.slices = (vocab + 7 + per - 1) / per;
     // lists of some 1024 elements a row in all, with room for two to four times as many
@@ -1367,6 +1368,12 @@ Plan plan_for(int vocab, int n_rows)
     return p;
 }
 size_t up16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
+size_t bytes_for(int vocab, int n_rows)
+{
+    const Plan p = plan_for(vocab, n_rows);
+    const size_t slices = static_cast<size_t>(p.slices) * n_rows;
+    return slices * sizeof(Header) + (slices << p.cap_log2) * sizeof(u64) + up16(static_cast<size_t>(n_rows) * sizeof(int));
+}
 
 template <int TYPE>
 cudaError_t launch(Rows R, const Settings &S, const Plan &p, int n_rows, int32_t *token, float *prob, cudaStream_t s)
@@ -1406,9 +1413,11 @@ extern "C" {
 size_t gq_sample_workspace_bytes(int vocab, int n_rows)
 {
     if (vocab < 1 || vocab > GQ_MAX_VOCAB || n_rows < 1 || n_rows > GQ_MAX_SAMPLE_ROWS) return 0;
-    const Plan p = plan_for(vocab, n_rows);
-    const size_t slices = static_cast<size_t>(p.slices) * n_rows;
-    return slices * sizeof(Header) + (slices << p.cap_log2) * sizeof(u64) + up16(static_cast<size_t>(n_rows) * sizeof(int));
+    // of either size of slices the larger the more rows: the most of up to n_rows is that of all, or of the most
+    // that take the small slices
+    const int few = kFineSlices / fine_slices(vocab);
+    const size_t most = few >= 1 && few < n_rows ? bytes_for(vocab, few) : 0, all = bytes_for(vocab, n_rows);
+    return most > all ? most : all;
 }
 
 int gq_sample(const void *logits, long long ldl, int type, const float *temperature, const int32_t *top_k,

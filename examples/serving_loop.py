@@ -36,8 +36,7 @@ class AdaptedBlock(AttentionBlock):
         self.lora_a = (torch.randn(n_adapters, rank, self.hidden, generator=g, device="cuda") * self.hidden ** -0.5).bfloat16()
         self.lora_b = (torch.randn(n_adapters, self.width, rank, generator=g, device="cuda") * 0.1).bfloat16()
         self.lora_scale = torch.full((n_adapters,), 0.5, device="cuda")
-        most = max(gq.gq_lora_workspace_bytes(rank, self.hidden, m) for m in range(1, self.qkv.shape[0] + 1))
-        self.lora_ws = torch.empty(most, dtype=torch.uint8, device="cuda")
+        self.lora_ws = torch.empty(gq.gq_lora_workspace_bytes(rank, self.hidden, self.qkv.shape[0]), dtype=torch.uint8, device="cuda")
 
     def step(self, x, table, kv_len, q_start, adapter, sequence):
         """x: f32[rows][hidden]; rows behind the last request (sequence -1) are computed and lead nowhere."""

@@ -40,7 +40,8 @@ extern "C" {
  *           stride.
  *   workspace  device memory, at least gq_lora_workspace_bytes bytes, scratch
  *           before and after the call.  Two calls that may run concurrently
- *           must not share it.
+ *           must not share it.  The size does not fall with M, K or rank: what the
+ *           largest batch needs serves every smaller one.
  * An adapter number of n_adapters or more, or a request number of n_seq or
  * more, counts as none, and the device status (gq_device_status) becomes
  * GQ_ERR_SHAPE.

@@ -47,7 +47,9 @@ extern "C" {
  *   token   int32[n_rows]; prob f32[n_rows] or NULL.
  *   workspace  device memory, 16-byte aligned, at least
  *           gq_sample_workspace_bytes bytes, scratch before and after the call.
- *           Two calls that may run concurrently must not share it.
+ *           Two calls that may run concurrently must not share it.  The size does
+ *           not fall with n_rows: for one vocab, what the largest batch needs serves
+ *           every smaller one.
  * Arithmetic: weights are whole numbers of 2^-43 of about the largest weight, each within
  * 2^-23 of itself and 2^-42 of the largest; their sums are exact.  So the
  * result does not depend on how the row was split, the same inputs give the
