@@ -281,7 +281,10 @@ extern "C" int gq_kv_plan(const int32_t *n_new, const int32_t *kv_len_in, const 
     int ctas = (items + kItemsPerCta - 1) / kItemsPerCta;
     ctas = ctas < 1 ? 1 : (ctas > kMaxCtas ? kMaxCtas : ctas);
     const size_t smem = 3 * (static_cast<size_t>(n_seq) + 1) * sizeof(int);
-    if (ctas_per_sm(reinterpret_cast<const void *>(k_kv_plan), kThreads, smem) < 1) return GQ_ERR_CUDA;
+    // asked for the most requests, whatever their number: the answers are kept, and there is room for some hundreds of
+    // different sizes of all kernels together
+    constexpr size_t kMostSmem = 3 * (GQ_MAX_PLAN_SEQ + 1) * sizeof(int);
+    if (ctas_per_sm(reinterpret_cast<const void *>(k_kv_plan), kThreads, kMostSmem) < 1) return GQ_ERR_CUDA;
     const uint32_t per = static_cast<uint32_t>(page_tokens / 16), per_mul = static_cast<uint32_t>(((1ull << 32) + per - 1) / per);
     Args a{n_new,    kv_len_in, ring_in, free_pages, block_table, kv_len, q_start, ring, nullptr, nullptr, nullptr,
            n_pages,  max_pages, page_tokens, n_seq,  n_tokens,    status_word(), per, per_mul};
