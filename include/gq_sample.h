@@ -28,7 +28,8 @@ extern "C" {
  *   top_k   if > 0: the first top_k of the order
  *   top_p   if < 1: of these the shortest beginning whose weight is at least
  *           top_p times the weight of all of these; always the first
- *   min_p   if > 0: of these the ones with w_i >= min_p; always the first
+ *   min_p   if > 0: of these the ones with w_i >= min_p, which counts as at most
+ *           1: then the ones that share the largest weight
  *   token   the first of the kept whose running sum of weights, in the order,
  *           exceeds u times the sum of all kept
  *   prob    its weight over that sum

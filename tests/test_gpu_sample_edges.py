@@ -38,3 +38,20 @@ def test_smaller_calls_in_the_workspace_of_the_largest():
         got, want = sample(x, "f32", **s, ws=guarded_ws[:size]), sample(x, "f32", **s)
         assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
         assert bool((guarded_ws[size:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("typ", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("vocab,ties", [(40, 3), (5000, 3), (70001, 3), (5000, 4000), (70001, 30000)])
+@pytest.mark.parametrize("m", [1.0, 1.5, 3e38, float("inf")])
+def test_a_min_p_of_one_or_more_keeps_what_ties_with_the_largest(vocab, ties, typ, m):
+    """Few ties, which the lists settle, and many, which are searched; a quarter of an octave lies below them."""
+    g = np.random.default_rng(ties)
+    x = np.full((4, vocab), 2.0) - 0.25 * g.integers(1, 9, (4, vocab))
+    at = np.sort(np.stack([g.choice(vocab, ties, replace=False) for _ in range(4)]), -1)
+    np.put_along_axis(x, at, 2.0, -1)
+    u = np.array([0.0, 0.4, 0.7, 0.9999], np.float32)
+    token, prob = sample(x, typ, m=m, u=u)
+    want = [at[r][int(np.floor(float(u[r]) * ties))] for r in range(4)]
+    assert token.tolist() == want
+    # a quotient of whole numbers brought to 24 bits each: three roundings
+    assert np.all(np.abs(prob.astype(np.float64) * ties - 1) <= 3 * 2.0 ** -24 * (1 + 2.0 ** -20))
