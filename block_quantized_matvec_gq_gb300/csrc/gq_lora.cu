@@ -82,11 +82,19 @@ __device__ __forceinline__ void mma_16(float (&d)[4], uint32_t a0, uint32_t a1, 
 // The 11 leading bits of x; the rest, x - head(x), is exact and tf32 keeps 11 bits of it.
 __device__ __forceinline__ float head(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFFE000u); }
 
-// A pair of numbers as 16-bit ones, and what that leaves of them (exact).
+// A pair of numbers as 16-bit ones, and what that leaves of them (exact).  The first piece of a number above the largest
+// bf16 stays at that instead of becoming infinite; what is infinite stays so in the second.  (f16: such numbers have been
+// scaled into the range, or are codes.)
 template <bool BF16>
-__device__ __forceinline__ uint32_t round2(float &a, float &b)
+__device__ __forceinline__ uint32_t round2(float &a, float &b, bool first)
 {
-    const uint32_t w = BF16 ? kv::f2_bf162(a, b) : kv::f2_half2(a, b);
+    uint32_t w;
+    if (!BF16)
+        w = kv::f2_half2(a, b);
+    else if (first)
+        asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    else
+        w = kv::f2_bf162(a, b);
     const float2 r = weights2<BF16>(w);
     a -= r.x;
     b -= r.y;
@@ -118,7 +126,7 @@ __device__ __forceinline__ void multiply_chunk(float (&acc)[MT][NT][4], GetA &&a
 #pragma unroll
             for (int p = 0; p < P; ++p)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) b[p][q][e] = round2<BF16>(y[2 * e], y[2 * e + 1]);
+                for (int e = 0; e < 4; ++e) b[p][q][e] = round2<BF16>(y[2 * e], y[2 * e + 1], p == 0);
         } else {
             x(q, v[q]);
         }
@@ -651,7 +659,7 @@ __device__ __forceinline__ void stage_v(char *vs, const float *__restrict__ V, l
         if (4 * lane < depth) {
 #pragma unroll
             for (int p = 0; p < kPiecesOf<BF16>; ++p) {
-                const uint32_t a = round2<BF16>(y[0], y[1]), b = round2<BF16>(y[2], y[3]);
+                const uint32_t a = round2<BF16>(y[0], y[1], p == 0), b = round2<BF16>(y[2], y[3], p == 0);
                 *reinterpret_cast<uint2 *>(vs + (p * TOKENS + tok) * pitch + 8 * lane) = make_uint2(a, b);
             }
         }

@@ -23,3 +23,26 @@ def test_smaller_calls_in_the_workspace_of_the_largest(q8):
         c = Case(M, K, rows, rank, 3, adapter, sequence, "bf16", q8, seed=M)
         assert np.array_equal(c.check(ws=ws[:size]), c.run()), M
         assert bool((ws[size:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("typ", ["f16", "bf16"])
+@pytest.mark.parametrize("M,prompts", [(5, False), (40, True)])
+def test_finite_numbers_beyond_the_largest_of_16_bits(M, prompts, typ):
+    """3.4e38 lies between the largest bf16 (3.3895e38) and the largest f32: an activation, and a number of A x."""
+    c = Case(M, 64, 36, 8, 2, [0, 1] if prompts else np.arange(M) % 3 - 1, runs([M // 2, M - M // 2]) if prompts else None, typ, False)
+    c.x[:, 5] = np.float32(3.4e38) * np.where(np.arange(M) % 2, 1, -1).astype(np.float32)
+    c.x[1, 5] = 1.0
+    c.A[:, 3, 5] = 1.0
+    c.B *= 2.0 ** -12
+    c.scale[:] = 1.0
+    assert np.all(np.isfinite(c.check()))
+
+
+@pytest.mark.parametrize("typ", ["f16", "bf16"])
+@pytest.mark.parametrize("M,prompts", [(5, False), (40, True)])
+def test_infinite_activations_give_no_finite_sums(M, prompts, typ):
+    c = Case(M, 64, 36, 8, 2, [0, 1] if prompts else np.zeros(M, int), runs([M // 2, M - M // 2]) if prompts else None, typ, False)
+    c.x[1, 5], c.x[2, 40] = np.inf, -np.inf
+    got = c.run()
+    bad = np.isin(np.arange(M), (1, 2))
+    assert not np.any(np.isfinite(got[bad])) and np.all(np.isfinite(got[~bad]))
