@@ -621,7 +621,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 // ---------------------------------------------------------------- Y = Y0 + scale B v
 // v in shared memory as pieces of 16 bits: kPiecesOf rows of TOKENS x pitch bytes,
 // then (f16) the factors that undo the scaling.  f16 has not v's range: a token's
-// v is scaled so that its largest lies in [2^13, 2^14), an exact power of two.
+// v is scaled so that its largest lies in [2^13, 2^14), an exact power of two.  The
+// second piece ends at f16's smallest step: half of it, 2^-25, is 2^-38 of the largest.
 __host__ __device__ constexpr int v_pitch(int depth) { return 2 * depth + (2 * depth % 128 == 0 ? 64 : 0); }  // (banks)
 __host__ __device__ constexpr int v_bytes(int depth, int tokens) { return 3 * tokens * v_pitch(depth) + 4 * tokens; }
 

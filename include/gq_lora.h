@@ -50,7 +50,12 @@ extern "C" {
  *   (2^-17 + 2^-32 K) |scale| sum_j |B_ij| sum_k |A_jk x_k|
  * (operands of 22 bits or more, f32 sums, those of the tensor cores truncated;
  * this is every rounding at its worst), and within 1e-6 of the added term in
- * the 2-norm.  A non-finite
+ * the 2-norm.  With f16 adapters a token's numbers scale (A x)_j are cut at
+ * 2^-38 of the largest of them: up to
+ *   2^-38 |scale| sum_j |B_ij| max_j sum_k |A_jk x_k|
+ * more, which shows only where a row of B takes none but numbers 21 octaves
+ * below the largest.  Numbers below 2^-126 may count as 0 on the way.
+ * A non-finite
  * x, A or B gives non-finite sums where the definition's are (NaN possibly for
  * an infinity), for the tokens of that adapter and that row alone.
  * Deterministic for the same arguments.

@@ -46,3 +46,43 @@ def test_infinite_activations_give_no_finite_sums(M, prompts, typ):
     got = c.run()
     bad = np.isin(np.arange(M), (1, 2))
     assert not np.any(np.isfinite(got[bad])) and np.all(np.isfinite(got[~bad]))
+
+
+def bound_of(c):
+    """Error bounds per element: the interface's three terms, the last with every activation, product and sum on the way
+    cut by as much as 2^-126."""
+    a, b = np.abs(c.A.double().cpu().numpy()), np.abs(c.B.double().cpu().numpy())
+    y, bound, _ = c.reference()
+    for i, ad in enumerate(c.of()):
+        if ad >= 0:
+            s, v = float(c.scale[ad]), a[ad] @ np.abs(c.x[i].astype(np.float64))
+            if c.typ == "f16":
+                bound[i] += 2.0 ** -38 * s * b[ad].sum(-1) * v.max()
+            bound[i] += 2.0 ** -126 * (s * (b[ad] @ (a[ad].sum(-1) + 2 * c.K + 2)) + 2 * c.rank + 2)
+    return y, bound
+
+
+@pytest.mark.parametrize("typ", ["f16", "bf16"])
+@pytest.mark.parametrize("M,prompts", [(6, False), (40, True)])
+def test_small_numbers_of_a_x_beside_large_ones(M, prompts, typ):
+    """Number 0 of A x is 2^30 times number 3, and the first half of the rows of B takes number 3 alone."""
+    c = Case(M, 64, 36, 8, 2, [0, 1] if prompts else np.arange(M) % 2, runs([M // 2, M - M // 2]) if prompts else None, typ, False)
+    c.x[:, :32] *= np.float32(2.0 ** 15)
+    c.x[:, 32:] *= np.float32(2.0 ** -15)
+    c.A[:, 3, :32] = 0.0
+    c.B[:, :18, :3] = 0.0
+    c.B[:, :18, 4:] = 0.0
+    c.y0[:, :18] = 0.0
+    y, bound = bound_of(c)
+    assert np.all(np.abs(c.run() - y) <= bound)
+
+
+@pytest.mark.parametrize("f", [2.0 ** -110, 2.0 ** -122, 2.0 ** -130, 2.0 ** -140])
+@pytest.mark.parametrize("typ", ["f16", "bf16"])
+@pytest.mark.parametrize("M,prompts", [(6, False), (40, True)])
+def test_activations_next_to_the_smallest(M, prompts, typ, f):
+    c = Case(M, 64, 36, 8, 2, [0, 1] if prompts else np.arange(M) % 2, runs([M // 2, M - M // 2]) if prompts else None, typ, False)
+    c.x = (c.x.astype(np.float64) * f).astype(np.float32)
+    c.y0[:] = 0.0
+    y, bound = bound_of(c)
+    assert np.all(np.abs(c.run() - y) <= bound)
