@@ -7,9 +7,10 @@
 //
 // Weights are whole numbers of 2^-43 of about the largest weight, w = M 2^(A - 31)
 // with A = rint(l log2(e) / T) and a 32-bit M: A and M depend on the logit and T
-// alone, so sums are exact integers in any order, the running weights and the
-// total agree to the last unit, and a slice can be summed before the row's
-// largest logit is known.
+// alone, so sums are integers, the same in any order, and a slice can be summed
+// before the row's largest logit is known.  A slice's sum is in units of its own
+// largest; brought to the row's, their total is up to a unit an element above the
+// running weights' last, and goes by how the row was cut.
 //
 //   scan   streams the row once, a slice per CTA held in registers: largest
 //          logit, sum of weights, and a list of the slice's leading elements.

@@ -34,8 +34,9 @@ extern "C" {
  *           exceeds u times the sum of all kept
  *   prob    its weight over that sum
  * T <= 0 takes the first of the order (prob 1).  A row without a candidate
- * gives token -1 and prob 0.  u counts as brought into [0, 1]: a u of 1 or more
- * gives the last kept, a NaN or a negative one the first.  T below 2^-100
+ * gives token -1 and prob 0.  u counts as brought into [0, 1]: a NaN or a
+ * negative one gives the first, a u of 1 or more the last of the kept that has
+ * weight (one some 43 octaves below the largest has none: no u draws it).  T below 2^-100
  * counts as 2^-100; an infinite T gives equal weights.  If the largest logit
  * is +infinity the infinite ones share the weight, whatever T is.  A NaN among T, top_p or
  * min_p gives token -1, prob 0 and GQ_ERR_SHAPE in the device status
@@ -52,10 +53,13 @@ extern "C" {
  *           not fall with n_rows: for one vocab, what the largest batch needs serves
  *           every smaller one.
  * Arithmetic: weights are whole numbers of 2^-43 of about the largest weight, each within
- * 2^-23 of itself and 2^-42 of the largest; their sums are exact.  So the
- * result does not depend on how the row was split, the same inputs give the
- * same token, and a token differs from that of exact weights only where
- * u (or top_p, min_p) lies within rounding of a boundary.
+ * 2^-23 of itself and 2^-42 of the largest, and added exactly.  The same call
+ * gives the same token and prob.  The weight of a whole row may be put together
+ * from parts of it, each in units of its own largest, and how a row is divided
+ * goes by n_rows: between batches it differs by less than vocab 2^-42 of the
+ * largest weight, so prob in its last bits.  A token differs from that of exact
+ * weights, or from that in another batch, only where u (or top_p, min_p) lies
+ * within rounding of a boundary.
  * Range: 1 <= vocab <= GQ_MAX_VOCAB, 0 <= n_rows <= GQ_MAX_SAMPLE_ROWS (0:
  * nothing to do).
  * Errors before the launches: GQ_ERR_FORMAT (type), GQ_ERR_NULL, GQ_ERR_ALIGN,

@@ -55,3 +55,28 @@ def test_a_min_p_of_one_or_more_keeps_what_ties_with_the_largest(vocab, ties, ty
     assert token.tolist() == want
     # a quotient of whole numbers brought to 24 bits each: three roundings
     assert np.all(np.abs(prob.astype(np.float64) * ties - 1) <= 3 * 2.0 ** -24 * (1 + 2.0 ** -20))
+
+
+@pytest.mark.parametrize("typ", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("u", [1.0, 2.0, float("inf")])
+def test_a_u_of_one_gives_the_last_kept_that_has_weight(u, typ):
+    g = np.random.default_rng(4)
+    low = {"f32": -3.4028235e38, "f16": -65504.0, "bf16": -3.3895314e38}[typ]
+    for vocab in (2, 300, 5000, 70001):
+        x = np.full((5, vocab), low)                        # masked with the lowest value
+        last = np.zeros(5, int)
+        x[0, :2] = 0.0, -40.0                               # 57 octaves below: no weight
+        x[1, :2] = 0.0, -20.0                               # 28 octaves below
+        last[1] = 1
+        some = min(vocab - 1, 3000)
+        x[2, g.permutation(vocab)[:some]] = 0.0             # as many equal ones, nothing else
+        last[2] = np.flatnonzero(x[2] == 0.0)[-1]
+        x[3] = 1.5                                          # all equal
+        last[3] = vocab - 1
+        at = g.choice(vocab, 2, replace=False)
+        x[4, at] = 0.0, -10.0
+        last[4] = at[1]
+        token, _ = sample(x, typ, u=u)
+        assert token.tolist() == last.tolist(), vocab
+        token, _ = sample(x, typ, u=u, T=[1.0, 0.4, 1.0, 1.0, 0.1], k=[0, 2, some, vocab // 2 + 1, 0])
+        assert token.tolist() == [0, 0, last[2], vocab // 2, at[0]], vocab
