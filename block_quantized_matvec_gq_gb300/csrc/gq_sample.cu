@@ -30,7 +30,8 @@
 //          share.
 //
 // What bounds it.  160 rows of 262144 f32 logits (168 MB), settings of all kinds,
-// 101 us: the scan 55 (issue; 20 instructions an element where weights are summed),
+// 101 us: the scan 55 (issue; 30 instructions an element on average: 10 to read it
+// and find the largest, 11 for the list, 22 for the weight where weights are summed),
 // the pick some 13, the search of the four to seven rows that need it 25: the pass
 // over the row 6, joining the histograms 4.6, and rounds over little data, barriers
 // of the cluster, and fetching code that runs once (unrolled passes took 16 us more
